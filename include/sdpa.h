@@ -260,6 +260,109 @@ SDPA_API int sdpa_rotary(sdpa_dtype dtype, int32_t B, int32_t N, int32_t S, int3
                          const int64_t* position_ids, int32_t rotary_dim, int32_t interleaved,
                          sdpa_stream_t stream);
 
+/* RMS norm of every query and key head followed by the rotary embedding, in one pass: with
+ * r = (mean(x^2) + eps)^-1/2 over the D channels of a head, u = x r weight and
+ * y = Rot(u), the rotation of sdpa_rotary; fp32 arithmetic, one rounding to dtype. */
+typedef struct {
+  int32_t struct_size;          /* must be sizeof(sdpa_qk_norm_params)                       */
+  int32_t B, Nq, Nkv, S, D;     /* D <= 256                                                  */
+  sdpa_dtype dtype;             /* element type of every tensor below                        */
+  sdpa_view q, k;               /* (B, Nq, S, D), (B, Nkv, S, D): the heads before the norm  */
+  const void* q_weight;         /* (D)                                                       */
+  const void* k_weight;         /* (D)                                                       */
+  float eps;                    /* finite, >= 0                                              */
+  /* Rotation as for sdpa_rotary: rank-2 caches (rotary_max_pos, R/2) with position_ids
+   * (B, S) int64, or rank-3 caches (B, S, R/2) without (rotary_max_pos = B*S); R = rotary_dim
+   * (0: D).  rotary_cos == NULL: no rotation. */
+  const void* rotary_cos;
+  const void* rotary_sin;
+  int64_t rotary_max_pos;
+  const int64_t* position_ids;
+  int32_t rotary_dim;
+  int32_t rotary_interleaved;
+} sdpa_qk_norm_params;
+
+/* Writes q_out (B, Nq, S, D) and k_out (B, Nkv, S, D).  An output may be its input's own view
+ * (in place) and overlaps nothing else.  Positions outside the cache are reported by
+ * sdpa_query_status as SDPA_ERR_INVALID (and clamped).  B*S*(Nq+Nkv) < 2^31.  Views whose
+ * pointers and strides are 16-byte multiples take the vector kernel. */
+SDPA_API int sdpa_qk_norm_rotary(const sdpa_qk_norm_params* p, sdpa_view q_out, sdpa_view k_out, sdpa_stream_t stream);
+
+/* Gradient of sdpa_qk_norm_rotary.  dq_out, dk_out: upstream gradients of its outputs; dq, dk:
+ * gradients of p->q, p->k; dq_weight, dk_weight: (D) gradients of the weights, summed over
+ * batch, tokens and heads in fp32 in a fixed order (results do not vary from run to run).
+ * With xh = x r and g = Rot^T(dy):  dweight = sum g xh,  dx = r (g w - xh mean(g w xh)).
+ * dq may be dq_out's own view and dk dk_out's; outputs overlap nothing else.  workspace:
+ * sdpa_qk_norm_workspace_size(p) bytes, 256-byte aligned. */
+SDPA_API int sdpa_qk_norm_rotary_bwd(const sdpa_qk_norm_params* p, sdpa_view dq_out, sdpa_view dk_out, sdpa_view dq,
+                                     sdpa_view dk, void* dq_weight, void* dk_weight, void* workspace,
+                                     size_t workspace_bytes, sdpa_stream_t stream);
+SDPA_API size_t sdpa_qk_norm_workspace_size(const sdpa_qk_norm_params* p);
+
+/* A ragged batch over a paged key/value cache.  The new tokens of all sequences lie one after
+ * another in packed rows; sequence b brings n_b = cu_new[b+1] - cu_new[b] of them and has
+ * T_b = kv_lens[b] keys, the new ones last: new token i sits at key position T_b - n_b + i.
+ * Key j lies in page page_table[b][j / page_size], slot j % page_size.  Offsets, lengths and
+ * page ids are device data and are checked on the device: sdpa_query_status reports one that is
+ * out of range as SDPA_ERR_INVALID, and nothing outside the given buffers is touched. */
+typedef struct {
+  int32_t struct_size;          /* must be sizeof(sdpa_paged_params)                         */
+  int32_t B;                    /* sequences                                                 */
+  int32_t tokens;               /* packed rows                                               */
+  int32_t Nq, Nkv, H, Hv;       /* as in sdpa_params                                         */
+  sdpa_dtype dtype;             /* element type of every tensor                              */
+  int32_t num_pages, page_size, max_pages;
+  sdpa_view k_pages, v_pages;   /* (num_pages, Nkv, page_size, H / Hv), any order of the first
+                                   three axes in memory                                      */
+  const int32_t* page_table;    /* (B, max_pages), rows page_table_stride apart; entries past a
+                                   sequence's keys are not read                              */
+  int64_t page_table_stride;
+  const int32_t* kv_lens;       /* (B): keys of each sequence, its new tokens included       */
+  const int32_t* cu_new;        /* (B + 1), cu_new[0] = 0, not decreasing; or NULL: every
+                                   sequence brings tokens / B rows                           */
+  /* sdpa_paged_append: rotation of the new keys at their positions, rank-2 caches
+   * (rotary_max_pos, R/2), R = rotary_dim (0: H).  rotary_cos == NULL: none. */
+  const void* rotary_cos;
+  const void* rotary_sin;
+  int64_t rotary_max_pos;
+  int32_t rotary_dim;
+  int32_t rotary_interleaved;
+  /* sdpa_paged_attn: as in sdpa_params; causal is NONE or LOWER_RIGHT (position T_b - n_b + i) */
+  int32_t has_scale;            /* 0: scale = 1/sqrt(H)                                      */
+  float scale;
+  float softcap;                /* <= 0: off                                                 */
+  int32_t causal;
+  int64_t window;               /* -1: unlimited; > 0: keys pos-window+1 .. pos (needs causal)*/
+  const void* head_sink;        /* (Nq), or NULL                                             */
+  int32_t max_new;              /* hint: most new tokens of one sequence (0: unknown).  It picks
+                                   the kernel; results hold for any value                    */
+} sdpa_paged_params;
+
+/* Writes the new keys k (packed, (tokens, Nkv, H): stride_s per token, stride_n per head,
+ * stride_b unused), turned by the angle of their position, and values v into the slots of
+ * positions T_b - n_b .. T_b - 1.  The pages must have room (T_b <= max_pages * page_size) and
+ * the slots of different new tokens must differ; every other slot keeps its contents.  Rows
+ * behind cu_new[B] are ignored; a token whose page id is out of range, and a sequence whose
+ * offsets or length are (T_b < n_b among them), is skipped and reported.  A position outside the
+ * rotary cache is reported and clamped.
+ * k_pages and v_pages may interleave (one pool holding both) but share no element.
+ * Alignment: pointers 16-byte aligned; strides of k, v and the pages multiples of 8 (16-bit) or
+ * 4 (f32); H and Hv such multiples, at most 256. */
+SDPA_API int sdpa_paged_append(const sdpa_paged_params* p, sdpa_view k, sdpa_view v, sdpa_stream_t stream);
+
+/* Attention of the new tokens q (packed, (tokens, Nq, H)) over the pages of their sequences,
+ * the new keys included (append them first): y (packed, (tokens, Nq, Hv)) with the scale,
+ * softcap, causal, window and head_sink rules of sdpa_attn_fwd.  One call takes single tokens,
+ * a few, chunks and any mixture.  A row with no admitted key is written as zeros; rows behind
+ * cu_new[B] are left as they were; what lies in slots past a sequence's keys does not matter
+ * (NaN included).  Lengths out of range are clamped and reported; a page id out of range is
+ * reported and its keys and values read as zeros.
+ * workspace: sdpa_paged_workspace_size(p) bytes (it depends on sizes, not on lengths), 256-byte
+ * aligned.  Alignment as for sdpa_paged_append. */
+SDPA_API int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace,
+                             size_t workspace_bytes, sdpa_stream_t stream);
+SDPA_API size_t sdpa_paged_workspace_size(const sdpa_paged_params* p);
+
 /* present[b, n, 0:P] = past[b, n, :]; present[b, n, P:P+L] = cur[b, n, :] (+ bias[n*D:(n+1)*D]
  * rounded once to dtype when bias is non-NULL).  (class Attention, past_key/past_value
  * and Result.present_key; MHA: present holds P+L positions; GQA: present holds the whole
@@ -271,9 +374,9 @@ SDPA_API int sdpa_kv_concat(sdpa_dtype dtype, int32_t B, int32_t N, int32_t P, i
                    sdpa_stream_t stream);
 
 /* Synchronises `stream`, then reads and clears the current device's status words: set when
- * a bounded wait of a kernel expires (SDPA_ERR_TIMEOUT) or a rotary position falls outside
- * its cache (SDPA_ERR_INVALID).  Returns SDPA_OK, one of those codes, or SDPA_ERR_CUDA when
- * the synchronisation itself failed. */
+ * a bounded wait of a kernel expires (SDPA_ERR_TIMEOUT), or a rotary position falls outside its
+ * cache or a page id, length or offset of a paged call outside its range (SDPA_ERR_INVALID).
+ * Returns SDPA_OK, one of those codes, or SDPA_ERR_CUDA when the synchronisation itself failed. */
 SDPA_API int sdpa_query_status(sdpa_stream_t stream);
 
 /* Message for the last error on the calling thread ("" when none).  Valid until the next

@@ -12,6 +12,8 @@
 #include <string>
 
 #include "internal.h"
+#include "paged.h"
+#include "paged_sched.cuh"
 #include "prefill_tc.h"
 
 namespace sdpa {
@@ -389,6 +391,222 @@ int run_concat_present(const Problem& r, sdpa_dtype dt, cudaStream_t st) {
   return e == cudaSuccess ? SDPA_OK : cuda_fail(e, "kv_concat launch");
 }
 
+// The rotary arguments shared by the query/key norm and the paged append: R (0: no rotation).
+int check_rotation(int dt, int D, const void* cos_c, const void* sin_c, int64_t max_pos, int rotary_dim, int interleaved,
+                   int* R) {
+  *R = 0;
+  if ((cos_c == nullptr) != (sin_c == nullptr))
+    return fail(SDPA_ERR_INVALID, "rotary_cos and rotary_sin must be given together");
+  if (!cos_c) {
+    if (rotary_dim) return fail(SDPA_ERR_NULL, "rotary_dim %d without rotary_cos / rotary_sin", rotary_dim);
+    return SDPA_OK;
+  }
+  const int r = rotary_dim ? rotary_dim : D;
+  if (r < 2 || r > D || r % 2)
+    return fail(SDPA_ERR_INVALID, "rotary_dim %d: must be even and in [2, D=%d] (0 means D)", rotary_dim, D);
+  if (interleaved != 0 && interleaved != 1) return fail(SDPA_ERR_INVALID, "rotary_interleaved must be 0 or 1");
+  if (max_pos < 1 || max_pos > ((int64_t)1 << 40)) return fail(SDPA_ERR_SHAPE, "rotary_max_pos %lld out of range", (long long)max_pos);
+  if (((uintptr_t)cos_c | (uintptr_t)sin_c) % esize(dt))
+    return fail(SDPA_ERR_ALIGNMENT, "rotary caches not aligned to the element size");
+  *R = r;
+  return SDPA_OK;
+}
+
+bool same_view(const sdpa_view& a, const sdpa_view& b) {
+  return a.data == b.data && a.stride_b == b.stride_b && a.stride_n == b.stride_n && a.stride_s == b.stride_s;
+}
+
+View to_view(const sdpa_view& v) { return View{v.data, v.stride_b, v.stride_n, v.stride_s}; }
+
+// Query/key norm: what the forward and the backward check alike.  ext: extents of q and k.
+int check_norm(const sdpa_qk_norm_params* p, NormJob* j, Extent ext[2]) {
+  if (!p) return fail(SDPA_ERR_NULL, "params is NULL");
+  if (p->struct_size != (int32_t)sizeof(sdpa_qk_norm_params))
+    return fail(SDPA_ERR_INVALID, "struct_size %d != sizeof(sdpa_qk_norm_params) %d", p->struct_size,
+                (int)sizeof(sdpa_qk_norm_params));
+  const int dt = p->dtype;
+  if (dt != SDPA_F32 && dt != SDPA_F16 && dt != SDPA_BF16) return fail(SDPA_ERR_INVALID, "dtype %d", dt);
+  if (p->B < 0 || p->S < 0 || p->Nq < 1 || p->Nkv < 1 || p->D < 1)
+    return fail(SDPA_ERR_SHAPE, "bad sizes (B=%d S=%d Nq=%d Nkv=%d D=%d)", p->B, p->S, p->Nq, p->Nkv, p->D);
+  if (p->D > 256) return fail(SDPA_ERR_UNSUPPORTED, "head sizes up to 256 (D=%d)", p->D);
+  if (!std::isfinite(p->eps) || p->eps < 0.f) return fail(SDPA_ERR_INVALID, "eps must be finite and not negative");
+  if ((double)p->B * p->S * ((double)p->Nq + p->Nkv) > 2147483647.0)
+    return fail(SDPA_ERR_OVERFLOW, "B*S*(Nq+Nkv) exceeds 2^31-1");
+  if (!p->q_weight || !p->k_weight) return fail(SDPA_ERR_NULL, "q_weight / k_weight is NULL");
+  if (((uintptr_t)p->q_weight | (uintptr_t)p->k_weight) % esize(dt))
+    return fail(SDPA_ERR_ALIGNMENT, "weights not aligned to the element size");
+  int R, rc;
+  if ((rc = check_rotation(dt, p->D, p->rotary_cos, p->rotary_sin, p->rotary_max_pos, p->rotary_dim,
+                           p->rotary_interleaved, &R)))
+    return rc;
+  if (R && !p->position_ids && p->rotary_max_pos != (int64_t)p->B * p->S && (int64_t)p->B * p->S > 0)
+    return fail(SDPA_ERR_SHAPE, "without position_ids the caches are (B, S, R/2): rotary_max_pos must be B*S=%lld",
+                (long long)p->B * p->S);
+  if ((uintptr_t)p->position_ids & 7u) return fail(SDPA_ERR_ALIGNMENT, "position_ids not 8-byte aligned");
+  if ((rc = check_view(p->q, "q", dt, p->B, p->Nq, p->S, p->D, true, false, &ext[0]))) return rc;
+  if ((rc = check_view(p->k, "k", dt, p->B, p->Nkv, p->S, p->D, true, false, &ext[1]))) return rc;
+  for (const sdpa_view* v : {&p->q, &p->k})
+    if ((uintptr_t)v->data % esize(dt)) return fail(SDPA_ERR_ALIGNMENT, "q / k not aligned to the element size");
+  *j = NormJob{};
+  j->side[0].x = to_view(p->q);
+  j->side[1].x = to_view(p->k);
+  j->side[0].w = p->q_weight;
+  j->side[1].w = p->k_weight;
+  j->side[0].N = p->Nq;
+  j->side[1].N = p->Nkv;
+  j->B = p->B; j->S = p->S; j->tokens = p->B * p->S; j->D = p->D; j->R = R;
+  j->interleaved = R ? p->rotary_interleaved : 0;
+  j->cos_c = p->rotary_cos; j->sin_c = p->rotary_sin;
+  j->positions = R ? p->position_ids : nullptr;
+  j->max_pos = p->rotary_max_pos;
+  j->eps = p->eps;
+  j->inv_D = 1.f / (float)p->D;
+  return SDPA_OK;
+}
+
+// Extents of the side inputs of the norm.
+void norm_side_inputs(const sdpa_qk_norm_params* p, const NormJob& j, Extent out[5]) {
+  const int es = esize(p->dtype);
+  const size_t cache = j.R ? (size_t)j.max_pos * (j.R / 2) * es : 0;
+  out[0] = flat(p->q_weight, (size_t)p->D * es, "q_weight");
+  out[1] = flat(p->k_weight, (size_t)p->D * es, "k_weight");
+  out[2] = flat(p->rotary_cos, cache, "rotary_cos");
+  out[3] = flat(p->rotary_sin, cache, "rotary_sin");
+  out[4] = flat(j.positions, (size_t)j.tokens * 8, "position_ids");
+}
+
+// The paged cache and the ragged batch, as both paged entry points check them.
+int check_paged(const sdpa_paged_params* p, Paged* g, Extent ext[2]) {
+  if (!p) return fail(SDPA_ERR_NULL, "params is NULL");
+  if (p->struct_size != (int32_t)sizeof(sdpa_paged_params))
+    return fail(SDPA_ERR_INVALID, "struct_size %d != sizeof(sdpa_paged_params) %d", p->struct_size,
+                (int)sizeof(sdpa_paged_params));
+  const int dt = p->dtype;
+  if (dt != SDPA_F32 && dt != SDPA_F16 && dt != SDPA_BF16) return fail(SDPA_ERR_INVALID, "dtype %d", dt);
+  if (p->B < 0 || p->tokens < 0 || p->num_pages < 0 || p->max_pages < 0)
+    return fail(SDPA_ERR_SHAPE, "negative size (B=%d tokens=%d num_pages=%d max_pages=%d)", p->B, p->tokens, p->num_pages,
+                p->max_pages);
+  if (p->Nq < 1 || p->Nkv < 1 || p->H < 1 || p->Hv < 1 || p->page_size < 1)
+    return fail(SDPA_ERR_SHAPE, "Nq, Nkv, H, Hv and page_size must be >= 1");
+  if (p->Nq % p->Nkv != 0)
+    return fail(SDPA_ERR_SHAPE, "q heads (%d) must be a multiple of kv heads (%d)", p->Nq, p->Nkv);
+  const int ve = vec_elems(dt);
+  if (p->H > 256 || p->Hv > 256 || p->H % ve || p->Hv % ve)
+    return fail(SDPA_ERR_UNSUPPORTED, "head sizes must be multiples of %d and at most 256 (H=%d Hv=%d)", ve, p->H, p->Hv);
+  if ((int64_t)p->max_pages * p->page_size > ((int64_t)1 << 30))
+    return fail(SDPA_ERR_OVERFLOW, "max_pages * page_size exceeds 2^30 keys");
+  if ((int64_t)p->tokens * p->Nq > ((int64_t)1 << 30)) return fail(SDPA_ERR_OVERFLOW, "tokens * Nq exceeds 2^30");
+  if (p->B > (1 << 24)) return fail(SDPA_ERR_OVERFLOW, "B exceeds 2^24");
+  if (!p->cu_new && p->B > 0 && p->tokens % p->B)
+    return fail(SDPA_ERR_SHAPE, "without cu_new every sequence brings tokens / B rows: tokens=%d, B=%d", p->tokens, p->B);
+  if (!p->cu_new && p->B == 0 && p->tokens) return fail(SDPA_ERR_SHAPE, "tokens=%d but B=0", p->tokens);
+  if (p->B > 0 && p->tokens > 0) {
+    if (!p->kv_lens) return fail(SDPA_ERR_NULL, "kv_lens is NULL");
+    if (!p->page_table && p->max_pages > 0) return fail(SDPA_ERR_NULL, "page_table is NULL");
+  }
+  if (((uintptr_t)p->kv_lens | (uintptr_t)p->cu_new | (uintptr_t)p->page_table) & 3u)
+    return fail(SDPA_ERR_ALIGNMENT, "kv_lens, cu_new and page_table must be 4-byte aligned");
+  if (p->B > 1 && p->page_table_stride < p->max_pages)
+    return fail(SDPA_ERR_INVALID, "page_table_stride %lld is smaller than max_pages %d", (long long)p->page_table_stride,
+                p->max_pages);
+  if (p->page_table_stride < 0 || p->page_table_stride > ((int64_t)1 << 40))
+    return fail(SDPA_ERR_OVERFLOW, "page_table_stride %lld out of range", (long long)p->page_table_stride);
+  int rc;
+  if ((rc = check_view(p->k_pages, "k_pages", dt, p->num_pages, p->Nkv, p->page_size, p->H, true, false, &ext[0]))) return rc;
+  if ((rc = check_view(p->v_pages, "v_pages", dt, p->num_pages, p->Nkv, p->page_size, p->Hv, true, false, &ext[1]))) return rc;
+  if ((rc = check_aligned_view(p->k_pages, "k_pages", dt))) return rc;
+  if ((rc = check_aligned_view(p->v_pages, "v_pages", dt))) return rc;
+  *g = Paged{};
+  g->B = p->B; g->tokens = p->tokens; g->Nq = p->Nq; g->Nkv = p->Nkv; g->H = p->H; g->Hv = p->Hv;
+  g->group = p->Nq / p->Nkv;
+  g->num_pages = p->num_pages; g->page_size = p->page_size; g->max_pages = p->max_pages;
+  g->cap = p->max_pages * p->page_size;
+  paged_magic(p->page_size, &g->page_mul, &g->page_shift);
+  g->kp = to_view(p->k_pages); g->vp = to_view(p->v_pages);
+  g->table = p->page_table; g->table_stride = p->page_table_stride;
+  g->lens = p->kv_lens; g->cu = p->cu_new;
+  g->uniform = p->cu_new || !p->B ? 0 : p->tokens / p->B;
+  return SDPA_OK;
+}
+
+void paged_side_inputs(const sdpa_paged_params* p, Extent out[3]) {
+  out[0] = flat(p->kv_lens, (size_t)p->B * 4, "kv_lens");
+  out[1] = flat(p->cu_new, ((size_t)p->B + 1) * 4, "cu_new");
+  out[2] = p->B && p->max_pages
+               ? flat(p->page_table, ((size_t)(p->B - 1) * (size_t)p->page_table_stride + p->max_pages) * 4, "page_table")
+               : Extent{};
+}
+
+// A view with its sizes, for telling interleaved views apart.
+struct Shaped {
+  sdpa_view v;
+  int64_t ext[3];                 // batch / page, head, row / slot
+  int64_t D;
+  Extent e;
+};
+
+// Whether two views share no element although their byte ranges may interleave (heads of one
+// packed projection, keys and values of one pool): with equal strides, along some axis each
+// view's part below that axis fits beside the other's in one step.
+bool disjoint(const Shaped& a, const Shaped& b, int es) {
+  if (!overlap(a.e, b.e)) return true;
+  const int64_t sa[3] = {a.v.stride_b, a.v.stride_n, a.v.stride_s}, sb[3] = {b.v.stride_b, b.v.stride_n, b.v.stride_s};
+  for (int x = 0; x < 3; ++x)
+    if (sa[x] != sb[x] && (a.ext[x] > 1 || b.ext[x] > 1)) return false;
+  const int64_t bytes = (int64_t)((intptr_t)b.v.data - (intptr_t)a.v.data);
+  if (bytes % es) return false;
+  const int64_t delta = bytes / es;
+  for (int x = 0; x < 3; ++x) {
+    const int64_t st = sa[x];
+    if ((a.ext[x] < 2 && b.ext[x] < 2) || st <= 0) continue;
+    int64_t fa = a.D, fb = b.D;
+    bool ok = true;
+    for (int y = 0; y < 3; ++y) {
+      if (y == x || (a.ext[y] < 2 && b.ext[y] < 2)) continue;
+      if (sa[y] < st) {
+        fa += (a.ext[y] - 1) * sa[y];
+        fb += (b.ext[y] - 1) * sa[y];
+      } else {
+        ok = ok && sa[y] % st == 0;
+      }
+    }
+    const int64_t d = ((delta % st) + st) % st;
+    if (ok && d >= fa && d + fb <= st) return true;
+  }
+  return false;
+}
+
+Shaped pool_shape(const sdpa_paged_params* p, const sdpa_view& v, int64_t D, const Extent& e) {
+  return Shaped{v, {p->num_pages, p->Nkv, p->page_size}, D, e};
+}
+Shaped head_shape(const sdpa_qk_norm_params* p, const sdpa_view& v, int N, const Extent& e) {
+  return Shaped{v, {p->B, N, p->S}, p->D, e};
+}
+
+int check_paged_attn(const sdpa_paged_params* p, PagedAttn* a, Extent ext[2]) {
+  int rc;
+  if ((rc = check_paged(p, &a->g, ext))) return rc;
+  if (p->causal != SDPA_CAUSAL_NONE && p->causal != SDPA_CAUSAL_LOWER_RIGHT)
+    return fail(SDPA_ERR_INVALID, "causal mode %d: the new tokens are the last ones of their sequence (none or lower right)",
+                p->causal);
+  if (p->window == 0 || p->window < -1 || p->window > 2147483647LL)
+    return fail(SDPA_ERR_INVALID, "window %lld: must be -1 or in [1, INT32_MAX]", (long long)p->window);
+  if (p->window > 0 && p->causal == SDPA_CAUSAL_NONE) return fail(SDPA_ERR_INVALID, "a local window needs causal masking");
+  if (!std::isfinite(p->softcap)) return fail(SDPA_ERR_INVALID, "softcap must be finite");
+  if (p->has_scale && !std::isfinite(p->scale)) return fail(SDPA_ERR_INVALID, "scale must be finite");
+  if (p->max_new < 0) return fail(SDPA_ERR_SHAPE, "max_new %d is negative", p->max_new);
+  if ((uintptr_t)p->head_sink % esize(p->dtype)) return fail(SDPA_ERR_ALIGNMENT, "head_sink not aligned to the element size");
+  a->q = a->y = View{};
+  a->scale = p->has_scale ? p->scale : (float)(1.0 / std::sqrt((double)p->H));
+  a->softcap = p->softcap > 0.f ? p->softcap : 0.f;
+  a->causal = p->causal != SDPA_CAUSAL_NONE;
+  // a window as wide as the table excludes nothing
+  a->window = p->window > 0 && p->window < (int64_t)a->g.cap ? (int)p->window : 0;
+  a->head_sink = p->head_sink;
+  a->max_new = a->g.uniform ? a->g.uniform : (p->max_new ? std::min(p->max_new, p->tokens) : p->tokens);
+  return SDPA_OK;
+}
+
 }  // namespace
 }  // namespace sdpa
 
@@ -688,27 +906,209 @@ int sdpa_attn_bwd(const sdpa_params* p, sdpa_view dy, sdpa_view dq, sdpa_view dk
   return SDPA_OK;
 }
 
+size_t sdpa_qk_norm_workspace_size(const sdpa_qk_norm_params* p) {
+  NormJob j;
+  Extent ext[2];
+  if (check_norm(p, &j, ext) != SDPA_OK) return 0;
+  return align256((size_t)kNormBwdMaxBlocks * p->D * sizeof(float));
+}
+
+int sdpa_qk_norm_rotary(const sdpa_qk_norm_params* p, sdpa_view q_out, sdpa_view k_out, sdpa_stream_t stream) {
+  NormJob j;
+  Extent in[2], out[2], side[5];
+  int rc;
+  if ((rc = check_norm(p, &j, in))) return rc;
+  const int dt = p->dtype;
+  if ((rc = check_view(q_out, "q_out", dt, p->B, p->Nq, p->S, p->D, true, false, &out[0]))) return rc;
+  if ((rc = check_view(k_out, "k_out", dt, p->B, p->Nkv, p->S, p->D, true, false, &out[1]))) return rc;
+  if (((uintptr_t)q_out.data | (uintptr_t)k_out.data) % esize(dt))
+    return fail(SDPA_ERR_ALIGNMENT, "outputs not aligned to the element size");
+  norm_side_inputs(p, j, side);
+  const int es = esize(dt);
+  const Shaped si[2] = {head_shape(p, p->q, p->Nq, in[0]), head_shape(p, p->k, p->Nkv, in[1])};
+  const Shaped so[2] = {head_shape(p, q_out, p->Nq, out[0]), head_shape(p, k_out, p->Nkv, out[1])};
+  for (int o = 0; o < 2; ++o) {
+    for (int i = 0; i < 2; ++i)
+      if (!(o == i && same_view(so[o].v, si[i].v)) && !disjoint(so[o], si[i], es))
+        return fail(SDPA_ERR_ALIAS, "output %s overlaps input %s", out[o].name, in[i].name);
+    for (const Extent& e : side)
+      if (overlap(out[o], e)) return fail(SDPA_ERR_ALIAS, "output %s overlaps input %s", out[o].name, e.name);
+  }
+  if (!disjoint(so[0], so[1], es)) return fail(SDPA_ERR_ALIAS, "outputs q_out / k_out overlap");
+  g_error.clear();
+  if (j.tokens == 0) return SDPA_OK;
+  j.side[0].y = to_view(q_out);
+  j.side[1].y = to_view(k_out);
+  const cudaError_t e = launch_qk_norm((sdpa_dtype)dt, j, nullptr, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rotary launch");
+  g_kernel = "qk_norm_rotary";
+  return SDPA_OK;
+}
+
+int sdpa_qk_norm_rotary_bwd(const sdpa_qk_norm_params* p, sdpa_view dq_out, sdpa_view dk_out, sdpa_view dq, sdpa_view dk,
+                            void* dq_weight, void* dk_weight, void* workspace, size_t workspace_bytes,
+                            sdpa_stream_t stream) {
+  NormJob j;
+  Extent in[4], out[4], side[5];
+  int rc;
+  if ((rc = check_norm(p, &j, in))) return rc;
+  const int dt = p->dtype;
+  if ((rc = check_view(dq_out, "dq_out", dt, p->B, p->Nq, p->S, p->D, true, false, &in[2]))) return rc;
+  if ((rc = check_view(dk_out, "dk_out", dt, p->B, p->Nkv, p->S, p->D, true, false, &in[3]))) return rc;
+  if ((rc = check_view(dq, "dq", dt, p->B, p->Nq, p->S, p->D, true, false, &out[0]))) return rc;
+  if ((rc = check_view(dk, "dk", dt, p->B, p->Nkv, p->S, p->D, true, false, &out[1]))) return rc;
+  if (!dq_weight || !dk_weight) return fail(SDPA_ERR_NULL, "dq_weight / dk_weight is NULL");
+  for (const void* ptr : {(const void*)dq_out.data, (const void*)dk_out.data, (const void*)dq.data, (const void*)dk.data,
+                          (const void*)dq_weight, (const void*)dk_weight})
+    if ((uintptr_t)ptr % esize(dt)) return fail(SDPA_ERR_ALIGNMENT, "gradients not aligned to the element size");
+  out[2] = flat(dq_weight, (size_t)p->D * esize(dt), "dq_weight");
+  out[3] = flat(dk_weight, (size_t)p->D * esize(dt), "dk_weight");
+  norm_side_inputs(p, j, side);
+  const int es = esize(dt);
+  const Shaped si[4] = {head_shape(p, p->q, p->Nq, in[0]), head_shape(p, p->k, p->Nkv, in[1]),
+                        head_shape(p, dq_out, p->Nq, in[2]), head_shape(p, dk_out, p->Nkv, in[3])};
+  const Shaped so[4] = {head_shape(p, dq, p->Nq, out[0]), head_shape(p, dk, p->Nkv, out[1]),
+                        Shaped{sdpa_view{dq_weight, 0, 0, 0}, {1, 1, 1}, p->D, out[2]},
+                        Shaped{sdpa_view{dk_weight, 0, 0, 0}, {1, 1, 1}, p->D, out[3]}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 4; ++i) {
+      // dq may be written over dq_out, dk over dk_out, row by row
+      const bool in_place = o < 2 && i == o + 2 && same_view(so[o].v, si[i].v);
+      if (!in_place && !disjoint(so[o], si[i], es))
+        return fail(SDPA_ERR_ALIAS, "output %s overlaps input %s", out[o].name, in[i].name);
+    }
+    for (const Extent& e : side)
+      if (overlap(out[o], e)) return fail(SDPA_ERR_ALIAS, "output %s overlaps input %s", out[o].name, e.name);
+    for (int i = 0; i < o; ++i)
+      if (!disjoint(so[o], so[i], es)) return fail(SDPA_ERR_ALIAS, "outputs %s / %s overlap", out[i].name, out[o].name);
+  }
+  const size_t need = align256((size_t)kNormBwdMaxBlocks * p->D * sizeof(float));
+  if (!workspace || workspace_bytes < need)
+    return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+  if ((uintptr_t)workspace & 255u) return fail(SDPA_ERR_ALIGNMENT, "workspace not 256-byte aligned");
+  const Extent ws = flat(workspace, need, "workspace");
+  for (const Extent& o : out)
+    if (overlap(ws, o)) return fail(SDPA_ERR_ALIAS, "workspace overlaps output %s", o.name);
+  for (const Extent& i : in)
+    if (overlap(ws, i)) return fail(SDPA_ERR_ALIAS, "workspace overlaps input %s", i.name);
+  g_error.clear();
+  j.side[0].dy = to_view(dq_out);
+  j.side[1].dy = to_view(dk_out);
+  j.side[0].y = to_view(dq);
+  j.side[1].y = to_view(dk);
+  j.side[0].dw = dq_weight;
+  j.side[1].dw = dk_weight;
+  const cudaError_t e = launch_qk_norm((sdpa_dtype)dt, j, reinterpret_cast<float*>(workspace),
+                                       reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rotary backward launch");
+  g_kernel = "qk_norm_rotary_bwd";
+  return SDPA_OK;
+}
+
+int sdpa_paged_append(const sdpa_paged_params* p, sdpa_view k, sdpa_view v, sdpa_stream_t stream) {
+  Paged g;
+  Extent pool[2], ek, ev, side[3];
+  int rc;
+  if ((rc = check_paged(p, &g, pool))) return rc;
+  const int dt = p->dtype;
+  PagedRot rot{};
+  if ((rc = check_rotation(dt, p->H, p->rotary_cos, p->rotary_sin, p->rotary_max_pos, p->rotary_dim,
+                           p->rotary_interleaved, &rot.R)))
+    return rc;
+  if ((rc = check_view(k, "k", dt, 1, p->Nkv, p->tokens, p->H, true, false, &ek))) return rc;
+  if ((rc = check_view(v, "v", dt, 1, p->Nkv, p->tokens, p->Hv, true, false, &ev))) return rc;
+  if ((rc = check_aligned_view(k, "k", dt))) return rc;
+  if ((rc = check_aligned_view(v, "v", dt))) return rc;
+  paged_side_inputs(p, side);
+  const size_t cache = rot.R ? (size_t)p->rotary_max_pos * (rot.R / 2) * esize(dt) : 0;
+  const Extent ins[] = {ek, ev, side[0], side[1], side[2], flat(p->rotary_cos, cache, "rotary_cos"),
+                        flat(p->rotary_sin, cache, "rotary_sin")};
+  for (const Extent& o : {pool[0], pool[1]})
+    for (const Extent& in : ins)
+      if (overlap(o, in)) return fail(SDPA_ERR_ALIAS, "output %s overlaps input %s", o.name, in.name);
+  if (!disjoint(pool_shape(p, p->k_pages, p->H, pool[0]), pool_shape(p, p->v_pages, p->Hv, pool[1]), esize(dt))) return fail(SDPA_ERR_ALIAS, "k_pages and v_pages overlap");
+  g_error.clear();
+  if (p->tokens == 0 || p->B == 0) return SDPA_OK;
+  rot.cos_c = p->rotary_cos; rot.sin_c = p->rotary_sin; rot.max_pos = p->rotary_max_pos;
+  rot.interleaved = rot.R ? p->rotary_interleaved : 0;
+  const cudaError_t e = launch_paged_append((sdpa_dtype)dt, g, to_view(k), to_view(v), rot,
+                                            reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_append launch");
+  g_kernel = "paged_append";
+  return SDPA_OK;
+}
+
+size_t sdpa_paged_workspace_size(const sdpa_paged_params* p) {
+  PagedAttn a;
+  Extent pool[2];
+  if (check_paged_attn(p, &a, pool) != SDPA_OK) return 0;
+  return paged_workspace(a, (sdpa_dtype)p->dtype);
+}
+
+int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace, size_t workspace_bytes,
+                    sdpa_stream_t stream) {
+  PagedAttn a;
+  Extent pool[2], eq, ey, side[3];
+  int rc;
+  if ((rc = check_paged_attn(p, &a, pool))) return rc;
+  const int dt = p->dtype;
+  if ((rc = check_view(q, "q", dt, 1, p->Nq, p->tokens, p->H, true, false, &eq))) return rc;
+  if ((rc = check_view(y, "y", dt, 1, p->Nq, p->tokens, p->Hv, true, false, &ey))) return rc;
+  if ((rc = check_aligned_view(q, "q", dt))) return rc;
+  if ((rc = check_aligned_view(y, "y", dt))) return rc;
+  const size_t need = paged_workspace(a, (sdpa_dtype)dt);
+  const Extent ws = flat(workspace, need, "workspace");
+  paged_side_inputs(p, side);
+  const Extent ins[] = {eq, pool[0], pool[1], side[0], side[1], side[2],
+                        flat(p->head_sink, (size_t)p->Nq * esize(dt), "head_sink")};
+  for (const Extent& in : ins) {
+    if (overlap(ey, in)) return fail(SDPA_ERR_ALIAS, "output y overlaps input %s", in.name);
+    if (overlap(ws, in)) return fail(SDPA_ERR_ALIAS, "workspace overlaps input %s", in.name);
+  }
+  if (overlap(ws, ey)) return fail(SDPA_ERR_ALIAS, "workspace overlaps output y");
+  if (!workspace || workspace_bytes < need)
+    return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+  if ((uintptr_t)workspace & 255u) return fail(SDPA_ERR_ALIGNMENT, "workspace not 256-byte aligned");
+  g_error.clear();
+  if (p->tokens == 0 || p->B == 0) return SDPA_OK;
+  a.q = to_view(q);
+  a.y = to_view(y);
+  const char* name = "";
+  const cudaError_t e = launch_paged_attn(a, (sdpa_dtype)dt, workspace, reinterpret_cast<cudaStream_t>(stream), &name);
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  g_kernel = name;
+  return SDPA_OK;
+}
+
 int sdpa_query_status(sdpa_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
-  int status = 0, rot_status = 0, qk_status = 0, bwd_status = 0;
+  int status = 0, rot_status = 0, qk_status = 0, bwd_status = 0, norm_status = 0, app_status = 0, paged_status = 0;
   e = take_prefill_status(&status);
   if (e == cudaSuccess) e = take_rotary_status(&rot_status);
   if (e == cudaSuccess) e = take_qk_status(&qk_status);
   if (e == cudaSuccess) e = take_bwd_status(&bwd_status);
+  if (e == cudaSuccess) e = take_norm_status(&norm_status);
+  if (e == cudaSuccess) e = take_paged_append_status(&app_status);
+  if (e == cudaSuccess) e = take_paged_attn_status(&paged_status);
   if (e != cudaSuccess) return cuda_fail(e, "status read");
   if (!status) status = qk_status;
   if (!status) status = bwd_status;
   // the bounds-checking build: the first failing index check of each kernel family
   int site = 0;
-  for (auto take : {take_bounds_prefill, take_bounds_decode, take_bounds_concat, take_bounds_simt}) {
+  for (auto take : {take_bounds_prefill, take_bounds_decode, take_bounds_concat, take_bounds_simt, take_bounds_norm,
+                    take_bounds_append, take_bounds_paged}) {
     int v = 0;
     if ((e = take(&v)) != cudaSuccess) return cuda_fail(e, "bounds status read");
     if (!site) site = v;
   }
   if (site) return fail(SDPA_ERR_BOUNDS, "an index check failed at site %d; the access was skipped", site);
   if (status) return fail(SDPA_ERR_TIMEOUT, "a bounded device wait expired (code %d)", status);
-  if (rot_status) return fail(SDPA_ERR_INVALID, "a rotary position fell outside its cos/sin cache");
+  if (rot_status || norm_status || (app_status & kPagedBadPosition))
+    return fail(SDPA_ERR_INVALID, "a rotary position fell outside its cos/sin cache");
+  if ((app_status | paged_status) & kPagedBadPage) return fail(SDPA_ERR_INVALID, "a page id fell outside [0, num_pages)");
+  if ((app_status | paged_status) & kPagedBadLength)
+    return fail(SDPA_ERR_INVALID, "kv_lens or cu_new contradict the batch or the page table's width");
   return SDPA_OK;
 }
 

@@ -1,0 +1,263 @@
+// How the attention over a paged cache is cut up, shared by its three kernels.
+//
+// A unit is TM consecutive packed rows (row r = token * group + head of the group) of one
+// (sequence, kv head); its cost is the number of TN-key tiles that some of its rows admits (at
+// least one, so that rows with no key are written too).  All units' tiles, laid end to end
+// (sequence, row block, kv head, tile), are dealt to the CTAs in equal contiguous shares, so
+// ragged lengths, few rows over many keys and many rows over few keys all fill the GPU alike,
+// and a CTA meets at most two units that it does not hold whole.  Those leave partial results
+// (m, l, unnormalised o) in two slots per CTA, which a second kernel joins.  The lengths stay on
+// the device: every CTA finds its share by summing the costs of all sequences.
+#pragma once
+
+#include "paged.h"
+#include "tc_ptx.cuh"
+
+namespace sdpa {
+
+// Where a CTA's share starts; tile > 0: inside a unit begun by an earlier CTA.
+struct ShareStart { int b, rb, kvh, tile; };
+
+struct PagedWs {
+  ShareStart* start;   // [ctas + 1]: the last entry counts the CTAs that have a share (in .b)
+  float* ml;           // [2 * ctas][TM][2]: running maximum (log2 units) and sum
+  float* o;            // [2 * ctas][TM][Hv]
+};
+__host__ __device__ inline size_t paged_ws_ml_off(int ctas) { return (((size_t)ctas + 1) * sizeof(ShareStart) + 255) & ~(size_t)255; }
+__host__ __device__ inline size_t paged_ws_o_off(int ctas, int tm) {
+  return paged_ws_ml_off(ctas) + (((size_t)2 * ctas * tm * 2 * sizeof(float) + 255) & ~(size_t)255);
+}
+inline size_t paged_ws_bytes(int ctas, int tm, int Hv) {
+  return paged_ws_o_off(ctas, tm) + (((size_t)2 * ctas * tm * Hv * sizeof(float) + 255) & ~(size_t)255);
+}
+inline PagedWs paged_ws(void* p, int ctas, int tm) {
+  char* c = reinterpret_cast<char*>(p);
+  return PagedWs{reinterpret_cast<ShareStart*>(c), reinterpret_cast<float*>(c + paged_ws_ml_off(ctas)),
+                 reinterpret_cast<float*>(c + paged_ws_o_off(ctas, tm))};
+}
+
+// CTAs per SM x most SMs a workspace is sized for.
+constexpr int kPagedMaxSms = 160;
+
+cudaError_t launch_paged_merge(const PagedAttn& a, sdpa_dtype dt, const PagedWs& ws, int ctas, int tm, cudaStream_t st);
+int paged_sms();
+// Fast division: the multiplier and shift of j / d for 0 <= j < 2^31.
+inline void paged_magic(int d, uint32_t* mul, uint32_t* shift) {
+  int l = 0;
+  while (((int64_t)1 << l) < d) ++l;
+  *shift = 31 + l;
+  *mul = (uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d);
+}
+
+#ifdef __CUDACC__
+// One row block of a sequence: rows, the keys some row admits, its tiles.
+struct RowBlock {
+  int row0, rows;      // packed rows of the sequence
+  int lo, hi;          // admitted keys [lo, hi] (hi < lo: none)
+  int tile0, tiles;    // first key tile, cost (>= 1)
+};
+template <int TM, int TN>
+__device__ __forceinline__ RowBlock row_block(const PagedAttn& a, const SeqInfo& s, int rb) {
+  RowBlock r;
+  const int all = s.n * a.g.group;
+  r.row0 = rb * TM;
+  r.rows = min(TM, all - r.row0);
+  const int i0 = r.row0 / a.g.group, i1 = (r.row0 + r.rows - 1) / a.g.group;
+  r.hi = a.causal ? s.T - s.n + i1 : s.T - 1;
+  r.lo = a.window > 0 ? max(0, s.T - s.n + i0 - a.window + 1) : 0;
+  r.tile0 = r.lo / TN;
+  r.tiles = r.hi >= r.lo ? r.hi / TN - r.tile0 + 1 : 1;
+  return r;
+}
+__device__ __forceinline__ int row_blocks(const PagedAttn& a, const SeqInfo& s, int TM) {
+  return (s.n * a.g.group + TM - 1) / TM;
+}
+
+// Admitted keys [lo, hi] of packed row r of a sequence (hi < lo: none).
+__device__ __forceinline__ void row_keys(const PagedAttn& a, const SeqInfo& s, int r, int& lo, int& hi) {
+  const int pos = s.T - s.n + r / a.g.group;
+  hi = a.causal ? pos : s.T - 1;
+  lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+}
+
+// Sum of the tile costs of sequence b's row blocks (one kv head), by one thread.
+template <int TM, int TN>
+__device__ __forceinline__ int seq_cost(const PagedAttn& a, const SeqInfo& s) {
+  int c = 0;
+  const int n = row_blocks(a, s, TM);
+  for (int rb = 0; rb < n; ++rb) c += row_block<TM, TN>(a, s, rb).tiles;
+  return c;
+}
+
+struct Share {
+  int64_t begin, count;    // the CTA's tiles of the whole
+  ShareStart at;
+  int active;              // CTAs that have a share
+};
+
+// Finds the share of CTA `cta` among `ctas`; called by all NT threads of the block.  min_share:
+// fewest tiles worth a CTA.
+template <int TM, int TN, int NT>
+__device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int ctas, int min_share, int* status) {
+  constexpr int kW = NT / 32;
+  __shared__ long long sh_sum[kW + 1];
+  __shared__ ShareStart sh_at;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  bool bad = false;
+
+  // costs of the sequences, NT at a time; sequences of several row blocks are summed by a warp
+  auto cost_of = [&](int b, SeqInfo& s) -> long long {
+    long long c = 0;
+    s = SeqInfo{0, 0, 0};
+    if (b < a.g.B) s = seq_info(a.g, b, bad);
+    const int nrb = row_blocks(a, s, TM);
+    if (nrb == 1) c = row_block<TM, TN>(a, s, 0).tiles;
+    unsigned many = __ballot_sync(0xffffffffu, nrb > 1);
+    while (many) {
+      const int src = __ffs(many) - 1;
+      many &= many - 1;
+      SeqInfo t;
+      t.t0 = 0;
+      t.n = __shfl_sync(0xffffffffu, s.n, src);
+      t.T = __shfl_sync(0xffffffffu, s.T, src);
+      const int n = row_blocks(a, t, TM);
+      long long part = 0;
+      for (int rb = lane; rb < n; rb += 32) part += row_block<TM, TN>(a, t, rb).tiles;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+      if (lane == src) c = part;
+    }
+    return c * a.g.Nkv;
+  };
+
+  long long total = 0;
+  SeqInfo s;
+  long long mine = 0;
+  for (int base = 0; base < a.g.B; base += NT) {
+    mine = cost_of(base + (int)threadIdx.x, s);
+    long long v = mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) sh_sum[warp] = v;
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < kW; ++w) total += sh_sum[w];
+    __syncthreads();
+  }
+  if (bad && cta == 0) atomicOr(status, kPagedBadLength);
+
+  Share r;
+  r.active = (int)min((long long)ctas, max(1ll, total / min_share));
+  if (total == 0) r.active = 0;
+  r.at = ShareStart{a.g.B, 0, 0, 0};
+  r.begin = r.count = 0;
+  if (cta >= r.active) return r;
+  r.begin = total * cta / r.active;
+  r.count = total * (cta + 1) / r.active - r.begin;
+
+  // the sequence that holds tile r.begin
+  long long before = 0;
+  for (int base = 0; base < a.g.B; base += NT) {
+    if (a.g.B > NT) mine = cost_of(base + (int)threadIdx.x, s);
+    long long v = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) sh_sum[warp] = v;
+    __syncthreads();
+    long long off = before, all = 0;
+#pragma unroll 1
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) off += sh_sum[w];
+      all += sh_sum[w];
+    }
+    const long long end = off + v, begin = end - mine;
+    // exactly one warp holds the tile; its lanes find the row block
+    const bool here = r.begin >= begin && r.begin < end;
+    const unsigned who = __ballot_sync(0xffffffffu, here);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      SeqInfo t;
+      t.t0 = 0;
+      t.n = __shfl_sync(0xffffffffu, s.n, src);
+      t.T = __shfl_sync(0xffffffffu, s.T, src);
+      const int n = row_blocks(a, t, TM);
+      long long o = r.begin - __shfl_sync(0xffffffffu, begin, src);
+      for (int rb0 = 0; rb0 < n; rb0 += 32) {
+        const int tiles = rb0 + lane < n ? row_block<TM, TN>(a, t, rb0 + lane).tiles : 0;
+        long long c = (long long)tiles * a.g.Nkv;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long u = __shfl_up_sync(0xffffffffu, c, d);
+          if (lane >= d) c += u;
+        }
+        const long long lo = c - (long long)tiles * a.g.Nkv;
+        if (o >= lo && o < c) {
+          const int k = (int)((o - lo) / tiles);
+          sh_at = ShareStart{base + warp * 32 + src, rb0 + lane, k, (int)(o - lo - (long long)k * tiles)};
+        }
+        const long long block = __shfl_sync(0xffffffffu, c, 31);
+        if (o < block) break;
+        o -= block;
+      }
+    }
+    __syncthreads();
+    before += all;
+    if (before > r.begin) break;
+  }
+  r.at = sh_at;
+  return r;
+}
+
+// Walks a share unit by unit.
+template <int TM, int TN>
+struct Walk {
+  int64_t left;
+  int b, rb, kvh, tile;
+  SeqInfo s;
+  RowBlock r;
+  bool first;
+  __device__ __forceinline__ Walk(const PagedAttn& a, const Share& sh)
+      : left(sh.count), b(sh.at.b), rb(sh.at.rb), kvh(sh.at.kvh), tile(sh.at.tile), first(true) {
+    if (left > 0) load(a);
+  }
+  __device__ __forceinline__ void load(const PagedAttn& a) {
+    bool bad = false;
+    s = seq_info(a.g, b, bad);
+    r = row_block<TM, TN>(a, s, rb);
+  }
+  __device__ __forceinline__ bool done() const { return left <= 0; }
+  // tiles of the present unit that belong to this CTA
+  __device__ __forceinline__ int take() const { return (int)min((int64_t)(r.tiles - tile), left); }
+  __device__ __forceinline__ bool begins() const { return tile == 0; }
+  __device__ __forceinline__ bool ends() const { return tile + take() == r.tiles; }
+  __device__ __forceinline__ bool whole() const { return begins() && ends(); }
+  __device__ __forceinline__ void next(const PagedAttn& a) {
+    left -= take();
+    tile = 0;
+    if (left <= 0) return;
+    if (++kvh < a.g.Nkv) return;
+    kvh = 0;
+    if (++rb < row_blocks(a, s, TM)) {
+      r = row_block<TM, TN>(a, s, rb);
+      return;
+    }
+    rb = 0;
+    bool bad = false;
+    while (++b < a.g.B) {
+      s = seq_info(a.g, b, bad);
+      if (s.n > 0) break;
+    }
+    if (b >= a.g.B) { left = 0; return; }
+    r = row_block<TM, TN>(a, s, 0);
+  }
+};
+
+// Lets the joining kernel be scheduled; it waits for this one's results itself.
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
+}  // namespace sdpa

@@ -1,0 +1,381 @@
+// Attention over a paged cache in fp32 arithmetic, for every type and head size, and the kernel
+// that joins the partial results of all three attention kernels.
+//
+// LPK lanes read one key or value row as 16-byte vectors; the 128 / LPK lane groups of a block
+// take different keys and keep their own running maximum, sum and accumulator of TM query rows,
+// joined in shared memory at the end of a unit.  It serves fp32 (whose sums the 16-bit tensor
+// products cannot carry) and head sizes that the tensor-core kernels do not tile.
+#include <algorithm>
+
+#include "paged_sched.cuh"
+
+namespace sdpa {
+
+static __device__ int g_paged_status;
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kTN = 64;          // keys per tile of the schedule
+constexpr int kCtasPerSm = 4;
+constexpr int kMinShare = 2;     // tiles
+
+// Final scale of row (head h): 1 / (l + sink term), 0 for a row with no key; m, l in log2 units.
+template <typename T>
+__device__ __forceinline__ float row_scale(const PagedAttn& a, int h, float m, float l) {
+  if (m == -INFINITY) return 0.f;
+  if (a.head_sink) l += exp2f(Elem<T>::to_f32(reinterpret_cast<const T*>(a.head_sink)[h]) * kLog2e - m);
+  return l > 0.f ? 1.f / l : 0.f;
+}
+
+template <typename T, int LPK, int NV, int TM>
+__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a, const PagedWs ws) {
+  constexpr int V = Elem<T>::kVec;
+  constexpr int KPI = kThreads / LPK;
+  constexpr int HM = LPK * NV * V;       // widest head
+  constexpr int kUnroll = 2;
+  extern __shared__ float smem[];        // [KPI][TM][HM]
+  __shared__ float sm_m[KPI][TM], sm_l[KPI][TM];
+  const Paged& g = a.g;
+  const int ctas = gridDim.x, cta = blockIdx.x;
+  const Share sh = find_share<TM, kTN, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
+  if (threadIdx.x == 0) {
+    if (cta == 0) ws.start[ctas].b = sh.active;
+    if (cta < sh.active) ws.start[cta] = sh.at;
+  }
+  pdl_launch_dependents();
+  const int grp = threadIdx.x / LPK, t = threadIdx.x % LPK;
+  const float cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+
+  for (Walk<TM, kTN> w(a, sh); !w.done(); w.next(a)) {
+    const int nr = w.r.rows;
+    float q[TM][NV * V], m[TM], l[TM], acc[TM][NV * V];
+    int lo[TM], hi[TM];
+#pragma unroll
+    for (int r = 0; r < TM; ++r) {
+      const int pr = w.r.row0 + min(r, nr - 1);
+      const T* row = reinterpret_cast<const T*>(a.q.p) +
+                     a.q.off(0, w.kvh * g.group + pr % g.group, w.s.t0 + pr / g.group);
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        const int c = (n * LPK + t) * V;
+        const uint4 u = c < g.H ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
+        unpack16<T>(u, q[r] + n * V);
+      }
+      row_keys(a, w.s, pr, lo[r], hi[r]);
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int e = 0; e < NV * V; ++e) acc[r][e] = 0.f;
+    }
+    const int64_t j_begin = (int64_t)(w.r.tile0 + w.tile) * kTN;
+    const int64_t j_end = min((int64_t)w.r.hi + 1, j_begin + (int64_t)w.take() * kTN);
+    const int32_t* table = g.table + (int64_t)w.b * g.table_stride;
+
+    for (int64_t base = j_begin; base < j_end; base += KPI * kUnroll) {
+      uint4 kv[kUnroll][NV], vv[kUnroll][NV];
+      int jj[kUnroll];
+      int id[kUnroll], slot[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t j = base + grp + u * KPI;
+        jj[u] = j < j_end ? (int)j : -1;
+        id[u] = -1;
+        slot[u] = 0;
+        if (jj[u] >= 0) {
+          const int pg = page_div(g, jj[u]);
+          slot[u] = jj[u] - pg * g.page_size;
+          id[u] = table[pg];
+          if (id[u] < 0 || id[u] >= g.num_pages) {
+            atomicOr(&g_paged_status, kPagedBadPage);
+            id[u] = -1;                    // read as zeros
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const T* kr = reinterpret_cast<const T*>(g.kp.p) + g.kp.off(id[u], w.kvh, slot[u]);
+        const T* vr = reinterpret_cast<const T*>(g.vp.p) + g.vp.off(id[u], w.kvh, slot[u]);
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+          const int c = (n * LPK + t) * V;
+          kv[u][n] = vv[u][n] = make_uint4(0u, 0u, 0u, 0u);
+          if (id[u] >= 0 && SDPA_IN_BOUNDS(jj[u] < g.cap && slot[u] < g.page_size, 521)) {
+            if (c < g.H) kv[u][n] = __ldg(reinterpret_cast<const uint4*>(kr + c));
+            if (c < g.Hv) vv[u][n] = __ldg(reinterpret_cast<const uint4*>(vr + c));
+          }
+        }
+      }
+      float s[TM][kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float kf[NV * V];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) unpack16<T>(kv[u][n], kf + n * V);
+#pragma unroll
+        for (int r = 0; r < TM; ++r) {
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < NV * V; ++e) dot = fmaf(q[r][e], kf[e], dot);
+#pragma unroll
+          for (int o = LPK / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+          if (a.softcap > 0.f) dot = a.softcap * tanhf(dot * cap_in);
+          else dot *= a.scale;
+          s[r][u] = (jj[u] >= lo[r] && jj[u] <= hi[r]) ? dot * kLog2e : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < TM; ++r) {
+        float mx = m[r];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) mx = fmaxf(mx, s[r][u]);
+        if (mx == -INFINITY) continue;
+        const float corr = exp2f(m[r] - mx);
+        l[r] *= corr;
+#pragma unroll
+        for (int e = 0; e < NV * V; ++e) acc[r][e] *= corr;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          if (s[r][u] == -INFINITY) continue;      // also keeps a masked key's value out
+          const float p = exp2f(s[r][u] - mx);
+          l[r] += p;
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            float vf[V];
+            unpack16<T>(vv[u][n], vf);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[r][n * V + e] = fmaf(p, vf[e], acc[r][n * V + e]);
+          }
+        }
+        m[r] = mx;
+      }
+    }
+
+    // join the lane groups
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < TM; ++r) {
+      if (t == 0) { sm_m[grp][r] = m[r]; sm_l[grp][r] = l[r]; }
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int e = 0; e < V; ++e) smem[(grp * TM + r) * HM + (n * LPK + t) * V + e] = acc[r][n * V + e];
+    }
+    __syncthreads();
+    const bool whole = w.whole();
+    const int64_t slot = 2 * (int64_t)cta + (w.begins() ? 1 : 0);
+    for (int x = threadIdx.x; x < nr * g.Hv; x += kThreads) {
+      const int r = x / g.Hv, d = x - r * g.Hv;
+      float M = -INFINITY;
+      for (int k = 0; k < KPI; ++k) M = fmaxf(M, sm_m[k][r]);
+      float O = 0.f, L = 0.f;
+      if (M != -INFINITY) {
+        for (int k = 0; k < KPI; ++k) {
+          if (sm_m[k][r] == -INFINITY) continue;
+          const float f = exp2f(sm_m[k][r] - M);
+          O = fmaf(f, smem[(k * TM + r) * HM + d], O);
+          L = fmaf(f, sm_l[k][r], L);
+        }
+      }
+      if (whole) {
+        const int pr = w.r.row0 + r, h = w.kvh * g.group + pr % g.group;
+        T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, w.s.t0 + pr / g.group);
+        if (SDPA_IN_BOUNDS(w.s.t0 + pr / g.group < g.tokens && h < g.Nq, 522))
+          y[d] = Elem<T>::from_f32(O * row_scale<T>(a, h, M, L));
+      } else if (SDPA_IN_BOUNDS(slot < 2 * ctas, 523)) {
+        ws.o[(slot * TM + r) * g.Hv + d] = O;
+        if (d == 0) {
+          ws.ml[(slot * TM + r) * 2] = M;
+          ws.ml[(slot * TM + r) * 2 + 1] = L;
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- joining the partial results
+
+constexpr int kMergeWarps = 4;
+
+// Block (c, y) joins rows [4y, 4y + 4) of the unit that CTA c's share starts inside of, if c is
+// the first such CTA of the unit; one warp per row.  The partials are those of CTA c - 1 (which
+// began the unit) and of the CTAs from c on whose shares start inside it, taken in that order.
+template <typename T, int TM, int TN>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const PagedAttn a, const PagedWs ws,
+                                                                       const int ctas) {
+  pdl_wait();
+  const Paged& g = a.g;
+  const int c = blockIdx.x + 1;
+  const int active = ws.start[ctas].b;
+  if (c >= active) return;
+  const ShareStart at = ws.start[c];
+  if (at.tile == 0) return;
+  auto inside = [&](const ShareStart& s) { return s.tile > 0 && s.b == at.b && s.rb == at.rb && s.kvh == at.kvh; };
+  if (inside(ws.start[c - 1])) return;
+  bool bad = false;
+  const SeqInfo s = seq_info(g, at.b, bad);
+  const RowBlock rbk = row_block<TM, TN>(a, s, at.rb);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kMergeWarps + warp;
+  if (r >= rbk.rows) return;
+  int n = 1;                                   // partials: CTA c - 1's second slot, then first slots
+  for (int k = c;; k += 32) {
+    const unsigned in = __ballot_sync(0xffffffffu, k + lane < active && inside(ws.start[min(k + lane, active - 1)]));
+    n += in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+    if (in != 0xffffffffu) break;
+  }
+  auto slot_of = [&](int i) -> int64_t { return ((i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c + i - 1)) * TM) + r; };
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, ws.ml[slot_of(i) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f, acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  if (M != -INFINITY) {
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int mine = i0 + lane;
+      float f = 0.f;
+      if (mine < n) {
+        const float mm = ws.ml[slot_of(mine) * 2];
+        f = mm == -INFINITY ? 0.f : exp2f(mm - M);
+        L = fmaf(f, ws.ml[slot_of(mine) * 2 + 1], L);
+      }
+      const int cnt = min(32, n - i0);
+#pragma unroll 4
+      for (int k = 0; k < cnt; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        const float* o = ws.o + slot_of(i0 + k) * g.Hv;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {          // 4 columns per lane, twice for Hv > 128
+          const int d = (e * 32 + lane) * 4;
+          if (d < g.Hv && fk != 0.f) {
+            const float4 v = *reinterpret_cast<const float4*>(o + d);
+            acc[4 * e] = fmaf(fk, v.x, acc[4 * e]);
+            acc[4 * e + 1] = fmaf(fk, v.y, acc[4 * e + 1]);
+            acc[4 * e + 2] = fmaf(fk, v.z, acc[4 * e + 2]);
+            acc[4 * e + 3] = fmaf(fk, v.w, acc[4 * e + 3]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  }
+  const int pr = rbk.row0 + r, h = at.kvh * g.group + pr % g.group;
+  const float inv = row_scale<T>(a, h, M, L);
+  T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, s.t0 + pr / g.group);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int d = (e * 32 + lane) * 4;
+    if (d < g.Hv && SDPA_IN_BOUNDS(s.t0 + pr / g.group < g.tokens, 524)) {
+      T out[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) out[k] = Elem<T>::from_f32(acc[4 * e + k] * inv);
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y + d) = *reinterpret_cast<const uint4*>(out);
+      else *reinterpret_cast<uint2*>(y + d) = *reinterpret_cast<const uint2*>(out);
+    }
+  }
+}
+
+template <typename T, int TM, int TN>
+cudaError_t merge_tn(const PagedAttn& a, const PagedWs& ws, int ctas, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)std::max(1, ctas - 1), (TM + kMergeWarps - 1) / kMergeWarps);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, TM, TN>, a, ws, ctas);
+  if (e == cudaSuccess) count_launch(1);
+  return e;
+}
+
+template <typename T>
+cudaError_t merge_t(const PagedAttn& a, const PagedWs& ws, int ctas, int tm, cudaStream_t st) {
+  switch (tm) {
+    case 1: return merge_tn<T, 1, kTN>(a, ws, ctas, st);
+    default: return merge_tn<T, 4, kTN>(a, ws, ctas, st);
+  }
+}
+
+// Rows per unit: the tokens of a uniform single-row batch need no more than one.
+int simt_tm(const PagedAttn& a) { return a.g.group == 1 && a.g.uniform == 1 ? 1 : 4; }
+
+template <typename T, int LPK, int NV, int TM>
+cudaError_t launch_simt(const PagedAttn& a, sdpa_dtype dt, void* wsp, int ctas, cudaStream_t st) {
+  const PagedWs ws = paged_ws(wsp, ctas, TM);
+  const size_t smem = sizeof(float) * (kThreads / LPK) * TM * LPK * NV * Elem<T>::kVec;
+  paged_simt_kernel<T, LPK, NV, TM><<<(unsigned)ctas, kThreads, smem, st>>>(a, ws);
+  count_launch(1);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? launch_paged_merge(a, dt, ws, ctas, TM, st) : e;
+}
+
+template <typename T, int TM>
+cudaError_t launch_width(const PagedAttn& a, sdpa_dtype dt, void* ws, int ctas, cudaStream_t st) {
+  constexpr int V = Elem<T>::kVec;
+  const int vecs = (std::max(a.g.H, a.g.Hv) + V - 1) / V;
+  if (vecs <= 8) return launch_simt<T, 8, 1, TM>(a, dt, ws, ctas, st);
+  if (vecs <= 16) return launch_simt<T, 16, 1, TM>(a, dt, ws, ctas, st);
+  if (vecs <= 32) return launch_simt<T, 32, 1, TM>(a, dt, ws, ctas, st);
+  return launch_simt<T, 32, 2, TM>(a, dt, ws, ctas, st);
+}
+
+template <typename T>
+cudaError_t launch_t(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st) {
+  const int ctas = paged_sms() * kCtasPerSm;
+  if (ctas <= 0) return cudaErrorInvalidDevice;
+  return simt_tm(a) == 1 ? launch_width<T, 1>(a, dt, ws, ctas, st) : launch_width<T, 4>(a, dt, ws, ctas, st);
+}
+
+}  // namespace
+
+int paged_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return std::min(n, kPagedMaxSms);
+}
+
+cudaError_t launch_paged_merge(const PagedAttn& a, sdpa_dtype dt, const PagedWs& ws, int ctas, int tm, cudaStream_t st) {
+  switch (dt) {
+    case SDPA_F32: return merge_t<float>(a, ws, ctas, tm, st);
+    case SDPA_F16: return merge_t<__half>(a, ws, ctas, tm, st);
+    default: return merge_t<__nv_bfloat16>(a, ws, ctas, tm, st);
+  }
+}
+
+PagedKernel paged_kernel(const PagedAttn&, sdpa_dtype) { return kPagedSimt; }
+
+size_t paged_workspace(const PagedAttn& a, sdpa_dtype) {
+  return paged_ws_bytes(kPagedMaxSms * kCtasPerSm, simt_tm(a), a.g.Hv);
+}
+
+cudaError_t launch_paged_attn(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name) {
+  *name = dt == SDPA_F32 ? "paged_simt_f32" : dt == SDPA_F16 ? "paged_simt_f16" : "paged_simt_bf16";
+  switch (dt) {
+    case SDPA_F32: return launch_t<float>(a, dt, ws, st);
+    case SDPA_F16: return launch_t<__half>(a, dt, ws, st);
+    default: return launch_t<__nv_bfloat16>(a, dt, ws, st);
+  }
+}
+
+cudaError_t take_paged_attn_status(int* status) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_paged_status, sizeof v);
+  if (e != cudaSuccess) return e;
+  *status = v;
+  if (v) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero);
+  }
+  return e;
+}
+
+SDPA_DEFINE_BOUNDS_TAKE(take_bounds_paged)
+
+}  // namespace sdpa

@@ -83,10 +83,42 @@ class sdpa_params(ctypes.Structure):
     ]
 
 
+class sdpa_qk_norm_params(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_int32),
+        ("B", ctypes.c_int32), ("Nq", ctypes.c_int32), ("Nkv", ctypes.c_int32),
+        ("S", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("q", sdpa_view), ("k", sdpa_view),
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+        ("rotary_cos", ctypes.c_void_p), ("rotary_sin", ctypes.c_void_p),
+        ("rotary_max_pos", ctypes.c_int64), ("position_ids", ctypes.c_void_p),
+        ("rotary_dim", ctypes.c_int32), ("rotary_interleaved", ctypes.c_int32),
+    ]
+
+
+class sdpa_paged_params(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_int32), ("B", ctypes.c_int32), ("tokens", ctypes.c_int32),
+        ("Nq", ctypes.c_int32), ("Nkv", ctypes.c_int32), ("H", ctypes.c_int32), ("Hv", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("k_pages", sdpa_view), ("v_pages", sdpa_view),
+        ("page_table", ctypes.c_void_p), ("page_table_stride", ctypes.c_int64),
+        ("kv_lens", ctypes.c_void_p), ("cu_new", ctypes.c_void_p),
+        ("rotary_cos", ctypes.c_void_p), ("rotary_sin", ctypes.c_void_p),
+        ("rotary_max_pos", ctypes.c_int64), ("rotary_dim", ctypes.c_int32),
+        ("rotary_interleaved", ctypes.c_int32),
+        ("has_scale", ctypes.c_int32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+        ("causal", ctypes.c_int32), ("window", ctypes.c_int64), ("head_sink", ctypes.c_void_p),
+        ("max_new", ctypes.c_int32),
+    ]
+
+
 EXPORTED = ("sdpa_attn_fwd", "sdpa_attn_decode", "sdpa_workspace_size", "sdpa_validate",
             "sdpa_kv_concat", "sdpa_query_status", "sdpa_last_error", "sdpa_last_kernel_name",
             "sdpa_version", "sdpa_launch_count", "sdpa_attn_decode_static", "sdpa_rotary",
-            "sdpa_attn_bwd")
+            "sdpa_attn_bwd", "sdpa_qk_norm_rotary", "sdpa_qk_norm_rotary_bwd", "sdpa_qk_norm_workspace_size",
+            "sdpa_paged_append", "sdpa_paged_attn", "sdpa_paged_workspace_size")
 
 _lib = None
 
@@ -120,6 +152,20 @@ def lib() -> ctypes.CDLL:
             [sdpa_view, sdpa_view, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
              ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]
         L.sdpa_rotary.restype = ctypes.c_int
+        NP, GP = ctypes.POINTER(sdpa_qk_norm_params), ctypes.POINTER(sdpa_paged_params)
+        L.sdpa_qk_norm_rotary.argtypes = [NP, sdpa_view, sdpa_view, ctypes.c_void_p]
+        L.sdpa_qk_norm_rotary.restype = ctypes.c_int
+        L.sdpa_qk_norm_rotary_bwd.argtypes = [NP] + [sdpa_view] * 4 + [ctypes.c_void_p] * 3 + \
+            [ctypes.c_size_t, ctypes.c_void_p]
+        L.sdpa_qk_norm_rotary_bwd.restype = ctypes.c_int
+        L.sdpa_qk_norm_workspace_size.argtypes = [NP]
+        L.sdpa_qk_norm_workspace_size.restype = ctypes.c_size_t
+        L.sdpa_paged_append.argtypes = [GP, sdpa_view, sdpa_view, ctypes.c_void_p]
+        L.sdpa_paged_append.restype = ctypes.c_int
+        L.sdpa_paged_attn.argtypes = [GP, sdpa_view, sdpa_view, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        L.sdpa_paged_attn.restype = ctypes.c_int
+        L.sdpa_paged_workspace_size.argtypes = [GP]
+        L.sdpa_paged_workspace_size.restype = ctypes.c_size_t
         L.sdpa_query_status.argtypes = [ctypes.c_void_p]
         L.sdpa_query_status.restype = ctypes.c_int
         for f in ("sdpa_last_error", "sdpa_last_kernel_name", "sdpa_version"):
@@ -399,6 +445,279 @@ def sdpa_rotary(x: torch.Tensor, cos_cache: torch.Tensor, sin_cache: torch.Tenso
                            _ptr(cos_cache, keep), _ptr(sin_cache, keep), max_pos, _ptr(pos, keep),
                            int(rotary_dim), 1 if interleaved else 0, _stream(stream))
     _check(rc)
+    return y
+
+
+class _OnDevice:
+    """The device and stream of one call: every tensor must be on one CUDA device, which becomes
+    current for the call; memory the binding allocates is kept for the stream the call runs on."""
+
+    def __init__(self, tensors: dict, stream):
+        given = {name: t for name, t in tensors.items() if t is not None}
+        for name, t in given.items():
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+        self.device = next(iter(given.values())).device
+        for name, t in given.items():
+            if t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+        self.guard = torch.cuda.device(self.device)
+        self.stream = stream
+
+    def __enter__(self):
+        self.guard.__enter__()
+        self.current = torch.cuda.current_stream(self.device)
+        self.handle = self.current.cuda_stream if self.stream is None else _stream(self.stream)
+        return self
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+    def keep(self, *allocated):
+        if self.handle != self.current.cuda_stream:
+            s = self.stream if hasattr(self.stream, "cuda_stream") else \
+                torch.cuda.ExternalStream(self.handle, device=self.device)
+            for t in allocated:
+                if t is not None and t.numel():
+                    t.record_stream(s)
+
+
+def _typed(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape=None):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _element_type(t: torch.Tensor) -> int:
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"unsupported type {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim, interleaved,
+                 num_heads, kv_num_heads):
+    """(params, 4-D views of q and k, tensors to keep) of the query/key norm."""
+    if q.dim() != k.dim() or q.dim() not in (3, 4):
+        raise ValueError("q and k must both be rank 3 (B, S, N*D) or both rank 4 (B, N, S, D)")
+    if q.dim() == 3 and not (num_heads and kv_num_heads):
+        raise ValueError("rank-3 inputs need num_heads and kv_num_heads")
+    q4, k4 = _rank4(q, num_heads, "q"), _rank4(k, kv_num_heads, "k")
+    B, Nq, S, D = q4.shape
+    if (k4.shape[0], k4.shape[2], k4.shape[3]) != (B, S, D):
+        raise ValueError(f"k {tuple(k4.shape)} does not match q {tuple(q4.shape)}")
+    keep: list = []
+    p = sdpa_qk_norm_params()
+    p.struct_size = ctypes.sizeof(sdpa_qk_norm_params)
+    p.B, p.Nq, p.Nkv, p.S, p.D = B, Nq, k4.shape[1], S, D
+    p.dtype = _element_type(q)
+    for name, t in (("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("cos_cache", cos_cache),
+                    ("sin_cache", sin_cache)):
+        _typed(t, name, q.dtype)
+    _typed(q_weight, "q_weight", q.dtype, (D,))
+    _typed(k_weight, "k_weight", q.dtype, (D,))
+    p.q, p.k = _view(q4, keep), _view(k4, keep)
+    p.q_weight, p.k_weight = _ptr(q_weight, keep), _ptr(k_weight, keep)
+    p.eps = float(eps)
+    p.rotary_dim, p.rotary_interleaved = int(rotary_dim), 1 if interleaved else 0
+    if (cos_cache is None) != (sin_cache is None):
+        raise ValueError("cos_cache and sin_cache must be given together")
+    if cos_cache is not None:
+        half = (int(rotary_dim) or D) // 2
+        if position_ids is None:
+            _typed(cos_cache, "cos_cache", q.dtype, (B, S, half))
+            p.rotary_max_pos = B * S
+        else:
+            if cos_cache.dim() != 2 or cos_cache.shape[1] != half:
+                raise ValueError(f"cos_cache must have shape (positions, {half}), got {tuple(cos_cache.shape)}")
+            if not position_ids.is_cuda:
+                raise ValueError("position_ids must be a CUDA tensor")
+            pos = position_ids.to(torch.int64).expand(B, S).contiguous()
+            p.position_ids = _ptr(pos, keep)
+            p.rotary_max_pos = cos_cache.shape[0]
+        _typed(sin_cache, "sin_cache", q.dtype, cos_cache.shape)
+        p.rotary_cos, p.rotary_sin = _ptr(cos_cache, keep), _ptr(sin_cache, keep)
+    elif position_ids is not None:
+        raise ValueError("position_ids without cos_cache / sin_cache")
+    return p, q4, k4, keep
+
+
+def _rank4(t: torch.Tensor, heads: Optional[int], name: str) -> torch.Tensor:
+    if t.dim() == 4:
+        return t
+    if t.shape[2] % heads:
+        raise ValueError(f"{name}: {t.shape[2]} channels are no multiple of {heads} heads")
+    return _heads4(t, heads)
+
+
+def _like(t: Optional[torch.Tensor], ref: torch.Tensor, name: str) -> torch.Tensor:
+    """t checked against ref's type and shape, or a new tensor of ref's shape."""
+    if t is None:
+        return torch.empty(ref.shape, dtype=ref.dtype, device=ref.device)
+    _typed(t, name, ref.dtype, ref.shape)
+    return t
+
+
+def sdpa_qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                        cos_cache: Optional[torch.Tensor] = None, sin_cache: Optional[torch.Tensor] = None,
+                        position_ids: Optional[torch.Tensor] = None, *, eps: float = 1e-6, rotary_dim: int = 0,
+                        interleaved: bool = False, num_heads: Optional[int] = None,
+                        kv_num_heads: Optional[int] = None, q_out: Optional[torch.Tensor] = None,
+                        k_out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of every query and key head, times its weight (D,), then the rotary embedding, in
+    one pass over rank-4 (B, N, S, D) or rank-3 (B, S, N*D) tensors (num_heads and kv_num_heads
+    given).  Caches as for sdpa_rotary; without caches there is no rotation.  Returns (q_out,
+    k_out) in the inputs' shapes; an output may be its input."""
+    with _OnDevice(dict(q=q, k=k, q_weight=q_weight, k_weight=k_weight, cos_cache=cos_cache, sin_cache=sin_cache,
+                        position_ids=position_ids, q_out=q_out, k_out=k_out), stream) as dev:
+        p, _, _, keep = _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim,
+                                     interleaved, num_heads, kv_num_heads)
+        q_out, k_out = _like(q_out, q, "q_out"), _like(k_out, k, "k_out")
+        dev.keep(q_out, k_out, *keep)
+        _check(lib().sdpa_qk_norm_rotary(ctypes.byref(p), _view(_rank4(q_out, num_heads, "q_out"), keep),
+                                         _view(_rank4(k_out, kv_num_heads, "k_out"), keep), dev.handle))
+    return q_out, k_out
+
+
+def sdpa_qk_norm_rotary_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch.Tensor,
+                            q_weight: torch.Tensor, k_weight: torch.Tensor,
+                            cos_cache: Optional[torch.Tensor] = None, sin_cache: Optional[torch.Tensor] = None,
+                            position_ids: Optional[torch.Tensor] = None, *, eps: float = 1e-6, rotary_dim: int = 0,
+                            interleaved: bool = False, num_heads: Optional[int] = None,
+                            kv_num_heads: Optional[int] = None, dq=None, dk=None, dq_weight=None, dk_weight=None,
+                            workspace=None, stream=None):
+    """Gradient of sdpa_qk_norm_rotary for the upstream gradients dq_out, dk_out of its outputs:
+    returns (dq, dk, dq_weight, dk_weight).  dq may be dq_out itself and dk dk_out."""
+    with _OnDevice(dict(q=q, k=k, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight, k_weight=k_weight,
+                        cos_cache=cos_cache, sin_cache=sin_cache, position_ids=position_ids, dq=dq, dk=dk,
+                        dq_weight=dq_weight, dk_weight=dk_weight, workspace=workspace), stream) as dev:
+        p, _, _, keep = _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim,
+                                     interleaved, num_heads, kv_num_heads)
+        _typed(dq_out, "dq_out", q.dtype, q.shape)
+        _typed(dk_out, "dk_out", k.dtype, k.shape)
+        dq, dk = _like(dq, q, "dq"), _like(dk, k, "dk")
+        dq_weight, dk_weight = _like(dq_weight, q_weight, "dq_weight"), _like(dk_weight, k_weight, "dk_weight")
+        if workspace is None:
+            workspace = torch.empty(max(1, int(lib().sdpa_qk_norm_workspace_size(ctypes.byref(p)))), dtype=torch.uint8,
+                                    device=dev.device)
+        dev.keep(dq, dk, dq_weight, dk_weight, workspace, *keep)
+        v = lambda t, n, name: _view(_rank4(t, n, name), keep)
+        _check(lib().sdpa_qk_norm_rotary_bwd(
+            ctypes.byref(p), v(dq_out, num_heads, "dq_out"), v(dk_out, kv_num_heads, "dk_out"),
+            v(dq, num_heads, "dq"), v(dk, kv_num_heads, "dk"), _ptr(dq_weight, keep), _ptr(dk_weight, keep),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), dev.handle))
+    return dq, dk, dq_weight, dk_weight
+
+
+def make_paged_params(k_pages, v_pages, page_table, kv_lens, tokens: int, Nq: int, *, cu_new=None,
+                      cos_cache=None, sin_cache=None, rotary_dim=0, interleaved=False, scale=None, softcap=0.0,
+                      causal="lower_right", window=-1, head_sink=None,
+                      max_new=None) -> Tuple[sdpa_paged_params, list]:
+    """Fills sdpa_paged_params.  Returns (params, tensors to keep alive)."""
+    keep: list = []
+    if k_pages.dim() != 4 or v_pages.dim() != 4:
+        raise ValueError("k_pages and v_pages are (pages, heads, slots, dim) views")
+    if v_pages.shape[:3] != k_pages.shape[:3]:
+        raise ValueError(f"v_pages {tuple(v_pages.shape)} does not match k_pages {tuple(k_pages.shape)}")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be (B, max_pages)")
+    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+        raise ValueError("the rows of page_table must be contiguous")
+    B = page_table.shape[0]
+    p = sdpa_paged_params()
+    p.struct_size = ctypes.sizeof(sdpa_paged_params)
+    p.dtype = _element_type(k_pages)
+    for name, t in (("v_pages", v_pages), ("cos_cache", cos_cache), ("sin_cache", sin_cache), ("head_sink", head_sink)):
+        _typed(t, name, k_pages.dtype)
+    _typed(page_table, "page_table", torch.int32)
+    _typed(kv_lens, "kv_lens", torch.int32, (B,))
+    _typed(cu_new, "cu_new", torch.int32, (B + 1,))
+    _typed(head_sink, "head_sink", k_pages.dtype, (Nq,))
+    p.B, p.tokens, p.Nq = B, tokens, Nq
+    p.num_pages, p.Nkv, p.page_size, p.H = k_pages.shape
+    p.Hv = v_pages.shape[3]
+    p.max_pages = page_table.shape[1]
+    p.k_pages, p.v_pages = _view(k_pages, keep), _view(v_pages, keep)
+    keep.append(page_table)
+    p.page_table, p.page_table_stride = page_table.data_ptr(), page_table.stride(0)
+    p.kv_lens, p.cu_new = _ptr(kv_lens, keep), _ptr(cu_new, keep)
+    if cos_cache is not None:
+        half = (int(rotary_dim) or p.H) // 2
+        if cos_cache.dim() != 2 or cos_cache.shape[1] != half:
+            raise ValueError(f"cos_cache must have shape (positions, {half}), got {tuple(cos_cache.shape)}")
+        _typed(sin_cache, "sin_cache", k_pages.dtype, cos_cache.shape)
+        p.rotary_max_pos = cos_cache.shape[0]
+    p.rotary_cos, p.rotary_sin = _ptr(cos_cache, keep), _ptr(sin_cache, keep)
+    p.rotary_dim, p.rotary_interleaved = int(rotary_dim), 1 if interleaved else 0
+    p.has_scale = 0 if scale is None else 1
+    p.scale = 0.0 if scale is None else float(scale)
+    p.softcap = float(softcap)
+    p.causal = CAUSAL[causal] if isinstance(causal, str) else int(causal)
+    p.window = int(window)
+    p.head_sink = _ptr(head_sink, keep)
+    p.max_new = 0 if max_new is None else int(max_new)
+    return p, keep
+
+
+def _packed(t: torch.Tensor, name: str, keep: list) -> sdpa_view:
+    """The C view of packed rows (tokens, heads, dim)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be packed rows (tokens, heads, dim)")
+    return _view(t.transpose(0, 1).unsqueeze(0), keep)
+
+
+def sdpa_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                      page_table: torch.Tensor, kv_lens: torch.Tensor, *, cu_new: Optional[torch.Tensor] = None,
+                      cos_cache: Optional[torch.Tensor] = None, sin_cache: Optional[torch.Tensor] = None,
+                      rotary_dim: int = 0, interleaved: bool = False,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Writes the new keys k and values v (packed rows (tokens, Nkv, H / Hv)) of a ragged batch
+    into their pages, the keys rotated at their positions when caches (positions, R/2) are given.
+
+    k_pages, v_pages: (pages, Nkv, slots, dim) views of the pools (a pool stored (pages, slots,
+    heads, dim) is passed with transpose(1, 2)); page_table (B, max_pages) int32; kv_lens (B,)
+    int32: keys of each sequence, its new tokens included; cu_new (B + 1,) int32: first row of
+    each sequence, or None when every sequence brings tokens / B rows.  Returns the pools."""
+    with _OnDevice(dict(k=k, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_lens=kv_lens,
+                        cu_new=cu_new, cos_cache=cos_cache, sin_cache=sin_cache), stream) as dev:
+        p, keep = make_paged_params(k_pages, v_pages, page_table, kv_lens, k.shape[0], k_pages.shape[1], cu_new=cu_new,
+                                    cos_cache=cos_cache, sin_cache=sin_cache, rotary_dim=rotary_dim,
+                                    interleaved=interleaved)
+        _typed(k, "k", k_pages.dtype, (k.shape[0], p.Nkv, p.H))
+        _typed(v, "v", k_pages.dtype, (k.shape[0], p.Nkv, p.Hv))
+        _check(lib().sdpa_paged_append(ctypes.byref(p), _packed(k, "k", keep), _packed(v, "v", keep), dev.handle))
+    return k_pages, v_pages
+
+
+def sdpa_paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                    kv_lens: torch.Tensor, *, cu_new: Optional[torch.Tensor] = None, max_new: Optional[int] = None,
+                    scale: Optional[float] = None, softcap: float = 0.0, causal="lower_right", window: int = -1,
+                    head_sink: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, workspace=None,
+                    stream=None) -> torch.Tensor:
+    """Attention of the new tokens q (packed rows (tokens, Nq, H)) over the pages of their
+    sequences; the new keys and values are in the pages already (sdpa_paged_append).  Page
+    arguments as there.  max_new: most new tokens of one sequence, where the caller knows it (it
+    picks the kernel; results do not depend on it).  Returns y (tokens, Nq, Hv); rows behind the
+    last sequence are not written."""
+    with _OnDevice(dict(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_lens=kv_lens, cu_new=cu_new,
+                        head_sink=head_sink, y=y, workspace=workspace), stream) as dev:
+        if q.dim() != 3:
+            raise ValueError("q must be packed rows (tokens, heads, dim)")
+        p, keep = make_paged_params(k_pages, v_pages, page_table, kv_lens, q.shape[0], q.shape[1], cu_new=cu_new,
+                                    scale=scale, softcap=softcap, causal=causal, window=window, head_sink=head_sink,
+                                    max_new=max_new)
+        _typed(q, "q", k_pages.dtype, (q.shape[0], q.shape[1], p.H))
+        if y is None:
+            y = torch.empty(q.shape[0], q.shape[1], p.Hv, dtype=q.dtype, device=q.device)
+        _typed(y, "y", q.dtype, (q.shape[0], q.shape[1], p.Hv))
+        if workspace is None:
+            workspace = torch.empty(max(1, int(lib().sdpa_paged_workspace_size(ctypes.byref(p)))), dtype=torch.uint8,
+                                    device=dev.device)
+        dev.keep(y, workspace)
+        _check(lib().sdpa_paged_attn(ctypes.byref(p), _packed(q, "q", keep), _packed(y, "y", keep),
+                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), dev.handle))
     return y
 
 
