@@ -1090,14 +1090,18 @@ int sdpa_query_status(sdpa_stream_t stream) {
   if (e == cudaSuccess) e = take_bwd_status(&bwd_status);
   if (e == cudaSuccess) e = take_norm_status(&norm_status);
   if (e == cudaSuccess) e = take_paged_append_status(&app_status);
-  if (e == cudaSuccess) e = take_paged_attn_status(&paged_status);
+  for (auto take : {take_paged_simt_status, take_paged_mma_status}) {
+    int v = 0;
+    if (e == cudaSuccess) e = take(&v);
+    paged_status |= v;
+  }
   if (e != cudaSuccess) return cuda_fail(e, "status read");
   if (!status) status = qk_status;
   if (!status) status = bwd_status;
   // the bounds-checking build: the first failing index check of each kernel family
   int site = 0;
   for (auto take : {take_bounds_prefill, take_bounds_decode, take_bounds_concat, take_bounds_simt, take_bounds_norm,
-                    take_bounds_append, take_bounds_paged}) {
+                    take_bounds_append, take_bounds_paged_simt, take_bounds_paged_mma}) {
     int v = 0;
     if ((e = take(&v)) != cudaSuccess) return cuda_fail(e, "bounds status read");
     if (!site) site = v;

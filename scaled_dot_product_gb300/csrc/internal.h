@@ -99,7 +99,8 @@ cudaError_t take_bounds_decode(int* site);
 cudaError_t take_bounds_concat(int* site);
 cudaError_t take_bounds_simt(int* site);
 cudaError_t take_bounds_append(int* site);
-cudaError_t take_bounds_paged(int* site);
+cudaError_t take_bounds_paged_simt(int* site);
+cudaError_t take_bounds_paged_mma(int* site);
 
 // Decode with the partials in the library's own device array (no workspace).
 size_t decode_static_scratch_bytes();

@@ -47,9 +47,13 @@ enum PagedKernel { kPagedSimt = 0, kPagedMma = 1, kPagedTc = 2 };
 PagedKernel paged_kernel(const PagedAttn& a, sdpa_dtype dt);
 size_t paged_workspace(const PagedAttn& a, sdpa_dtype dt);
 cudaError_t launch_paged_attn(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
+bool paged_mma_supported(const PagedAttn& a, sdpa_dtype dt);
+size_t paged_mma_workspace(const PagedAttn& a);
+cudaError_t launch_paged_mma(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
 
 cudaError_t take_paged_append_status(int* status);
-cudaError_t take_paged_attn_status(int* status);
+cudaError_t take_paged_simt_status(int* status);
+cudaError_t take_paged_mma_status(int* status);
 
 #ifdef __CUDACC__
 // Status bits of the device words: reported by sdpa_query_status as SDPA_ERR_INVALID.

@@ -255,6 +255,14 @@ struct Walk {
   }
 };
 
+// Final scale of row (head h): 1 / (l + sink term), 0 for a row with no key; m, l in log2 units.
+template <typename T>
+__device__ __forceinline__ float row_scale(const PagedAttn& a, int h, float m, float l) {
+  if (m == -INFINITY) return 0.f;
+  if (a.head_sink) l += exp2f(Elem<T>::to_f32(reinterpret_cast<const T*>(a.head_sink)[h]) * kLog2e - m);
+  return l > 0.f ? 1.f / l : 0.f;
+}
+
 // Lets the joining kernel be scheduled; it waits for this one's results itself.
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -20,14 +20,6 @@ constexpr int kTN = 64;          // keys per tile of the schedule
 constexpr int kCtasPerSm = 4;
 constexpr int kMinShare = 2;     // tiles
 
-// Final scale of row (head h): 1 / (l + sink term), 0 for a row with no key; m, l in log2 units.
-template <typename T>
-__device__ __forceinline__ float row_scale(const PagedAttn& a, int h, float m, float l) {
-  if (m == -INFINITY) return 0.f;
-  if (a.head_sink) l += exp2f(Elem<T>::to_f32(reinterpret_cast<const T*>(a.head_sink)[h]) * kLog2e - m);
-  return l > 0.f ? 1.f / l : 0.f;
-}
-
 template <typename T, int LPK, int NV, int TM>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a, const PagedWs ws) {
   constexpr int V = Elem<T>::kVec;
@@ -68,8 +60,9 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a,
 #pragma unroll
       for (int e = 0; e < NV * V; ++e) acc[r][e] = 0.f;
     }
-    const int64_t j_begin = (int64_t)(w.r.tile0 + w.tile) * kTN;
-    const int64_t j_end = min((int64_t)w.r.hi + 1, j_begin + (int64_t)w.take() * kTN);
+    const int64_t j_tile = (int64_t)(w.r.tile0 + w.tile) * kTN;
+    const int64_t j_begin = max(j_tile, (int64_t)w.r.lo);      // pages below a window are not read
+    const int64_t j_end = min((int64_t)w.r.hi + 1, j_tile + (int64_t)w.take() * kTN);
     const int32_t* table = g.table + (int64_t)w.b * g.table_stride;
 
     for (int64_t base = j_begin; base < j_end; base += KPI * kUnroll) {
@@ -298,7 +291,10 @@ template <typename T>
 cudaError_t merge_t(const PagedAttn& a, const PagedWs& ws, int ctas, int tm, cudaStream_t st) {
   switch (tm) {
     case 1: return merge_tn<T, 1, kTN>(a, ws, ctas, st);
-    default: return merge_tn<T, 4, kTN>(a, ws, ctas, st);
+    case 4: return merge_tn<T, 4, kTN>(a, ws, ctas, st);
+    case 16: return merge_tn<T, 16, kTN>(a, ws, ctas, st);
+    case 32: return merge_tn<T, 32, kTN>(a, ws, ctas, st);
+    default: return merge_tn<T, 64, kTN>(a, ws, ctas, st);
   }
 }
 
@@ -349,13 +345,17 @@ cudaError_t launch_paged_merge(const PagedAttn& a, sdpa_dtype dt, const PagedWs&
   }
 }
 
-PagedKernel paged_kernel(const PagedAttn&, sdpa_dtype) { return kPagedSimt; }
+PagedKernel paged_kernel(const PagedAttn& a, sdpa_dtype dt) {
+  return paged_mma_supported(a, dt) ? kPagedMma : kPagedSimt;
+}
 
-size_t paged_workspace(const PagedAttn& a, sdpa_dtype) {
+size_t paged_workspace(const PagedAttn& a, sdpa_dtype dt) {
+  if (paged_kernel(a, dt) == kPagedMma) return paged_mma_workspace(a);
   return paged_ws_bytes(kPagedMaxSms * kCtasPerSm, simt_tm(a), a.g.Hv);
 }
 
 cudaError_t launch_paged_attn(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name) {
+  if (paged_kernel(a, dt) == kPagedMma) return launch_paged_mma(a, dt, ws, st, name);
   *name = dt == SDPA_F32 ? "paged_simt_f32" : dt == SDPA_F16 ? "paged_simt_f16" : "paged_simt_bf16";
   switch (dt) {
     case SDPA_F32: return launch_t<float>(a, dt, ws, st);
@@ -364,7 +364,7 @@ cudaError_t launch_paged_attn(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaS
   }
 }
 
-cudaError_t take_paged_attn_status(int* status) {
+cudaError_t take_paged_simt_status(int* status) {
   int v = 0;
   cudaError_t e = cudaMemcpyFromSymbol(&v, g_paged_status, sizeof v);
   if (e != cudaSuccess) return e;
@@ -376,6 +376,6 @@ cudaError_t take_paged_attn_status(int* status) {
   return e;
 }
 
-SDPA_DEFINE_BOUNDS_TAKE(take_bounds_paged)
+SDPA_DEFINE_BOUNDS_TAKE(take_bounds_paged_simt)
 
 }  // namespace sdpa
