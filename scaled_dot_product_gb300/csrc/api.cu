@@ -1095,13 +1095,18 @@ int sdpa_query_status(sdpa_stream_t stream) {
     if (e == cudaSuccess) e = take(&v);
     paged_status |= v;
   }
+  int tc_status = 0, tc_timeout = 0;
+  if (e == cudaSuccess) e = take_paged_tc_status(&tc_status, &tc_timeout);
+  paged_status |= tc_status;
   if (e != cudaSuccess) return cuda_fail(e, "status read");
   if (!status) status = qk_status;
   if (!status) status = bwd_status;
+  if (!status) status = tc_timeout;
   // the bounds-checking build: the first failing index check of each kernel family
   int site = 0;
   for (auto take : {take_bounds_prefill, take_bounds_decode, take_bounds_concat, take_bounds_simt, take_bounds_norm,
-                    take_bounds_append, take_bounds_paged_simt, take_bounds_paged_mma}) {
+                    take_bounds_append, take_bounds_paged_simt, take_bounds_paged_mma,
+                    take_bounds_paged_tc}) {
     int v = 0;
     if ((e = take(&v)) != cudaSuccess) return cuda_fail(e, "bounds status read");
     if (!site) site = v;

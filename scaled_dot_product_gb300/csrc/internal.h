@@ -101,6 +101,7 @@ cudaError_t take_bounds_simt(int* site);
 cudaError_t take_bounds_append(int* site);
 cudaError_t take_bounds_paged_simt(int* site);
 cudaError_t take_bounds_paged_mma(int* site);
+cudaError_t take_bounds_paged_tc(int* site);
 
 // Decode with the partials in the library's own device array (no workspace).
 size_t decode_static_scratch_bytes();

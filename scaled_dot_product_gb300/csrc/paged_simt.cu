@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a,
 
 constexpr int kMergeWarps = 4;
 
-// Block (c, y) joins rows [4y, 4y + 4) of the unit that CTA c's share starts inside of, if c is
-// the first such CTA of the unit; one warp per row.  The partials are those of CTA c - 1 (which
+// The blocks (c, .) join the rows of the unit that CTA c's share starts inside of, if c is the
+// first such CTA of the unit; a warp takes every (4 gridDim.y)-th row.  The partials are those of CTA c - 1 (which
 // began the unit) and of the CTAs from c on whose shares start inside it, taken in that order.
 template <typename T, int TM, int TN>
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const PagedAttn a, const PagedWs ws,
@@ -209,64 +209,64 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Pag
   const SeqInfo s = seq_info(g, at.b, bad);
   const RowBlock rbk = row_block<TM, TN>(a, s, at.rb);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kMergeWarps + warp;
-  if (r >= rbk.rows) return;
   int n = 1;                                   // partials: CTA c - 1's second slot, then first slots
   for (int k = c;; k += 32) {
     const unsigned in = __ballot_sync(0xffffffffu, k + lane < active && inside(ws.start[min(k + lane, active - 1)]));
     n += in == 0xffffffffu ? 32 : __ffs(~in) - 1;
     if (in != 0xffffffffu) break;
   }
-  auto slot_of = [&](int i) -> int64_t { return ((i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c + i - 1)) * TM) + r; };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, ws.ml[slot_of(i) * 2]);
+  for (int r = blockIdx.y * kMergeWarps + warp; r < rbk.rows; r += gridDim.y * kMergeWarps) {
+    auto slot_of = [&](int i) -> int64_t { return ((i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c + i - 1)) * TM) + r; };
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, ws.ml[slot_of(i) * 2]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f, acc[8];
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f, acc[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  if (M != -INFINITY) {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int mine = i0 + lane;
-      float f = 0.f;
-      if (mine < n) {
-        const float mm = ws.ml[slot_of(mine) * 2];
-        f = mm == -INFINITY ? 0.f : exp2f(mm - M);
-        L = fmaf(f, ws.ml[slot_of(mine) * 2 + 1], L);
-      }
-      const int cnt = min(32, n - i0);
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    if (M != -INFINITY) {
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int mine = i0 + lane;
+        float f = 0.f;
+        if (mine < n) {
+          const float mm = ws.ml[slot_of(mine) * 2];
+          f = mm == -INFINITY ? 0.f : exp2f(mm - M);
+          L = fmaf(f, ws.ml[slot_of(mine) * 2 + 1], L);
+        }
+        const int cnt = min(32, n - i0);
 #pragma unroll 4
-      for (int k = 0; k < cnt; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, k);
-        const float* o = ws.o + slot_of(i0 + k) * g.Hv;
+        for (int k = 0; k < cnt; ++k) {
+          const float fk = __shfl_sync(0xffffffffu, f, k);
+          const float* o = ws.o + slot_of(i0 + k) * g.Hv;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {          // 4 columns per lane, twice for Hv > 128
-          const int d = (e * 32 + lane) * 4;
-          if (d < g.Hv && fk != 0.f) {
-            const float4 v = *reinterpret_cast<const float4*>(o + d);
-            acc[4 * e] = fmaf(fk, v.x, acc[4 * e]);
-            acc[4 * e + 1] = fmaf(fk, v.y, acc[4 * e + 1]);
-            acc[4 * e + 2] = fmaf(fk, v.z, acc[4 * e + 2]);
-            acc[4 * e + 3] = fmaf(fk, v.w, acc[4 * e + 3]);
+          for (int e = 0; e < 2; ++e) {          // 4 columns per lane, twice for Hv > 128
+            const int d = (e * 32 + lane) * 4;
+            if (d < g.Hv && fk != 0.f) {
+              const float4 v = *reinterpret_cast<const float4*>(o + d);
+              acc[4 * e] = fmaf(fk, v.x, acc[4 * e]);
+              acc[4 * e + 1] = fmaf(fk, v.y, acc[4 * e + 1]);
+              acc[4 * e + 2] = fmaf(fk, v.z, acc[4 * e + 2]);
+              acc[4 * e + 3] = fmaf(fk, v.w, acc[4 * e + 3]);
+            }
           }
         }
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     }
+    const int pr = rbk.row0 + r, h = at.kvh * g.group + pr % g.group;
+    const float inv = row_scale<T>(a, h, M, L);
+    T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, s.t0 + pr / g.group);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  }
-  const int pr = rbk.row0 + r, h = at.kvh * g.group + pr % g.group;
-  const float inv = row_scale<T>(a, h, M, L);
-  T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, s.t0 + pr / g.group);
+    for (int e = 0; e < 2; ++e) {
+      const int d = (e * 32 + lane) * 4;
+      if (d < g.Hv && SDPA_IN_BOUNDS(s.t0 + pr / g.group < g.tokens, 524)) {
+        T out[4];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int d = (e * 32 + lane) * 4;
-    if (d < g.Hv && SDPA_IN_BOUNDS(s.t0 + pr / g.group < g.tokens, 524)) {
-      T out[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) out[k] = Elem<T>::from_f32(acc[4 * e + k] * inv);
-      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y + d) = *reinterpret_cast<const uint4*>(out);
-      else *reinterpret_cast<uint2*>(y + d) = *reinterpret_cast<const uint2*>(out);
+        for (int k = 0; k < 4; ++k) out[k] = Elem<T>::from_f32(acc[4 * e + k] * inv);
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y + d) = *reinterpret_cast<const uint4*>(out);
+        else *reinterpret_cast<uint2*>(y + d) = *reinterpret_cast<const uint2*>(out);
+      }
     }
   }
 }
@@ -274,7 +274,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Pag
 template <typename T, int TM, int TN>
 cudaError_t merge_tn(const PagedAttn& a, const PagedWs& ws, int ctas, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)std::max(1, ctas - 1), (TM + kMergeWarps - 1) / kMergeWarps);
+  // at most 8 blocks a unit: most of them find nothing to join
+  cfg.gridDim = dim3((unsigned)std::max(1, ctas - 1), (unsigned)std::min(8, (TM + kMergeWarps - 1) / kMergeWarps));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute at{};
@@ -294,7 +295,8 @@ cudaError_t merge_t(const PagedAttn& a, const PagedWs& ws, int ctas, int tm, cud
     case 4: return merge_tn<T, 4, kTN>(a, ws, ctas, st);
     case 16: return merge_tn<T, 16, kTN>(a, ws, ctas, st);
     case 32: return merge_tn<T, 32, kTN>(a, ws, ctas, st);
-    default: return merge_tn<T, 64, kTN>(a, ws, ctas, st);
+    case 64: return merge_tn<T, 64, kTN>(a, ws, ctas, st);
+    default: return merge_tn<T, 256, 128>(a, ws, ctas, st);
   }
 }
 
@@ -346,16 +348,25 @@ cudaError_t launch_paged_merge(const PagedAttn& a, sdpa_dtype dt, const PagedWs&
 }
 
 PagedKernel paged_kernel(const PagedAttn& a, sdpa_dtype dt) {
+  if (paged_tc_supported(a, dt)) return kPagedTc;
   return paged_mma_supported(a, dt) ? kPagedMma : kPagedSimt;
 }
 
 size_t paged_workspace(const PagedAttn& a, sdpa_dtype dt) {
-  if (paged_kernel(a, dt) == kPagedMma) return paged_mma_workspace(a);
+  switch (paged_kernel(a, dt)) {
+    case kPagedTc: return paged_tc_workspace(a);
+    case kPagedMma: return paged_mma_workspace(a);
+    default: break;
+  }
   return paged_ws_bytes(kPagedMaxSms * kCtasPerSm, simt_tm(a), a.g.Hv);
 }
 
 cudaError_t launch_paged_attn(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name) {
-  if (paged_kernel(a, dt) == kPagedMma) return launch_paged_mma(a, dt, ws, st, name);
+  switch (paged_kernel(a, dt)) {
+    case kPagedTc: return launch_paged_tc(a, dt, ws, st, name);
+    case kPagedMma: return launch_paged_mma(a, dt, ws, st, name);
+    default: break;
+  }
   *name = dt == SDPA_F32 ? "paged_simt_f32" : dt == SDPA_F16 ? "paged_simt_f16" : "paged_simt_bf16";
   switch (dt) {
     case SDPA_F32: return launch_t<float>(a, dt, ws, st);

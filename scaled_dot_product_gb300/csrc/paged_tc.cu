@@ -1,0 +1,690 @@
+// Attention over a paged cache for chunks of new tokens: fp16 / bf16, H == Hv in {64, 128}, page
+// sizes that are multiples of 8.
+//
+// Bound by the tensor cores.  A unit is 256 packed rows (token x group head) of one (sequence,
+// kv head): two 128-row tiles that stream the same keys and values; a unit of at most 128 rows
+// leaves the second tile out.  One CTA per SM walks its share (paged_sched.cuh) of all units'
+// 128-key tiles:
+//
+//   warp 0      producer: K_0, V_0, K_1, ... into the ring by TMA.  A tile is 128 / box boxes of
+//               box = gcd(page_size, 128) rows, each inside one page; lane i looks up and issues
+//               box i
+//   warp 1      tensor products (one elected lane issues): S_X = Q_X K^T, O_X += P_X V with P
+//               read from tensor memory.  Rows of V that no box brought (past the sequence's keys,
+//               below every window) it sets to zero first, since 0 x NaN is not 0
+//   warps 2-3   query rows of the next unit (16-byte asynchronous copies: packed rows of a ragged
+//               batch need not start at a multiple of the box TMA would copy)
+//   warps 4-7   softmax of tile 0, one thread per row; warps 8-11 softmax of tile 1
+//
+// Running maxima move only when they grow by more than 2^8.  Every wait is bounded: on expiry the
+// kernel raises an abort flag, lets its own copies and products finish, frees its tensor memory
+// and records SDPA_ERR_TIMEOUT.
+#include <algorithm>
+#include <cstdlib>
+#include <mutex>
+#include <type_traits>
+
+#include "paged_sched.cuh"
+#include "prefill_tc.h"
+
+namespace sdpa {
+
+static __device__ int g_paged_status;
+static __device__ int g_paged_timeout;
+
+namespace {
+
+using namespace ptx;
+
+constexpr int kBM = 128, kTM = 256, kTN = 128;
+constexpr int kThreads = 384;
+constexpr int kMinShare = 4;
+// Register split: the control warpgroup shrinks to kCtlRegs, the softmax warpgroups grow to
+// kSmxRegs; the sum stays within the launch's kThreads x kLaunchRegs, which the host checks.
+constexpr int kLaunchRegs = 168, kCtlRegs = 88, kSmxRegs = 208;
+static_assert(kCtlRegs * 128 + kSmxRegs * 256 <= kLaunchRegs * kThreads, "register split");
+constexpr float kRescale = 8.f;      // log2 units
+
+template <int H>
+struct Cfg {
+  static constexpr int kRegions = H / 64;
+  static constexpr int kRegionBytes = 128 * 128;
+  static constexpr int kTile = 128 * H * 2;
+  static constexpr int kKVOff = 2 * kTile;                          // two Q tiles first
+  static constexpr int kYWarp = 32 * 128;                           // output staging per softmax warp
+  static constexpr int kFit = (232448 - 1024 - kKVOff - 8 * kYWarp) / kTile;
+  static constexpr int kStages = kFit < 10 ? kFit : 10;
+  static constexpr int kYOff = kKVOff + kStages * kTile;
+  static constexpr int kSmem = kYOff + 8 * kYWarp + 1024;
+  static_assert(kSmem <= 232448 && kStages >= 4, "shared memory");
+  // with H = 128 P_X overwrites S_X's first columns
+  static constexpr bool kAlias = H == 128;
+  static constexpr int kO0 = 256, kO1 = 256 + H;
+  static constexpr int kP0 = kAlias ? 0 : 256 + 2 * H, kP1 = kAlias ? 128 : kP0 + 64;
+};
+
+struct TcArgs {
+  PagedAttn a;
+  PagedWs ws;
+  int box, boxes;                    // rows per box, boxes per tile
+  int k_ds, k_dn, k_db, v_ds, v_dn, v_db;   // tensor-map dimension of slot / head / page
+  float scale_log2, cap_in, cap_log2;
+  int pre;                           // scale <= 0: scores are scaled before the maximum
+  uint64_t wait_ns;
+};
+
+__device__ __forceinline__ void perm_coords(int ds, int dn, int db, int s, int n, int b, int* c) {
+  c[0] = ds == 1 ? s : (dn == 1 ? n : b);
+  c[1] = ds == 2 ? s : (dn == 2 ? n : b);
+  c[2] = ds == 3 ? s : (dn == 3 ? n : b);
+}
+
+// Keys outside [elo, ehi] of a 128-key segment take -inf: per 32 columns one bit set, then one
+// test and one select per key.
+__device__ __forceinline__ void clip(float (&s)[128], int elo, int ehi) {
+#pragma unroll
+  for (int c0 = 0; c0 < 128; c0 += 32) {
+    const int lo = max(elo - c0, 0), hi = min(ehi - c0, 31);
+    const uint32_t up = 0xffffffffu >> (31 - max(hi, 0));
+    const uint32_t m = (lo <= hi) ? (up & (0xffffffffu << min(lo, 31))) : 0u;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) s[c0 + e] = ((m >> e) & 1u) ? s[c0 + e] : -INFINITY;
+  }
+}
+
+// Rows of key tile kt that the boxes bring: [first, last) of 128.
+__device__ __forceinline__ void box_rows(const TcArgs& t, const SeqInfo& s, const RowBlock& r, int kt, int& first, int& last) {
+  first = max(0, min(kTN, r.lo - r.lo % t.box - kt * kTN));
+  last = max(first, min(kTN, s.T - kt * kTN));
+}
+
+template <int H, bool BF, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                    const __grid_constant__ TcArgs t) {
+  using C = Cfg<H>;
+  using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+  using Wk = Walk<kTM, kTN>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
+  __shared__ __align__(8) uint64_t bar_qready, bar_qempty, bar_drain, bar_sfull[2], bar_sfree[2], bar_pfull[2], bar_odone[2];
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_flag;
+  const PagedAttn& a = t.a;
+  const Paged& g = a.g;
+  const int ctas = gridDim.x, cta = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sQ = smem_u32(smem), sKV = sQ + C::kKVOff;
+  auto b_full = [&](int s) { return smem_u32(&bar_full[s]); };
+  auto b_empty = [&](int s) { return smem_u32(&bar_empty[s]); };
+  auto b_sfull = [&](int x) { return smem_u32(&bar_sfull[x]); };
+  auto b_sfree = [&](int x) { return smem_u32(&bar_sfree[x]); };
+  auto b_pfull = [&](int x) { return smem_u32(&bar_pfull[x]); };
+  auto b_odone = [&](int x) { return smem_u32(&bar_odone[x]); };
+  const uint32_t b_qready = smem_u32(&bar_qready), b_qempty = smem_u32(&bar_qempty), b_drain = smem_u32(&bar_drain);
+  volatile int* abortp = &abort_flag;
+  constexpr uint64_t kDrainNs = 2000000000ull;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < C::kStages; ++s) { mbar_init(b_full(s), 1); mbar_init(b_empty(s), 1); }
+    mbar_init(b_qready, 2);
+    mbar_init(b_qempty, 1);
+    mbar_init(b_drain, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(b_sfull(x), 1);
+      mbar_init(b_sfree(x), kBM);
+      mbar_init(b_pfull(x), kBM);
+      mbar_init(b_odone(x), 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_sh), 512);
+    tmem_relinquish();
+  }
+  const Share sh = find_share<kTM, kTN, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
+  if (threadIdx.x == 0) {
+    if (cta == 0) t.ws.start[ctas].b = sh.active;
+    if (cta < sh.active) t.ws.start[cta] = sh.at;
+  }
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abortp, t.wait_ns));
+  };
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
+
+  if (warp == 0) {
+    // ================================================================ producer
+    if (lane == 0) {
+      prefetch_tmap(&tk);
+      prefetch_tmap(&tv);
+    }
+    int seq = 0;
+    bool ok = true;
+    for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
+      const int n = w.take(), kt0 = w.r.tile0 + w.tile;
+      const int32_t* table = g.table + (int64_t)w.b * g.table_stride;
+      // page of this lane's box of tile kt (-1: the box is not brought)
+      auto page_of = [&](int j) -> int {
+        if (j >= n) return -1;
+        int first, last;
+        box_rows(t, w.s, w.r, kt0 + j, first, last);
+        const int row = lane * t.box;
+        if (lane >= t.boxes || row < first || row >= last) return -1;
+        int id = table[page_div(g, (kt0 + j) * kTN + row)];
+        if (id < 0 || id >= g.num_pages) {
+          atomicOr(&g_paged_status, kPagedBadPage);
+          id = g.num_pages;              // outside the map: the box is filled with zeros
+        }
+        return id;
+      };
+      auto load = [&](bool is_v, int j, int id) -> bool {
+        const int st = seq % C::kStages;
+        if (seq >= C::kStages && !wait_all(b_empty(st), ((seq / C::kStages) - 1) & 1)) return false;
+        const unsigned brought = __ballot_sync(0xffffffffu, id >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(b_full(st), __popc(brought) * t.box * H * 2);
+        __syncwarp();
+        if (id >= 0 && SDPA_IN_BOUNDS(st < C::kStages && lane * t.box < kTN && w.kvh < g.Nkv, 541)) {
+          const int row = lane * t.box, key = (kt0 + j) * kTN + row;
+          const int slot = key - page_div(g, key) * g.page_size;
+          int c[3];
+          if (is_v) perm_coords(t.v_ds, t.v_dn, t.v_db, slot, w.kvh, id, c);
+          else perm_coords(t.k_ds, t.k_dn, t.k_db, slot, w.kvh, id, c);
+#pragma unroll
+          for (int r = 0; r < C::kRegions; ++r)
+            tma_load_4d(sKV + st * C::kTile + r * C::kRegionBytes + row * 128, is_v ? &tv : &tk, b_full(st), 64 * r, c[0],
+                        c[1], c[2]);
+        }
+        __syncwarp();
+        ++seq;
+        return true;
+      };
+      int id = page_of(0);
+      ok = load(false, 0, id);
+      for (int j = 0; j < n && ok; ++j) {
+        const int next = page_of(j + 1);
+        if constexpr (C::kAlias) {
+          ok = load(true, j, id);
+          if (ok && j + 1 < n) ok = load(false, j + 1, next);
+        } else {
+          if (j + 1 < n) ok = load(false, j + 1, next);
+          if (ok) ok = load(true, j, id);
+        }
+        id = next;
+      }
+    }
+    if (__any_sync(0xffffffffu, !ok || *abortp)) {
+      // some role gave up: let every copy already issued land before the CTA can exit
+      for (int s = 0; s < C::kStages && s < seq; ++s) {
+        const int last = s + ((seq - 1 - s) / C::kStages) * C::kStages;
+        mbar_wait_bounded(b_full(s), (last / C::kStages) & 1, nullptr, kDrainNs);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ================================================================ tensor products
+    const uint32_t leader = elect_one();
+    auto commit = [&](uint32_t bar) {
+      if (leader) mma_commit(bar);
+    };
+    constexpr uint32_t kIdQK = idesc_f16(BF, kBM, kTN, false);
+    constexpr uint32_t kIdPV = idesc_f16(BF, kBM, H, true);
+    const uint32_t tO[2] = {tmem + C::kO0, tmem + C::kO1}, tP[2] = {tmem + C::kP0, tmem + C::kP1};
+    const uint64_t dQ0 = desc_sw128(sQ, 16, 1024), dK0 = desc_sw128(sKV, 16, 1024);
+    const uint64_t dV0 = desc_sw128(sKV, C::kRegionBytes, 1024);
+    int seq = 0, it = 0;
+    int ns[2] = {0, 0}, np[2] = {0, 0};      // S issued, P consumed, per tile
+    auto wait_full = [&]() -> bool {
+      const bool ok = wait_all(b_full(seq % C::kStages), (seq / C::kStages) & 1);
+      tc_fence_after();
+      return ok;
+    };
+    auto issue_S = [&](int x, int st) {
+      const uint64_t dq = dQ0 + (uint64_t)((x * C::kTile) >> 4), dk = dK0 + (uint64_t)((st * C::kTile) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < H / 16; ++kk) {
+        const uint64_t off = (uint64_t)(((kk / 4) * C::kRegionBytes + (kk % 4) * 32) >> 4);
+        if (leader) mma_f16_ss(tmem + 128 * x, dq + off, dk + off, kIdQK, kk > 0);
+      }
+    };
+    auto issue_PV = [&](int x, int st, bool acc) {
+      const uint64_t dv = dV0 + (uint64_t)((st * C::kTile) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kTN / 16; ++kk)
+        if (leader) mma_f16_ts(tO[x], tP[x] + kk * 8, dv + (uint64_t)((kk * 2048) >> 4), kIdPV, (acc || kk > 0) ? 1u : 0u);
+    };
+    auto wait_sfree = [&](int x) -> bool {
+      if (C::kAlias || ns[x] == 0) return true;
+      const bool ok = wait_all(b_sfree(x), (ns[x] - 1) & 1);
+      tc_fence_after();
+      return ok;
+    };
+    bool ok = true;
+    for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
+      const int n = w.take(), kt0 = w.r.tile0 + w.tile, nx = w.r.rows > kBM ? 2 : 1;
+      // rows of V tile j that no box brought become zeros
+      auto zero_v = [&](int j, int st) {
+        int first, last;
+        box_rows(t, w.s, w.r, kt0 + j, first, last);
+        if (first == 0 && last == kTN) return;
+        for (int i = lane; i < kTN * 8; i += 32) {
+          const int row = i >> 3;
+          if (row < first || row >= last) {
+#pragma unroll
+            for (int r = 0; r < C::kRegions; ++r)
+              st_shared_v4(sKV + st * C::kTile + r * C::kRegionBytes + i * 16, 0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      if (!(ok = wait_all(b_qready, it & 1))) break;
+      tc_fence_after();
+      ++it;
+      if (!(ok = wait_full())) break;
+      {
+        const int st = seq % C::kStages;
+        for (int x = 0; x < nx && ok; ++x) {
+          if (!(ok = wait_sfree(x))) break;
+          issue_S(x, st);
+          commit(b_sfull(x));
+          ++ns[x];
+        }
+        if (!ok) break;
+        if (n == 1) commit(b_qempty);
+        commit(b_empty(st));
+        ++seq;
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const bool more = j + 1 < n;
+        if constexpr (C::kAlias) {
+          // P_X(j) lives in S_X's columns: PV_X(j) first, then S_X(j+1), whose sfull also says
+          // that PV_X(j) is done; the unit's last PV_X completes on odone_X
+          const int vst = seq % C::kStages;
+          if (!(ok = wait_full())) break;
+          zero_v(j, vst);
+          ++seq;
+          const int kst = seq % C::kStages;
+          for (int x = 0; x < nx && ok; ++x) {
+            if (!(ok = wait_all(b_pfull(x), np[x] & 1))) break;
+            tc_fence_after();
+            ++np[x];
+            issue_PV(x, vst, j > 0);
+            if (more) {
+              if (x == 0 && !(ok = wait_full())) break;
+              issue_S(x, kst);
+              commit(b_sfull(x));
+              ++ns[x];
+            } else {
+              commit(b_odone(x));
+            }
+          }
+          if (!ok) break;
+          if (more && j + 2 == n) commit(b_qempty);
+          commit(b_empty(vst));
+          if (more) {
+            commit(b_empty(kst));
+            ++seq;
+          }
+        } else {
+          if (more) {
+            const int kst = seq % C::kStages;
+            if (!(ok = wait_full())) break;
+            ++seq;
+            for (int x = 0; x < nx && ok; ++x) {
+              if (!(ok = wait_sfree(x))) break;
+              issue_S(x, kst);
+              commit(b_sfull(x));
+              ++ns[x];
+            }
+            if (!ok) break;
+            if (j + 2 == n) commit(b_qempty);
+            commit(b_empty(kst));
+          }
+          const int vst = seq % C::kStages;
+          if (!(ok = wait_full())) break;
+          zero_v(j, vst);
+          ++seq;
+          for (int x = 0; x < nx && ok; ++x) {
+            if (!(ok = wait_all(b_pfull(x), np[x] & 1))) break;
+            tc_fence_after();
+            ++np[x];
+            issue_PV(x, vst, j > 0);
+            commit(b_odone(x));
+          }
+          if (!ok) break;
+          commit(b_empty(vst));
+        }
+      }
+    }
+    // every product this thread issued completes before the CTA frees its tensor memory
+    commit(b_drain);
+    mbar_wait_bounded(b_drain, 0, nullptr, kDrainNs);
+    __syncwarp();
+  } else if (warp < 4) {
+    // ================================================================ query rows
+    const int x = warp - 2;
+    constexpr int CPR = H / 8;                       // 16-byte chunks of a row
+    const int chunk = lane % CPR, rin = lane / CPR;
+    int it = 0;
+    bool ok = true;
+    for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
+      if (it > 0 && !(ok = wait_all(b_qempty, (it - 1) & 1))) break;
+      ++it;
+      if (x * kBM < w.r.rows) {
+        const uint32_t dst = sQ + x * C::kTile + (chunk >> 3) * C::kRegionBytes;
+#pragma unroll 4
+        for (int r0 = 0; r0 < kBM; r0 += 32 / CPR) {
+          const int r = r0 + rin;
+          const bool take = x * kBM + r < w.r.rows;
+          const int pr = w.r.row0 + (take ? x * kBM + r : 0);
+          const int tok = pr / g.group;
+          const T* src = reinterpret_cast<const T*>(a.q.p) + a.q.off(0, w.kvh * g.group + pr - tok * g.group, w.s.t0 + tok) +
+                         chunk * 8;
+          const uint32_t d = dst + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src),
+                       "r"(take && SDPA_IN_BOUNDS(w.s.t0 + tok < g.tokens, 542) ? 16 : 0) : "memory");
+        }
+        cp_async_commit();
+        cp_async_wait_all();
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_qready);
+    }
+  } else {
+    // ================================================================ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSmxRegs));
+    const int x = (warp - 4) >> 2, sub = warp & 3;
+    const int row = sub * 32 + lane;                 // row of the tile == tensor-memory lane
+    const uint32_t trow = tmem + ((uint32_t)(sub * 32) << 16);
+    const uint32_t tS = trow + 128 * x, tO = trow + (x ? C::kO1 : C::kO0), tP = trow + (x ? C::kP1 : C::kP0);
+    const uint32_t sY = sQ + C::kYOff + (uint32_t)(x * 4 + sub) * C::kYWarp;
+    const float kfac = CAP || t.pre ? 1.f : t.scale_log2;
+    int cs = 0, co = 0;                              // sfull / odone phases waited
+    bool ok = true;
+    for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
+      if (x * kBM >= w.r.rows) continue;
+      const int n = w.take(), kt0 = w.r.tile0 + w.tile;
+      const bool valid = x * kBM + row < w.r.rows;
+      const int pr = w.r.row0 + (valid ? x * kBM + row : 0);
+      int lo = 1, hi = 0;
+      if (valid) row_keys(a, w.s, pr, lo, hi);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        if (!(ok = wait_all(b_sfull(x), cs & 1))) break;
+        ++cs;
+        tc_fence_after();
+        float s[128];
+        {
+          uint32_t u[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, u + c * 32);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 128; ++e) s[e] = __uint_as_float(u[e]);
+        }
+        if constexpr (!C::kAlias) {
+          tc_fence_before();
+          mbar_arrive(b_sfree(x));
+        }
+        if constexpr (CAP) {
+          // cap tanh(u) in log2 units: 1 - 2 / (e^2u + 1), absolute error about 2^-23 of the cap
+          const float c2 = 2.f * kLog2e * t.cap_in;
+#pragma unroll
+          for (int e = 0; e < 128; ++e)
+            s[e] = t.cap_log2 * (1.f - __fdividef(2.f, ex2_approx(s[e] * c2) + 1.f));
+        } else if (t.pre) {
+#pragma unroll
+          for (int e = 0; e < 128; ++e) s[e] *= t.scale_log2;
+        }
+        const int key0 = (kt0 + j) * kTN;
+        if (!(lo <= key0 && key0 + kTN - 1 <= hi)) clip(s, lo - key0, hi - key0);
+        float mx8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx8[k] = fmaxf(s[k], s[k + 8]);
+#pragma unroll
+        for (int e = 16; e < 128; e += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx8[k] = fmax3(mx8[k], s[e + k], s[e + 8 + k]);
+        const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+        const float m_new = fmaxf(m, mx * kfac);
+        const bool need = m_new > m + kRescale;      // true for a row's first keys: m = -inf
+        float corr = 1.f;
+        if (need) {
+          corr = ex2_approx(m - m_new);
+          m = m_new;
+        }
+        // rows with nothing admitted yet: exponent -inf, weight 0
+        const float negm = (m == -INFINITY) ? -INFINITY : -m;
+        const f2_t kf2 = f2_pack(kfac, kfac), nm2 = f2_pack(negm, negm);
+        f2_t acc[4] = {f2_zero(), f2_zero(), f2_zero(), f2_zero()};
+        uint32_t pw[64];
+#pragma unroll
+        for (int e = 0; e < 128; e += 2) {
+          float z0, z1;
+          f2_unpack(f2_fma(f2_pack(s[e], s[e + 1]), kf2, nm2), z0, z1);
+          const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
+          acc[(e >> 1) & 3] = f2_add(acc[(e >> 1) & 3], f2_pack(p0, p1));
+          pw[e >> 1] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+        }
+        float r0, r1, r2, r3;
+        f2_unpack(f2_add(acc[0], acc[1]), r0, r1);
+        f2_unpack(f2_add(acc[2], acc[3]), r2, r3);
+        l = l * corr + ((r0 + r1) + (r2 + r3));
+        if (j > 0) {
+          // PV_X(j-1) has read P_X and O_X holds it (with P in S's columns, sfull said so)
+          if constexpr (!C::kAlias) {
+            if (!(ok = wait_all(b_odone(x), co & 1))) break;
+            ++co;
+            tc_fence_after();
+          }
+          if (__any_sync(0xffffffffu, need)) {
+            const f2_t c2 = f2_pack(corr, corr);
+#pragma unroll
+            for (int c = 0; c < H / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float v0, v1;
+                f2_unpack(f2_mul(f2_pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), c2), v0, v1);
+                o[e] = __float_as_uint(v0);
+                o[e + 1] = __float_as_uint(v1);
+              }
+              tmem_st32(tO + c * 32, o);
+            }
+            tmem_st_wait();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_st32(tP + c * 32, pw + c * 32);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(b_pfull(x));
+      }
+      if (!ok) break;
+
+      // ---- the unit's rows, or their partial results
+      if (!(ok = wait_all(b_odone(x), co & 1))) break;
+      ++co;
+      tc_fence_after();
+      const bool whole = w.whole();
+      const int live = min(32, w.r.rows - x * kBM - sub * 32);       // rows of this warp
+      if (whole) {
+        const int tok = pr / g.group, h = w.kvh * g.group + pr - tok * g.group;
+        const float inv = row_scale<T>(a, h, m, l);
+        const long long yrow = (long long)(reinterpret_cast<uintptr_t>(a.y.p) + (uintptr_t)(a.y.off(0, h, w.s.t0 + tok) * 2));
+#pragma unroll
+        for (int c = 0; c < H / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + c * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t wv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float v0 = __uint_as_float(o[q * 8 + 2 * e]) * inv, v1 = __uint_as_float(o[q * 8 + 2 * e + 1]) * inv;
+              wv[e] = BF ? pack_bf16x2(v0, v1) : pack_f16x2(v0, v1);
+            }
+            const int c16 = (c & 1) * 4 + q;
+            st_shared_v4(sY + lane * 128 + ((c16 ^ (lane & 7)) << 4), wv[0], wv[1], wv[2], wv[3]);
+          }
+          if (c & 1) {
+            // 64 columns of 32 rows are staged: eight lanes store 128 bytes of a row
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int rr = i * 4 + (lane >> 3), c16 = lane & 7;
+              const long long dst = __shfl_sync(0xffffffffu, yrow, rr);
+              uint4 v;
+              ld_shared_v4(sY + rr * 128 + ((c16 ^ (rr & 7)) << 4), v.x, v.y, v.z, v.w);
+              if (rr < live && SDPA_IN_BOUNDS(w.s.t0 + w.s.n <= g.tokens, 543))
+                *reinterpret_cast<uint4*>((uintptr_t)dst + (c >> 1) * 128 + c16 * 16) = v;
+            }
+            __syncwarp();
+          }
+        }
+      } else {
+        const int64_t base = (2 * (int64_t)cta + (w.begins() ? 1 : 0)) * kTM + x * kBM + sub * 32;
+        if (lane < live && SDPA_IN_BOUNDS(base + lane < (int64_t)2 * ctas * kTM, 544)) {
+          t.ws.ml[(base + lane) * 2] = m;
+          t.ws.ml[(base + lane) * 2 + 1] = l;
+        }
+#pragma unroll
+        for (int c = 0; c < H / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + c * 32, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_shared_v4(sY + lane * 128 + ((q ^ (lane & 7)) << 4), o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = i * 4 + (lane >> 3), q = lane & 7;
+            uint4 v;
+            ld_shared_v4(sY + rr * 128 + ((q ^ (rr & 7)) << 4), v.x, v.y, v.z, v.w);
+            if (rr < live && SDPA_IN_BOUNDS(base + rr < (int64_t)2 * ctas * kTM, 545))
+              *reinterpret_cast<uint4*>(t.ws.o + (base + rr) * H + c * 32 + q * 4) = v;
+          }
+          __syncwarp();
+        }
+      }
+      // these tensor-memory reads are complete before this thread's next P store, which the MMA
+      // warp waits for before the next unit's first PV overwrites O
+    }
+  }
+
+  // ---- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && abort_flag) atomicExch(&g_paged_timeout, (int)SDPA_ERR_TIMEOUT);
+}
+
+// ---------------------------------------------------------------- host side
+
+uint64_t wait_limit_ns() {
+  static const uint64_t v = [] {
+    const char* e = std::getenv("SDPA_WAIT_LIMIT_NS");
+    return e ? std::strtoull(e, nullptr, 10) : 4000000000ull;
+  }();
+  return v;
+}
+
+template <int H, bool BF, bool CAP>
+cudaError_t launch_cap(const CUtensorMap& tk, const CUtensorMap& tv, const TcArgs& t, int ctas, cudaStream_t st) {
+  using C = Cfg<H>;
+  auto* kernel = paged_tc_kernel<H, BF, CAP>;
+  // per device: set at every call (the attribute belongs to the current context)
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaFuncAttributes fa{};
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
+  // with fewer registers at launch the softmax warps' request could never be met
+  if (e == cudaSuccess && fa.numRegs < kLaunchRegs) e = cudaErrorLaunchOutOfResources;
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)ctas, kThreads, C::kSmem, st>>>(tk, tv, t);
+  count_launch(1);
+  return cudaGetLastError();
+}
+
+template <int H>
+cudaError_t launch_h(bool bf, bool cap, const CUtensorMap& tk, const CUtensorMap& tv, const TcArgs& t, int ctas,
+                     cudaStream_t st) {
+  if (bf) return cap ? launch_cap<H, true, true>(tk, tv, t, ctas, st) : launch_cap<H, true, false>(tk, tv, t, ctas, st);
+  return cap ? launch_cap<H, false, true>(tk, tv, t, ctas, st) : launch_cap<H, false, false>(tk, tv, t, ctas, st);
+}
+
+}  // namespace
+
+// More rows of a sequence than paged_mma's widest unit holds, and pages that boxes of at least
+// eight rows tile.
+bool paged_tc_supported(const PagedAttn& a, sdpa_dtype dt) {
+  if (dt == SDPA_F32 || a.g.H != a.g.Hv || (a.g.H != 64 && a.g.H != 128)) return false;
+  if (a.g.page_size % 8 || a.g.num_pages < 1) return false;
+  for (const View* v : {&a.g.kp, &a.g.vp})
+    for (int64_t s : {v->sb, v->sh, v->ss})
+      if (s >= ((int64_t)1 << 38)) return false;
+  return (int64_t)a.max_new * a.g.group > 64;
+}
+
+size_t paged_tc_workspace(const PagedAttn& a) { return paged_ws_bytes(kPagedMaxSms, kTM, a.g.Hv); }
+
+cudaError_t launch_paged_tc(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaStream_t st, const char** name) {
+  const int ctas = paged_sms();
+  if (ctas <= 0) return cudaErrorInvalidDevice;
+  TcArgs t{};
+  t.a = a;
+  t.ws = paged_ws(wsp, ctas, kTM);
+  t.box = kTN;
+  while (a.g.page_size % t.box) t.box >>= 1;
+  t.boxes = kTN / t.box;
+  t.scale_log2 = a.scale * kLog2e;
+  t.pre = !(a.scale > 0.f);
+  t.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+  t.cap_log2 = a.softcap * kLog2e;
+  t.wait_ns = wait_limit_ns();
+  CUtensorMap tk, tv;
+  if (!tc_make_map(&tk, a.g.kp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, a.g.H, &t.k_ds, &t.k_dn, &t.k_db, t.box) ||
+      !tc_make_map(&tv, a.g.vp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, a.g.Hv, &t.v_ds, &t.v_dn, &t.v_db, t.box))
+    return cudaErrorInvalidValue;
+  const bool bf = dt == SDPA_BF16, cap = a.softcap > 0.f;
+  cudaError_t e;
+  if (a.g.H == 128) {
+    *name = bf ? "paged_tc_bf16_h128" : "paged_tc_f16_h128";
+    e = launch_h<128>(bf, cap, tk, tv, t, ctas, st);
+  } else {
+    *name = bf ? "paged_tc_bf16_h64" : "paged_tc_f16_h64";
+    e = launch_h<64>(bf, cap, tk, tv, t, ctas, st);
+  }
+  return e == cudaSuccess ? launch_paged_merge(a, dt, t.ws, ctas, kTM, st) : e;
+}
+
+cudaError_t take_paged_tc_status(int* status, int* timeout) {
+  int v[2] = {0, 0};
+  cudaError_t e = cudaMemcpyFromSymbol(&v[0], g_paged_status, sizeof v[0]);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v[1], g_paged_timeout, sizeof v[1]);
+  if (e != cudaSuccess) return e;
+  *status = v[0];
+  *timeout = v[1];
+  const int zero = 0;
+  if (v[0]) e = cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero);
+  if (e == cudaSuccess && v[1]) e = cudaMemcpyToSymbol(g_paged_timeout, &zero, sizeof zero);
+  return e;
+}
+
+SDPA_DEFINE_BOUNDS_TAKE(take_bounds_paged_tc)
+
+}  // namespace sdpa
