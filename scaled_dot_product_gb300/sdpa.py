@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -448,108 +449,134 @@ def sdpa_rotary(x: torch.Tensor, cos_cache: torch.Tensor, sin_cache: torch.Tenso
     return y
 
 
-class _OnDevice:
-    """The device and stream of one call: every tensor must be on one CUDA device, which becomes
-    current for the call; memory the binding allocates is kept for the stream the call runs on."""
+# ----------------------------------------------------------------------------------------
+# Query/key norm and paged cache.  Single-token calls are shorter on the GPU than their
+# marshalling, so these fill their structs in one struct.pack and take strides directly
+# instead of building view tensors.
+# ----------------------------------------------------------------------------------------
 
-    def __init__(self, tensors: dict, stream):
-        given = {name: t for name, t in tensors.items() if t is not None}
-        for name, t in given.items():
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor")
-        self.device = next(iter(given.values())).device
-        for name, t in given.items():
-            if t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        self.guard = torch.cuda.device(self.device)
-        self.stream = stream
+_NORM_FIELDS = struct.Struct("@7i4x4q4qPPf4xPPqPii")
+_PAGED_FIELDS = struct.Struct("@11i4x4q4qPqPPPPqiiiffiqPi4x")
+assert _NORM_FIELDS.size == ctypes.sizeof(sdpa_qk_norm_params)
+assert _PAGED_FIELDS.size == ctypes.sizeof(sdpa_paged_params)
 
-    def __enter__(self):
-        self.guard.__enter__()
-        self.current = torch.cuda.current_stream(self.device)
-        self.handle = self.current.cuda_stream if self.stream is None else _stream(self.stream)
-        return self
 
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+def _place(stream, tensors: tuple, names: str) -> Tuple[int, int]:
+    """(device, stream handle) of a call.  Every given tensor must be on that CUDA device; the
+    default stream is the device's current one."""
+    d = tensors[0].get_device()
+    for i, t in enumerate(tensors):
+        if t is not None and (d < 0 or t.get_device() != d):
+            raise ValueError(f"{names.split()[i]} must be a CUDA tensor on the device of {names.split()[0]}, "
+                             f"got {t.device} and {tensors[0].device}")
+    if stream is None:
+        return d, torch._C._cuda_getCurrentRawStream(d)
+    return d, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
-    def keep(self, *allocated):
-        if self.handle != self.current.cuda_stream:
-            s = self.stream if hasattr(self.stream, "cuda_stream") else \
-                torch.cuda.ExternalStream(self.handle, device=self.device)
-            for t in allocated:
-                if t is not None and t.numel():
-                    t.record_stream(s)
+
+def _call(device: int, fn, *args):
+    """fn(*args) with `device` current; raises on a non-zero status."""
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    else:
+        rc = fn(*args)
+    if rc:
+        _check(rc)
+
+
+def _keep_for(stream, device: int, handle: int, *allocated):
+    """Memory the binding allocated for a call on a stream the caller named belongs to that stream
+    until the call's work is done."""
+    if stream is None or handle == torch._C._cuda_getCurrentRawStream(device):
+        return
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=device)
+    for t in allocated:
+        if t is not None and t.numel():
+            t.record_stream(s)
 
 
 def _typed(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape=None):
     if t is None:
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _flat_ptr(t: Optional[torch.Tensor], name: str) -> int:
+    if t is None:
+        return 0
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 def _element_type(t: torch.Tensor) -> int:
-    if t.dtype not in _DTYPES:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"unsupported type {t.dtype}")
-    return _DTYPES[t.dtype]
+    return dt
+
+
+def _head_view(t: torch.Tensor, D: int, name: str) -> Tuple[int, int, int, int]:
+    """(pointer, batch stride, head stride, row stride) of a rank-4 (B, N, S, D) or rank-3
+    (B, S, N*D) tensor."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if len(st) == 4:
+        return t.data_ptr(), st[0], st[1], st[2]
+    return t.data_ptr(), st[0], D, st[1]
 
 
 def _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim, interleaved,
                  num_heads, kv_num_heads):
-    """(params, 4-D views of q and k, tensors to keep) of the query/key norm."""
-    if q.dim() != k.dim() or q.dim() not in (3, 4):
+    """(params, head size, position ids to keep) of the query/key norm."""
+    if q.dim() == 4:
+        B, Nq, S, D = q.shape
+        if k.dim() != 4 or k.shape[0] != B or k.shape[2] != S or k.shape[3] != D:
+            raise ValueError(f"k {tuple(k.shape)} does not match q {tuple(q.shape)}")
+        Nkv = k.shape[1]
+    elif q.dim() == 3 and k.dim() == 3:
+        if not (num_heads and kv_num_heads):
+            raise ValueError("rank-3 inputs need num_heads and kv_num_heads")
+        Nq, Nkv = num_heads, kv_num_heads
+        B, S, wide = q.shape
+        D = wide // Nq
+        if wide != D * Nq or k.shape != (B, S, D * Nkv):
+            raise ValueError(f"{Nq} and {Nkv} heads do not fit q {tuple(q.shape)} and k {tuple(k.shape)}")
+    else:
         raise ValueError("q and k must both be rank 3 (B, S, N*D) or both rank 4 (B, N, S, D)")
-    if q.dim() == 3 and not (num_heads and kv_num_heads):
-        raise ValueError("rank-3 inputs need num_heads and kv_num_heads")
-    q4, k4 = _rank4(q, num_heads, "q"), _rank4(k, kv_num_heads, "k")
-    B, Nq, S, D = q4.shape
-    if (k4.shape[0], k4.shape[2], k4.shape[3]) != (B, S, D):
-        raise ValueError(f"k {tuple(k4.shape)} does not match q {tuple(q4.shape)}")
-    keep: list = []
-    p = sdpa_qk_norm_params()
-    p.struct_size = ctypes.sizeof(sdpa_qk_norm_params)
-    p.B, p.Nq, p.Nkv, p.S, p.D = B, Nq, k4.shape[1], S, D
-    p.dtype = _element_type(q)
-    for name, t in (("k", k), ("q_weight", q_weight), ("k_weight", k_weight), ("cos_cache", cos_cache),
-                    ("sin_cache", sin_cache)):
-        _typed(t, name, q.dtype)
-    _typed(q_weight, "q_weight", q.dtype, (D,))
-    _typed(k_weight, "k_weight", q.dtype, (D,))
-    p.q, p.k = _view(q4, keep), _view(k4, keep)
-    p.q_weight, p.k_weight = _ptr(q_weight, keep), _ptr(k_weight, keep)
-    p.eps = float(eps)
-    p.rotary_dim, p.rotary_interleaved = int(rotary_dim), 1 if interleaved else 0
-    if (cos_cache is None) != (sin_cache is None):
-        raise ValueError("cos_cache and sin_cache must be given together")
+    dt = q.dtype
+    _typed(k, "k", dt)
+    _typed(q_weight, "q_weight", dt, (D,))
+    _typed(k_weight, "k_weight", dt, (D,))
+    rotary_dim = int(rotary_dim)
+    rows, pos = 0, None
     if cos_cache is not None:
-        half = (int(rotary_dim) or D) // 2
+        half = (rotary_dim or D) // 2
         if position_ids is None:
-            _typed(cos_cache, "cos_cache", q.dtype, (B, S, half))
-            p.rotary_max_pos = B * S
+            _typed(cos_cache, "cos_cache", dt, (B, S, half))
+            rows = B * S
         else:
-            if cos_cache.dim() != 2 or cos_cache.shape[1] != half:
-                raise ValueError(f"cos_cache must have shape (positions, {half}), got {tuple(cos_cache.shape)}")
-            if not position_ids.is_cuda:
-                raise ValueError("position_ids must be a CUDA tensor")
-            pos = position_ids.to(torch.int64).expand(B, S).contiguous()
-            p.position_ids = _ptr(pos, keep)
-            p.rotary_max_pos = cos_cache.shape[0]
-        _typed(sin_cache, "sin_cache", q.dtype, cos_cache.shape)
-        p.rotary_cos, p.rotary_sin = _ptr(cos_cache, keep), _ptr(sin_cache, keep)
-    elif position_ids is not None:
-        raise ValueError("position_ids without cos_cache / sin_cache")
-    return p, q4, k4, keep
-
-
-def _rank4(t: torch.Tensor, heads: Optional[int], name: str) -> torch.Tensor:
-    if t.dim() == 4:
-        return t
-    if t.shape[2] % heads:
-        raise ValueError(f"{name}: {t.shape[2]} channels are no multiple of {heads} heads")
-    return _heads4(t, heads)
+            _typed(cos_cache, "cos_cache", dt, (cos_cache.shape[0], half))
+            pos = position_ids
+            if pos.dtype is not torch.int64 or pos.shape != (B, S) or not pos.is_contiguous():
+                pos = pos.to(torch.int64).expand(B, S).contiguous()
+            rows = cos_cache.shape[0]
+        if sin_cache is None:
+            raise ValueError("cos_cache and sin_cache must be given together")
+        _typed(sin_cache, "sin_cache", dt, cos_cache.shape)
+    elif sin_cache is not None or position_ids is not None:
+        raise ValueError("sin_cache or position_ids without cos_cache")
+    p = sdpa_qk_norm_params.from_buffer_copy(_NORM_FIELDS.pack(
+        _NORM_FIELDS.size, B, Nq, Nkv, S, D, _element_type(q), *_head_view(q, D, "q"), *_head_view(k, D, "k"),
+        _flat_ptr(q_weight, "q_weight"), _flat_ptr(k_weight, "k_weight"), eps, _flat_ptr(cos_cache, "cos_cache"),
+        _flat_ptr(sin_cache, "sin_cache"), rows, 0 if pos is None else pos.data_ptr(), rotary_dim,
+        1 if interleaved else 0))
+    return p, D, pos
 
 
 def _like(t: Optional[torch.Tensor], ref: torch.Tensor, name: str) -> torch.Tensor:
@@ -570,14 +597,14 @@ def sdpa_qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor
     one pass over rank-4 (B, N, S, D) or rank-3 (B, S, N*D) tensors (num_heads and kv_num_heads
     given).  Caches as for sdpa_rotary; without caches there is no rotation.  Returns (q_out,
     k_out) in the inputs' shapes; an output may be its input."""
-    with _OnDevice(dict(q=q, k=k, q_weight=q_weight, k_weight=k_weight, cos_cache=cos_cache, sin_cache=sin_cache,
-                        position_ids=position_ids, q_out=q_out, k_out=k_out), stream) as dev:
-        p, _, _, keep = _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim,
-                                     interleaved, num_heads, kv_num_heads)
-        q_out, k_out = _like(q_out, q, "q_out"), _like(k_out, k, "k_out")
-        dev.keep(q_out, k_out, *keep)
-        _check(lib().sdpa_qk_norm_rotary(ctypes.byref(p), _view(_rank4(q_out, num_heads, "q_out"), keep),
-                                         _view(_rank4(k_out, kv_num_heads, "k_out"), keep), dev.handle))
+    d, handle = _place(stream, (q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, q_out, k_out),
+                       "q k q_weight k_weight cos_cache sin_cache position_ids q_out k_out")
+    p, D, pos = _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim, interleaved,
+                             num_heads, kv_num_heads)
+    q_out, k_out = _like(q_out, q, "q_out"), _like(k_out, k, "k_out")
+    _keep_for(stream, d, handle, q_out, k_out, pos)
+    _call(d, lib().sdpa_qk_norm_rotary, p, sdpa_view(*_head_view(q_out, D, "q_out")),
+          sdpa_view(*_head_view(k_out, D, "k_out")), handle)
     return q_out, k_out
 
 
@@ -590,82 +617,74 @@ def sdpa_qk_norm_rotary_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tens
                             workspace=None, stream=None):
     """Gradient of sdpa_qk_norm_rotary for the upstream gradients dq_out, dk_out of its outputs:
     returns (dq, dk, dq_weight, dk_weight).  dq may be dq_out itself and dk dk_out."""
-    with _OnDevice(dict(q=q, k=k, dq_out=dq_out, dk_out=dk_out, q_weight=q_weight, k_weight=k_weight,
-                        cos_cache=cos_cache, sin_cache=sin_cache, position_ids=position_ids, dq=dq, dk=dk,
-                        dq_weight=dq_weight, dk_weight=dk_weight, workspace=workspace), stream) as dev:
-        p, _, _, keep = _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim,
-                                     interleaved, num_heads, kv_num_heads)
-        _typed(dq_out, "dq_out", q.dtype, q.shape)
-        _typed(dk_out, "dk_out", k.dtype, k.shape)
-        dq, dk = _like(dq, q, "dq"), _like(dk, k, "dk")
-        dq_weight, dk_weight = _like(dq_weight, q_weight, "dq_weight"), _like(dk_weight, k_weight, "dk_weight")
-        if workspace is None:
-            workspace = torch.empty(max(1, int(lib().sdpa_qk_norm_workspace_size(ctypes.byref(p)))), dtype=torch.uint8,
-                                    device=dev.device)
-        dev.keep(dq, dk, dq_weight, dk_weight, workspace, *keep)
-        v = lambda t, n, name: _view(_rank4(t, n, name), keep)
-        _check(lib().sdpa_qk_norm_rotary_bwd(
-            ctypes.byref(p), v(dq_out, num_heads, "dq_out"), v(dk_out, kv_num_heads, "dk_out"),
-            v(dq, num_heads, "dq"), v(dk, kv_num_heads, "dk"), _ptr(dq_weight, keep), _ptr(dk_weight, keep),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), dev.handle))
+    d, handle = _place(stream, (q, k, dq_out, dk_out, q_weight, k_weight, cos_cache, sin_cache, position_ids, dq, dk,
+                                dq_weight, dk_weight, workspace),
+                       "q k dq_out dk_out q_weight k_weight cos_cache sin_cache position_ids dq dk dq_weight dk_weight "
+                       "workspace")
+    p, D, pos = _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim, interleaved,
+                             num_heads, kv_num_heads)
+    _typed(dq_out, "dq_out", q.dtype, q.shape)
+    _typed(dk_out, "dk_out", k.dtype, k.shape)
+    dq, dk = _like(dq, q, "dq"), _like(dk, k, "dk")
+    dq_weight, dk_weight = _like(dq_weight, q_weight, "dq_weight"), _like(dk_weight, k_weight, "dk_weight")
+    if workspace is None:
+        workspace = torch.empty(max(1, lib().sdpa_qk_norm_workspace_size(p)), dtype=torch.uint8, device=q.device)
+    _keep_for(stream, d, handle, dq, dk, dq_weight, dk_weight, workspace, pos)
+    v = lambda t, name: sdpa_view(*_head_view(t, D, name))
+    _call(d, lib().sdpa_qk_norm_rotary_bwd, p, v(dq_out, "dq_out"), v(dk_out, "dk_out"), v(dq, "dq"), v(dk, "dk"),
+          _flat_ptr(dq_weight, "dq_weight"), _flat_ptr(dk_weight, "dk_weight"), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), handle)
     return dq, dk, dq_weight, dk_weight
+
+
+def _pool_view(t: torch.Tensor, name: str) -> Tuple[int, int, int, int]:
+    sb, sh, ss, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), sb, sh, ss
 
 
 def make_paged_params(k_pages, v_pages, page_table, kv_lens, tokens: int, Nq: int, *, cu_new=None,
                       cos_cache=None, sin_cache=None, rotary_dim=0, interleaved=False, scale=None, softcap=0.0,
-                      causal="lower_right", window=-1, head_sink=None,
-                      max_new=None) -> Tuple[sdpa_paged_params, list]:
-    """Fills sdpa_paged_params.  Returns (params, tensors to keep alive)."""
-    keep: list = []
+                      causal="lower_right", window=-1, head_sink=None, max_new=None) -> sdpa_paged_params:
+    """Fills sdpa_paged_params (the caller keeps the tensors alive)."""
+    dt = k_pages.dtype
     if k_pages.dim() != 4 or v_pages.dim() != 4:
         raise ValueError("k_pages and v_pages are (pages, heads, slots, dim) views")
-    if v_pages.shape[:3] != k_pages.shape[:3]:
-        raise ValueError(f"v_pages {tuple(v_pages.shape)} does not match k_pages {tuple(k_pages.shape)}")
+    pages, Nkv, slots, H = k_pages.shape
+    Hv = v_pages.shape[3]
+    _typed(v_pages, "v_pages", dt, (pages, Nkv, slots, Hv))
     if page_table.dim() != 2:
         raise ValueError("page_table must be (B, max_pages)")
-    if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+    B, width = page_table.shape
+    table_stride, entry_stride = page_table.stride()
+    if entry_stride != 1 and width > 1:
         raise ValueError("the rows of page_table must be contiguous")
-    B = page_table.shape[0]
-    p = sdpa_paged_params()
-    p.struct_size = ctypes.sizeof(sdpa_paged_params)
-    p.dtype = _element_type(k_pages)
-    for name, t in (("v_pages", v_pages), ("cos_cache", cos_cache), ("sin_cache", sin_cache), ("head_sink", head_sink)):
-        _typed(t, name, k_pages.dtype)
     _typed(page_table, "page_table", torch.int32)
     _typed(kv_lens, "kv_lens", torch.int32, (B,))
     _typed(cu_new, "cu_new", torch.int32, (B + 1,))
-    _typed(head_sink, "head_sink", k_pages.dtype, (Nq,))
-    p.B, p.tokens, p.Nq = B, tokens, Nq
-    p.num_pages, p.Nkv, p.page_size, p.H = k_pages.shape
-    p.Hv = v_pages.shape[3]
-    p.max_pages = page_table.shape[1]
-    p.k_pages, p.v_pages = _view(k_pages, keep), _view(v_pages, keep)
-    keep.append(page_table)
-    p.page_table, p.page_table_stride = page_table.data_ptr(), page_table.stride(0)
-    p.kv_lens, p.cu_new = _ptr(kv_lens, keep), _ptr(cu_new, keep)
+    _typed(head_sink, "head_sink", dt, (Nq,))
+    rotary_dim = int(rotary_dim)
+    rows = 0
     if cos_cache is not None:
-        half = (int(rotary_dim) or p.H) // 2
-        if cos_cache.dim() != 2 or cos_cache.shape[1] != half:
-            raise ValueError(f"cos_cache must have shape (positions, {half}), got {tuple(cos_cache.shape)}")
-        _typed(sin_cache, "sin_cache", k_pages.dtype, cos_cache.shape)
-        p.rotary_max_pos = cos_cache.shape[0]
-    p.rotary_cos, p.rotary_sin = _ptr(cos_cache, keep), _ptr(sin_cache, keep)
-    p.rotary_dim, p.rotary_interleaved = int(rotary_dim), 1 if interleaved else 0
-    p.has_scale = 0 if scale is None else 1
-    p.scale = 0.0 if scale is None else float(scale)
-    p.softcap = float(softcap)
-    p.causal = CAUSAL[causal] if isinstance(causal, str) else int(causal)
-    p.window = int(window)
-    p.head_sink = _ptr(head_sink, keep)
-    p.max_new = 0 if max_new is None else int(max_new)
-    return p, keep
+        _typed(cos_cache, "cos_cache", dt, (cos_cache.shape[0], (rotary_dim or H) // 2))
+        _typed(sin_cache, "sin_cache", dt, cos_cache.shape)
+        rows = cos_cache.shape[0]
+    return sdpa_paged_params.from_buffer_copy(_PAGED_FIELDS.pack(
+        _PAGED_FIELDS.size, B, tokens, Nq, Nkv, H, Hv, _element_type(k_pages), pages, slots, width,
+        *_pool_view(k_pages, "k_pages"), *_pool_view(v_pages, "v_pages"), page_table.data_ptr(), table_stride,
+        _flat_ptr(kv_lens, "kv_lens"), _flat_ptr(cu_new, "cu_new"), _flat_ptr(cos_cache, "cos_cache"),
+        _flat_ptr(sin_cache, "sin_cache"), rows, rotary_dim, 1 if interleaved else 0, 0 if scale is None else 1,
+        0.0 if scale is None else scale, softcap, CAUSAL[causal] if isinstance(causal, str) else int(causal), int(window),
+        _flat_ptr(head_sink, "head_sink"), 0 if max_new is None else int(max_new)))
 
 
-def _packed(t: torch.Tensor, name: str, keep: list) -> sdpa_view:
+def _packed(t: torch.Tensor, name: str) -> sdpa_view:
     """The C view of packed rows (tokens, heads, dim)."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be packed rows (tokens, heads, dim)")
-    return _view(t.transpose(0, 1).unsqueeze(0), keep)
+    ss, sh, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return sdpa_view(t.data_ptr(), 0, sh, ss)
 
 
 def sdpa_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -680,14 +699,18 @@ def sdpa_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v
     heads, dim) is passed with transpose(1, 2)); page_table (B, max_pages) int32; kv_lens (B,)
     int32: keys of each sequence, its new tokens included; cu_new (B + 1,) int32: first row of
     each sequence, or None when every sequence brings tokens / B rows.  Returns the pools."""
-    with _OnDevice(dict(k=k, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_lens=kv_lens,
-                        cu_new=cu_new, cos_cache=cos_cache, sin_cache=sin_cache), stream) as dev:
-        p, keep = make_paged_params(k_pages, v_pages, page_table, kv_lens, k.shape[0], k_pages.shape[1], cu_new=cu_new,
-                                    cos_cache=cos_cache, sin_cache=sin_cache, rotary_dim=rotary_dim,
-                                    interleaved=interleaved)
-        _typed(k, "k", k_pages.dtype, (k.shape[0], p.Nkv, p.H))
-        _typed(v, "v", k_pages.dtype, (k.shape[0], p.Nkv, p.Hv))
-        _check(lib().sdpa_paged_append(ctypes.byref(p), _packed(k, "k", keep), _packed(v, "v", keep), dev.handle))
+    d, handle = _place(stream, (k, v, k_pages, v_pages, page_table, kv_lens, cu_new, cos_cache, sin_cache),
+                       "k v k_pages v_pages page_table kv_lens cu_new cos_cache sin_cache")
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k and v must be packed rows (tokens, heads, dim)")
+    if (cos_cache is None) != (sin_cache is None):
+        raise ValueError("cos_cache and sin_cache must be given together")
+    tokens, Nkv, H = k.shape
+    p = make_paged_params(k_pages, v_pages, page_table, kv_lens, tokens, Nkv, cu_new=cu_new, cos_cache=cos_cache,
+                          sin_cache=sin_cache, rotary_dim=rotary_dim, interleaved=interleaved)
+    _typed(k, "k", k_pages.dtype, (tokens, k_pages.shape[1], k_pages.shape[3]))
+    _typed(v, "v", k_pages.dtype, (tokens, Nkv, v_pages.shape[3]))
+    _call(d, lib().sdpa_paged_append, p, _packed(k, "k"), _packed(v, "v"), handle)
     return k_pages, v_pages
 
 
@@ -699,25 +722,27 @@ def sdpa_paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     """Attention of the new tokens q (packed rows (tokens, Nq, H)) over the pages of their
     sequences; the new keys and values are in the pages already (sdpa_paged_append).  Page
     arguments as there.  max_new: most new tokens of one sequence, where the caller knows it (it
-    picks the kernel; results do not depend on it).  Returns y (tokens, Nq, Hv); rows behind the
+    picks the kernel; results hold for any value).  Returns y (tokens, Nq, Hv); rows behind the
     last sequence are not written."""
-    with _OnDevice(dict(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_lens=kv_lens, cu_new=cu_new,
-                        head_sink=head_sink, y=y, workspace=workspace), stream) as dev:
-        if q.dim() != 3:
-            raise ValueError("q must be packed rows (tokens, heads, dim)")
-        p, keep = make_paged_params(k_pages, v_pages, page_table, kv_lens, q.shape[0], q.shape[1], cu_new=cu_new,
-                                    scale=scale, softcap=softcap, causal=causal, window=window, head_sink=head_sink,
-                                    max_new=max_new)
-        _typed(q, "q", k_pages.dtype, (q.shape[0], q.shape[1], p.H))
-        if y is None:
-            y = torch.empty(q.shape[0], q.shape[1], p.Hv, dtype=q.dtype, device=q.device)
-        _typed(y, "y", q.dtype, (q.shape[0], q.shape[1], p.Hv))
-        if workspace is None:
-            workspace = torch.empty(max(1, int(lib().sdpa_paged_workspace_size(ctypes.byref(p)))), dtype=torch.uint8,
-                                    device=dev.device)
-        dev.keep(y, workspace)
-        _check(lib().sdpa_paged_attn(ctypes.byref(p), _packed(q, "q", keep), _packed(y, "y", keep),
-                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), dev.handle))
+    d, handle = _place(stream, (q, k_pages, v_pages, page_table, kv_lens, cu_new, head_sink, y, workspace),
+                       "q k_pages v_pages page_table kv_lens cu_new head_sink y workspace")
+    if q.dim() != 3:
+        raise ValueError("q must be packed rows (tokens, heads, dim)")
+    tokens, Nq, H = q.shape
+    p = make_paged_params(k_pages, v_pages, page_table, kv_lens, tokens, Nq, cu_new=cu_new, scale=scale, softcap=softcap,
+                          causal=causal, window=window, head_sink=head_sink, max_new=max_new)
+    dt = k_pages.dtype
+    _typed(q, "q", dt, (tokens, Nq, k_pages.shape[3]))
+    shape = (tokens, Nq, v_pages.shape[3])
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=q.device)
+    _typed(y, "y", dt, shape)
+    L = lib()
+    if workspace is None:
+        workspace = torch.empty(max(1, L.sdpa_paged_workspace_size(p)), dtype=torch.uint8, device=q.device)
+    _keep_for(stream, d, handle, y, workspace)
+    _call(d, L.sdpa_paged_attn, p, _packed(q, "q"), _packed(y, "y"), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size(), handle)
     return y
 
 

@@ -118,7 +118,7 @@ def paged(over=(), *, B=2, tokens=4, Nq=4, Nkv=2, H=64, Hv=64, pages=6, page=16,
     kp, vp = z(pages, Nkv, page, H), z(pages, Nkv, page, Hv)
     table, lens = torch.zeros(B, width, dtype=torch.int32), torch.zeros(B, dtype=torch.int32)
     cu = torch.zeros(B + 1, dtype=torch.int32)
-    p, keep = sdpa.make_paged_params(kp, vp, table, lens, tokens, Nq, cu_new=cu)
+    p, keep = sdpa.make_paged_params(kp, vp, table, lens, tokens, Nq, cu_new=cu), [lens, cu]
     for n, v in dict(over).items():
         setattr(p, n, v)
     rows = dict(q=z(tokens, Nq, H), k=z(tokens, Nkv, H), v=z(tokens, Nkv, Hv), y=z(tokens, Nq, Hv), kp=kp, vp=vp, table=table)
@@ -127,12 +127,12 @@ def paged(over=(), *, B=2, tokens=4, Nq=4, Nkv=2, H=64, Hv=64, pages=6, page=16,
 
 def append_code(p, rows, keep, **over):
     t = dict(rows, **over)
-    return sdpa.lib().sdpa_paged_append(ctypes.byref(p), sdpa._packed(t["k"], "k", keep), sdpa._packed(t["v"], "v", keep), None)
+    return sdpa.lib().sdpa_paged_append(ctypes.byref(p), sdpa._packed(t["k"], "k"), sdpa._packed(t["v"], "v"), None)
 
 
 def attn_code(p, rows, keep, where=256, size=1 << 40, **over):
     t = dict(rows, **over)
-    return sdpa.lib().sdpa_paged_attn(ctypes.byref(p), sdpa._packed(t["q"], "q", keep), sdpa._packed(t["y"], "y", keep), where,
+    return sdpa.lib().sdpa_paged_attn(ctypes.byref(p), sdpa._packed(t["q"], "q"), sdpa._packed(t["y"], "y"), where,
                                       size, None)
 
 
