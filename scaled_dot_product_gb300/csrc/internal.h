@@ -61,7 +61,7 @@ struct NormJob {
   float eps, inv_D;
 };
 // Most blocks of the backward: each leaves D partial sums of dw in the workspace.
-constexpr int kNormBwdMaxBlocks = 152 * 4;
+constexpr int kNormBwdMaxBlocks = 152 * 2;
 // part == nullptr: forward; else the backward with its partial sums there.
 cudaError_t launch_qk_norm(sdpa_dtype dt, const NormJob& j, float* part, cudaStream_t st);
 cudaError_t take_norm_status(int* status);

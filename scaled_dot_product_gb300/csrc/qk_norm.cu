@@ -7,15 +7,16 @@
 // All arithmetic is fp32; each output is rounded once to the element type.
 //
 // Bytes bound both directions: x (and dy) are read once and y (dx) is written once.  LPR lanes
-// share one row; a lane holds two 16-byte vectors, in the split pair layout the two halves of
-// the same pairs, so the rotation needs no exchange between lanes and the row's sum is a
-// shuffle over LPR lanes.  One group of lanes takes HPG heads of one token, so the cos/sin row
-// and the weights are read once for them and HPG x 32 bytes are in flight per lane.
+// share one row, one 16-byte vector each; the row's sum is a shuffle over them, and in the split
+// pair layout the packed partners come from another lane.  (Two vectors a lane, pairs together,
+// save those shuffles but took 118 registers forward and 174 backward, and the loads in flight
+// with them: 20.9 and 98.7 us on the shapes below.)
 // Shapes or pointers that do not allow 16-byte vectors take the scalar kernels (one warp per
-// row, the row in shared memory).
+// row, the row in shared memory), as do fp32 heads of more than 128 channels.
 #include <algorithm>
 
 #include "internal.h"
+#include "tc_ptx.cuh"
 
 namespace sdpa {
 
@@ -23,13 +24,16 @@ static __device__ int g_norm_status;
 
 namespace {
 
+using namespace ptx;
+
 constexpr int kThreads = 256;
+constexpr int kFwdThreads = 128;
 constexpr int kMaxD = 256;
 
-// Cache row of token (b, s); rows outside the cache are recorded and clamped.
-__device__ __forceinline__ int64_t cache_row(const NormJob& j, int tok) {
-  int64_t row = tok;
-  if (j.positions) row = j.positions[tok];
+// Position of token tok, and its row in the caches: a position outside them is recorded and
+// clamped.
+__device__ __forceinline__ int64_t position(const NormJob& j, int tok) { return j.positions ? j.positions[tok] : tok; }
+__device__ __forceinline__ int64_t cache_row(const NormJob& j, int64_t row) {
   if (row < 0 || row >= j.max_pos) {
     atomicExch(&g_norm_status, 1);
     row = row < 0 ? 0 : j.max_pos - 1;
@@ -52,123 +56,174 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// The two vectors a lane owns: their first channels (-1: none) and whether they are rotated.
-template <typename T, bool kInter>
-struct Lane {
-  static constexpr int V = 16 / (int)sizeof(T);
-  int c0, c1;
-  bool rot0, rot1;
-  __device__ __forceinline__ Lane(int u, int D, int R) {
-    if (kInter) {
-      c0 = 2 * u * V;
-      c1 = c0 + V;
-      rot0 = c0 < R;
-      rot1 = c1 < R;
+// 16 bytes of T as pairs of floats, and back (one rounding).
+template <typename T>
+__device__ __forceinline__ void to_pairs(const uint4& u, f2_t* f) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};      // a bf16 is the upper half of its float
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = f2_pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+  } else {
+    float x[V];
+    unpack16<T>(u, x);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) f[e] = f2_pack(x[2 * e], x[2 * e + 1]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 from_pairs(const f2_t* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 8 / (int)sizeof(T); ++e) {
+    float lo, hi;
+    f2_unpack(f[e], lo, hi);
+    if constexpr (sizeof(T) == 4) {
+      w[2 * e] = __float_as_uint(lo);
+      w[2 * e + 1] = __float_as_uint(hi);
     } else {
-      const int urot = R / (2 * V);
-      rot0 = rot1 = u < urot;
-      c0 = rot0 ? u * V : R + 2 * (u - urot) * V;
-      c1 = rot0 ? c0 + R / 2 : c0 + V;
-    }
-    if (c0 >= D) { c0 = -1; rot0 = false; }
-    if (c1 >= D) { c1 = -1; rot1 = false; }
-  }
-  // cos / sin of the lane's V pairs
-  __device__ __forceinline__ void load_cs(const T* cr, const T* sr, float* c, float* s) const {
-    if (kInter) {
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e) {
-        c[e] = rot0 ? Elem<T>::to_f32(cr[c0 / 2 + e]) : 1.f;
-        s[e] = rot0 ? Elem<T>::to_f32(sr[c0 / 2 + e]) : 0.f;
-        c[V / 2 + e] = rot1 ? Elem<T>::to_f32(cr[c1 / 2 + e]) : 1.f;
-        s[V / 2 + e] = rot1 ? Elem<T>::to_f32(sr[c1 / 2 + e]) : 0.f;
-      }
-    } else if (rot0) {
-      unpack16<T>(*reinterpret_cast<const uint4*>(cr + c0), c);
-      unpack16<T>(*reinterpret_cast<const uint4*>(sr + c0), s);
+      w[e] = std::is_same<T, __half>::value ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
     }
   }
-  // f: the lane's 2V channels in place; sgn = -1 turns back
-  __device__ __forceinline__ void rotate(float* f, const float* c, const float* s, float sgn) const {
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float pair_sum(f2_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return lo + hi;
+}
+
+// A lane owns one 16-byte vector of its row, channels c0 .. c0 + V - 1.  The rotation of every
+// channel is x C + mate(x) S with a signed sine S: the mate is the neighbour in the vector
+// (adjacent pairs) or the same place of the vector `half` vectors away, in another lane of the row
+// (split pairs; as packed words four shuffles).  Channels that are not rotated have C = 1 and a
+// mate of 0.
+template <typename T, bool kInter, int LPR>
+struct Lane {
+  static constexpr int V = 16 / (int)sizeof(T), P = V / 2;
+  int c0, mate, ci;                // mate's lane, first cos / sin entry
+  bool live, rot, second;          // has channels; is rotated; holds the second of its pairs
+  uint4 cw, sw;                    // packed cos and sin (adjacent pairs: the first half)
+  __device__ __forceinline__ Lane(int u, int D, int R) : c0(u * V), mate(u), ci(0), live(u * V < D), rot(u * V < R), second(false) {
+    cw = sw = make_uint4(0u, 0u, 0u, 0u);
     if (kInter) {
-      if (rot0 || rot1) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) turn(f[2 * e], f[2 * e + 1], c[e], sgn * s[e]);
-      }
-    } else if (rot0) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) turn(f[e], f[V + e], c[e], sgn * s[e]);
+      ci = c0 / 2;
+    } else if (rot) {
+      const int half = R / (2 * V);
+      second = u >= half;
+      mate = second ? u - half : u + half;
+      ci = min(u, mate) * V;
     }
+  }
+  __device__ __forceinline__ uint4 load(const T* row) const {
+    return live ? *reinterpret_cast<const uint4*>(row + c0) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void load_cs(const T* cr, const T* sr) {
+    if (!rot) return;
+    if constexpr (kInter) {
+      const uint2 c = *reinterpret_cast<const uint2*>(cr + ci), s = *reinterpret_cast<const uint2*>(sr + ci);
+      cw.x = c.x; cw.y = c.y;
+      sw.x = s.x; sw.y = s.y;
+    } else {
+      cw = *reinterpret_cast<const uint4*>(cr + ci);
+      sw = *reinterpret_cast<const uint4*>(sr + ci);
+    }
+  }
+  // C and S of the lane's channels; dir = -1 turns back
+  __device__ __forceinline__ void factors(f2_t* C, f2_t* S, float dir) const {
+    float c[V], s[V];
+    unpack16<T>(cw, c);
+    unpack16<T>(sw, s);
+    if constexpr (kInter) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        C[e] = f2_pack(rot ? c[e] : 1.f, rot ? c[e] : 1.f);
+        S[e] = f2_pack(-dir * s[e], dir * s[e]);
+      }
+    } else {
+      // x1 c - x2 s in the first half, x2 c + x1 s in the second
+      const float sg = second ? dir : -dir;
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        C[e] = f2_pack(rot ? c[2 * e] : 1.f, rot ? c[2 * e + 1] : 1.f);
+        S[e] = f2_pack(sg * s[2 * e], sg * s[2 * e + 1]);
+      }
+    }
+  }
+  // The mates of the lane's channels; x are its own pairs, w the same as packed words.
+  __device__ __forceinline__ void mates(const uint4& w, const f2_t* x, f2_t* m) const {
+    if constexpr (kInter) {
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        float lo, hi;
+        f2_unpack(x[e], lo, hi);
+        m[e] = rot ? f2_pack(hi, lo) : f2_zero();
+      }
+    } else {
+      uint4 v = make_uint4(__shfl_sync(0xffffffffu, w.x, mate, LPR), __shfl_sync(0xffffffffu, w.y, mate, LPR),
+                           __shfl_sync(0xffffffffu, w.z, mate, LPR), __shfl_sync(0xffffffffu, w.w, mate, LPR));
+      if (!rot) v = make_uint4(0u, 0u, 0u, 0u);
+      to_pairs<T>(v, m);
+    }
+  }
+  __device__ __forceinline__ void store(T* row, const f2_t* f) const {
+    if (live) *reinterpret_cast<uint4*>(row + c0) = from_pairs<T>(f);
   }
 };
 
-template <typename T>
-__device__ __forceinline__ uint4 load_vec(const T* row, int c) {
-  return c >= 0 ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
-}
-
-template <typename T>
-__device__ __forceinline__ void store_vec(T* row, int c, const float* f) {
-  if (c < 0) return;
-  constexpr int V = 16 / (int)sizeof(T);
-  uint4 u;
-  T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-  for (int x = 0; x < V; ++x) e[x] = Elem<T>::from_f32(f[x]);
-  *reinterpret_cast<uint4*>(row + c) = u;
-}
-
 // ---------------------------------------------------------------- forward
 
+// One group of LPR lanes takes HPG heads of one token: the cos/sin row and the weights are read
+// once for them and folded into two factors a channel, y = r (x (w C) + mate(x) (mate(w) S)), and
+// HPG x 16 bytes are in flight per lane.
 template <typename T, bool kInter, int LPR, int HPG>
-__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormJob j, const int q_blocks) {
-  constexpr int V = 16 / (int)sizeof(T);
+__global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(const NormJob j, const int q_blocks) {
+  constexpr int V = 16 / (int)sizeof(T), P = V / 2;
   const bool is_k = (int)blockIdx.x >= q_blocks;
   const NormSide& sd = j.side[is_k];
   const int chunks = (sd.N + HPG - 1) / HPG;
-  const unsigned task = (blockIdx.x - (is_k ? q_blocks : 0)) * (unsigned)(kThreads / LPR) + threadIdx.x / LPR;
-  const int u = threadIdx.x % LPR;
+  const unsigned task = (blockIdx.x - (is_k ? q_blocks : 0)) * (unsigned)(kFwdThreads / LPR) + threadIdx.x / LPR;
   const unsigned tok = task / (unsigned)chunks;
   const int h0 = (int)(task - tok * (unsigned)chunks) * HPG;
   const bool live = tok < (unsigned)j.tokens;
   const int b = live ? (int)(tok / (unsigned)j.S) : 0, s = live ? (int)(tok - (unsigned)b * (unsigned)j.S) : 0;
-  const Lane<T, kInter> ln(u, j.D, j.R);
+  const int nh = live ? min(HPG, sd.N - h0) : 0;
+  Lane<T, kInter, LPR> ln(threadIdx.x % LPR, j.D, j.R);
   const T* x0 = reinterpret_cast<const T*>(sd.x.p) + sd.x.off(b, h0, s);
   T* y0 = reinterpret_cast<T*>(const_cast<void*>(sd.y.p)) + sd.y.off(b, h0, s);
-  const int nh = live ? min(HPG, sd.N - h0) : 0;
 
-  uint4 xa[HPG], xb[HPG];
+  uint4 xw[HPG];
 #pragma unroll
   for (int i = 0; i < HPG; ++i)
-    if (i < nh && SDPA_IN_BOUNDS(b < j.B && h0 + i < sd.N && ln.c0 + V <= j.D && ln.c1 + V <= j.D, 501)) {
-      xa[i] = load_vec(x0 + i * sd.x.sh, ln.c0);
-      xb[i] = load_vec(x0 + i * sd.x.sh, ln.c1);
-    } else {
-      xa[i] = xb[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-  float c[V], sn[V], w[2 * V];
+    xw[i] = i < nh && SDPA_IN_BOUNDS(b < j.B && h0 + i < sd.N && s < j.S, 501) ? ln.load(x0 + i * sd.x.sh)
+                                                                                : make_uint4(0u, 0u, 0u, 0u);
+  const uint4 ww = ln.load(reinterpret_cast<const T*>(sd.w));
   if (j.R > 0 && live) {
-    const int64_t row = cache_row(j, (int)tok) * (j.R / 2);
-    ln.load_cs(reinterpret_cast<const T*>(j.cos_c) + row, reinterpret_cast<const T*>(j.sin_c) + row, c, sn);
+    const int64_t row = cache_row(j, position(j, (int)tok)) * (j.R / 2);
+    ln.load_cs(reinterpret_cast<const T*>(j.cos_c) + row, reinterpret_cast<const T*>(j.sin_c) + row);
   }
-  unpack16<T>(load_vec(reinterpret_cast<const T*>(sd.w), ln.c0), w);
-  unpack16<T>(load_vec(reinterpret_cast<const T*>(sd.w), ln.c1), w + V);
+  f2_t A[P], Bf[P], w[P], m[P];
+  ln.factors(A, Bf, 1.f);
+  to_pairs<T>(ww, w);
+  ln.mates(ww, w, m);
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    A[e] = f2_mul(A[e], w[e]);
+    Bf[e] = f2_mul(Bf[e], m[e]);
+  }
 #pragma unroll
   for (int i = 0; i < HPG; ++i) {
-    float f[2 * V];
-    unpack16<T>(xa[i], f);
-    unpack16<T>(xb[i], f + V);
-    float ss = 0.f;
+    f2_t x[P];
+    to_pairs<T>(xw[i], x);
+    ln.mates(xw[i], x, m);
+    f2_t ss = f2_zero();
 #pragma unroll
-    for (int e = 0; e < 2 * V; ++e) ss = fmaf(f[e], f[e], ss);
-    const float r = rsqrtf(row_sum<LPR>(ss) * j.inv_D + j.eps);
-    if (i < nh) {
+    for (int e = 0; e < P; ++e) ss = f2_fma(x[e], x[e], ss);
+    const float r = rsqrtf(row_sum<LPR>(pair_sum(ss)) * j.inv_D + j.eps);
+    const f2_t r2 = f2_pack(r, r);
 #pragma unroll
-      for (int e = 0; e < 2 * V; ++e) f[e] = f[e] * r * w[e];
-      ln.rotate(f, c, sn, 1.f);
-      store_vec(y0 + i * sd.y.sh, ln.c0, f);
-      store_vec(y0 + i * sd.y.sh, ln.c1, f + V);
-    }
+    for (int e = 0; e < P; ++e) x[e] = f2_mul(f2_fma(x[e], A[e], f2_mul(m[e], Bf[e])), r2);
+    if (i < nh) ln.store(y0 + i * sd.y.sh, x);
   }
 }
 
@@ -201,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_scalar_kernel(const NormJob
     for (int d = lane; d < j.D; d += 32) f[d] = f[d] * r * Elem<T>::to_f32(w[d]);
     __syncwarp();
     const int half = j.R / 2;
-    const int64_t crow = j.R > 0 ? cache_row(j, tok) * half : 0;
+    const int64_t crow = j.R > 0 ? cache_row(j, position(j, tok)) * half : 0;
     for (int d = lane; d < half; d += 32) {
       const int i1 = interleaved ? 2 * d : d, i2 = interleaved ? 2 * d + 1 : d + half;
       float a = f[i1], p = f[i2];
@@ -218,94 +273,144 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_scalar_kernel(const NormJob
 // ---------------------------------------------------------------- backward
 
 // Persistent: blocks [0, q_blocks) walk the query tasks, the others the key tasks, so a lane
-// accumulates dw for the one weight vector of its side.  Each block leaves its D sums in
-// part[blockIdx.x]; norm_dw_kernel adds them in block order, so results do not vary from run
-// to run.
-template <typename T, bool kInter, int LPR, int HPG>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormJob j, const int q_blocks,
-                                                            float* __restrict__ part) {
-  constexpr int V = 16 / (int)sizeof(T);
+// accumulates dw for the one weight vector of its side.  A task is up to kHeads heads of one
+// token, taken kPair at a time, whose sums' shuffles overlap; the next pair's x and dy are on their
+// way meanwhile.  Each block leaves its D sums in part[blockIdx.x]; norm_dw_kernel adds them in
+// block order, so results do not vary from run to run.
+constexpr int kHeads = 8, kPair = 2;
+constexpr int kBwdBlocks = 2;
+template <typename T, bool kInter, int LPR>
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_bwd_kernel(const NormJob j, const int q_blocks,
+                                                                        float* __restrict__ part) {
+  constexpr int V = 16 / (int)sizeof(T), P = V / 2;
   constexpr int kGroups = kThreads / LPR;
-  __shared__ float red[kGroups][LPR * 2 * V + 1];
+  __shared__ float red[kGroups][LPR * V + 1];
   const bool is_k = (int)blockIdx.x >= q_blocks;
   const NormSide& sd = j.side[is_k];
   const unsigned nblk = is_k ? gridDim.x - q_blocks : q_blocks;
   const unsigned blk = is_k ? blockIdx.x - q_blocks : blockIdx.x;
-  const unsigned chunks = (unsigned)(sd.N + HPG - 1) / HPG;
+  const unsigned chunks = (unsigned)(sd.N + kHeads - 1) / kHeads;
   const unsigned tasks = (unsigned)j.tokens * chunks;
   const int u = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-  const Lane<T, kInter> ln(u, j.D, j.R);
-  float w[2 * V], dw[2 * V];
-  unpack16<T>(load_vec(reinterpret_cast<const T*>(sd.w), ln.c0), w);
-  unpack16<T>(load_vec(reinterpret_cast<const T*>(sd.w), ln.c1), w + V);
+  Lane<T, kInter, LPR> ln(u, j.D, j.R);
+  f2_t w[P], dw[P], C[P], S[P];
+  to_pairs<T>(ln.load(reinterpret_cast<const T*>(sd.w)), w);
 #pragma unroll
-  for (int e = 0; e < 2 * V; ++e) dw[e] = 0.f;
+  for (int e = 0; e < P; ++e) dw[e] = f2_zero();
 
-  // every thread of the block runs the same number of passes (the shuffles need whole warps)
-  for (unsigned t0 = blk * kGroups; t0 < tasks; t0 += nblk * kGroups) {
+  // Every group of a block runs kHeads / kPair steps per task (the shuffles need whole warps); heads
+  // past the task's nh, and tasks past the last (nh = 0), touch no memory.
+  const T *xr = nullptr, *gr = nullptr;
+  T* dr = nullptr;
+  int nh = 0;
+  unsigned tok = 0;
+  int64_t pos = 0;                   // of the task to come: on its way before place() needs it
+  auto look_ahead = [&](unsigned t0) {
     const unsigned task = t0 + grp;
-    const bool live = task < tasks;
-    const unsigned tok = live ? task / chunks : 0u;
-    const int h0 = live ? (int)(task - tok * chunks) * HPG : 0;
+    if (t0 >= tasks || task >= tasks) return;
+    tok = task / chunks;
+    if (j.R > 0) pos = position(j, (int)tok);
+  };
+  auto place = [&](unsigned t0) {
+    const unsigned task = t0 + grp;
+    nh = 0;
+    if (t0 >= tasks || task >= tasks) return;
+    const int h0 = (int)(task - tok * chunks) * kHeads;
     const int b = (int)(tok / (unsigned)j.S), s = (int)(tok - (unsigned)b * (unsigned)j.S);
-    const int nh = live ? min(HPG, sd.N - h0) : 0;
-    const T* x0 = reinterpret_cast<const T*>(sd.x.p) + sd.x.off(b, h0, s);
-    const T* g0 = reinterpret_cast<const T*>(sd.dy.p) + sd.dy.off(b, h0, s);
-    T* d0 = reinterpret_cast<T*>(const_cast<void*>(sd.y.p)) + sd.y.off(b, h0, s);
-    uint4 xa[HPG], xb[HPG], ga[HPG], gb[HPG];
-#pragma unroll
-    for (int i = 0; i < HPG; ++i)
-      if (i < nh && SDPA_IN_BOUNDS(b < j.B && h0 + i < sd.N && ln.c0 + V <= j.D && ln.c1 + V <= j.D, 502)) {
-        xa[i] = load_vec(x0 + i * sd.x.sh, ln.c0);
-        xb[i] = load_vec(x0 + i * sd.x.sh, ln.c1);
-        ga[i] = load_vec(g0 + i * sd.dy.sh, ln.c0);
-        gb[i] = load_vec(g0 + i * sd.dy.sh, ln.c1);
-      } else {
-        xa[i] = xb[i] = ga[i] = gb[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    float c[V], sn[V];
-    if (j.R > 0 && live) {
-      const int64_t row = cache_row(j, (int)tok) * (j.R / 2);
-      ln.load_cs(reinterpret_cast<const T*>(j.cos_c) + row, reinterpret_cast<const T*>(j.sin_c) + row, c, sn);
+    nh = min(kHeads, sd.N - h0);
+    xr = reinterpret_cast<const T*>(sd.x.p) + sd.x.off(b, h0, s);
+    gr = reinterpret_cast<const T*>(sd.dy.p) + sd.dy.off(b, h0, s);
+    dr = reinterpret_cast<T*>(const_cast<void*>(sd.y.p)) + sd.y.off(b, h0, s);
+    if (!SDPA_IN_BOUNDS(b < j.B && h0 + nh <= sd.N && s < j.S, 502)) nh = 0;
+    if (j.R > 0) {
+      const int64_t row = cache_row(j, pos) * (j.R / 2);
+      ln.load_cs(reinterpret_cast<const T*>(j.cos_c) + row, reinterpret_cast<const T*>(j.sin_c) + row);
     }
+  };
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 x[kPair], g[kPair];
+  // the kPair heads from i on of the task that `place` set
+  auto fetch = [&](int i, uint4* xv, uint4* gv) {
 #pragma unroll
-    for (int i = 0; i < HPG; ++i) {
-      float f[2 * V], g[2 * V];
-      unpack16<T>(xa[i], f);
-      unpack16<T>(xb[i], f + V);
-      unpack16<T>(ga[i], g);
-      unpack16<T>(gb[i], g + V);
-      if (i < nh) ln.rotate(g, c, sn, -1.f);
-      float ss = 0.f, dot = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2 * V; ++e) {
-        ss = fmaf(f[e], f[e], ss);
-        dot = fmaf(g[e] * w[e], f[e], dot);
+    for (int k = 0; k < kPair; ++k) {
+      xv[k] = gv[k] = zero;
+      if (i + k < nh) {
+        xv[k] = ln.load(xr);
+        gv[k] = ln.load(gr);
+        xr += sd.x.sh;
+        gr += sd.dy.sh;
       }
-      const float r = rsqrtf(row_sum<LPR>(ss) * j.inv_D + j.eps);
-      const float mean = row_sum<LPR>(dot) * r * j.inv_D;      // mean(g w xh)
-      if (i < nh) {
+    }
+  };
+  look_ahead(blk * kGroups);
+  place(blk * kGroups);
+  fetch(0, x, g);
+  for (unsigned t0 = blk * kGroups; t0 < tasks; t0 += nblk * kGroups) {
+    ln.factors(C, S, -1.f);
+    const int n = nh;
+    T* d = dr;
+    look_ahead(t0 + nblk * kGroups);
+#pragma unroll 1
+    for (int i = 0; i < kHeads; i += kPair) {
+      uint4 xn[kPair], gn[kPair];
+      if (i + kPair < kHeads) {
+        fetch(i + kPair, xn, gn);
+      } else {
+        place(t0 + nblk * kGroups);
+        fetch(0, xn, gn);
+      }
+      f2_t f[kPair][P], q[kPair][P], m[kPair][P];
+      float ss[kPair], dot[kPair];
 #pragma unroll
-        for (int e = 0; e < 2 * V; ++e) {
-          const float xh = f[e] * r;
-          dw[e] = fmaf(g[e], xh, dw[e]);
-          f[e] = r * fmaf(-xh, mean, g[e] * w[e]);
+      for (int k = 0; k < kPair; ++k) {
+        to_pairs<T>(x[k], f[k]);
+        to_pairs<T>(g[k], q[k]);
+        ln.mates(g[k], q[k], m[k]);
+        f2_t s2 = f2_zero(), d2 = f2_zero();
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          q[k][e] = f2_fma(q[k][e], C[e], f2_mul(m[k][e], S[e]));
+          m[k][e] = f2_mul(q[k][e], w[e]);
+          s2 = f2_fma(f[k][e], f[k][e], s2);
+          d2 = f2_fma(m[k][e], f[k][e], d2);
         }
-        store_vec(d0 + i * sd.y.sh, ln.c0, f);
-        store_vec(d0 + i * sd.y.sh, ln.c1, f + V);
+        ss[k] = pair_sum(s2);
+        dot[k] = pair_sum(d2);
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < kPair; ++k) {
+          ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], o);
+          dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], o);
+        }
+#pragma unroll
+      for (int k = 0; k < kPair; ++k) {
+        const float r = rsqrtf(ss[k] * j.inv_D + j.eps);
+        const float mean = dot[k] * r * j.inv_D;      // mean(g w xh)
+        if (i + k < n) {
+          const f2_t r2 = f2_pack(r, r), rm = f2_pack(-r * mean, -r * mean);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const f2_t xh = f2_mul(f[k][e], r2);
+            dw[e] = f2_fma(q[k][e], xh, dw[e]);
+            f[k][e] = f2_fma(xh, rm, f2_mul(m[k][e], r2));
+          }
+          ln.store(d, f[k]);
+          d += sd.y.sh;
+        }
+        x[k] = xn[k];
+        g[k] = gn[k];
       }
     }
   }
 #pragma unroll
-  for (int e = 0; e < 2 * V; ++e) red[grp][u * 2 * V + e] = dw[e];
+  for (int e = 0; e < P; ++e) f2_unpack(dw[e], red[grp][u * V + 2 * e], red[grp][u * V + 2 * e + 1]);
   __syncthreads();
-  for (int x = threadIdx.x; x < LPR * 2 * V; x += kThreads) {
+  for (int d = threadIdx.x; d < j.D; d += kThreads) {
     float sum = 0.f;
-    for (int g = 0; g < kGroups; ++g) sum += red[g][x];
-    const Lane<T, kInter> lx(x / (2 * V), j.D, j.R);
-    const int e = x % (2 * V);
-    const int ch = e < V ? lx.c0 : lx.c1;
-    if (ch >= 0) part[(int64_t)blockIdx.x * j.D + ch + (e < V ? e : e - V)] = sum;
+    for (int k = 0; k < kGroups; ++k) sum += red[k][d];
+    part[(int64_t)blockIdx.x * j.D + d] = sum;
   }
 }
 
@@ -341,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_scalar_kernel(const NormJob
     const float r = rsqrtf(row_sum<32>(ss) * j.inv_D + j.eps);
     __syncwarp();
     const int half = j.R / 2;
-    const int64_t crow = j.R > 0 ? cache_row(j, tok) * half : 0;
+    const int64_t crow = j.R > 0 ? cache_row(j, position(j, tok)) * half : 0;
     for (int d = lane; d < half; d += 32) {
       const int i1 = interleaved ? 2 * d : d, i2 = interleaved ? 2 * d + 1 : d + half;
       turn(g[i1], g[i2], Elem<T>::to_f32(reinterpret_cast<const T*>(j.cos_c)[crow + d]),
@@ -398,43 +503,41 @@ bool vec_view(const View& v, int V) {
   return ((uintptr_t)v.p & 15u) == 0 && v.sb % V == 0 && v.sh % V == 0 && v.ss % V == 0;
 }
 
+// Lanes per row: one 16-byte vector each, as a power of two; 0 when the row has more than a warp's.
+template <typename T>
+int lanes_per_row(const NormJob& j) {
+  const int nv = j.D / (16 / (int)sizeof(T));
+  int l = 4;
+  while (l < nv) l *= 2;
+  return l <= 32 ? l : 0;
+}
+
 template <typename T>
 bool vec_ok(const NormJob& j, bool bwd) {
   constexpr int V = 16 / (int)sizeof(T);
-  if (j.D % V || (j.interleaved ? j.R % V : j.R % (2 * V))) return false;
-  if (j.R && !j.interleaved && (((uintptr_t)j.cos_c | (uintptr_t)j.sin_c) & 15u)) return false;
+  if (j.D % V || !lanes_per_row<T>(j) || (j.interleaved ? j.R % V : j.R % (2 * V))) return false;
+  if (j.R && (((uintptr_t)j.cos_c | (uintptr_t)j.sin_c) & (j.interleaved ? 7u : 15u))) return false;
   for (const NormSide& s : j.side) {
     if (((uintptr_t)s.w & 15u) || !vec_view(s.x, V) || !vec_view(s.y, V) || (bwd && !vec_view(s.dy, V))) return false;
   }
   return true;
 }
 
-// Lanes per row: the row's 16-byte vectors two to a lane, as a power of two.
-template <typename T>
-int lanes_per_row(const NormJob& j) {
-  constexpr int V = 16 / (int)sizeof(T);
-  const int nv = j.D / V;
-  const int items = j.interleaved ? (nv + 1) / 2 : j.R / (2 * V) + ((j.D - j.R) / V + 1) / 2;
-  int l = 4;
-  while (l < items) l *= 2;
-  return l;
-}
-
-// Heads per lane group: four once that still leaves every SM about 1024 threads, else one.
+// Heads per lane group of the forward: four once that still leaves every SM 2048 threads, else one.
 int heads_per_group(const NormJob& j, int lpr) {
   const int64_t threads = (int64_t)j.tokens * (j.side[0].N + j.side[1].N) * lpr;
-  return threads / 4 >= (int64_t)152 * 1024 ? 4 : 1;
+  return threads / 4 >= (int64_t)152 * 2048 ? 4 : 1;
 }
 
-int side_blocks(const NormJob& j, int side, int lpr, int hpg) {
+int side_blocks(const NormJob& j, int side, int threads, int lpr, int hpg) {
   const int64_t tasks = (int64_t)j.tokens * ((j.side[side].N + hpg - 1) / hpg);
-  return (int)((tasks + kThreads / lpr - 1) / (kThreads / lpr));
+  return (int)((tasks + threads / lpr - 1) / (threads / lpr));
 }
 
 template <typename T, bool kInter, int LPR, int HPG>
 cudaError_t run_fwd(const NormJob& j, cudaStream_t st) {
-  const int qb = side_blocks(j, 0, LPR, HPG), kb = side_blocks(j, 1, LPR, HPG);
-  norm_fwd_kernel<T, kInter, LPR, HPG><<<(unsigned)(qb + kb), kThreads, 0, st>>>(j, qb);
+  const int qb = side_blocks(j, 0, kFwdThreads, LPR, HPG), kb = side_blocks(j, 1, kFwdThreads, LPR, HPG);
+  norm_fwd_kernel<T, kInter, LPR, HPG><<<(unsigned)(qb + kb), kFwdThreads, 0, st>>>(j, qb);
   count_launch(1);
   return cudaGetLastError();
 }
@@ -456,11 +559,11 @@ cudaError_t finish_dw(const NormJob& j, float* part, int qb, int kb, cudaStream_
   return cudaGetLastError();
 }
 
-template <typename T, bool kInter, int LPR, int HPG>
+template <typename T, bool kInter, int LPR>
 cudaError_t run_bwd(const NormJob& j, float* part, cudaStream_t st) {
   int qb, kb;
-  bwd_blocks(j, side_blocks(j, 0, LPR, HPG), side_blocks(j, 1, LPR, HPG), &qb, &kb);
-  norm_bwd_kernel<T, kInter, LPR, HPG><<<(unsigned)(qb + kb), kThreads, 0, st>>>(j, qb, part);
+  bwd_blocks(j, side_blocks(j, 0, kThreads, LPR, kHeads), side_blocks(j, 1, kThreads, LPR, kHeads), &qb, &kb);
+  norm_bwd_kernel<T, kInter, LPR><<<(unsigned)(qb + kb), kThreads, 0, st>>>(j, qb, part);
   count_launch(1);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? finish_dw<T>(j, part, qb, kb, st) : e;
@@ -468,9 +571,8 @@ cudaError_t run_bwd(const NormJob& j, float* part, cudaStream_t st) {
 
 template <typename T, bool kInter, int LPR>
 cudaError_t run_lpr(const NormJob& j, float* part, cudaStream_t st) {
-  const bool many = heads_per_group(j, LPR) == 4;
-  if (part) return many ? run_bwd<T, kInter, LPR, 2>(j, part, st) : run_bwd<T, kInter, LPR, 1>(j, part, st);
-  return many ? run_fwd<T, kInter, LPR, 4>(j, st) : run_fwd<T, kInter, LPR, 1>(j, st);
+  if (part) return run_bwd<T, kInter, LPR>(j, part, st);
+  return heads_per_group(j, LPR) == 4 ? run_fwd<T, kInter, LPR, 4>(j, st) : run_fwd<T, kInter, LPR, 1>(j, st);
 }
 
 template <typename T, bool kInter>
