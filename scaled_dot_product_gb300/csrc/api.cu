@@ -495,6 +495,8 @@ int check_paged(const sdpa_paged_params* p, Paged* g, Extent ext[2]) {
     return fail(SDPA_ERR_UNSUPPORTED, "head sizes must be multiples of %d and at most 256 (H=%d Hv=%d)", ve, p->H, p->Hv);
   if ((int64_t)p->max_pages * p->page_size > ((int64_t)1 << 30))
     return fail(SDPA_ERR_OVERFLOW, "max_pages * page_size exceeds 2^30 keys");
+  if ((int64_t)p->max_pages * p->page_size * p->Nkv > ((int64_t)1 << 36))
+    return fail(SDPA_ERR_OVERFLOW, "max_pages * page_size * Nkv exceeds 2^36 keys");
   if ((int64_t)p->tokens * p->Nq > ((int64_t)1 << 30)) return fail(SDPA_ERR_OVERFLOW, "tokens * Nq exceeds 2^30");
   if (p->B > (1 << 24)) return fail(SDPA_ERR_OVERFLOW, "B exceeds 2^24");
   if (!p->cu_new && p->B > 0 && p->tokens % p->B)

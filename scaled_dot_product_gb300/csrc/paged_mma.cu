@@ -7,9 +7,9 @@
 // tenth of the time the bytes take; tcgen05 tiles of 128 rows would be mostly empty here and
 // their scores would pass through tensor memory.  A CTA is four warps: WM of them hold 16 rows
 // each, the other factor WK = 4 / WM splits the 64 keys of a tile, each warp with its own
-// running maximum, sum and accumulator, joined at the end of a unit.  Tiles arrive by 16-byte
+// running maximum, sum and accumulator, joined through shared memory at the end of a unit.  Tiles arrive by 16-byte
 // asynchronous copies, whose addresses go through the page table row by row, so a tile may span
-// pages of any size; the page ids of a tile are fetched one tile earlier than its rows.  Rows
+// pages of any size; page ids are fetched 64 at a time, a tile before they are needed.  Rows
 // past a sequence's keys are filled with zeros.  Copies run ahead of the products across unit
 // boundaries.
 #include <algorithm>
@@ -37,8 +37,8 @@ struct Cfg {
   static constexpr int kRow = H * 2;                       // bytes of a row
   static constexpr int kTile = kTN * kRow;
   static constexpr int kStages = 3 * 128 / H;
-  static constexpr int kJoin = WK > 1 ? TM * H * 4 : 0;    // joining buffer, fp32
-  static constexpr int kSmem = kStages * 2 * kTile + kJoin;
+  static constexpr int kSmem = kStages * 2 * kTile;
+  static_assert(2 * kTile == 4 * 16 * H * 4, "a stage holds the four warps' accumulators");
   static constexpr int CPR = kRow / 16;                    // 16-byte chunks of a row
   static constexpr int kPass = kThreads / CPR;             // rows copied per pass
 };
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
   using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
   constexpr int WK = C::WK, TM = C::TM, KW = C::KW, NT = KW / 8;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float sm_m[WK][TM], sm_l[WK][TM];
+  __shared__ float sm_m[WK][TM], sm_l[WK][TM], sm_f[WK][TM];
   const Paged& g = a.g;
   const int ctas = gridDim.x, cta = blockIdx.x;
   const Share sh = find_share<TM, kTN, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
@@ -105,101 +105,127 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wm = warp / WK, wk = warp % WK;
   const uint32_t sb = smem_u32(smem);
-  float* join = reinterpret_cast<float*>(smem + C::kStages * 2 * C::kTile);
 
-  // ---- the copying side: its own walk over the share, kStages - 1 tiles ahead
-  Walk<TM, kTN> wl(a, sh);
-  int lt = 0;                         // tile of wl's unit
-  int id0 = -1, id1 = -1;             // page ids of the next tile's keys lane and lane + 32
-  auto key_at = [&]() { return (wl.r.tile0 + wl.tile + lt) * kTN; };
-  auto admitted = [&](int key) { return key >= wl.r.lo && key <= wl.r.hi; };
-  auto fetch_ids = [&]() {
-    if (wl.done()) return;
-    const int32_t* table = g.table + (int64_t)wl.b * g.table_stride;
-    const int k0 = key_at() + lane, k1 = k0 + 32;
-    id0 = id1 = -1;                   // keys that no row admits: zeros
-    if (admitted(k0)) id0 = table[page_div(g, k0)];
-    if (admitted(k1)) id1 = table[page_div(g, k1)];
-  };
-  const int chunk = threadIdx.x % C::CPR, row_in = threadIdx.x / C::CPR;
-  const T* kbase = reinterpret_cast<const T*>(g.kp.p) + chunk * 8;
-  const T* vbase = reinterpret_cast<const T*>(g.vp.p) + chunk * 8;
-  auto copy_tile = [&](int st) {
-    if (!wl.done()) {
-      const int k0 = key_at();
-      // ids out of range are reported and read as zeros
-      const bool bad0 = (unsigned)id0 >= (unsigned)g.num_pages, bad1 = (unsigned)id1 >= (unsigned)g.num_pages;
-      if ((bad0 && admitted(k0 + lane)) || (bad1 && admitted(k0 + lane + 32))) atomicOr(&g_paged_status, kPagedBadPage);
-      if (bad0) id0 = -1;
-      if (bad1) id1 = -1;
-      const uint32_t sk = sb + st * 2 * C::kTile;
-#pragma unroll
-      for (int p = 0; p < kTN / C::kPass; ++p) {
-        const int r = p * C::kPass + row_in;
-        const int key = k0 + r;
-        const int a0 = __shfl_sync(0xffffffffu, id0, r & 31), a1 = __shfl_sync(0xffffffffu, id1, r & 31);
-        const int id = r < 32 ? a0 : a1;
-        const bool take = id >= 0 && SDPA_IN_BOUNDS(key < g.cap && id < g.num_pages, 531);
-        const int slot = key - page_div(g, key) * g.page_size;
-        const T* ks = take ? kbase + g.kp.off(id, wl.kvh, slot) : kbase;
-        const T* vs = take ? vbase + g.vp.off(id, wl.kvh, slot) : vbase;
-        const uint32_t d = sk + r * C::kRow + ((chunk ^ (r & 7)) << 4);
-        cp_async16_or_zero(d, ks, take);
-        cp_async16_or_zero(d + C::kTile, vs, take);
-      }
-      if (++lt == wl.take()) {
-        lt = 0;
-        wl.next(a);
-      }
-      fetch_ids();
-    }
-    cp_async_commit();
-  };
-  fetch_ids();
-#pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) copy_tile(s);
-
-  int st = 0;                         // stage of the tile to compute
-  const float cap_log2 = a.softcap * kLog2e, cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
-  const float kfac = a.softcap > 0.f ? 1.f : a.scale * kLog2e;
-  // fragment addresses: lane -> row and 16-byte chunk of the four 8x8 matrices of one load
-  const int kr = wk * KW + ((lane >> 4) << 3) + (lane & 7), kc = (lane >> 3) & 1;
-  const int vr = wk * KW + (((lane >> 3) & 1) << 3) + (lane & 7), vc = lane >> 4;
-
-  for (Walk<TM, kTN> w(a, sh); !w.done(); w.next(a)) {
-    // rows of this thread: wm * 16 + lane / 4 and 8 further
-    int lo[2], hi[2], prow[2];
-    uint32_t qf[H / 16][4];
+  // ---- query fragments of a unit, straight from memory: rows lane / 4 and 8 further of 16
+  uint32_t qf[H / 16][4];
+  auto load_q = [&](const Walk<TM, kTN>& w) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      prow[x] = wm * 16 + (lane >> 2) + 8 * x;
-      const int pr = w.r.row0 + min(prow[x], w.r.rows - 1);
-      row_keys(a, w.s, pr, lo[x], hi[x]);
+      const int pr = w.r.row0 + min(wm * 16 + (lane >> 2) + 8 * x, w.r.rows - 1);
+      const int tok = pr / g.group;
       const uint32_t* qr = reinterpret_cast<const uint32_t*>(
-          reinterpret_cast<const T*>(a.q.p) + a.q.off(0, w.kvh * g.group + pr % g.group, w.s.t0 + pr / g.group));
+          reinterpret_cast<const T*>(a.q.p) + a.q.off(0, w.kvh * g.group + pr - tok * g.group, w.s.t0 + tok));
 #pragma unroll
       for (int kk = 0; kk < H / 16; ++kk) {
         qf[kk][x] = qr[kk * 8 + (lane & 3)];
         qf[kk][2 + x] = qr[kk * 8 + 4 + (lane & 3)];
       }
     }
-    int full_lo, full_hi, tmp;       // keys every row of the unit admits
-    row_keys(a, w.s, w.r.row0, tmp, full_hi);
-    row_keys(a, w.s, w.r.row0 + w.r.rows - 1, full_lo, tmp);
+  };
+  Walk<TM, kTN> w(a, sh);
 
-    float o[H / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  // ---- the copying side: its own walk over the share, kStages - 1 tiles ahead.  The ids of 64
+  // pages are at hand, one or two per lane; when the next tile reaches beyond them the following
+  // 64 are fetched, one tile before they are needed.
+  Walk<TM, kTN> wl = w;
+  int lt = 0;                         // tile of wl's unit
+  int wbase = 0, id0 = -1, id1 = -1;  // pages wbase + lane and wbase + 32 + lane of wl's sequence
+  bool fresh = true;                  // wl entered another unit
+  const T *kbase = nullptr, *vbase = nullptr;
+  const int chunk = threadIdx.x % C::CPR, row_in = threadIdx.x / C::CPR;
+  const bool same = g.kp.sb == g.vp.sb && g.kp.ss == g.vp.ss;
+  auto fetch_ids = [&]() {
+    const int k0 = (wl.r.tile0 + wl.tile + lt) * kTN;
+    const int last = page_div(g, max(0, min(k0 + kTN - 1, wl.r.hi)));
+    if (!fresh && last < wbase + 64) return;
+    wbase = page_div(g, max(k0, wl.r.lo));
+    const int32_t* table = g.table + (int64_t)wl.b * g.table_stride + wbase;
+    const int end = wl.r.hi >= wl.r.lo ? page_div(g, wl.r.hi) - wbase : -1;     // last page some row admits
+    id0 = lane <= end ? table[lane] : -1;
+    id1 = lane + 32 <= end ? table[lane + 32] : -1;
+    if (fresh) {
+      kbase = reinterpret_cast<const T*>(g.kp.p) + g.kp.sh * wl.kvh + chunk * 8;
+      vbase = reinterpret_cast<const T*>(g.vp.p) + g.vp.sh * wl.kvh + chunk * 8;
+      fresh = false;
+    }
+  };
+  auto copy_tile = [&](int st) {
+    if (!wl.done()) {
+      const int k0 = (wl.r.tile0 + wl.tile + lt) * kTN;
+      const uint32_t sk = sb + st * 2 * C::kTile;
 #pragma unroll
-    for (int n = 0; n < H / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+      for (int p = 0; p < kTN / C::kPass; ++p) {
+        const int r = p * C::kPass + row_in;
+        const int key = k0 + r, pg = page_div(g, key), i = pg - wbase;
+        const int a0 = __shfl_sync(0xffffffffu, id0, i & 31), a1 = __shfl_sync(0xffffffffu, id1, i & 31);
+        const int id = i < 32 ? a0 : a1;
+        bool take = key >= wl.r.lo && key <= wl.r.hi;      // other keys: zeros, their pages are not read
+        if (take && (unsigned)id >= (unsigned)g.num_pages) {
+          atomicOr(&g_paged_status, kPagedBadPage);
+          take = false;
+        }
+        take = take && SDPA_IN_BOUNDS(i >= 0 && i < 64 && key < g.cap, 531);
+        const int slot = key - pg * g.page_size;
+        const int64_t ko = take ? id * g.kp.sb + slot * g.kp.ss : 0;
+        const int64_t vo = same ? ko : take ? id * g.vp.sb + slot * g.vp.ss : 0;
+        const uint32_t d = sk + r * C::kRow + ((chunk ^ (r & 7)) << 4);
+        cp_async16_or_zero(d, kbase + ko, take);
+        cp_async16_or_zero(d + C::kTile, vbase + vo, take);
+      }
+      if (++lt == wl.take()) {
+        lt = 0;
+        wl.next(a);
+        fresh = true;
+      }
+      if (!wl.done()) fetch_ids();
+    }
+    cp_async_commit();
+  };
+  fetch_ids();
+  load_q(w);
 
-    const int n_tiles = w.take();
-    for (int t = 0; t < n_tiles; ++t) {
+  const float cap_log2 = a.softcap * kLog2e, cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+  const float kfac = a.softcap > 0.f ? 1.f : a.scale * kLog2e;
+  // fragment addresses: lane -> row and 16-byte chunk of the four 8x8 matrices of one load
+  const int kr = wk * KW + ((lane >> 4) << 3) + (lane & 7), kc = (lane >> 3) & 1;
+  const int vr = wk * KW + (((lane >> 3) & 1) << 3) + (lane & 7), vc = lane >> 4;
+  const int prow = wm * 16 + (lane >> 2);      // this thread's rows of the unit: prow and prow + 8
+
+  int lo[2], hi[2], full_lo = 0, full_hi = 0;  // admitted keys of the two rows, of every row
+  float o[H / 8][4], m[2], l[2];
+  int t = 0;                                   // tile of w's unit
+  // One loop for filling the ring, the products and the units' ends: straight-line code runs once
+  // per call from a cold instruction cache, which short calls feel (3 us a section, measured).
+  int put = 0;                                 // stage the next copy goes to
+#pragma unroll 1
+  for (int ahead = C::kStages - 1;;) {
+    if (ahead == 0) {
       cp_async_wait<C::kStages - 2>();
       __syncthreads();               // the tile is there, and the previous one has been read
-      copy_tile(st == 0 ? C::kStages - 1 : st - 1);
-      const uint32_t sk = sb + st * 2 * C::kTile, sv = sk + C::kTile;
-      st = st + 1 == C::kStages ? 0 : st + 1;
+    }
+    copy_tile(put);
+    put = put + 1 == C::kStages ? 0 : put + 1;
+    if (ahead > 0) {
+      --ahead;
+      continue;
+    }
+    const uint32_t sk = sb + put * 2 * C::kTile, sv = sk + C::kTile;   // the oldest tile's stage
+    if (t == 0) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        row_keys(a, w.s, w.r.row0 + min(prow + 8 * x, w.r.rows - 1), lo[x], hi[x]);
+        m[x] = -INFINITY;
+        l[x] = 0.f;
+      }
+      int tmp;
+      row_keys(a, w.s, w.r.row0, tmp, full_hi);
+      row_keys(a, w.s, w.r.row0 + w.r.rows - 1, full_lo, tmp);
+#pragma unroll
+      for (int n = 0; n < H / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    }
+    {
       const int key0 = (w.r.tile0 + w.tile + t) * kTN + wk * KW;
 
       float s[NT][4];
@@ -286,100 +312,78 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
       }
     }
 
-    // ---- end of the unit's tiles in this share
-    l[0] = quad_sum(l[0]);
-    l[1] = quad_sum(l[1]);
+    if (++t < w.take()) continue;
+
+    // ---- end of the unit's tiles in this share; the next unit's query rows are on their way
+    // while its results are joined and written.  The warps' accumulators, as they lie in registers
+    // (float4 n of lane i at [warp][n][i]), go to the stage of the tile just read, which the next
+    // copy fills only after the barrier above.
     const bool whole = w.whole();
     const int64_t slot = 2 * (int64_t)cta + (w.begins() ? 1 : 0);
-    float M[2] = {m[0], m[1]}, L[2] = {l[0], l[1]};
-    if constexpr (WK > 1) {
-      __syncthreads();               // the previous unit's reads of the buffers are over
+    const int rows = w.r.rows, row0 = w.r.row0, t0 = w.s.t0, head0 = w.kvh * g.group;
+    w.next(a);
+    t = 0;
+    if (!w.done()) load_q(w);
+    __syncthreads();                 // every warp has read the tile
+    float4* acc = reinterpret_cast<float4*>(smem + (sk - sb));
+#pragma unroll
+    for (int n = 0; n < H / 8; ++n) acc[(warp * (H / 8) + n) * 32 + lane] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] = quad_sum(l[x]);
       if ((lane & 3) == 0) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          sm_m[wk][prow[x]] = m[x];
-          sm_l[wk][prow[x]] = l[x];
-        }
-      }
-      __syncthreads();
-      float f[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        M[x] = -INFINITY;
-        for (int k = 0; k < WK; ++k) M[x] = fmaxf(M[x], sm_m[k][prow[x]]);
-        L[x] = 0.f;
-        for (int k = 0; k < WK; ++k) {
-          const float mk = sm_m[k][prow[x]];
-          if (mk != -INFINITY) L[x] = fmaf(ex2_approx(mk - M[x]), sm_l[k][prow[x]], L[x]);
-        }
-        f[x] = m[x] == -INFINITY ? 0.f : ex2_approx(m[x] - M[x]);
-      }
-      for (int k = 0; k < WK; ++k) {
-        if (wk == k) {
-#pragma unroll
-          for (int n = 0; n < H / 8; ++n)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              // columns rotated by the row, so that a quad's rows fall into different banks
-              float2* d = reinterpret_cast<float2*>(join + prow[x] * H + ((n * 8 + 2 * (lane & 3) + 8 * prow[x]) & (H - 1)));
-              const float2 v = make_float2(o[n][2 * x] * f[x], o[n][2 * x + 1] * f[x]);
-              if (k == 0) *d = v;
-              else *d = make_float2(d->x + v.x, d->y + v.y);
-            }
-        }
-        __syncthreads();
-      }
-      if (wk == 0 && (lane & 3) == 0) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (prow[x] >= w.r.rows) continue;
-          if (!whole) {
-            ws.ml[(slot * TM + prow[x]) * 2] = M[x];
-            ws.ml[(slot * TM + prow[x]) * 2 + 1] = L[x];
-          }
-          const int pr = w.r.row0 + prow[x];
-          sm_l[0][prow[x]] = row_scale<T>(a, w.kvh * g.group + pr % g.group, M[x], L[x]);
-        }
-      }
-      __syncthreads();
-      for (int i = threadIdx.x; i < w.r.rows * (H / 4); i += kThreads) {
-        const int r = i / (H / 4), c = (i % (H / 4)) * 4;
-        const float4 v = *reinterpret_cast<const float4*>(join + r * H + ((c + 8 * r) & (H - 1)));
-        if (whole) {
-          const int pr = w.r.row0 + r, h = w.kvh * g.group + pr % g.group;
-          T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, w.s.t0 + pr / g.group);
-          const float sc = sm_l[0][r];
-          if (SDPA_IN_BOUNDS(w.s.t0 + pr / g.group < g.tokens && h < g.Nq, 532))
-            *reinterpret_cast<uint2*>(y + c) = make_uint2(pack2<BF>(v.x * sc, v.y * sc), pack2<BF>(v.z * sc, v.w * sc));
-        } else if (SDPA_IN_BOUNDS(slot < 2 * ctas, 533)) {
-          *reinterpret_cast<float4*>(ws.o + (slot * TM + r) * H + c) = v;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (prow[x] >= w.r.rows) continue;
-        const int pr = w.r.row0 + prow[x], h = w.kvh * g.group + pr % g.group;
-        if (whole) {
-          const float sc = row_scale<T>(a, h, M[x], L[x]);
-          T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, w.s.t0 + pr / g.group);
-          if (SDPA_IN_BOUNDS(w.s.t0 + pr / g.group < g.tokens && h < g.Nq, 534)) {
-#pragma unroll
-            for (int n = 0; n < H / 8; ++n)
-              *reinterpret_cast<uint32_t*>(y + n * 8 + 2 * (lane & 3)) = pack2<BF>(o[n][2 * x] * sc, o[n][2 * x + 1] * sc);
-          }
-        } else if (SDPA_IN_BOUNDS(slot < 2 * ctas, 535)) {
-          if ((lane & 3) == 0) {
-            ws.ml[(slot * TM + prow[x]) * 2] = M[x];
-            ws.ml[(slot * TM + prow[x]) * 2 + 1] = L[x];
-          }
-#pragma unroll
-          for (int n = 0; n < H / 8; ++n)
-            *reinterpret_cast<float2*>(ws.o + (slot * TM + prow[x]) * H + n * 8 + 2 * (lane & 3)) =
-                make_float2(o[n][2 * x], o[n][2 * x + 1]);
-        }
+        sm_m[wk][prow + 8 * x] = m[x];
+        sm_l[wk][prow + 8 * x] = l[x];
       }
     }
+    __syncthreads();
+    if ((int)threadIdx.x < rows) {
+      const int r = threadIdx.x;
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int k = 0; k < WK; ++k) M = fmaxf(M, sm_m[k][r]);
+      float f[WK];
+#pragma unroll
+      for (int k = 0; k < WK; ++k) {
+        f[k] = sm_m[k][r] == -INFINITY ? 0.f : ex2_approx(sm_m[k][r] - M);
+        L = fmaf(f[k], sm_l[k][r], L);
+      }
+      float sc = 1.f;
+      if (whole) {
+        sc = row_scale<T>(a, head0 + (row0 + r) % g.group, M, L);
+      } else if (SDPA_IN_BOUNDS(slot < 2 * ctas, 533)) {
+        *reinterpret_cast<float2*>(ws.ml + (slot * TM + r) * 2) = make_float2(M, L);
+      }
+#pragma unroll
+      for (int k = 0; k < WK; ++k) sm_f[k][r] = f[k] * sc;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < rows * (H / 4); i += kThreads) {
+      // row r, columns c .. c + 3: two lanes' halves of one fragment per warp
+      const int r = i / (H / 4), c = (i % (H / 4)) * 4;
+      const float2* src = reinterpret_cast<const float2*>(acc) +
+                          ((((r >> 4) * WK) * (H / 8) + (c >> 3)) * 32 + (r & 7) * 4 + ((c & 4) >> 1)) * 2 + ((r >> 3) & 1);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < WK; ++k) {
+        const float f = sm_f[k][r];
+        const float2 p = src[k * (H / 8) * 64], q = src[k * (H / 8) * 64 + 2];
+        v.x = fmaf(f, p.x, v.x);
+        v.y = fmaf(f, p.y, v.y);
+        v.z = fmaf(f, q.x, v.z);
+        v.w = fmaf(f, q.y, v.w);
+      }
+      if (whole) {
+        const int pr = row0 + r, tok = pr / g.group, h = head0 + pr - tok * g.group;
+        T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, t0 + tok);
+        if (SDPA_IN_BOUNDS(t0 + tok < g.tokens && h < g.Nq, 532))
+          *reinterpret_cast<uint2*>(y + c) = make_uint2(pack2<BF>(v.x, v.y), pack2<BF>(v.z, v.w));
+      } else if (SDPA_IN_BOUNDS(slot < 2 * ctas, 534)) {
+        *reinterpret_cast<float4*>(ws.o + (slot * TM + r) * H + c) = v;
+      }
+    }
+    if (w.done()) break;
   }
   cp_async_wait<0>();
 }
@@ -395,7 +399,7 @@ template <bool BF, int H, int WM>
 cudaError_t launch_wm(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaStream_t st) {
   using C = Cfg<H, WM>;
   // 228 KB per SM, of which each CTA takes 1 KB for itself
-  static_assert(C::kSmem + 2 * C::WK * C::TM * 4 + 128 + 1024 <= 233472 / kCtasPerSm, "shared memory");
+  static_assert(C::kSmem + 3 * C::WK * C::TM * 4 + 128 + 1024 <= 233472 / kCtasPerSm, "shared memory");
   const int ctas = paged_sms() * kCtasPerSm;
   if (ctas <= 0) return cudaErrorInvalidDevice;
   // per device: set at every call (the attribute belongs to the current context)

@@ -147,13 +147,23 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
   if (bad && cta == 0) atomicOr(status, kPagedBadLength);
 
   Share r;
-  r.active = (int)min((long long)ctas, max(1ll, total / min_share));
+  r.active = total >= (long long)ctas * min_share ? ctas : max(1, (int)total / min_share);
   if (total == 0) r.active = 0;
   r.at = ShareStart{a.g.B, 0, 0, 0};
   r.begin = r.count = 0;
   if (cta >= r.active) return r;
-  r.begin = total * cta / r.active;
-  r.count = total * (cta + 1) / r.active - r.begin;
+  // total / active tiles each, the first total % active CTAs one more (32-bit divisions where
+  // they do: a 64-bit one takes a microsecond's fraction that short calls feel)
+  long long each, more;
+  if (total < (1ll << 32)) {
+    each = (unsigned)total / (unsigned)r.active;
+    more = (unsigned)total - (unsigned)each * (unsigned)r.active;
+  } else {
+    each = total / r.active;
+    more = total - each * r.active;
+  }
+  r.begin = cta * each + min((long long)cta, more);
+  r.count = each + (cta < more ? 1 : 0);
 
   // the sequence that holds tile r.begin
   long long before = 0;
@@ -195,8 +205,9 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
         }
         const long long lo = c - (long long)tiles * a.g.Nkv;
         if (o >= lo && o < c) {
-          const int k = (int)((o - lo) / tiles);
-          sh_at = ShareStart{base + warp * 32 + src, rb0 + lane, k, (int)(o - lo - (long long)k * tiles)};
+          // within one row block: fewer than Nkv * tiles, which fits 32 bits with room
+          const unsigned in = (unsigned)(o - lo), k = in / (unsigned)tiles;
+          sh_at = ShareStart{base + warp * 32 + src, rb0 + lane, (int)k, (int)(in - k * (unsigned)tiles)};
         }
         const long long block = __shfl_sync(0xffffffffu, c, 31);
         if (o < block) break;

@@ -200,11 +200,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Pag
   const Paged& g = a.g;
   const int c = blockIdx.x + 1;
   const int active = ws.start[ctas].b;
-  if (c >= active) return;
-  const ShareStart at = ws.start[c];
-  if (at.tile == 0) return;
+  const ShareStart at = ws.start[c], before = ws.start[c - 1];      // read at once; of use if c < active
+  if (c >= active || at.tile == 0) return;
   auto inside = [&](const ShareStart& s) { return s.tile > 0 && s.b == at.b && s.rb == at.rb && s.kvh == at.kvh; };
-  if (inside(ws.start[c - 1])) return;
+  if (inside(before)) return;
   bool bad = false;
   const SeqInfo s = seq_info(g, at.b, bad);
   const RowBlock rbk = row_block<TM, TN>(a, s, at.rb);
