@@ -1092,18 +1092,18 @@ int sdpa_query_status(sdpa_stream_t stream) {
   if (e == cudaSuccess) e = take_bwd_status(&bwd_status);
   if (e == cudaSuccess) e = take_norm_status(&norm_status);
   if (e == cudaSuccess) e = take_paged_append_status(&app_status);
-  for (auto take : {take_paged_simt_status, take_paged_mma_status}) {
-    int v = 0;
-    if (e == cudaSuccess) e = take(&v);
+  if (e == cudaSuccess) e = take_paged_simt_status(&paged_status);
+  int paged_timeout = 0;
+  for (auto take : {take_paged_mma_status, take_paged_tc_status}) {
+    int v = 0, late = 0;
+    if (e == cudaSuccess) e = take(&v, &late);
     paged_status |= v;
+    paged_timeout |= late;
   }
-  int tc_status = 0, tc_timeout = 0;
-  if (e == cudaSuccess) e = take_paged_tc_status(&tc_status, &tc_timeout);
-  paged_status |= tc_status;
   if (e != cudaSuccess) return cuda_fail(e, "status read");
   if (!status) status = qk_status;
   if (!status) status = bwd_status;
-  if (!status) status = tc_timeout;
+  if (!status) status = paged_timeout;
   // the bounds-checking build: the first failing index check of each kernel family
   int site = 0;
   for (auto take : {take_bounds_prefill, take_bounds_decode, take_bounds_concat, take_bounds_simt, take_bounds_norm,

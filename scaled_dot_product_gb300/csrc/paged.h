@@ -52,11 +52,13 @@ size_t paged_mma_workspace(const PagedAttn& a);
 cudaError_t launch_paged_mma(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
 
 cudaError_t take_paged_append_status(int* status);
+// Whether TMA boxes of at least eight rows tile the pages.
+bool paged_boxes(const PagedAttn& a);
 bool paged_tc_supported(const PagedAttn& a, sdpa_dtype dt);
 size_t paged_tc_workspace(const PagedAttn& a);
 cudaError_t launch_paged_tc(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
 cudaError_t take_paged_simt_status(int* status);
-cudaError_t take_paged_mma_status(int* status);
+cudaError_t take_paged_mma_status(int* status, int* timeout);
 cudaError_t take_paged_tc_status(int* status, int* timeout);
 
 #ifdef __CUDACC__

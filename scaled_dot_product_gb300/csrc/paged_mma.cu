@@ -5,27 +5,38 @@
 // block) whatever the number of grouped heads.  The packed rows of a unit (token x group head)
 // fill the 16 rows of warp-level matrix products (m16n8k16, fp32 accumulators), which need a
 // tenth of the time the bytes take; tcgen05 tiles of 128 rows would be mostly empty here and
-// their scores would pass through tensor memory.  A CTA is four warps: WM of them hold 16 rows
-// each, the other factor WK = 4 / WM splits the 64 keys of a tile, each warp with its own
-// running maximum, sum and accumulator, joined through shared memory at the end of a unit.  Tiles arrive by 16-byte
-// asynchronous copies, whose addresses go through the page table row by row, so a tile may span
-// pages of any size; page ids are fetched 64 at a time, a tile before they are needed.  Rows
-// past a sequence's keys are filled with zeros.  Copies run ahead of the products across unit
-// boundaries.
+// their scores would pass through tensor memory.  Two CTAs share an SM.  A CTA is one producer
+// warp and four product warps: WM of these hold 16 rows each, the other factor WK = 4 / WM splits
+// the 64 keys of a tile, each warp with its own running maximum, sum and accumulator, joined
+// through shared memory at the end of a unit.
+//
+// The producer keeps a ring of 96 KB per CTA full across unit boundaries.  Pages of a multiple of
+// 8 slots come by TMA, in boxes of gcd(page_size, 64) rows, each lane issuing one box of one
+// 64-column region of K or V; other pages by 16-byte asynchronous copies, row by row through the
+// page table.  (When the product warps issued the copies themselves, a third of their
+// instructions went into addresses, and a single-token batch of 4.48 GB took 851 us.)  Rows of V that
+// no copy brought (past the sequence's keys, below every window) are set to zero before they are
+// multiplied, since 0 x NaN is not 0.  Every wait is bounded: on expiry the kernel raises an abort
+// flag, goes through its loops without waiting, lets its own copies finish and records
+// SDPA_ERR_TIMEOUT.
 #include <algorithm>
-#include <mutex>
+#include <cstdlib>
+#include <type_traits>
 
 #include "paged_sched.cuh"
+#include "prefill_tc.h"
 
 namespace sdpa {
 
 static __device__ int g_paged_status;
+static __device__ int g_paged_timeout;
 
 namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 128;
+constexpr int kProducts = 128;       // threads of the product warps
+constexpr int kThreads = kProducts + 32;
 constexpr int kTN = 64;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinShare = 2;
@@ -34,13 +45,20 @@ constexpr float kRescale = 8.f;      // log2 units a maximum may grow before o i
 template <int H, int WM>
 struct Cfg {
   static constexpr int WK = 4 / WM, TM = 16 * WM, KW = kTN / WK;
-  static constexpr int kRow = H * 2;                       // bytes of a row
-  static constexpr int kTile = kTN * kRow;
+  static constexpr int kRegions = H / 64;                  // 64-column regions: rows of 128 bytes
+  static constexpr int kRegion = kTN * 128;
+  static constexpr int kTile = kRegions * kRegion;
   static constexpr int kStages = 3 * 128 / H;
-  static constexpr int kSmem = kStages * 2 * kTile;
+  static constexpr int kSmem = kStages * 2 * kTile + 1024; // + alignment slack
   static_assert(2 * kTile == 4 * 16 * H * 4, "a stage holds the four warps' accumulators");
-  static constexpr int CPR = kRow / 16;                    // 16-byte chunks of a row
-  static constexpr int kPass = kThreads / CPR;             // rows copied per pass
+};
+
+struct MmaArgs {
+  PagedAttn a;
+  PagedWs ws;
+  int box;                           // rows per TMA box; 0: row by row
+  int k_ds, k_dn, k_db, v_ds, v_dn, v_db;   // tensor-map dimension of slot / head / page
+  uint64_t wait_ns;
 };
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t* r) {
@@ -82,18 +100,39 @@ __device__ __forceinline__ float quad_sum(float x) {
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 template <bool BF, int H, int WM>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const PagedAttn a, const PagedWs ws) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    paged_mma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                     const __grid_constant__ MmaArgs args) {
   using C = Cfg<H, WM>;
   using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
+  using Wk = Walk<C::TM, kTN>;
   constexpr int WK = C::WK, TM = C::TM, KW = C::KW, NT = KW / 8;
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
   __shared__ float sm_m[WK][TM], sm_l[WK][TM], sm_f[WK][TM];
+  __shared__ int abort_flag;
+  const PagedAttn& a = args.a;
+  const PagedWs& ws = args.ws;
   const Paged& g = a.g;
   const int ctas = gridDim.x, cta = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sb = (smem_u32(smem_raw) + 1023) & ~1023u;
+  auto b_full = [&](int s) { return smem_u32(&bar_full[s]); };
+  auto b_empty = [&](int s) { return smem_u32(&bar_empty[s]); };
+  volatile int* abortp = &abort_flag;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(b_full(s), args.box ? 1 : 32);
+      mbar_init(b_empty(s), kProducts / 32);
+    }
+    fence_mbar_init();
+  }
   const Share sh = find_share<TM, kTN, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
   if (threadIdx.x == 0) {
     if (cta == 0) ws.start[ctas].b = sh.active;
@@ -101,14 +140,134 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
   }
   pdl_launch_dependents();
   if (sh.count == 0) return;
+  __syncthreads();
+  Wk w(a, sh);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == kProducts / 32) {
+    // ================================================================ producer
+    int st = 0, it = 0;               // stage, turns of the ring
+    bool ok = true;
+    // the stage is free, or the call is being given up
+    auto wait_free = [&]() {
+      if (it > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(b_empty(st), (it - 1) & 1, abortp, args.wait_ns));
+      return ok;
+    };
+    auto advance = [&]() {
+      if (++st == C::kStages) { st = 0; ++it; }
+    };
+    if (args.box) {
+      // lane: box (lane & 7), K or V (bit 3), region (bit 4)
+      const bool is_v = lane & 8;
+      const int row = (lane & 7) * args.box, region = lane >> 4;
+      const bool mine = row < kTN && region < C::kRegions;
+      const CUtensorMap* map = is_v ? &tv : &tk;
+      if (lane < 16 && (lane & 7) == 0) prefetch_tmap(map);
+      // page of this lane's box of the t-th tile of w's unit (-1: the box is not brought)
+      auto page_of = [&](int t) -> int {
+        if (!mine || w.done() || t >= w.take()) return -1;
+        const int key = (w.r.tile0 + w.tile + t) * kTN + row;
+        if (key >= w.s.T || key + args.box <= w.r.lo) return -1;
+        return g.table[(int64_t)w.b * g.table_stride + page_div(g, key)];
+      };
+      auto brought = [&](int t) {
+        const int key = (w.r.tile0 + w.tile + t) * kTN + row;
+        return mine && key < w.s.T && key + args.box > w.r.lo;
+      };
+      int id = page_of(0);
+      while (!w.done() && wait_free()) {
+        const int n = w.take();
+        for (int t = 0; t < n && wait_free(); ++t) {
+          const bool take = brought(t);
+          const int key = (w.r.tile0 + w.tile + t) * kTN + row;
+          if (take && (unsigned)id >= (unsigned)g.num_pages) {
+            atomicOr(&g_paged_status, kPagedBadPage);
+            id = g.num_pages;          // outside the map: the box is filled with zeros
+          }
+          const unsigned all = __ballot_sync(0xffffffffu, take);
+          if (lane == 0) mbar_arrive_expect_tx(b_full(st), __popc(all) * args.box * 128);
+          __syncwarp();
+          if (take && SDPA_IN_BOUNDS(st < C::kStages && row + args.box <= kTN && w.kvh < g.Nkv, 531)) {
+            const int slot = key - page_div(g, key) * g.page_size;
+            const int ds = is_v ? args.v_ds : args.k_ds, dn = is_v ? args.v_dn : args.k_dn;
+            const int c1 = ds == 1 ? slot : dn == 1 ? w.kvh : id, c2 = ds == 2 ? slot : dn == 2 ? w.kvh : id,
+                      c3 = ds == 3 ? slot : dn == 3 ? w.kvh : id;
+            tma_load_4d(sb + st * 2 * C::kTile + (is_v ? C::kTile : 0) + region * C::kRegion + row * 128, map, b_full(st),
+                        64 * region, c1, c2, c3);
+          }
+          __syncwarp();
+          advance();
+          if (t + 1 < n) id = page_of(t + 1);      // arrives while the ring is waited for
+        }
+        if (!ok) break;
+        w.next(a);
+        id = page_of(0);
+      }
+    } else {
+      // rows lane / 8 and on, 16-byte chunk lane % 8 of each region; the ids of 64 pages are at hand,
+      // two per lane, and the next ones are fetched when a tile reaches beyond them
+      const int chunk = lane & 7, row_in = lane >> 3;
+      int wbase = 0, id0 = -1, id1 = -1;
+      while (!w.done() && ok) {
+        const int n = w.take();
+        const int32_t* table = g.table + (int64_t)w.b * g.table_stride;
+        const T* kb = reinterpret_cast<const T*>(g.kp.p) + g.kp.sh * w.kvh + chunk * 8;
+        const T* vb = reinterpret_cast<const T*>(g.vp.p) + g.vp.sh * w.kvh + chunk * 8;
+        const int end = w.r.hi >= w.r.lo ? page_div(g, w.r.hi) : -1;       // last page some row admits
+        int have = -1;                 // last page at hand
+        for (int t = 0; t < n; ++t) {
+          const int k0 = (w.r.tile0 + w.tile + t) * kTN;
+          if (end >= 0 && page_div(g, min(k0 + kTN - 1, w.r.hi)) > have) {
+            wbase = page_div(g, max(k0, w.r.lo));
+            have = wbase + 63;
+            id0 = wbase + lane <= end ? table[wbase + lane] : -1;
+            id1 = wbase + 32 + lane <= end ? table[wbase + 32 + lane] : -1;
+          }
+          if (!wait_free()) break;
+#pragma unroll 4
+          for (int p = 0; p < kTN / 4; ++p) {
+            const int r = p * 4 + row_in, key = k0 + r, pg = page_div(g, key), i = pg - wbase;
+            const int a0 = __shfl_sync(0xffffffffu, id0, i & 31), a1 = __shfl_sync(0xffffffffu, id1, i & 31);
+            const int id = i < 32 ? a0 : a1;
+            bool take = key >= w.r.lo && key <= w.r.hi;      // other keys: zeros, their pages are not read
+            if (take && (unsigned)id >= (unsigned)g.num_pages) {
+              atomicOr(&g_paged_status, kPagedBadPage);
+              take = false;
+            }
+            take = take && SDPA_IN_BOUNDS(i >= 0 && i < 64 && key < g.cap, 532);
+            const int slot = key - pg * g.page_size;
+            const T* ks = kb + (take ? id * g.kp.sb + slot * g.kp.ss : 0);
+            const T* vs = vb + (take ? id * g.vp.sb + slot * g.vp.ss : 0);
+            const uint32_t d = sb + st * 2 * C::kTile + r * 128 + ((chunk ^ (r & 7)) << 4);
+#pragma unroll
+            for (int reg = 0; reg < C::kRegions; ++reg) {
+              cp_async16_or_zero(d + reg * C::kRegion, ks + reg * 64, take);
+              cp_async16_or_zero(d + C::kTile + reg * C::kRegion, vs + reg * 64, take);
+            }
+          }
+          cp_async_arrive(b_full(st));
+          advance();
+        }
+        if (ok) w.next(a);
+      }
+    }
+    if (!ok || *abortp) {
+      // given up: copies already issued land before the CTA can exit
+      constexpr uint64_t kDrainNs = 2000000000ull;
+      cp_async_wait_all();
+      for (int s = 0; s < C::kStages; ++s) {
+        const int turns = it + (s < st ? 1 : 0);
+        if (turns > 0) mbar_wait_bounded(b_full(s), (turns - 1) & 1, nullptr, kDrainNs);
+      }
+      if (lane == 0) atomicExch(&g_paged_timeout, (int)SDPA_ERR_TIMEOUT);
+    }
+    return;
+  }
+
+  // ================================================================ products
   const int wm = warp / WK, wk = warp % WK;
-  const uint32_t sb = smem_u32(smem);
-
-  // ---- query fragments of a unit, straight from memory: rows lane / 4 and 8 further of 16
   uint32_t qf[H / 16][4];
-  auto load_q = [&](const Walk<TM, kTN>& w) {
+  // query fragments of a unit, straight from memory: rows lane / 4 and 8 further of 16
+  auto load_q = [&]() {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int pr = w.r.row0 + min(wm * 16 + (lane >> 2) + 8 * x, w.r.rows - 1);
@@ -122,94 +281,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
       }
     }
   };
-  Walk<TM, kTN> w(a, sh);
-
-  // ---- the copying side: its own walk over the share, kStages - 1 tiles ahead.  The ids of 64
-  // pages are at hand, one or two per lane; when the next tile reaches beyond them the following
-  // 64 are fetched, one tile before they are needed.
-  Walk<TM, kTN> wl = w;
-  int lt = 0;                         // tile of wl's unit
-  int wbase = 0, id0 = -1, id1 = -1;  // pages wbase + lane and wbase + 32 + lane of wl's sequence
-  bool fresh = true;                  // wl entered another unit
-  const T *kbase = nullptr, *vbase = nullptr;
-  const int chunk = threadIdx.x % C::CPR, row_in = threadIdx.x / C::CPR;
-  const bool same = g.kp.sb == g.vp.sb && g.kp.ss == g.vp.ss;
-  auto fetch_ids = [&]() {
-    const int k0 = (wl.r.tile0 + wl.tile + lt) * kTN;
-    const int last = page_div(g, max(0, min(k0 + kTN - 1, wl.r.hi)));
-    if (!fresh && last < wbase + 64) return;
-    wbase = page_div(g, max(k0, wl.r.lo));
-    const int32_t* table = g.table + (int64_t)wl.b * g.table_stride + wbase;
-    const int end = wl.r.hi >= wl.r.lo ? page_div(g, wl.r.hi) - wbase : -1;     // last page some row admits
-    id0 = lane <= end ? table[lane] : -1;
-    id1 = lane + 32 <= end ? table[lane + 32] : -1;
-    if (fresh) {
-      kbase = reinterpret_cast<const T*>(g.kp.p) + g.kp.sh * wl.kvh + chunk * 8;
-      vbase = reinterpret_cast<const T*>(g.vp.p) + g.vp.sh * wl.kvh + chunk * 8;
-      fresh = false;
-    }
-  };
-  auto copy_tile = [&](int st) {
-    if (!wl.done()) {
-      const int k0 = (wl.r.tile0 + wl.tile + lt) * kTN;
-      const uint32_t sk = sb + st * 2 * C::kTile;
-#pragma unroll
-      for (int p = 0; p < kTN / C::kPass; ++p) {
-        const int r = p * C::kPass + row_in;
-        const int key = k0 + r, pg = page_div(g, key), i = pg - wbase;
-        const int a0 = __shfl_sync(0xffffffffu, id0, i & 31), a1 = __shfl_sync(0xffffffffu, id1, i & 31);
-        const int id = i < 32 ? a0 : a1;
-        bool take = key >= wl.r.lo && key <= wl.r.hi;      // other keys: zeros, their pages are not read
-        if (take && (unsigned)id >= (unsigned)g.num_pages) {
-          atomicOr(&g_paged_status, kPagedBadPage);
-          take = false;
-        }
-        take = take && SDPA_IN_BOUNDS(i >= 0 && i < 64 && key < g.cap, 531);
-        const int slot = key - pg * g.page_size;
-        const int64_t ko = take ? id * g.kp.sb + slot * g.kp.ss : 0;
-        const int64_t vo = same ? ko : take ? id * g.vp.sb + slot * g.vp.ss : 0;
-        const uint32_t d = sk + r * C::kRow + ((chunk ^ (r & 7)) << 4);
-        cp_async16_or_zero(d, kbase + ko, take);
-        cp_async16_or_zero(d + C::kTile, vbase + vo, take);
-      }
-      if (++lt == wl.take()) {
-        lt = 0;
-        wl.next(a);
-        fresh = true;
-      }
-      if (!wl.done()) fetch_ids();
-    }
-    cp_async_commit();
-  };
-  fetch_ids();
-  load_q(w);
-
+  load_q();
   const float cap_log2 = a.softcap * kLog2e, cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
   const float kfac = a.softcap > 0.f ? 1.f : a.scale * kLog2e;
-  // fragment addresses: lane -> row and 16-byte chunk of the four 8x8 matrices of one load
-  const int kr = wk * KW + ((lane >> 4) << 3) + (lane & 7), kc = (lane >> 3) & 1;
-  const int vr = wk * KW + (((lane >> 3) & 1) << 3) + (lane & 7), vc = lane >> 4;
+  // fragment addresses in a region: lane -> row and 16-byte chunk of the four 8x8 matrices of a load;
+  // the chunk of a later column block is the same address with other bits flipped
+  const int kr = wk * KW + ((lane >> 4) << 3) + (lane & 7);
+  const uint32_t koff = kr * 128 + ((((lane >> 3) & 1) ^ (kr & 7)) << 4);
+  const int vr = wk * KW + (((lane >> 3) & 1) << 3) + (lane & 7);
+  const uint32_t voff = vr * 128 + (((lane >> 4) ^ (vr & 7)) << 4);
   const int prow = wm * 16 + (lane >> 2);      // this thread's rows of the unit: prow and prow + 8
 
   int lo[2], hi[2], full_lo = 0, full_hi = 0;  // admitted keys of the two rows, of every row
   float o[H / 8][4], m[2], l[2];
-  int t = 0;                                   // tile of w's unit
-  // One loop for filling the ring, the products and the units' ends: straight-line code runs once
-  // per call from a cold instruction cache, which short calls feel (3 us a section, measured).
-  int put = 0;                                 // stage the next copy goes to
+  int t = 0, st = 0, phase = 0;                // tile of w's unit, stage and its phase
+  bool ok = true;
+  // One loop for the products and the units' ends: straight-line code runs once per call from a
+  // cold instruction cache, which short calls feel (up to 3 us a section, measured).
 #pragma unroll 1
-  for (int ahead = C::kStages - 1;;) {
-    if (ahead == 0) {
-      cp_async_wait<C::kStages - 2>();
-      __syncthreads();               // the tile is there, and the previous one has been read
-    }
-    copy_tile(put);
-    put = put + 1 == C::kStages ? 0 : put + 1;
-    if (ahead > 0) {
-      --ahead;
-      continue;
-    }
-    const uint32_t sk = sb + put * 2 * C::kTile, sv = sk + C::kTile;   // the oldest tile's stage
+  while (true) {
     if (t == 0) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -225,8 +315,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     }
+    const uint32_t sk = sb + st * 2 * C::kTile, sv = sk + C::kTile;
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(b_full(st), phase, abortp, args.wait_ns));
     {
-      const int key0 = (w.r.tile0 + w.tile + t) * kTN + wk * KW;
+      const int tile_key = (w.r.tile0 + w.tile + t) * kTN, key0 = tile_key + wk * KW;
+      if (args.box && (tile_key + kTN > w.s.T || tile_key < w.r.lo)) {
+        // this warp's rows of V that no box brought become zeros
+        const int first = w.r.lo - w.r.lo % args.box - tile_key, last = w.s.T - tile_key;
+        for (int i = lane; i < KW * 8; i += 32) {
+          const int r = wk * KW + (i >> 3);
+          if (r < first || r >= last) {
+#pragma unroll
+            for (int reg = 0; reg < C::kRegions; ++reg)
+              st_shared_v4(sv + reg * C::kRegion + r * 128 + (i & 7) * 16, 0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();      // before a later box is written here
+        __syncwarp();
+      }
 
       float s[NT][4];
 #pragma unroll
@@ -238,8 +344,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
           uint32_t b[4];
-          const int r = kr + n * 8, c = kk * 2 + kc;
-          ldsm_x4(sk + r * C::kRow + ((c ^ (r & 7)) << 4), b);
+          ldsm_x4(sk + (kk >> 2) * C::kRegion + n * 1024 + (koff ^ ((kk & 3) * 32)), b);
           mma<BF>(s[n], qf[kk], b);
           mma<BF>(s[n + 1], qf[kk], b + 2);
         }
@@ -304,28 +409,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
 #pragma unroll
         for (int n = 0; n < H / 8; n += 2) {
           uint32_t b[4];
-          const int r = vr + kt * 16, c = n + vc;
-          ldsm_x4_t(sv + r * C::kRow + ((c ^ (r & 7)) << 4), b);
+          ldsm_x4_t(sv + (n >> 3) * C::kRegion + kt * 2048 + (voff ^ ((n & 7) * 16)), b);
           mma<BF>(o[n], p, b);
           mma<BF>(o[n + 1], p, b + 2);
         }
       }
     }
 
-    if (++t < w.take()) continue;
+    const int done_st = st;
+    if (++st == C::kStages) { st = 0; phase ^= 1; }
+    if (++t < w.take()) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_empty(done_st));
+      continue;
+    }
 
     // ---- end of the unit's tiles in this share; the next unit's query rows are on their way
     // while its results are joined and written.  The warps' accumulators, as they lie in registers
-    // (float4 n of lane i at [warp][n][i]), go to the stage of the tile just read, which the next
-    // copy fills only after the barrier above.
+    // (float4 n of lane i at [warp][n][i]), go to the stage of the tile just read, which is handed
+    // back to the producer afterwards.
     const bool whole = w.whole();
     const int64_t slot = 2 * (int64_t)cta + (w.begins() ? 1 : 0);
     const int rows = w.r.rows, row0 = w.r.row0, t0 = w.s.t0, head0 = w.kvh * g.group;
     w.next(a);
     t = 0;
-    if (!w.done()) load_q(w);
-    __syncthreads();                 // every warp has read the tile
-    float4* acc = reinterpret_cast<float4*>(smem + (sk - sb));
+    if (!w.done()) load_q();
+    named_bar_sync(1, kProducts);    // every warp has read the tile
+    float4* acc = reinterpret_cast<float4*>(smem_raw + (sk - smem_u32(smem_raw)));
 #pragma unroll
     for (int n = 0; n < H / 8; ++n) acc[(warp * (H / 8) + n) * 32 + lane] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
 #pragma unroll
@@ -336,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
         sm_l[wk][prow + 8 * x] = l[x];
       }
     }
-    __syncthreads();
+    named_bar_sync(1, kProducts);
     if ((int)threadIdx.x < rows) {
       const int r = threadIdx.x;
       float M = -INFINITY, L = 0.f;
@@ -357,9 +467,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
 #pragma unroll
       for (int k = 0; k < WK; ++k) sm_f[k][r] = f[k] * sc;
     }
-    __syncthreads();
+    named_bar_sync(1, kProducts);
 #pragma unroll 1
-    for (int i = threadIdx.x; i < rows * (H / 4); i += kThreads) {
+    for (int i = threadIdx.x; i < rows * (H / 4); i += kProducts) {
       // row r, columns c .. c + 3: two lanes' halves of one fragment per warp
       const int r = i / (H / 4), c = (i % (H / 4)) * 4;
       const float2* src = reinterpret_cast<const float2*>(acc) +
@@ -384,8 +494,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
       }
     }
     if (w.done()) break;
+    fence_proxy_async_smem();        // the accumulators, before a box is written there
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_empty(done_st));
   }
-  cp_async_wait<0>();
+  if (!ok && lane == 0) atomicExch(&g_paged_timeout, (int)SDPA_ERR_TIMEOUT);
 }
 
 // Rows per unit: the smallest of 16, 32 and 64 that holds all rows of a sequence with max_new
@@ -393,6 +506,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_mma_kernel(const P
 int mma_tm(const PagedAttn& a) {
   const int64_t rows = (int64_t)a.max_new * a.g.group;
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+uint64_t wait_limit_ns() {
+  static const uint64_t v = [] {
+    const char* e = std::getenv("SDPA_WAIT_LIMIT_NS");
+    return e ? std::strtoull(e, nullptr, 10) : 4000000000ull;
+  }();
+  return v;
 }
 
 template <bool BF, int H, int WM>
@@ -405,11 +526,22 @@ cudaError_t launch_wm(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaStream_t
   // per device: set at every call (the attribute belongs to the current context)
   cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<BF, H, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const PagedWs ws = paged_ws(wsp, ctas, C::TM);
-  paged_mma_kernel<BF, H, WM><<<(unsigned)ctas, kThreads, C::kSmem, st>>>(a, ws);
+  MmaArgs t{};
+  t.a = a;
+  t.ws = paged_ws(wsp, ctas, C::TM);
+  t.wait_ns = wait_limit_ns();
+  CUtensorMap tk{}, tv{};
+  if (paged_boxes(a)) {
+    t.box = kTN;
+    while (a.g.page_size % t.box) t.box >>= 1;
+    if (!tc_make_map(&tk, a.g.kp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, H, &t.k_ds, &t.k_dn, &t.k_db, t.box) ||
+        !tc_make_map(&tv, a.g.vp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, H, &t.v_ds, &t.v_dn, &t.v_db, t.box))
+      return cudaErrorInvalidValue;
+  }
+  paged_mma_kernel<BF, H, WM><<<(unsigned)ctas, kThreads, C::kSmem, st>>>(tk, tv, t);
   count_launch(1);
   e = cudaGetLastError();
-  return e == cudaSuccess ? launch_paged_merge(a, dt, ws, ctas, C::TM, st) : e;
+  return e == cudaSuccess ? launch_paged_merge(a, dt, t.ws, ctas, C::TM, st) : e;
 }
 
 template <bool BF, int H>
@@ -441,15 +573,16 @@ cudaError_t launch_paged_mma(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaSt
   return bf ? launch_h<true, 64>(a, dt, ws, st) : launch_h<false, 64>(a, dt, ws, st);
 }
 
-cudaError_t take_paged_mma_status(int* status) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_paged_status, sizeof v);
+cudaError_t take_paged_mma_status(int* status, int* timeout) {
+  int v[2] = {0, 0};
+  cudaError_t e = cudaMemcpyFromSymbol(&v[0], g_paged_status, sizeof v[0]);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v[1], g_paged_timeout, sizeof v[1]);
   if (e != cudaSuccess) return e;
-  *status = v;
-  if (v) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero);
-  }
+  *status = v[0];
+  *timeout = v[1];
+  const int zero = 0;
+  if (v[0]) e = cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero);
+  if (e == cudaSuccess && v[1]) e = cudaMemcpyToSymbol(g_paged_timeout, &zero, sizeof zero);
   return e;
 }
 

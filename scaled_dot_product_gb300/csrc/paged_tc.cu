@@ -629,15 +629,18 @@ cudaError_t launch_h(bool bf, bool cap, const CUtensorMap& tk, const CUtensorMap
 
 }  // namespace
 
-// More rows of a sequence than paged_mma's widest unit holds, and pages that boxes of at least
-// eight rows tile.
-bool paged_tc_supported(const PagedAttn& a, sdpa_dtype dt) {
-  if (dt == SDPA_F32 || a.g.H != a.g.Hv || (a.g.H != 64 && a.g.H != 128)) return false;
+bool paged_boxes(const PagedAttn& a) {
   if (a.g.page_size % 8 || a.g.num_pages < 1) return false;
   for (const View* v : {&a.g.kp, &a.g.vp})
     for (int64_t s : {v->sb, v->sh, v->ss})
       if (s >= ((int64_t)1 << 38)) return false;
-  return (int64_t)a.max_new * a.g.group > 64;
+  return true;
+}
+
+// More rows of a sequence than paged_mma's widest unit holds.
+bool paged_tc_supported(const PagedAttn& a, sdpa_dtype dt) {
+  if (dt == SDPA_F32 || a.g.H != a.g.Hv || (a.g.H != 64 && a.g.H != 128)) return false;
+  return paged_boxes(a) && (int64_t)a.max_new * a.g.group > 64;
 }
 
 size_t paged_tc_workspace(const PagedAttn& a) { return paged_ws_bytes(kPagedMaxSms, kTM, a.g.Hv); }
