@@ -524,6 +524,7 @@ int check_paged(const sdpa_paged_params* p, Paged* g, Extent ext[2]) {
   g->num_pages = p->num_pages; g->page_size = p->page_size; g->max_pages = p->max_pages;
   g->cap = p->max_pages * p->page_size;
   paged_magic(p->page_size, &g->page_mul, &g->page_shift);
+  paged_magic(g->group, &g->group_mul, &g->group_shift);
   g->kp = to_view(p->k_pages); g->vp = to_view(p->v_pages);
   g->table = p->page_table; g->table_stride = p->page_table_stride;
   g->lens = p->kv_lens; g->cu = p->cu_new;

@@ -14,6 +14,7 @@ struct Paged {
   int num_pages, page_size, max_pages;
   int cap;                        // max_pages * page_size: keys the table can address
   uint32_t page_mul, page_shift;  // j / page_size = (j * page_mul) >> page_shift for 0 <= j < 2^31
+  uint32_t group_mul, group_shift;          // r / group likewise
   View kp, vp;                    // (num_pages, Nkv, page_size, H / Hv)
   const int32_t* table;
   int64_t table_stride;
@@ -67,6 +68,10 @@ enum { kPagedBadPage = 1, kPagedBadLength = 2, kPagedBadPosition = 4 };
 
 __device__ __forceinline__ int page_div(const Paged& g, int j) {
   return (int)(((uint64_t)(uint32_t)j * g.page_mul) >> g.page_shift);
+}
+
+__device__ __forceinline__ int group_div(const Paged& g, int r) {
+  return (int)(((uint64_t)(uint32_t)r * g.group_mul) >> g.group_shift);
 }
 
 // New-token rows [t0, t0 + n) and keys T of sequence b, clamped to what the arrays can hold

@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int pr = w.r.row0 + min(wm * 16 + (lane >> 2) + 8 * x, w.r.rows - 1);
-      const int tok = pr / g.group;
+      const int tok = group_div(g, pr);
       const uint32_t* qr = reinterpret_cast<const uint32_t*>(
           reinterpret_cast<const T*>(a.q.p) + a.q.off(0, w.kvh * g.group + pr - tok * g.group, w.s.t0 + tok));
 #pragma unroll
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
       float sc = 1.f;
       if (whole) {
-        sc = row_scale<T>(a, head0 + (row0 + r) % g.group, M, L);
+        sc = row_scale<T>(a, head0 + row0 + r - group_div(g, row0 + r) * g.group, M, L);
       } else if (SDPA_IN_BOUNDS(slot < 2 * ctas, 533)) {
         *reinterpret_cast<float2*>(ws.ml + (slot * TM + r) * 2) = make_float2(M, L);
       }
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         v.w = fmaf(f, q.y, v.w);
       }
       if (whole) {
-        const int pr = row0 + r, tok = pr / g.group, h = head0 + pr - tok * g.group;
+        const int pr = row0 + r, tok = group_div(g, pr), h = head0 + pr - tok * g.group;
         T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, t0 + tok);
         if (SDPA_IN_BOUNDS(t0 + tok < g.tokens && h < g.Nq, 532))
           *reinterpret_cast<uint2*>(y + c) = make_uint2(pack2<BF>(v.x, v.y), pack2<BF>(v.z, v.w));

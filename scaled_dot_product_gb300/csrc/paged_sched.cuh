@@ -62,7 +62,7 @@ __device__ __forceinline__ RowBlock row_block(const PagedAttn& a, const SeqInfo&
   const int all = s.n * a.g.group;
   r.row0 = rb * TM;
   r.rows = min(TM, all - r.row0);
-  const int i0 = r.row0 / a.g.group, i1 = (r.row0 + r.rows - 1) / a.g.group;
+  const int i0 = group_div(a.g, r.row0), i1 = group_div(a.g, r.row0 + r.rows - 1);
   r.hi = a.causal ? s.T - s.n + i1 : s.T - 1;
   r.lo = a.window > 0 ? max(0, s.T - s.n + i0 - a.window + 1) : 0;
   r.tile0 = r.lo / TN;
@@ -75,7 +75,7 @@ __device__ __forceinline__ int row_blocks(const PagedAttn& a, const SeqInfo& s, 
 
 // Admitted keys [lo, hi] of packed row r of a sequence (hi < lo: none).
 __device__ __forceinline__ void row_keys(const PagedAttn& a, const SeqInfo& s, int r, int& lo, int& hi) {
-  const int pos = s.T - s.n + r / a.g.group;
+  const int pos = s.T - s.n + group_div(a.g, r);
   hi = a.causal ? pos : s.T - 1;
   lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
 }

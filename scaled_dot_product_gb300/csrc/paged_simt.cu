@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a,
     for (int r = 0; r < TM; ++r) {
       const int pr = w.r.row0 + min(r, nr - 1);
       const T* row = reinterpret_cast<const T*>(a.q.p) +
-                     a.q.off(0, w.kvh * g.group + pr % g.group, w.s.t0 + pr / g.group);
+                     a.q.off(0, w.kvh * g.group + pr - group_div(g, pr) * g.group, w.s.t0 + group_div(g, pr));
 #pragma unroll
       for (int n = 0; n < NV; ++n) {
         const int c = (n * LPK + t) * V;
@@ -171,9 +171,9 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a,
         }
       }
       if (whole) {
-        const int pr = w.r.row0 + r, h = w.kvh * g.group + pr % g.group;
-        T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, w.s.t0 + pr / g.group);
-        if (SDPA_IN_BOUNDS(w.s.t0 + pr / g.group < g.tokens && h < g.Nq, 522))
+        const int pr = w.r.row0 + r, h = w.kvh * g.group + pr - group_div(g, pr) * g.group;
+        T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, w.s.t0 + group_div(g, pr));
+        if (SDPA_IN_BOUNDS(w.s.t0 + group_div(g, pr) < g.tokens && h < g.Nq, 522))
           y[d] = Elem<T>::from_f32(O * row_scale<T>(a, h, M, L));
       } else if (SDPA_IN_BOUNDS(slot < 2 * ctas, 523)) {
         ws.o[(slot * TM + r) * g.Hv + d] = O;
@@ -188,14 +188,24 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a,
 
 // ---------------------------------------------------------------- joining the partial results
 
-constexpr int kMergeWarps = 4;
+constexpr int kMergeThreads = 256;
 
-// The blocks (c, .) join the rows of the unit that CTA c's share starts inside of, if c is the
-// first such CTA of the unit; a warp takes every (4 gridDim.y)-th row.  The partials are those of CTA c - 1 (which
-// began the unit) and of the CTAs from c on whose shares start inside it, taken in that order.
+// How a joined unit is cut: a block takes `rows` rows (8, 16 or 32) and `cols` groups of four
+// columns; with fewer than 256 of these items, 256 / (rows * cols) threads share one, each taking
+// a part of the partial results.
+struct MergeCut { int rows, cols; };
+
+// The blocks (c, .) join the unit that CTA c's share starts inside of, if c is the first such CTA of
+// the unit.  The partials are those of CTA c - 1 (which began the unit) and of the CTAs from c on
+// whose shares start inside it, taken in that order.  Bound by latency: a chain of five dependent
+// loads, so rows and columns are spread over threads rather than taken in turn (a warp per row,
+// eight rows in turn, took 25 us where two partials of every unit of 256 rows were joined).
 template <typename T, int TM, int TN>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const PagedAttn a, const PagedWs ws,
-                                                                       const int ctas) {
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttn a, const PagedWs ws, const int ctas,
+                                                                    const MergeCut cut) {
+  __shared__ float sm_m[32], sm_inv[32];
+  __shared__ long long sm_y[32];
+  __shared__ float4 part[kMergeThreads];
   pdl_wait();
   const Paged& g = a.g;
   const int c = blockIdx.x + 1;
@@ -207,82 +217,101 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Pag
   bool bad = false;
   const SeqInfo s = seq_info(g, at.b, bad);
   const RowBlock rbk = row_block<TM, TN>(a, s, at.rb);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, cols_all = g.Hv / 4;
+  const int row0 = (int)blockIdx.y * cut.rows, col0 = (int)blockIdx.z * cut.cols;
+  if (row0 >= rbk.rows) return;
   int n = 1;                                   // partials: CTA c - 1's second slot, then first slots
   for (int k = c;; k += 32) {
     const unsigned in = __ballot_sync(0xffffffffu, k + lane < active && inside(ws.start[min(k + lane, active - 1)]));
     n += in == 0xffffffffu ? 32 : __ffs(~in) - 1;
     if (in != 0xffffffffu) break;
   }
-  for (int r = blockIdx.y * kMergeWarps + warp; r < rbk.rows; r += gridDim.y * kMergeWarps) {
-    auto slot_of = [&](int i) -> int64_t { return ((i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c + i - 1)) * TM) + r; };
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, ws.ml[slot_of(i) * 2]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, acc[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    if (M != -INFINITY) {
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const int mine = i0 + lane;
-        float f = 0.f;
-        if (mine < n) {
-          const float mm = ws.ml[slot_of(mine) * 2];
-          f = mm == -INFINITY ? 0.f : exp2f(mm - M);
-          L = fmaf(f, ws.ml[slot_of(mine) * 2 + 1], L);
-        }
-        const int cnt = min(32, n - i0);
-#pragma unroll 4
-        for (int k = 0; k < cnt; ++k) {
-          const float fk = __shfl_sync(0xffffffffu, f, k);
-          const float* o = ws.o + slot_of(i0 + k) * g.Hv;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {          // 4 columns per lane, twice for Hv > 128
-            const int d = (e * 32 + lane) * 4;
-            if (d < g.Hv && fk != 0.f) {
-              const float4 v = *reinterpret_cast<const float4*>(o + d);
-              acc[4 * e] = fmaf(fk, v.x, acc[4 * e]);
-              acc[4 * e + 1] = fmaf(fk, v.y, acc[4 * e + 1]);
-              acc[4 * e + 2] = fmaf(fk, v.z, acc[4 * e + 2]);
-              acc[4 * e + 3] = fmaf(fk, v.w, acc[4 * e + 3]);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  auto slot_of = [&](int i) -> int64_t { return (i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c + i - 1)) * TM; };
+
+  // maximum and sum of each row, 256 / rows threads (8, 16 or 32) a row
+  {
+    const int tpr = kMergeThreads / cut.rows, r = threadIdx.x / tpr, sub = threadIdx.x % tpr;
+    const bool live = row0 + r < rbk.rows;
+    float M = -INFINITY, L = 0.f;
+    for (int i = sub; i < n && live; i += tpr) {
+      const float2 v = *reinterpret_cast<const float2*>(ws.ml + (slot_of(i) + row0 + r) * 2);
+      const float mn = fmaxf(M, v.x);
+      if (mn != -INFINITY) L = L * exp2f(M - mn) + v.y * exp2f(v.x - mn);
+      M = mn;
     }
-    const int pr = rbk.row0 + r, h = at.kvh * g.group + pr % g.group;
-    const float inv = row_scale<T>(a, h, M, L);
-    T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, s.t0 + pr / g.group);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int d = (e * 32 + lane) * 4;
-      if (d < g.Hv && SDPA_IN_BOUNDS(s.t0 + pr / g.group < g.tokens, 524)) {
-        T out[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) out[k] = Elem<T>::from_f32(acc[4 * e + k] * inv);
-        if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y + d) = *reinterpret_cast<const uint4*>(out);
-        else *reinterpret_cast<uint2*>(y + d) = *reinterpret_cast<const uint2*>(out);
+    for (int o = tpr / 2; o > 0; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
+      const float mn = fmaxf(M, m2);
+      if (mn != -INFINITY) L = L * exp2f(M - mn) + l2 * exp2f(m2 - mn);
+      M = mn;
+    }
+    if (sub == 0 && live) {
+      const int pr = rbk.row0 + row0 + r, h = at.kvh * g.group + pr - group_div(g, pr) * g.group;
+      sm_m[r] = M;
+      sm_inv[r] = row_scale<T>(a, h, M, L);
+      sm_y[r] = a.y.off(0, h, s.t0 + group_div(g, pr));
+    }
+  }
+  __syncthreads();
+
+  const int items = cut.rows * cut.cols, share = max(1, kMergeThreads / items);      // threads of one item
+  const int per = kMergeThreads / share, g0 = threadIdx.x / per;
+  for (int x = threadIdx.x % per; x < items; x += per) {
+    const int r = x / cut.cols, d = (col0 + x % cut.cols) * 4;
+    const bool live = row0 + r < rbk.rows && d < cols_all * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+      const float M = sm_m[r];
+#pragma unroll 4
+      for (int i = g0; i < n; i += share) {
+        const int64_t at_row = slot_of(i) + row0 + r;
+        const float mm = ws.ml[at_row * 2];
+        const float4 o = *reinterpret_cast<const float4*>(ws.o + at_row * g.Hv + d);
+        const float f = mm == -INFINITY ? 0.f : exp2f(mm - M);
+        v.x = fmaf(f, o.x, v.x);
+        v.y = fmaf(f, o.y, v.y);
+        v.z = fmaf(f, o.z, v.z);
+        v.w = fmaf(f, o.w, v.w);
       }
+    }
+    if (share > 1) {                           // one pass: items < 256
+      part[threadIdx.x] = v;
+      __syncthreads();
+      if (g0 > 0) return;
+      for (int k = 1; k < share; ++k) {
+        const float4 w = part[threadIdx.x + k * per];
+        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+      }
+    }
+    if (live && SDPA_IN_BOUNDS(s.t0 + group_div(g, rbk.row0 + row0 + r) < g.tokens, 524)) {
+      const float inv = sm_inv[r];
+      T out[4] = {Elem<T>::from_f32(v.x * inv), Elem<T>::from_f32(v.y * inv), Elem<T>::from_f32(v.z * inv),
+                  Elem<T>::from_f32(v.w * inv)};
+      T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + sm_y[r] + d;
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(out);
+      else *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(out);
     }
   }
 }
 
 template <typename T, int TM, int TN>
 cudaError_t merge_tn(const PagedAttn& a, const PagedWs& ws, int ctas, cudaStream_t st) {
+  // Few units are cut into many partials each (16 and more): then 8 rows and 32 columns a block, four threads an
+  // item.  Otherwise whole rows, 16 (or 32 of a 256-row unit) a block.
+  const int cols = a.g.Hv / 4;
+  const bool few = TM <= 64 && (int64_t)a.g.B * a.g.Nkv < ctas / 16;
+  const MergeCut cut = few ? MergeCut{8, 8} : MergeCut{TM == 256 ? 32 : 16, cols};
   cudaLaunchConfig_t cfg{};
-  // at most 8 blocks a unit: most of them find nothing to join
-  cfg.gridDim = dim3((unsigned)std::max(1, ctas - 1), (unsigned)std::min(8, (TM + kMergeWarps - 1) / kMergeWarps));
-  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.gridDim = dim3((unsigned)std::max(1, ctas - 1), (unsigned)((TM + cut.rows - 1) / cut.rows),
+                     (unsigned)((cols + cut.cols - 1) / cut.cols));
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, TM, TN>, a, ws, ctas);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, TM, TN>, a, ws, ctas, cut);
   if (e == cudaSuccess) count_launch(1);
   return e;
 }

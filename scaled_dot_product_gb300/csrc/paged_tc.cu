@@ -12,8 +12,8 @@
 //   warp 1      tensor products (one elected lane issues): S_X = Q_X K^T, O_X += P_X V with P
 //               read from tensor memory.  Rows of V that no box brought (past the sequence's keys,
 //               below every window) it sets to zero first, since 0 x NaN is not 0
-//   warps 2-3   query rows of the next unit (16-byte asynchronous copies: packed rows of a ragged
-//               batch need not start at a multiple of the box TMA would copy)
+//               box i.  The next unit's query rows come by TMA too where the group divides 128
+//   warps 2-3   query rows by 16-byte asynchronous copies for the other groups
 //   warps 4-7   softmax of tile 0, one thread per row; warps 8-11 softmax of tile 1
 //
 // Running maxima move only when they grow by more than 2^8.  Every wait is bounded: on expiry the
@@ -69,6 +69,7 @@ struct TcArgs {
   int box, boxes;                    // rows per box, boxes per tile
   int k_ds, k_dn, k_db, v_ds, v_dn, v_db;   // tensor-map dimension of slot / head / page
   float scale_log2, cap_in, cap_log2;
+  int q_tma;                         // query rows by TMA: boxes of one group's heads x 128 / group tokens
   int pre;                           // scale <= 0: scores are scaled before the maximum
   uint64_t wait_ns;
 };
@@ -100,7 +101,8 @@ __device__ __forceinline__ void box_rows(const TcArgs& t, const SeqInfo& s, cons
 
 template <int H, bool BF, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_tc_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                    const __grid_constant__ CUtensorMap tv,
                     const __grid_constant__ TcArgs t) {
   using C = Cfg<H>;
   using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < C::kStages; ++s) { mbar_init(b_full(s), 1); mbar_init(b_empty(s), 1); }
-    mbar_init(b_qready, 2);
+    mbar_init(b_qready, t.q_tma ? 1 : 2);
     mbar_init(b_qempty, 1);
     mbar_init(b_drain, 1);
     for (int x = 0; x < 2; ++x) {
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tmap(&tk);
       prefetch_tmap(&tv);
     }
-    int seq = 0;
+    int seq = 0, it = 0;
     bool ok = true;
     for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
       const int n = w.take(), kt0 = w.r.tile0 + w.tile;
@@ -207,6 +209,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int id = page_of(0);
       ok = load(false, 0, id);
+      if (ok && t.q_tma) {
+        // the previous unit's last S products have read its query tiles; rows of the box behind the
+        // unit's belong to other rows and are masked
+        if (it > 0 && !(ok = wait_all(b_qempty, (it - 1) & 1))) break;
+        const int nx = w.r.rows > kBM ? 2 : 1;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(b_qready, nx * C::kTile);
+          for (int x = 0; x < nx; ++x)
+            for (int r = 0; r < C::kRegions; ++r)
+              tma_load_4d(sQ + x * C::kTile + r * C::kRegionBytes, &tq, b_qready, 64 * r, w.kvh * g.group,
+                          w.s.t0 + group_div(g, w.r.row0 + x * kBM), 0);
+        }
+        __syncwarp();
+        ++it;
+      }
       for (int j = 0; j < n && ok; ++j) {
         const int next = page_of(j + 1);
         if constexpr (C::kAlias) {
@@ -221,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (__any_sync(0xffffffffu, !ok || *abortp)) {
       // some role gave up: let every copy already issued land before the CTA can exit
+      if (it > 0) mbar_wait_bounded(b_qready, (it - 1) & 1, nullptr, kDrainNs);
       for (int s = 0; s < C::kStages && s < seq; ++s) {
         const int last = s + ((seq - 1 - s) / C::kStages) * C::kStages;
         mbar_wait_bounded(b_full(s), (last / C::kStages) & 1, nullptr, kDrainNs);
@@ -374,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int chunk = lane % CPR, rin = lane / CPR;
     int it = 0;
     bool ok = true;
-    for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
+    for (Wk w(a, sh); ok && !t.q_tma && !w.done(); w.next(a)) {
       if (it > 0 && !(ok = wait_all(b_qempty, (it - 1) & 1))) break;
       ++it;
       if (x * kBM < w.r.rows) {
@@ -384,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = r0 + rin;
           const bool take = x * kBM + r < w.r.rows;
           const int pr = w.r.row0 + (take ? x * kBM + r : 0);
-          const int tok = pr / g.group;
+          const int tok = group_div(g, pr);
           const T* src = reinterpret_cast<const T*>(a.q.p) + a.q.off(0, w.kvh * g.group + pr - tok * g.group, w.s.t0 + tok) +
                          chunk * 8;
           const uint32_t d = dst + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
@@ -519,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = w.whole();
       const int live = min(32, w.r.rows - x * kBM - sub * 32);       // rows of this warp
       if (whole) {
-        const int tok = pr / g.group, h = w.kvh * g.group + pr - tok * g.group;
+        const int tok = group_div(g, pr), h = w.kvh * g.group + pr - tok * g.group;
         const float inv = row_scale<T>(a, h, m, l);
         const long long yrow = (long long)(reinterpret_cast<uintptr_t>(a.y.p) + (uintptr_t)(a.y.off(0, h, w.s.t0 + tok) * 2));
 #pragma unroll
@@ -605,7 +623,7 @@ uint64_t wait_limit_ns() {
 }
 
 template <int H, bool BF, bool CAP>
-cudaError_t launch_cap(const CUtensorMap& tk, const CUtensorMap& tv, const TcArgs& t, int ctas, cudaStream_t st) {
+cudaError_t launch_cap(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TcArgs& t, int ctas, cudaStream_t st) {
   using C = Cfg<H>;
   auto* kernel = paged_tc_kernel<H, BF, CAP>;
   // per device: set at every call (the attribute belongs to the current context)
@@ -615,16 +633,16 @@ cudaError_t launch_cap(const CUtensorMap& tk, const CUtensorMap& tv, const TcArg
   // with fewer registers at launch the softmax warps' request could never be met
   if (e == cudaSuccess && fa.numRegs < kLaunchRegs) e = cudaErrorLaunchOutOfResources;
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)ctas, kThreads, C::kSmem, st>>>(tk, tv, t);
+  kernel<<<(unsigned)ctas, kThreads, C::kSmem, st>>>(tq, tk, tv, t);
   count_launch(1);
   return cudaGetLastError();
 }
 
 template <int H>
-cudaError_t launch_h(bool bf, bool cap, const CUtensorMap& tk, const CUtensorMap& tv, const TcArgs& t, int ctas,
-                     cudaStream_t st) {
-  if (bf) return cap ? launch_cap<H, true, true>(tk, tv, t, ctas, st) : launch_cap<H, true, false>(tk, tv, t, ctas, st);
-  return cap ? launch_cap<H, false, true>(tk, tv, t, ctas, st) : launch_cap<H, false, false>(tk, tv, t, ctas, st);
+cudaError_t launch_h(bool bf, bool cap, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                     const TcArgs& t, int ctas, cudaStream_t st) {
+  if (bf) return cap ? launch_cap<H, true, true>(tq, tk, tv, t, ctas, st) : launch_cap<H, true, false>(tq, tk, tv, t, ctas, st);
+  return cap ? launch_cap<H, false, true>(tq, tk, tv, t, ctas, st) : launch_cap<H, false, false>(tq, tk, tv, t, ctas, st);
 }
 
 }  // namespace
@@ -664,13 +682,27 @@ cudaError_t launch_paged_tc(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaSt
       !tc_make_map(&tv, a.g.vp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, a.g.Hv, &t.v_ds, &t.v_dn, &t.v_db, t.box))
     return cudaErrorInvalidValue;
   const bool bf = dt == SDPA_BF16, cap = a.softcap > 0.f;
+  CUtensorMap tq{};
+  if (kBM % a.g.group == 0 && a.q.sh <= a.q.ss && a.q.ss < ((int64_t)1 << 38)) {
+    // (D, head, token): a box is 64 columns x one group's heads x 128 / group tokens, so its rows lie
+    // in packed order
+    const cuuint64_t dims[4] = {(cuuint64_t)a.g.H, (cuuint64_t)a.g.Nq, (cuuint64_t)a.g.tokens, 1};
+    const int64_t sh = a.g.Nq > 1 ? a.q.sh : a.g.H, ss = a.g.tokens > 1 ? a.q.ss : std::max<int64_t>(a.q.ss, sh * a.g.Nq);
+    const cuuint64_t strides[3] = {(cuuint64_t)sh * 2, (cuuint64_t)ss * 2, (cuuint64_t)ss * 2 * a.g.tokens};
+    const cuuint32_t box[4] = {64, (cuuint32_t)a.g.group, (cuuint32_t)(kBM / a.g.group), 1}, step[4] = {1, 1, 1, 1};
+    auto enc = tc_encode_fn();
+    t.q_tma = strides[2] < ((cuuint64_t)1 << 40) && enc &&
+              enc(&tq, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(a.q.p),
+                  dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  }
   cudaError_t e;
   if (a.g.H == 128) {
     *name = bf ? "paged_tc_bf16_h128" : "paged_tc_f16_h128";
-    e = launch_h<128>(bf, cap, tk, tv, t, ctas, st);
+    e = launch_h<128>(bf, cap, tq, tk, tv, t, ctas, st);
   } else {
     *name = bf ? "paged_tc_bf16_h64" : "paged_tc_f16_h64";
-    e = launch_h<64>(bf, cap, tk, tv, t, ctas, st);
+    e = launch_h<64>(bf, cap, tq, tk, tv, t, ctas, st);
   }
   return e == cudaSuccess ? launch_paged_merge(a, dt, t.ws, ctas, kTM, st) : e;
 }
