@@ -39,7 +39,8 @@ constexpr int kProducts = 128;       // threads of the product warps
 constexpr int kThreads = kProducts + 32;
 constexpr int kTN = 64;
 constexpr int kCtasPerSm = 2;
-constexpr int kMinShare = 2;
+constexpr int kOV = 1;                // a unit's cost beside its tiles, in tiles
+constexpr int kMinShare = 3;
 constexpr float kRescale = 8.f;      // log2 units a maximum may grow before o is rescaled
 
 template <int H, int WM>
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                      const __grid_constant__ MmaArgs args) {
   using C = Cfg<H, WM>;
   using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-  using Wk = Walk<C::TM, kTN>;
+  using Wk = Walk<C::TM, kTN, kOV>;
   constexpr int WK = C::WK, TM = C::TM, KW = C::KW, NT = KW / 8;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     fence_mbar_init();
   }
-  const Share sh = find_share<TM, kTN, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
+  const Share sh = find_share<TM, kTN, kOV, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
   if (threadIdx.x == 0) {
     if (cta == 0) ws.start[ctas].b = sh.active;
     if (cta < sh.active) ws.start[cta] = sh.at;
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (sh.count == 0) return;
   __syncthreads();
   Wk w(a, sh);
+  if (w.done()) return;
 
   if (warp == kProducts / 32) {
     // ================================================================ producer

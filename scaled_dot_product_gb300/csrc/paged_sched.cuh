@@ -2,10 +2,12 @@
 //
 // A unit is TM consecutive packed rows (row r = token * group + head of the group) of one
 // (sequence, kv head); its cost is the number of TN-key tiles that some of its rows admits (at
-// least one, so that rows with no key are written too).  All units' tiles, laid end to end
-// (sequence, row block, kv head, tile), are dealt to the CTAs in equal contiguous shares, so
-// ragged lengths, few rows over many keys and many rows over few keys all fill the GPU alike,
-// and a CTA meets at most two units that it does not hold whole.  Those leave partial results
+// least one, so that rows with no key are written too) and OV more for its query rows and its
+// results, in tiles' time.  All units, laid end to end (sequence, row block, kv head, tile), are
+// dealt to the CTAs in equal contiguous shares of that cost, so ragged lengths, few rows over many
+// keys and many rows over few keys all fill the GPU alike, and a CTA meets at most two units that
+// it does not hold whole.  (Without OV, the CTA that gets the first, shortest row blocks of a
+// causal prompt had 40 units of one or two tiles and took twice as long as the others.)  Those leave partial results
 // (m, l, unnormalised o) in two slots per CTA, which a second kernel joins.  The lengths stay on
 // the device: every CTA finds its share by summing the costs of all sequences.
 #pragma once
@@ -80,28 +82,20 @@ __device__ __forceinline__ void row_keys(const PagedAttn& a, const SeqInfo& s, i
   lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
 }
 
-// Sum of the tile costs of sequence b's row blocks (one kv head), by one thread.
-template <int TM, int TN>
-__device__ __forceinline__ int seq_cost(const PagedAttn& a, const SeqInfo& s) {
-  int c = 0;
-  const int n = row_blocks(a, s, TM);
-  for (int rb = 0; rb < n; ++rb) c += row_block<TM, TN>(a, s, rb).tiles;
-  return c;
-}
-
 struct Share {
-  int64_t begin, count;    // the CTA's tiles of the whole
+  int64_t count;           // the CTA's part of the whole cost, from its first unit's tile on
   ShareStart at;
   int active;              // CTAs that have a share
 };
 
 // Finds the share of CTA `cta` among `ctas`; called by all NT threads of the block.  min_share:
-// fewest tiles worth a CTA.
-template <int TM, int TN, int NT>
+// least cost worth a CTA.
+template <int TM, int TN, int OV, int NT>
 __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int ctas, int min_share, int* status) {
   constexpr int kW = NT / 32;
   __shared__ long long sh_sum[kW + 1];
   __shared__ ShareStart sh_at;
+  __shared__ int sh_back;          // cost before begin_at that counts to the CTA's first unit
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool bad = false;
 
@@ -111,7 +105,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
     s = SeqInfo{0, 0, 0};
     if (b < a.g.B) s = seq_info(a.g, b, bad);
     const int nrb = row_blocks(a, s, TM);
-    if (nrb == 1) c = row_block<TM, TN>(a, s, 0).tiles;
+    if (nrb == 1) c = row_block<TM, TN>(a, s, 0).tiles + OV;
     unsigned many = __ballot_sync(0xffffffffu, nrb > 1);
     while (many) {
       const int src = __ffs(many) - 1;
@@ -122,7 +116,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
       t.T = __shfl_sync(0xffffffffu, s.T, src);
       const int n = row_blocks(a, t, TM);
       long long part = 0;
-      for (int rb = lane; rb < n; rb += 32) part += row_block<TM, TN>(a, t, rb).tiles;
+      for (int rb = lane; rb < n; rb += 32) part += row_block<TM, TN>(a, t, rb).tiles + OV;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
       if (lane == src) c = part;
@@ -150,7 +144,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
   r.active = total >= (long long)ctas * min_share ? ctas : max(1, (int)total / min_share);
   if (total == 0) r.active = 0;
   r.at = ShareStart{a.g.B, 0, 0, 0};
-  r.begin = r.count = 0;
+  r.count = 0;
   if (cta >= r.active) return r;
   // total / active tiles each, the first total % active CTAs one more (32-bit divisions where
   // they do: a 64-bit one takes a microsecond's fraction that short calls feel)
@@ -162,10 +156,10 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
     each = total / r.active;
     more = total - each * r.active;
   }
-  r.begin = cta * each + min((long long)cta, more);
+  const long long begin_at = cta * each + min((long long)cta, more);
   r.count = each + (cta < more ? 1 : 0);
 
-  // the sequence that holds tile r.begin
+  // the sequence that holds begin_at
   long long before = 0;
   for (int base = 0; base < a.g.B; base += NT) {
     if (a.g.B > NT) mine = cost_of(base + (int)threadIdx.x, s);
@@ -184,8 +178,8 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
       all += sh_sum[w];
     }
     const long long end = off + v, begin = end - mine;
-    // exactly one warp holds the tile; its lanes find the row block
-    const bool here = r.begin >= begin && r.begin < end;
+    // exactly one warp holds it; its lanes find the row block
+    const bool here = begin_at >= begin && begin_at < end;
     const unsigned who = __ballot_sync(0xffffffffu, here);
     if (who) {
       const int src = __ffs(who) - 1;
@@ -194,20 +188,22 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
       t.n = __shfl_sync(0xffffffffu, s.n, src);
       t.T = __shfl_sync(0xffffffffu, s.T, src);
       const int n = row_blocks(a, t, TM);
-      long long o = r.begin - __shfl_sync(0xffffffffu, begin, src);
+      long long o = begin_at - __shfl_sync(0xffffffffu, begin, src);
       for (int rb0 = 0; rb0 < n; rb0 += 32) {
-        const int tiles = rb0 + lane < n ? row_block<TM, TN>(a, t, rb0 + lane).tiles : 0;
-        long long c = (long long)tiles * a.g.Nkv;
+        const int cost = rb0 + lane < n ? row_block<TM, TN>(a, t, rb0 + lane).tiles + OV : 0;
+        long long c = (long long)cost * a.g.Nkv;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const long long u = __shfl_up_sync(0xffffffffu, c, d);
           if (lane >= d) c += u;
         }
-        const long long lo = c - (long long)tiles * a.g.Nkv;
+        const long long lo = c - (long long)cost * a.g.Nkv;
         if (o >= lo && o < c) {
-          // within one row block: fewer than Nkv * tiles, which fits 32 bits with room
-          const unsigned in = (unsigned)(o - lo), k = in / (unsigned)tiles;
-          sh_at = ShareStart{base + warp * 32 + src, rb0 + lane, (int)k, (int)(in - k * (unsigned)tiles)};
+          // within one row block: fewer than Nkv * cost, which fits 32 bits with room
+          const unsigned in = (unsigned)(o - lo), k = in / (unsigned)cost;
+          const int off = (int)(in - k * (unsigned)cost);
+          sh_at = ShareStart{base + warp * 32 + src, rb0 + lane, (int)k, max(0, off - OV)};
+          sh_back = min(off, OV);
         }
         const long long block = __shfl_sync(0xffffffffu, c, 31);
         if (o < block) break;
@@ -216,39 +212,43 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
     }
     __syncthreads();
     before += all;
-    if (before > r.begin) break;
+    if (before > begin_at) break;
   }
   r.at = sh_at;
+  // a share that starts in a unit's OV has the unit's first tile; one that starts behind it goes on
+  // from that tile
+  if (sh_at.tile == 0) r.count += sh_back;
   return r;
 }
 
-// Walks a share unit by unit.
-template <int TM, int TN>
+// Walks a share unit by unit.  The CTA takes the tiles [tile, tile + take()) of the present unit.
+template <int TM, int TN, int OV>
 struct Walk {
-  int64_t left;
+  int64_t left;            // cost left, from the present unit's tile on (its OV included if tile = 0)
   int b, rb, kvh, tile;
   SeqInfo s;
   RowBlock r;
-  bool first;
   __device__ __forceinline__ Walk(const PagedAttn& a, const Share& sh)
-      : left(sh.count), b(sh.at.b), rb(sh.at.rb), kvh(sh.at.kvh), tile(sh.at.tile), first(true) {
-    if (left > 0) load(a);
-  }
-  __device__ __forceinline__ void load(const PagedAttn& a) {
-    bool bad = false;
-    s = seq_info(a.g, b, bad);
-    r = row_block<TM, TN>(a, s, rb);
+      : left(sh.count), b(sh.at.b), rb(sh.at.rb), kvh(sh.at.kvh), tile(sh.at.tile) {
+    if (left > 0) {
+      bool bad = false;
+      s = seq_info(a.g, b, bad);
+      r = row_block<TM, TN>(a, s, rb);
+    }
+    if (take() <= 0) left = 0;
   }
   __device__ __forceinline__ bool done() const { return left <= 0; }
-  // tiles of the present unit that belong to this CTA
-  __device__ __forceinline__ int take() const { return (int)min((int64_t)(r.tiles - tile), left); }
+  __device__ __forceinline__ int take() const { return (int)min((int64_t)(r.tiles - tile), left - (tile == 0 ? OV : 0)); }
   __device__ __forceinline__ bool begins() const { return tile == 0; }
   __device__ __forceinline__ bool ends() const { return tile + take() == r.tiles; }
   __device__ __forceinline__ bool whole() const { return begins() && ends(); }
   __device__ __forceinline__ void next(const PagedAttn& a) {
-    left -= take();
+    left -= take() + (tile == 0 ? OV : 0);
     tile = 0;
-    if (left <= 0) return;
+    if (left <= OV) {      // what is left is in the next unit's OV, and that unit is another CTA's
+      left = 0;
+      return;
+    }
     if (++kvh < a.g.Nkv) return;
     kvh = 0;
     if (++rb < row_blocks(a, s, TM)) {

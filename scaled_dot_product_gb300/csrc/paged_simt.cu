@@ -18,7 +18,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kTN = 64;          // keys per tile of the schedule
 constexpr int kCtasPerSm = 4;
-constexpr int kMinShare = 2;     // tiles
+constexpr int kOV = 1;                // a unit's cost beside its tiles, in tiles
+constexpr int kMinShare = 2;
 
 template <typename T, int LPK, int NV, int TM>
 __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a, const PagedWs ws) {
@@ -30,7 +31,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a,
   __shared__ float sm_m[KPI][TM], sm_l[KPI][TM];
   const Paged& g = a.g;
   const int ctas = gridDim.x, cta = blockIdx.x;
-  const Share sh = find_share<TM, kTN, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
+  const Share sh = find_share<TM, kTN, kOV, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
   if (threadIdx.x == 0) {
     if (cta == 0) ws.start[ctas].b = sh.active;
     if (cta < sh.active) ws.start[cta] = sh.at;
@@ -39,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a,
   const int grp = threadIdx.x / LPK, t = threadIdx.x % LPK;
   const float cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
 
-  for (Walk<TM, kTN> w(a, sh); !w.done(); w.next(a)) {
+  for (Walk<TM, kTN, kOV> w(a, sh); !w.done(); w.next(a)) {
     const int nr = w.r.rows;
     float q[TM][NV * V], m[TM], l[TM], acc[TM][NV * V];
     int lo[TM], hi[TM];

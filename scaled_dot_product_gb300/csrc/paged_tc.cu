@@ -38,7 +38,8 @@ using namespace ptx;
 
 constexpr int kBM = 128, kTM = 256, kTN = 128;
 constexpr int kThreads = 384;
-constexpr int kMinShare = 4;
+constexpr int kOV = 2;                // a unit's cost beside its tiles, in tiles
+constexpr int kMinShare = 6;
 // Register split: the control warpgroup shrinks to kCtlRegs, the softmax warpgroups grow to
 // kSmxRegs; the sum stays within the launch's kThreads x kLaunchRegs, which the host checks.
 constexpr int kLaunchRegs = 168, kCtlRegs = 88, kSmxRegs = 208;
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ TcArgs t) {
   using C = Cfg<H>;
   using T = typename std::conditional<BF, __nv_bfloat16, __half>::type;
-  using Wk = Walk<kTM, kTN>;
+  using Wk = Walk<kTM, kTN, kOV>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&tmem_sh), 512);
     tmem_relinquish();
   }
-  const Share sh = find_share<kTM, kTN, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
+  const Share sh = find_share<kTM, kTN, kOV, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
   if (threadIdx.x == 0) {
     if (cta == 0) t.ws.start[ctas].b = sh.active;
     if (cta < sh.active) t.ws.start[cta] = sh.at;
