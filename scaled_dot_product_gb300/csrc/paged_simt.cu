@@ -17,16 +17,18 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTN = 64;          // keys per tile of the schedule
-constexpr int kCtasPerSm = 4;
+
+constexpr int log2i(int x) { return x <= 1 ? 0 : 1 + log2i(x / 2); }
+constexpr int kCtasPerSm = 3;
 constexpr int kOV = 1;                // a unit's cost beside its tiles, in tiles
 constexpr int kMinShare = 2;
 
 template <typename T, int LPK, int NV, int TM>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a, const PagedWs ws) {
+__global__ void __launch_bounds__(kThreads, NV == 1 ? kCtasPerSm : 2) paged_simt_kernel(const PagedAttn a, const PagedWs ws) {
   constexpr int V = Elem<T>::kVec;
   constexpr int KPI = kThreads / LPK;
   constexpr int HM = LPK * NV * V;       // widest head
-  constexpr int kUnroll = 2;
+  constexpr int kUnroll = NV == 1 ? 4 : 2;
   extern __shared__ float smem[];        // [KPI][TM][HM]
   __shared__ float sm_m[KPI][TM], sm_l[KPI][TM];
   const Paged& g = a.g;
@@ -39,11 +41,18 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a,
   pdl_launch_dependents();
   const int grp = threadIdx.x / LPK, t = threadIdx.x % LPK;
   const float cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
+  // Scores of a step: score r * kUnroll + u of row r and key u.  After SC exchanges a lane holds the sums
+  // of R of them, of one row, from key my_u on; UB exchanges span the lanes of a row.
+  constexpr int NS = TM * kUnroll, SC = log2i(NS) < log2i(LPK) ? log2i(NS) : log2i(LPK), R = NS >> SC;
+  constexpr int UB = log2i(kUnroll) - log2i(R);
+  static_assert(R <= kUnroll, "a lane's scores belong to one row");
+  const int first = (t >> (log2i(LPK) - SC)) << (log2i(NS) - SC);
+  const int my_row = first / kUnroll, my_u = first % kUnroll;
+  auto lane_of = [](int score) { return (score >> (log2i(NS) - SC)) << (log2i(LPK) - SC); };
 
   for (Walk<TM, kTN, kOV> w(a, sh); !w.done(); w.next(a)) {
     const int nr = w.r.rows;
-    float q[TM][NV * V], m[TM], l[TM], acc[TM][NV * V];
-    int lo[TM], hi[TM];
+    float q[TM][NV * V], acc[TM][NV * V];
 #pragma unroll
     for (int r = 0; r < TM; ++r) {
       const int pr = w.r.row0 + min(r, nr - 1);
@@ -55,52 +64,59 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a,
         const uint4 u = c < g.H ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
         unpack16<T>(u, q[r] + n * V);
       }
-      row_keys(a, w.s, pr, lo[r], hi[r]);
-      m[r] = -INFINITY;
-      l[r] = 0.f;
 #pragma unroll
       for (int e = 0; e < NV * V; ++e) acc[r][e] = 0.f;
     }
+    // this lane's row of the scores: its keys, running maximum and part of the sum
+    int lo, hi;
+    row_keys(a, w.s, w.r.row0 + min(my_row, nr - 1), lo, hi);
+    float m = -INFINITY, l = 0.f;
     const int64_t j_tile = (int64_t)(w.r.tile0 + w.tile) * kTN;
     const int64_t j_begin = max(j_tile, (int64_t)w.r.lo);      // pages below a window are not read
     const int64_t j_end = min((int64_t)w.r.hi + 1, j_tile + (int64_t)w.take() * kTN);
     const int32_t* table = g.table + (int64_t)w.b * g.table_stride;
 
-    for (int64_t base = j_begin; base < j_end; base += KPI * kUnroll) {
-      uint4 kv[kUnroll][NV], vv[kUnroll][NV];
-      int jj[kUnroll];
-      int id[kUnroll], slot[kUnroll];
+    // keys of one step: those at base + grp + u * KPI.  Their rows are loaded one step ahead, the ids of
+    // their pages two.
+    constexpr int kStep = KPI * kUnroll;
+    auto load_ids = [&](int64_t base, int* id) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int64_t j = base + grp + u * KPI;
-        jj[u] = j < j_end ? (int)j : -1;
-        id[u] = -1;
-        slot[u] = 0;
-        if (jj[u] >= 0) {
-          const int pg = page_div(g, jj[u]);
-          slot[u] = jj[u] - pg * g.page_size;
-          id[u] = table[pg];
-          if (id[u] < 0 || id[u] >= g.num_pages) {
-            atomicOr(&g_paged_status, kPagedBadPage);
-            id[u] = -1;                    // read as zeros
-          }
-        }
+        id[u] = j < j_end ? table[page_div(g, (int)j)] : -1;
       }
+    };
+    auto load_rows = [&](int64_t base, const int* id, uint4 (&kv)[kUnroll][NV], uint4 (&vv)[kUnroll][NV]) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const T* kr = reinterpret_cast<const T*>(g.kp.p) + g.kp.off(id[u], w.kvh, slot[u]);
-        const T* vr = reinterpret_cast<const T*>(g.vp.p) + g.vp.off(id[u], w.kvh, slot[u]);
+        const int64_t j = base + grp + u * KPI;
+        const int key = (int)min(j, (int64_t)g.cap), slot = key - page_div(g, key) * g.page_size;
+        bool take = j < j_end;
+        if (take && (unsigned)id[u] >= (unsigned)g.num_pages) {
+          atomicOr(&g_paged_status, kPagedBadPage);
+          take = false;                    // read as zeros
+        }
+        take = take && SDPA_IN_BOUNDS(key < g.cap && slot < g.page_size, 521);
+        const T* kr = reinterpret_cast<const T*>(g.kp.p) + g.kp.off(id[u], w.kvh, slot);
+        const T* vr = reinterpret_cast<const T*>(g.vp.p) + g.vp.off(id[u], w.kvh, slot);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
           const int c = (n * LPK + t) * V;
-          kv[u][n] = vv[u][n] = make_uint4(0u, 0u, 0u, 0u);
-          if (id[u] >= 0 && SDPA_IN_BOUNDS(jj[u] < g.cap && slot[u] < g.page_size, 521)) {
-            if (c < g.H) kv[u][n] = __ldg(reinterpret_cast<const uint4*>(kr + c));
-            if (c < g.Hv) vv[u][n] = __ldg(reinterpret_cast<const uint4*>(vr + c));
-          }
+          kv[u][n] = take && c < g.H ? __ldg(reinterpret_cast<const uint4*>(kr + c)) : make_uint4(0u, 0u, 0u, 0u);
+          vv[u][n] = take && c < g.Hv ? __ldg(reinterpret_cast<const uint4*>(vr + c)) : make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      float s[TM][kUnroll];
+    };
+    int id[kUnroll];
+    load_ids(j_begin, id);
+#pragma unroll 1
+    for (int64_t base = j_begin; base < j_end; base += kStep) {
+      uint4 kv[kUnroll][NV], vv[kUnroll][NV];
+      load_rows(base, id, kv, vv);
+      load_ids(base + kStep, id);
+      // every lane's part of the step's TM x kUnroll scores, then their sums dealt to the lanes: at each
+      // exchange a lane keeps the half of the scores that its lane bit names
+      float s[NS];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         float kf[NV * V];
@@ -111,45 +127,78 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedAttn a,
           float dot = 0.f;
 #pragma unroll
           for (int e = 0; e < NV * V; ++e) dot = fmaf(q[r][e], kf[e], dot);
-#pragma unroll
-          for (int o = LPK / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-          if (a.softcap > 0.f) dot = a.softcap * tanhf(dot * cap_in);
-          else dot *= a.scale;
-          s[r][u] = (jj[u] >= lo[r] && jj[u] <= hi[r]) ? dot * kLog2e : -INFINITY;
+          s[r * kUnroll + u] = dot;
         }
       }
 #pragma unroll
-      for (int r = 0; r < TM; ++r) {
-        float mx = m[r];
+      for (int k = 0; k < SC; ++k) {
+        const int o = LPK >> (k + 1), half = NS >> (k + 1);
+        const bool up = t & o;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) mx = fmaxf(mx, s[r][u]);
-        if (mx == -INFINITY) continue;
-        const float corr = exp2f(m[r] - mx);
-        l[r] *= corr;
-#pragma unroll
-        for (int e = 0; e < NV * V; ++e) acc[r][e] *= corr;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          if (s[r][u] == -INFINITY) continue;      // also keeps a masked key's value out
-          const float p = exp2f(s[r][u] - mx);
-          l[r] += p;
-#pragma unroll
-          for (int n = 0; n < NV; ++n) {
-            float vf[V];
-            unpack16<T>(vv[u][n], vf);
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[r][n * V + e] = fmaf(p, vf[e], acc[r][n * V + e]);
-          }
+        for (int i = 0; i < half; ++i) {
+          const float give = up ? s[i] : s[i + half];
+          s[i] = (up ? s[i + half] : s[i]) + __shfl_xor_sync(0xffffffffu, give, o);
         }
-        m[r] = mx;
+      }
+#pragma unroll
+      for (int o = LPK >> (SC + 1); o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < R; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int64_t j = base + grp + (my_u + i) * KPI;
+        float v = a.softcap > 0.f ? a.softcap * tanhf(s[i] * cap_in) : s[i] * a.scale;
+        v = (j < j_end && j >= lo && j <= hi) ? v * kLog2e : -INFINITY;
+        s[i] = v;
+        mx = fmaxf(mx, v);
+      }
+#pragma unroll
+      for (int o = 0; o < UB; ++o) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1 << (log2i(LPK) - SC + o)));
+      float corr = 1.f;
+      const bool need = mx > m;
+      if (need) {
+        corr = exp2f(m - mx);
+        m = mx;
+        l *= corr;
+      }
+      if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+        for (int r = 0; r < TM; ++r) {
+          const float c = __shfl_sync(0xffffffffu, corr, lane_of(r * kUnroll), LPK);
+#pragma unroll
+          for (int e = 0; e < NV * V; ++e) acc[r][e] *= c;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        s[i] = s[i] == -INFINITY ? 0.f : exp2f(s[i] - m);
+        l += s[i];
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        float vf[NV * V];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) unpack16<T>(vv[u][n], vf + n * V);
+#pragma unroll
+        for (int r = 0; r < TM; ++r) {
+          const float p = __shfl_sync(0xffffffffu, s[(r * kUnroll + u) & (R - 1)], lane_of(r * kUnroll + u), LPK);
+#pragma unroll
+          for (int e = 0; e < NV * V; ++e) acc[r][e] = fmaf(p, vf[e], acc[r][e]);
+        }
       }
     }
+#pragma unroll
+    for (int o = 0; o < UB; ++o) l += __shfl_xor_sync(0xffffffffu, l, 1 << (log2i(LPK) - SC + o));
 
     // join the lane groups
     __syncthreads();
+    if (t == lane_of(my_row * kUnroll)) {
+      sm_m[grp][my_row] = m;
+      sm_l[grp][my_row] = l;
+    }
 #pragma unroll
     for (int r = 0; r < TM; ++r) {
-      if (t == 0) { sm_m[grp][r] = m[r]; sm_l[grp][r] = l[r]; }
 #pragma unroll
       for (int n = 0; n < NV; ++n)
 #pragma unroll

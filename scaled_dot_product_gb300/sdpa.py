@@ -582,6 +582,8 @@ def _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, e
 def _like(t: Optional[torch.Tensor], ref: torch.Tensor, name: str) -> torch.Tensor:
     """t checked against ref's type and shape, or a new tensor of ref's shape."""
     if t is None:
+        if ref.is_contiguous():
+            return torch.empty_like(ref)       # the same tensor, allocated with less argument parsing
         return torch.empty(ref.shape, dtype=ref.dtype, device=ref.device)
     _typed(t, name, ref.dtype, ref.shape)
     return t
@@ -735,7 +737,7 @@ def sdpa_paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     _typed(q, "q", dt, (tokens, Nq, k_pages.shape[3]))
     shape = (tokens, Nq, v_pages.shape[3])
     if y is None:
-        y = torch.empty(shape, dtype=dt, device=q.device)
+        y = torch.empty_like(q) if q.shape == shape and q.is_contiguous() else torch.empty(shape, dtype=dt, device=q.device)
     _typed(y, "y", dt, shape)
     L = lib()
     if workspace is None:
