@@ -1,7 +1,8 @@
 """Builds libsdpa.so in-tree with nvcc for sm_103a (no cmake).
 
 Each translation unit under csrc/ is compiled in parallel to an object in _build/,
-then linked into scaled_dot_product_gb300/libsdpa.so.  Up-to-date objects are reused.
+then linked into scaled_dot_product_gb300/libsdpa.so; csrc/binding.cpp, the native part of the
+Python binding, becomes scaled_dot_product_gb300/_binding.so.  Up-to-date objects are reused.
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -42,6 +44,38 @@ def _stale(target: str, deps) -> bool:
 LIB_BOUNDS = os.path.join(PKG, "libsdpa_bounds.so")
 
 
+# The marshalling module of sdpa.py (Python's and torch's C++ headers; no CUDA).
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
+
+
+def build_binding(verbose: bool = False) -> str:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    # built against one interpreter and one torch: a stamp names them
+    stamp = os.path.join(BUILD, "binding.stamp")
+    what = f"{sys.version}\n{torch.__version__}\n"
+    old = open(stamp).read() if os.path.exists(stamp) else ""
+    if old == what and not _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "sdpa.h"), __file__]):
+        return BINDING
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", BINDING_SRC, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"), "-L", os.path.join(root, "lib"),
+           "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(what)
+    return BINDING
+
+
 def build(verbose: bool = False, extra_flags=None, bounds_check: bool = False) -> str:
     nvcc = _nvcc()
     build_dir = BUILD + ("_bounds" if bounds_check else "")
@@ -65,8 +99,10 @@ def build(verbose: bool = False, extra_flags=None, bounds_check: bool = False) -
                 print(r.stderr, file=sys.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(sources), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(sources) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(compile_one, sources))
+        binding.result()
     if _stale(lib_path, objs):
         tmp = lib_path + f".tmp{os.getpid()}"
         cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"]

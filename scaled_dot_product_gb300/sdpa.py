@@ -1,16 +1,17 @@
 """Python binding of libsdpa.so (argument marshalling only).
 
 The functions here carry the names of the C entry points declared in include/sdpa.h and
-do nothing but turn torch tensors into the C structs, pick the caller's current CUDA
-stream, and raise on a non-zero status.  Every step of the computation runs in the
+do nothing but turn torch tensors into the C structs (the query/key norm and the paged calls
+through the native csrc/binding.cpp), pick the caller's current CUDA stream, and raise on a
+non-zero status.  Every step of the computation runs in the
 library's CUDA kernels; there is no fallback of any kind: if libsdpa.so is missing or
 fails to load, every call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 from typing import Optional, Tuple
 
 import torch
@@ -451,142 +452,73 @@ def sdpa_rotary(x: torch.Tensor, cos_cache: torch.Tensor, sin_cache: torch.Tenso
 
 # ----------------------------------------------------------------------------------------
 # Query/key norm and paged cache.  Single-token calls are shorter on the GPU than their
-# marshalling, so these fill their structs in one struct.pack and take strides directly
-# instead of building view tensors.
+# marshalling in Python (2 to 12 us against 12 to 16), so csrc/binding.cpp fills their structs.
 # ----------------------------------------------------------------------------------------
 
-_NORM_FIELDS = struct.Struct("@7i4x4q4qPPf4xPPqPii")
-_PAGED_FIELDS = struct.Struct("@11i4x4q4qPqPPPPqiiiffiqPi4x")
-assert _NORM_FIELDS.size == ctypes.sizeof(sdpa_qk_norm_params)
-assert _PAGED_FIELDS.size == ctypes.sizeof(sdpa_paged_params)
+BINDING_PATH = os.path.join(_PKG, "_binding.so")
+_binding = None
+_entries: dict = {}
 
 
-def _place(stream, tensors: tuple, names: str) -> Tuple[int, int]:
-    """(device, stream handle) of a call.  Every given tensor must be on that CUDA device; the
-    default stream is the device's current one."""
-    d = tensors[0].get_device()
-    for i, t in enumerate(tensors):
-        if t is not None and (d < 0 or t.get_device() != d):
-            raise ValueError(f"{names.split()[i]} must be a CUDA tensor on the device of {names.split()[0]}, "
-                             f"got {t.device} and {tensors[0].device}")
-    if stream is None:
-        return d, torch._C._cuda_getCurrentRawStream(d)
-    return d, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _native():
+    """(marshalling module, addresses of the library's entry points); raises if it is missing."""
+    global _binding
+    if _binding is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is not built: run `python -c 'import __graft_entry__ as g; g.build()'` "
+                               f"(there is no fallback)")
+        spec = importlib.util.spec_from_file_location("_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding = module
+    L = lib()
+    if _entries.get("library") is not L:
+        _entries.update({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in EXPORTED}, library=L)
+    return _binding, _entries
 
 
-def _call(device: int, fn, *args):
-    """fn(*args) with `device` current; raises on a non-zero status."""
-    if torch.cuda.current_device() != device:
-        with torch.cuda.device(device):
-            rc = fn(*args)
-    else:
-        rc = fn(*args)
-    if rc:
-        _check(rc)
+def _here(t: torch.Tensor, stream) -> bool:
+    """Whether a call on t's device takes the current device and its current stream."""
+    d = t.get_device()
+    return stream is None and (d < 0 or d == torch.cuda.current_device())
 
 
-def _keep_for(stream, device: int, handle: int, *allocated):
-    """Memory the binding allocated for a call on a stream the caller named belongs to that stream
-    until the call's work is done."""
-    if stream is None or handle == torch._C._cuda_getCurrentRawStream(device):
-        return
-    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=device)
-    for t in allocated:
-        if t is not None and t.numel():
-            t.record_stream(s)
+def _handle(t: torch.Tensor) -> int:
+    d = t.get_device()
+    return torch._C._cuda_getCurrentRawStream(d) if d >= 0 else 0
 
 
-def _typed(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape=None):
-    if t is None:
-        return
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _elsewhere(first: torch.Tensor, stream, call, allocated) -> object:
+    """call(handle) with first's device current, on `stream` (default: that device's current one).
+    Tensors the binding allocated for it belong to that stream until its work is done."""
+    with torch.cuda.device(first.device):
+        here = _handle(first)
+        handle = here if stream is None else _stream(stream)
+        r = call(handle)
+        if handle != here:
+            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=first.device)
+            for t in allocated:
+                if t is not None and t.numel():
+                    t.record_stream(s)
+    return r
 
 
-def _flat_ptr(t: Optional[torch.Tensor], name: str) -> int:
-    if t is None:
-        return 0
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _raised(r):
+    if type(r) is int:
+        _check(r)
+    return r
 
 
-def _element_type(t: torch.Tensor) -> int:
-    dt = _DTYPES.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"unsupported type {t.dtype}")
-    return dt
+def _new(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _head_view(t: torch.Tensor, D: int, name: str) -> Tuple[int, int, int, int]:
-    """(pointer, batch stride, head stride, row stride) of a rank-4 (B, N, S, D) or rank-3
-    (B, S, N*D) tensor."""
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    if len(st) == 4:
-        return t.data_ptr(), st[0], st[1], st[2]
-    return t.data_ptr(), st[0], D, st[1]
-
-
-def _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim, interleaved,
-                 num_heads, kv_num_heads):
-    """(params, head size, position ids to keep) of the query/key norm."""
-    if q.dim() == 4:
-        B, Nq, S, D = q.shape
-        if k.dim() != 4 or k.shape[0] != B or k.shape[2] != S or k.shape[3] != D:
-            raise ValueError(f"k {tuple(k.shape)} does not match q {tuple(q.shape)}")
-        Nkv = k.shape[1]
-    elif q.dim() == 3 and k.dim() == 3:
-        if not (num_heads and kv_num_heads):
-            raise ValueError("rank-3 inputs need num_heads and kv_num_heads")
-        Nq, Nkv = num_heads, kv_num_heads
-        B, S, wide = q.shape
-        D = wide // Nq
-        if wide != D * Nq or k.shape != (B, S, D * Nkv):
-            raise ValueError(f"{Nq} and {Nkv} heads do not fit q {tuple(q.shape)} and k {tuple(k.shape)}")
-    else:
-        raise ValueError("q and k must both be rank 3 (B, S, N*D) or both rank 4 (B, N, S, D)")
-    dt = q.dtype
-    _typed(k, "k", dt)
-    _typed(q_weight, "q_weight", dt, (D,))
-    _typed(k_weight, "k_weight", dt, (D,))
-    rotary_dim = int(rotary_dim)
-    rows, pos = 0, None
-    if cos_cache is not None:
-        half = (rotary_dim or D) // 2
-        if position_ids is None:
-            _typed(cos_cache, "cos_cache", dt, (B, S, half))
-            rows = B * S
-        else:
-            _typed(cos_cache, "cos_cache", dt, (cos_cache.shape[0], half))
-            pos = position_ids
-            if pos.dtype is not torch.int64 or pos.shape != (B, S) or not pos.is_contiguous():
-                pos = pos.to(torch.int64).expand(B, S).contiguous()
-            rows = cos_cache.shape[0]
-        if sin_cache is None:
-            raise ValueError("cos_cache and sin_cache must be given together")
-        _typed(sin_cache, "sin_cache", dt, cos_cache.shape)
-    elif sin_cache is not None or position_ids is not None:
-        raise ValueError("sin_cache or position_ids without cos_cache")
-    p = sdpa_qk_norm_params.from_buffer_copy(_NORM_FIELDS.pack(
-        _NORM_FIELDS.size, B, Nq, Nkv, S, D, _element_type(q), *_head_view(q, D, "q"), *_head_view(k, D, "k"),
-        _flat_ptr(q_weight, "q_weight"), _flat_ptr(k_weight, "k_weight"), eps, _flat_ptr(cos_cache, "cos_cache"),
-        _flat_ptr(sin_cache, "sin_cache"), rows, 0 if pos is None else pos.data_ptr(), rotary_dim,
-        1 if interleaved else 0))
-    return p, D, pos
-
-
-def _like(t: Optional[torch.Tensor], ref: torch.Tensor, name: str) -> torch.Tensor:
-    """t checked against ref's type and shape, or a new tensor of ref's shape."""
-    if t is None:
-        if ref.is_contiguous():
-            return torch.empty_like(ref)       # the same tensor, allocated with less argument parsing
-        return torch.empty(ref.shape, dtype=ref.dtype, device=ref.device)
-    _typed(t, name, ref.dtype, ref.shape)
-    return t
+def _direct_positions(position_ids, q, num_heads):
+    """position_ids as the kernels read them: (B, S) int64, contiguous."""
+    if position_ids is None:
+        return None
+    B, S = q.shape[0], q.shape[2 if q.dim() == 4 else 1]
+    return position_ids.to(torch.int64).expand(B, S).contiguous()
 
 
 def sdpa_qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
@@ -599,15 +531,16 @@ def sdpa_qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor
     one pass over rank-4 (B, N, S, D) or rank-3 (B, S, N*D) tensors (num_heads and kv_num_heads
     given).  Caches as for sdpa_rotary; without caches there is no rotation.  Returns (q_out,
     k_out) in the inputs' shapes; an output may be its input."""
-    d, handle = _place(stream, (q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, q_out, k_out),
-                       "q k q_weight k_weight cos_cache sin_cache position_ids q_out k_out")
-    p, D, pos = _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim, interleaved,
-                             num_heads, kv_num_heads)
-    q_out, k_out = _like(q_out, q, "q_out"), _like(k_out, k, "k_out")
-    _keep_for(stream, d, handle, q_out, k_out, pos)
-    _call(d, lib().sdpa_qk_norm_rotary, p, sdpa_view(*_head_view(q_out, D, "q_out")),
-          sdpa_view(*_head_view(k_out, D, "k_out")), handle)
-    return q_out, k_out
+    b, entry = _native()
+    if _here(q, stream):
+        return _raised(b.qk_norm_rotary(entry["sdpa_qk_norm_rotary"], _handle(q), q, k, q_weight, k_weight, cos_cache,
+                                        sin_cache, position_ids, eps, rotary_dim, interleaved, num_heads or 0,
+                                        kv_num_heads or 0, q_out, k_out))
+    q_out, k_out = _new(q) if q_out is None else q_out, _new(k) if k_out is None else k_out
+    pos = _direct_positions(position_ids, q, num_heads)
+    return _raised(_elsewhere(q, stream, lambda h: b.qk_norm_rotary(
+        entry["sdpa_qk_norm_rotary"], h, q, k, q_weight, k_weight, cos_cache, sin_cache, pos, eps, rotary_dim, interleaved,
+        num_heads or 0, kv_num_heads or 0, q_out, k_out), (q_out, k_out, pos)))
 
 
 def sdpa_qk_norm_rotary_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch.Tensor,
@@ -619,74 +552,37 @@ def sdpa_qk_norm_rotary_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tens
                             workspace=None, stream=None):
     """Gradient of sdpa_qk_norm_rotary for the upstream gradients dq_out, dk_out of its outputs:
     returns (dq, dk, dq_weight, dk_weight).  dq may be dq_out itself and dk dk_out."""
-    d, handle = _place(stream, (q, k, dq_out, dk_out, q_weight, k_weight, cos_cache, sin_cache, position_ids, dq, dk,
-                                dq_weight, dk_weight, workspace),
-                       "q k dq_out dk_out q_weight k_weight cos_cache sin_cache position_ids dq dk dq_weight dk_weight "
-                       "workspace")
-    p, D, pos = _norm_params(q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps, rotary_dim, interleaved,
-                             num_heads, kv_num_heads)
-    _typed(dq_out, "dq_out", q.dtype, q.shape)
-    _typed(dk_out, "dk_out", k.dtype, k.shape)
-    dq, dk = _like(dq, q, "dq"), _like(dk, k, "dk")
-    dq_weight, dk_weight = _like(dq_weight, q_weight, "dq_weight"), _like(dk_weight, k_weight, "dk_weight")
+    b, entry = _native()
+    fn, size = entry["sdpa_qk_norm_rotary_bwd"], entry["sdpa_qk_norm_workspace_size"]
+    if _here(q, stream):
+        return _raised(b.qk_norm_rotary_bwd(fn, size, _handle(q), q, k, q_weight, k_weight, cos_cache, sin_cache,
+                                            position_ids, eps, rotary_dim, interleaved, num_heads or 0, kv_num_heads or 0,
+                                            dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace))
+    outs = [_new(like) if t is None else t for t, like in ((dq, q), (dk, k), (dq_weight, q_weight), (dk_weight, k_weight))]
+    pos = _direct_positions(position_ids, q, num_heads)
     if workspace is None:
-        workspace = torch.empty(max(1, lib().sdpa_qk_norm_workspace_size(p)), dtype=torch.uint8, device=q.device)
-    _keep_for(stream, d, handle, dq, dk, dq_weight, dk_weight, workspace, pos)
-    v = lambda t, name: sdpa_view(*_head_view(t, D, name))
-    _call(d, lib().sdpa_qk_norm_rotary_bwd, p, v(dq_out, "dq_out"), v(dk_out, "dk_out"), v(dq, "dq"), v(dk, "dk"),
-          _flat_ptr(dq_weight, "dq_weight"), _flat_ptr(dk_weight, "dk_weight"), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), handle)
-    return dq, dk, dq_weight, dk_weight
+        workspace = torch.empty(QK_NORM_WORKSPACE, dtype=torch.uint8, device=q.device)
+    return _raised(_elsewhere(q, stream, lambda h: b.qk_norm_rotary_bwd(
+        fn, size, h, q, k, q_weight, k_weight, cos_cache, sin_cache, pos, eps, rotary_dim, interleaved, num_heads or 0,
+        kv_num_heads or 0, dq_out, dk_out, *outs, workspace), (*outs, workspace, pos)))
 
 
-def _pool_view(t: torch.Tensor, name: str) -> Tuple[int, int, int, int]:
-    sb, sh, ss, sd = t.stride()
-    if sd != 1 and t.shape[3] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), sb, sh, ss
+# Most bytes the backward's workspace takes (sdpa_qk_norm_workspace_size at D = 256).
+QK_NORM_WORKSPACE = 1 << 20
+
+
+def _causal(causal) -> int:
+    return CAUSAL[causal] if isinstance(causal, str) else int(causal)
 
 
 def make_paged_params(k_pages, v_pages, page_table, kv_lens, tokens: int, Nq: int, *, cu_new=None,
                       cos_cache=None, sin_cache=None, rotary_dim=0, interleaved=False, scale=None, softcap=0.0,
                       causal="lower_right", window=-1, head_sink=None, max_new=None) -> sdpa_paged_params:
-    """Fills sdpa_paged_params (the caller keeps the tensors alive)."""
-    dt = k_pages.dtype
-    if k_pages.dim() != 4 or v_pages.dim() != 4:
-        raise ValueError("k_pages and v_pages are (pages, heads, slots, dim) views")
-    pages, Nkv, slots, H = k_pages.shape
-    Hv = v_pages.shape[3]
-    _typed(v_pages, "v_pages", dt, (pages, Nkv, slots, Hv))
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be (B, max_pages)")
-    B, width = page_table.shape
-    table_stride, entry_stride = page_table.stride()
-    if entry_stride != 1 and width > 1:
-        raise ValueError("the rows of page_table must be contiguous")
-    _typed(page_table, "page_table", torch.int32)
-    _typed(kv_lens, "kv_lens", torch.int32, (B,))
-    _typed(cu_new, "cu_new", torch.int32, (B + 1,))
-    _typed(head_sink, "head_sink", dt, (Nq,))
-    rotary_dim = int(rotary_dim)
-    rows = 0
-    if cos_cache is not None:
-        _typed(cos_cache, "cos_cache", dt, (cos_cache.shape[0], (rotary_dim or H) // 2))
-        _typed(sin_cache, "sin_cache", dt, cos_cache.shape)
-        rows = cos_cache.shape[0]
-    return sdpa_paged_params.from_buffer_copy(_PAGED_FIELDS.pack(
-        _PAGED_FIELDS.size, B, tokens, Nq, Nkv, H, Hv, _element_type(k_pages), pages, slots, width,
-        *_pool_view(k_pages, "k_pages"), *_pool_view(v_pages, "v_pages"), page_table.data_ptr(), table_stride,
-        _flat_ptr(kv_lens, "kv_lens"), _flat_ptr(cu_new, "cu_new"), _flat_ptr(cos_cache, "cos_cache"),
-        _flat_ptr(sin_cache, "sin_cache"), rows, rotary_dim, 1 if interleaved else 0, 0 if scale is None else 1,
-        0.0 if scale is None else scale, softcap, CAUSAL[causal] if isinstance(causal, str) else int(causal), int(window),
-        _flat_ptr(head_sink, "head_sink"), 0 if max_new is None else int(max_new)))
-
-
-def _packed(t: torch.Tensor, name: str) -> sdpa_view:
-    """The C view of packed rows (tokens, heads, dim)."""
-    ss, sh, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return sdpa_view(t.data_ptr(), 0, sh, ss)
+    """The sdpa_paged_params of a call (the caller keeps the tensors alive)."""
+    b, _ = _native()
+    return sdpa_paged_params.from_buffer_copy(b.paged_params(
+        tokens, Nq, k_pages, v_pages, page_table, kv_lens, cu_new, cos_cache, sin_cache, rotary_dim, interleaved, scale,
+        softcap, _causal(causal), window, head_sink, max_new or 0))
 
 
 def sdpa_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -701,18 +597,10 @@ def sdpa_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v
     heads, dim) is passed with transpose(1, 2)); page_table (B, max_pages) int32; kv_lens (B,)
     int32: keys of each sequence, its new tokens included; cu_new (B + 1,) int32: first row of
     each sequence, or None when every sequence brings tokens / B rows.  Returns the pools."""
-    d, handle = _place(stream, (k, v, k_pages, v_pages, page_table, kv_lens, cu_new, cos_cache, sin_cache),
-                       "k v k_pages v_pages page_table kv_lens cu_new cos_cache sin_cache")
-    if k.dim() != 3 or v.dim() != 3:
-        raise ValueError("k and v must be packed rows (tokens, heads, dim)")
-    if (cos_cache is None) != (sin_cache is None):
-        raise ValueError("cos_cache and sin_cache must be given together")
-    tokens, Nkv, H = k.shape
-    p = make_paged_params(k_pages, v_pages, page_table, kv_lens, tokens, Nkv, cu_new=cu_new, cos_cache=cos_cache,
-                          sin_cache=sin_cache, rotary_dim=rotary_dim, interleaved=interleaved)
-    _typed(k, "k", k_pages.dtype, (tokens, k_pages.shape[1], k_pages.shape[3]))
-    _typed(v, "v", k_pages.dtype, (tokens, Nkv, v_pages.shape[3]))
-    _call(d, lib().sdpa_paged_append, p, _packed(k, "k"), _packed(v, "v"), handle)
+    b, entry = _native()
+    call = lambda h: b.paged_append(entry["sdpa_paged_append"], h, k, v, k_pages, v_pages, page_table, kv_lens, cu_new,
+                                    cos_cache, sin_cache, rotary_dim, interleaved)
+    _raised(call(_handle(k)) if _here(k, stream) else _elsewhere(k, stream, call, ()))
     return k_pages, v_pages
 
 
@@ -726,26 +614,19 @@ def sdpa_paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     arguments as there.  max_new: most new tokens of one sequence, where the caller knows it (it
     picks the kernel; results hold for any value).  Returns y (tokens, Nq, Hv); rows behind the
     last sequence are not written."""
-    d, handle = _place(stream, (q, k_pages, v_pages, page_table, kv_lens, cu_new, head_sink, y, workspace),
-                       "q k_pages v_pages page_table kv_lens cu_new head_sink y workspace")
-    if q.dim() != 3:
-        raise ValueError("q must be packed rows (tokens, heads, dim)")
-    tokens, Nq, H = q.shape
-    p = make_paged_params(k_pages, v_pages, page_table, kv_lens, tokens, Nq, cu_new=cu_new, scale=scale, softcap=softcap,
-                          causal=causal, window=window, head_sink=head_sink, max_new=max_new)
-    dt = k_pages.dtype
-    _typed(q, "q", dt, (tokens, Nq, k_pages.shape[3]))
-    shape = (tokens, Nq, v_pages.shape[3])
+    b, entry = _native()
+    fn, size, mode = entry["sdpa_paged_attn"], entry["sdpa_paged_workspace_size"], _causal(causal)
+    call = lambda h: b.paged_attn(fn, size, h, q, k_pages, v_pages, page_table, kv_lens, cu_new, scale, softcap, mode, window,
+                                  head_sink, max_new or 0, y, workspace)
+    if _here(q, stream):
+        return _raised(call(_handle(q)))
     if y is None:
-        y = torch.empty_like(q) if q.shape == shape and q.is_contiguous() else torch.empty(shape, dtype=dt, device=q.device)
-    _typed(y, "y", dt, shape)
-    L = lib()
+        y = torch.empty(*q.shape[:2], v_pages.shape[3], dtype=q.dtype, device=q.device)
     if workspace is None:
-        workspace = torch.empty(max(1, L.sdpa_paged_workspace_size(p)), dtype=torch.uint8, device=q.device)
-    _keep_for(stream, d, handle, y, workspace)
-    _call(d, L.sdpa_paged_attn, p, _packed(q, "q"), _packed(y, "y"), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size(), handle)
-    return y
+        p = make_paged_params(k_pages, v_pages, page_table, kv_lens, q.shape[0], q.shape[1], cu_new=cu_new, scale=scale,
+                              softcap=softcap, causal=causal, window=window, head_sink=head_sink, max_new=max_new)
+        workspace = torch.empty(max(1, lib().sdpa_paged_workspace_size(p)), dtype=torch.uint8, device=q.device)
+    return _raised(_elsewhere(q, stream, call, (y, workspace)))
 
 
 def sdpa_query_status(stream=None) -> int:

@@ -125,14 +125,19 @@ def paged(over=(), *, B=2, tokens=4, Nq=4, Nkv=2, H=64, Hv=64, pages=6, page=16,
     return p, rows, keep
 
 
+def packed(t):
+    """The C view of packed rows (tokens, heads, dim)."""
+    return sdpa.sdpa_view(t.data_ptr(), 0, t.stride(1), t.stride(0))
+
+
 def append_code(p, rows, keep, **over):
     t = dict(rows, **over)
-    return sdpa.lib().sdpa_paged_append(ctypes.byref(p), sdpa._packed(t["k"], "k"), sdpa._packed(t["v"], "v"), None)
+    return sdpa.lib().sdpa_paged_append(ctypes.byref(p), packed(t["k"]), packed(t["v"]), None)
 
 
 def attn_code(p, rows, keep, where=256, size=1 << 40, **over):
     t = dict(rows, **over)
-    return sdpa.lib().sdpa_paged_attn(ctypes.byref(p), sdpa._packed(t["q"], "q"), sdpa._packed(t["y"], "y"), where,
+    return sdpa.lib().sdpa_paged_attn(ctypes.byref(p), packed(t["q"]), packed(t["y"]), where,
                                       size, None)
 
 
