@@ -127,6 +127,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   auto b_empty = [&](int s) { return smem_u32(&bar_empty[s]); };
   volatile int* abortp = &abort_flag;
   if (threadIdx.x == 0) {
+    if (args.box) {
+      prefetch_tmap(&tk);
+      prefetch_tmap(&tv);
+    }
     abort_flag = 0;
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(b_full(s), args.box ? 1 : 32);
@@ -163,7 +167,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const int row = (lane & 7) * args.box, region = lane >> 4;
       const bool mine = row < kTN && region < C::kRegions;
       const CUtensorMap* map = is_v ? &tv : &tk;
-      if (lane < 16 && (lane & 7) == 0) prefetch_tmap(map);
       // page of this lane's box of the t-th tile of w's unit (-1: the box is not brought)
       auto page_of = [&](int t) -> int {
         if (!mine || w.done() || t >= w.take()) return -1;

@@ -85,6 +85,7 @@ __device__ __forceinline__ void row_keys(const PagedAttn& a, const SeqInfo& s, i
 struct Share {
   int64_t count;           // the CTA's part of the whole cost, from its first unit's tile on
   ShareStart at;
+  SeqInfo s;               // of sequence at.b
   int active;              // CTAs that have a share
 };
 
@@ -95,6 +96,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
   constexpr int kW = NT / 32;
   __shared__ long long sh_sum[kW + 1];
   __shared__ ShareStart sh_at;
+  __shared__ SeqInfo sh_s;
   __shared__ int sh_back;          // cost before begin_at that counts to the CTA's first unit
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool bad = false;
@@ -144,6 +146,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
   r.active = total >= (long long)ctas * min_share ? ctas : max(1, (int)total / min_share);
   if (total == 0) r.active = 0;
   r.at = ShareStart{a.g.B, 0, 0, 0};
+  r.s = SeqInfo{0, 0, 0};
   r.count = 0;
   if (cta >= r.active) return r;
   // total / active tiles each, the first total % active CTAs one more (32-bit divisions where
@@ -184,7 +187,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
     if (who) {
       const int src = __ffs(who) - 1;
       SeqInfo t;
-      t.t0 = 0;
+      t.t0 = __shfl_sync(0xffffffffu, s.t0, src);
       t.n = __shfl_sync(0xffffffffu, s.n, src);
       t.T = __shfl_sync(0xffffffffu, s.T, src);
       const int n = row_blocks(a, t, TM);
@@ -204,6 +207,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
           const int off = (int)(in - k * (unsigned)cost);
           sh_at = ShareStart{base + warp * 32 + src, rb0 + lane, (int)k, max(0, off - OV)};
           sh_back = min(off, OV);
+          sh_s = t;
         }
         const long long block = __shfl_sync(0xffffffffu, c, 31);
         if (o < block) break;
@@ -215,6 +219,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
     if (before > begin_at) break;
   }
   r.at = sh_at;
+  r.s = sh_s;
   // a share that starts in a unit's OV has the unit's first tile; one that starts behind it goes on
   // from that tile
   if (sh_at.tile == 0) r.count += sh_back;
@@ -229,13 +234,9 @@ struct Walk {
   SeqInfo s;
   RowBlock r;
   __device__ __forceinline__ Walk(const PagedAttn& a, const Share& sh)
-      : left(sh.count), b(sh.at.b), rb(sh.at.rb), kvh(sh.at.kvh), tile(sh.at.tile) {
-    if (left > 0) {
-      bool bad = false;
-      s = seq_info(a.g, b, bad);
-      r = row_block<TM, TN>(a, s, rb);
-    }
-    if (take() <= 0) left = 0;
+      : left(sh.count), b(sh.at.b), rb(sh.at.rb), kvh(sh.at.kvh), tile(sh.at.tile), s(sh.s) {
+    if (left > 0) r = row_block<TM, TN>(a, s, rb);
+    if (left > 0 && take() <= 0) left = 0;
   }
   __device__ __forceinline__ bool done() const { return left <= 0; }
   __device__ __forceinline__ int take() const { return (int)min((int64_t)(r.tiles - tile), left - (tile == 0 ? OV : 0)); }

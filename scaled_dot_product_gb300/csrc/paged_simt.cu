@@ -258,25 +258,82 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   __shared__ float4 part[kMergeThreads];
   pdl_wait();
   const Paged& g = a.g;
-  const int c = blockIdx.x + 1;
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  // one look at the starts of CTAs c - 1 .. c + 30 (and of c - 1 alone: entries behind the active ones
+  // are not used)
   const int active = ws.start[ctas].b;
-  const ShareStart at = ws.start[c], before = ws.start[c - 1];      // read at once; of use if c < active
-  if (c >= active || at.tile == 0) return;
+  const ShareStart mine = ws.start[min(c - 1 + lane, ctas - 1)];
+  if (c >= active) return;
+  ShareStart at;
+  at.b = __shfl_sync(0xffffffffu, mine.b, 1);
+  at.rb = __shfl_sync(0xffffffffu, mine.rb, 1);
+  at.kvh = __shfl_sync(0xffffffffu, mine.kvh, 1);
+  at.tile = __shfl_sync(0xffffffffu, mine.tile, 1);
+  if (at.tile == 0) return;
   auto inside = [&](const ShareStart& s) { return s.tile > 0 && s.b == at.b && s.rb == at.rb && s.kvh == at.kvh; };
-  if (inside(before)) return;
+  unsigned in = __ballot_sync(0xffffffffu, c - 1 + lane < active && inside(mine));
+  if (in & 1u) return;                         // an earlier CTA joins this unit
+  int n = 1 + __ffs(~(in >> 1)) - 1;           // partials: CTA c - 1's second slot, then first slots
+  for (int k = c + 31; n == 32 + (k - c - 31);) {
+    in = __ballot_sync(0xffffffffu, k + lane < active && inside(ws.start[min(k + lane, active - 1)]));
+    const int more = in == 0xffffffffu ? 32 : __ffs(~in) - 1;
+    n += more;
+    k += 32;
+    if (more < 32) break;
+  }
   bool bad = false;
   const SeqInfo s = seq_info(g, at.b, bad);
-  const RowBlock rbk = row_block<TM, TN>(a, s, at.rb);
-  const int lane = threadIdx.x & 31, cols_all = g.Hv / 4;
+  const int cols_all = g.Hv / 4;
   const int row0 = (int)blockIdx.y * cut.rows, col0 = (int)blockIdx.z * cut.cols;
-  if (row0 >= rbk.rows) return;
-  int n = 1;                                   // partials: CTA c - 1's second slot, then first slots
-  for (int k = c;; k += 32) {
-    const unsigned in = __ballot_sync(0xffffffffu, k + lane < active && inside(ws.start[min(k + lane, active - 1)]));
-    n += in == 0xffffffffu ? 32 : __ffs(~in) - 1;
-    if (in != 0xffffffffu) break;
-  }
   auto slot_of = [&](int i) -> int64_t { return (i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c + i - 1)) * TM; };
+
+  const int items = cut.rows * cut.cols, share = max(1, kMergeThreads / items);      // threads of one item
+  if (n <= 4 && share == 1) {
+    // Few partials: a thread reads all of an item's at once, beside the lengths, and finds the row's
+    // maximum and sum by itself.  (Every slot of a joined unit holds TM rows; those past the unit's
+    // rows are not used.)
+    for (int x = threadIdx.x; x < items; x += kMergeThreads) {
+      const int r = row0 + x / cut.cols, d = (col0 + x % cut.cols) * 4;
+      if (r >= TM || d >= cols_all * 4) continue;
+      float2 ml[4];
+      float4 o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) {
+          ml[i] = *reinterpret_cast<const float2*>(ws.ml + (slot_of(i) + r) * 2);
+          o[i] = *reinterpret_cast<const float4*>(ws.o + (slot_of(i) + r) * g.Hv + d);
+        } else {
+          ml[i] = make_float2(-INFINITY, 0.f);
+          o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      const RowBlock rbk = row_block<TM, TN>(a, s, at.rb);
+      if (r >= rbk.rows) continue;
+      const int pr = rbk.row0 + r, tok = s.t0 + group_div(g, pr), h = at.kvh * g.group + pr - group_div(g, pr) * g.group;
+      const float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+      float L = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= n || ml[i].x == -INFINITY) continue;
+        const float f = exp2f(ml[i].x - M);
+        L = fmaf(f, ml[i].y, L);
+        v.x = fmaf(f, o[i].x, v.x);
+        v.y = fmaf(f, o[i].y, v.y);
+        v.z = fmaf(f, o[i].z, v.z);
+        v.w = fmaf(f, o[i].w, v.w);
+      }
+      const float inv = row_scale<T>(a, h, M, L);
+      T out[4] = {Elem<T>::from_f32(v.x * inv), Elem<T>::from_f32(v.y * inv), Elem<T>::from_f32(v.z * inv),
+                  Elem<T>::from_f32(v.w * inv)};
+      T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, tok) + d;
+      if (!SDPA_IN_BOUNDS(tok < g.tokens && h < g.Nq, 525)) continue;
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(out);
+      else *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(out);
+    }
+    return;
+  }
+  const RowBlock rbk = row_block<TM, TN>(a, s, at.rb);
+  if (row0 >= rbk.rows) return;
 
   // maximum and sum of each row, 256 / rows threads (8, 16 or 32) a row
   {
@@ -304,7 +361,6 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   }
   __syncthreads();
 
-  const int items = cut.rows * cut.cols, share = max(1, kMergeThreads / items);      // threads of one item
   const int per = kMergeThreads / share, g0 = threadIdx.x / per;
   for (int x = threadIdx.x % per; x < items; x += per) {
     const int r = x / cut.cols, d = (col0 + x % cut.cols) * 4;

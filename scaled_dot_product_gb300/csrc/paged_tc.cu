@@ -130,6 +130,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint64_t kDrainNs = 2000000000ull;
 
   if (threadIdx.x == 0) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+    if (t.q_tma) prefetch_tmap(&tq);
     abort_flag = 0;
     for (int s = 0; s < C::kStages; ++s) { mbar_init(b_full(s), 1); mbar_init(b_empty(s), 1); }
     mbar_init(b_qready, t.q_tma ? 1 : 2);
@@ -164,10 +167,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ================================================================ producer
-    if (lane == 0) {
-      prefetch_tmap(&tk);
-      prefetch_tmap(&tv);
-    }
     int seq = 0, it = 0;
     bool ok = true;
     for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
