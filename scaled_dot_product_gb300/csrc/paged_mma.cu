@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const int tile_key = (w.r.tile0 + w.tile + t) * kTN, key0 = tile_key + wk * KW;
       if (args.box && (tile_key + kTN > w.s.T || tile_key < w.r.lo)) {
         // this warp's rows of V that no box brought become zeros
-        const int first = w.r.lo - w.r.lo % args.box - tile_key, last = w.s.T - tile_key;
+        const int first = (w.r.lo & -args.box) - tile_key, last = w.s.T - tile_key;
         for (int i = lane; i < KW * 8; i += 32) {
           const int r = wk * KW + (i >> 3);
           if (r < first || r >= last) {
@@ -539,8 +539,10 @@ cudaError_t launch_wm(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaStream_t
   if (paged_boxes(a)) {
     t.box = kTN;
     while (a.g.page_size % t.box) t.box >>= 1;
-    if (!tc_make_map(&tk, a.g.kp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, H, &t.k_ds, &t.k_dn, &t.k_db, t.box) ||
-        !tc_make_map(&tv, a.g.vp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, H, &t.v_ds, &t.v_dn, &t.v_db, t.box))
+    // a head's row is one 128-byte line at H = 64: fetching 256 bytes would bring another head's
+    const CUtensorMapL2promotion promote = H == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    if (!tc_make_map(&tk, a.g.kp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, H, &t.k_ds, &t.k_dn, &t.k_db, t.box, promote) ||
+        !tc_make_map(&tv, a.g.vp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, H, &t.v_ds, &t.v_dn, &t.v_db, t.box, promote))
       return cudaErrorInvalidValue;
   }
   paged_mma_kernel<BF, H, WM><<<(unsigned)ctas, kThreads, C::kSmem, st>>>(tk, tv, t);

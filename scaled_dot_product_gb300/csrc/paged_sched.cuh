@@ -4,7 +4,8 @@
 // (sequence, kv head); its cost is the number of TN-key tiles that some of its rows admits (at
 // least one, so that rows with no key are written too) and OV more for its query rows and its
 // results, in tiles' time.  All units, laid end to end (sequence, row block, kv head, tile), are
-// dealt to the CTAs in equal contiguous shares of that cost, so ragged lengths, few rows over many
+// dealt to the CTAs in equal contiguous shares of that cost (in units of 256 rows, a tile of more
+// than 128 rows counts twice), so ragged lengths, few rows over many
 // keys and many rows over few keys all fill the GPU alike, and a CTA meets at most two units that
 // it does not hold whole.  (Without OV, the CTA that gets the first, shortest row blocks of a
 // causal prompt had 40 units of one or two tiles and took twice as long as the others.)  Those leave partial results
@@ -56,7 +57,8 @@ inline void paged_magic(int d, uint32_t* mul, uint32_t* shift) {
 struct RowBlock {
   int row0, rows;      // packed rows of the sequence
   int lo, hi;          // admitted keys [lo, hi] (hi < lo: none)
-  int tile0, tiles;    // first key tile, cost (>= 1)
+  int tile0, tiles;    // first key tile, tiles (>= 1)
+  int weight;          // cost of a tile
 };
 template <int TM, int TN>
 __device__ __forceinline__ RowBlock row_block(const PagedAttn& a, const SeqInfo& s, int rb) {
@@ -69,6 +71,7 @@ __device__ __forceinline__ RowBlock row_block(const PagedAttn& a, const SeqInfo&
   r.lo = a.window > 0 ? max(0, s.T - s.n + i0 - a.window + 1) : 0;
   r.tile0 = r.lo / TN;
   r.tiles = r.hi >= r.lo ? r.hi / TN - r.tile0 + 1 : 1;
+  r.weight = TM > 128 && r.rows > 128 ? 2 : 1;
   return r;
 }
 __device__ __forceinline__ int row_blocks(const PagedAttn& a, const SeqInfo& s, int TM) {
@@ -82,8 +85,11 @@ __device__ __forceinline__ void row_keys(const PagedAttn& a, const SeqInfo& s, i
   lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
 }
 
+__device__ __forceinline__ int unit_cost(const RowBlock& r, int OV) { return r.tiles * r.weight + OV; }
+
 struct Share {
-  int64_t count;           // the CTA's part of the whole cost, from its first unit's tile on
+  int64_t count;           // the CTA's part of the whole cost
+  int pos;                 // where it starts in its first unit's cost
   ShareStart at;
   SeqInfo s;               // of sequence at.b
   int active;              // CTAs that have a share
@@ -97,7 +103,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
   __shared__ long long sh_sum[kW + 1];
   __shared__ ShareStart sh_at;
   __shared__ SeqInfo sh_s;
-  __shared__ int sh_back;          // cost before begin_at that counts to the CTA's first unit
+  __shared__ int sh_pos;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool bad = false;
 
@@ -107,7 +113,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
     s = SeqInfo{0, 0, 0};
     if (b < a.g.B) s = seq_info(a.g, b, bad);
     const int nrb = row_blocks(a, s, TM);
-    if (nrb == 1) c = row_block<TM, TN>(a, s, 0).tiles + OV;
+    if (nrb == 1) c = unit_cost(row_block<TM, TN>(a, s, 0), OV);
     unsigned many = __ballot_sync(0xffffffffu, nrb > 1);
     while (many) {
       const int src = __ffs(many) - 1;
@@ -118,7 +124,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
       t.T = __shfl_sync(0xffffffffu, s.T, src);
       const int n = row_blocks(a, t, TM);
       long long part = 0;
-      for (int rb = lane; rb < n; rb += 32) part += row_block<TM, TN>(a, t, rb).tiles + OV;
+      for (int rb = lane; rb < n; rb += 32) part += unit_cost(row_block<TM, TN>(a, t, rb), OV);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
       if (lane == src) c = part;
@@ -148,6 +154,7 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
   r.at = ShareStart{a.g.B, 0, 0, 0};
   r.s = SeqInfo{0, 0, 0};
   r.count = 0;
+  r.pos = 0;
   if (cta >= r.active) return r;
   // total / active tiles each, the first total % active CTAs one more (32-bit divisions where
   // they do: a 64-bit one takes a microsecond's fraction that short calls feel)
@@ -193,7 +200,8 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
       const int n = row_blocks(a, t, TM);
       long long o = begin_at - __shfl_sync(0xffffffffu, begin, src);
       for (int rb0 = 0; rb0 < n; rb0 += 32) {
-        const int cost = rb0 + lane < n ? row_block<TM, TN>(a, t, rb0 + lane).tiles + OV : 0;
+        const RowBlock block = row_block<TM, TN>(a, t, min(rb0 + lane, n - 1));
+        const int cost = rb0 + lane < n ? unit_cost(block, OV) : 0;
         long long c = (long long)cost * a.g.Nkv;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -205,13 +213,13 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
           // within one row block: fewer than Nkv * cost, which fits 32 bits with room
           const unsigned in = (unsigned)(o - lo), k = in / (unsigned)cost;
           const int off = (int)(in - k * (unsigned)cost);
-          sh_at = ShareStart{base + warp * 32 + src, rb0 + lane, (int)k, max(0, off - OV)};
-          sh_back = min(off, OV);
+          sh_at = ShareStart{base + warp * 32 + src, rb0 + lane, (int)k, max(0, off - OV) / block.weight};
+          sh_pos = off;
           sh_s = t;
         }
-        const long long block = __shfl_sync(0xffffffffu, c, 31);
-        if (o < block) break;
-        o -= block;
+        const long long sum = __shfl_sync(0xffffffffu, c, 31);
+        if (o < sum) break;
+        o -= sum;
       }
     }
     __syncthreads();
@@ -220,50 +228,53 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
   }
   r.at = sh_at;
   r.s = sh_s;
-  // a share that starts in a unit's OV has the unit's first tile; one that starts behind it goes on
-  // from that tile
-  if (sh_at.tile == 0) r.count += sh_back;
+  r.pos = sh_pos;
   return r;
 }
 
-// Walks a share unit by unit.  The CTA takes the tiles [tile, tile + take()) of the present unit.
+// Walks a share unit by unit.  The CTA takes the tiles [tile, tile + take()) of the present unit: those
+// whose cost, behind the unit's OV, ends in the share.  (A share of at least two tiles' weight that
+// starts inside a unit has a tile of it; one that ends in a unit's OV leaves it to the next CTA.)
 template <int TM, int TN, int OV>
 struct Walk {
-  int64_t left;            // cost left, from the present unit's tile on (its OV included if tile = 0)
-  int b, rb, kvh, tile;
+  int64_t left;            // cost left, from pos on
+  int pos;                 // of the present unit's cost
+  int b, rb, kvh, tile, upto;
   SeqInfo s;
   RowBlock r;
   __device__ __forceinline__ Walk(const PagedAttn& a, const Share& sh)
-      : left(sh.count), b(sh.at.b), rb(sh.at.rb), kvh(sh.at.kvh), tile(sh.at.tile), s(sh.s) {
-    if (left > 0) r = row_block<TM, TN>(a, s, rb);
-    if (left > 0 && take() <= 0) left = 0;
+      : left(sh.count), pos(sh.pos), b(sh.at.b), rb(sh.at.rb), kvh(sh.at.kvh), tile(sh.at.tile), upto(0), s(sh.s) {
+    if (left > 0) {
+      r = row_block<TM, TN>(a, s, rb);
+      bound();
+    }
+  }
+  __device__ __forceinline__ void bound() {
+    upto = (int)min((int64_t)r.tiles, max((int64_t)0, pos + left - OV) / r.weight);
+    if (upto <= tile) left = 0;
   }
   __device__ __forceinline__ bool done() const { return left <= 0; }
-  __device__ __forceinline__ int take() const { return (int)min((int64_t)(r.tiles - tile), left - (tile == 0 ? OV : 0)); }
+  __device__ __forceinline__ int take() const { return upto - tile; }
   __device__ __forceinline__ bool begins() const { return tile == 0; }
-  __device__ __forceinline__ bool ends() const { return tile + take() == r.tiles; }
-  __device__ __forceinline__ bool whole() const { return begins() && ends(); }
+  __device__ __forceinline__ bool whole() const { return tile == 0 && upto == r.tiles; }
   __device__ __forceinline__ void next(const PagedAttn& a) {
-    left -= take() + (tile == 0 ? OV : 0);
-    tile = 0;
-    if (left <= OV) {      // what is left is in the next unit's OV, and that unit is another CTA's
-      left = 0;
-      return;
-    }
-    if (++kvh < a.g.Nkv) return;
-    kvh = 0;
-    if (++rb < row_blocks(a, s, TM)) {
+    left -= unit_cost(r, OV) - pos;
+    pos = tile = 0;
+    if (left <= 0) return;
+    if (++kvh == a.g.Nkv) {
+      kvh = 0;
+      if (++rb >= row_blocks(a, s, TM)) {
+        rb = 0;
+        bool bad = false;
+        while (++b < a.g.B) {
+          s = seq_info(a.g, b, bad);
+          if (s.n > 0) break;
+        }
+        if (b >= a.g.B) { left = 0; return; }
+      }
       r = row_block<TM, TN>(a, s, rb);
-      return;
     }
-    rb = 0;
-    bool bad = false;
-    while (++b < a.g.B) {
-      s = seq_info(a.g, b, bad);
-      if (s.n > 0) break;
-    }
-    if (b >= a.g.B) { left = 0; return; }
-    r = row_block<TM, TN>(a, s, 0);
+    bound();
   }
 };
 

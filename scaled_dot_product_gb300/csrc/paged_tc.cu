@@ -2,18 +2,19 @@
 // sizes that are multiples of 8.
 //
 // Bound by the tensor cores.  A unit is 256 packed rows (token x group head) of one (sequence,
-// kv head): two 128-row tiles that stream the same keys and values; a unit of at most 128 rows
-// leaves the second tile out.  One CTA per SM walks its share (paged_sched.cuh) of all units'
+// kv head): two 128-row tiles that stream the same keys and values.  A unit of at most 128 rows (a
+// single token beside chunks) has one tile of rows; there the two softmax warpgroups take turns with
+// the keys, even tiles and odd ones with their own maximum, sum and accumulator, joined at its end.  One CTA per SM walks its share (paged_sched.cuh) of all units'
 // 128-key tiles:
 //
-//   warp 0      producer: K_0, V_0, K_1, ... into the ring by TMA.  A tile is 128 / box boxes of
-//               box = gcd(page_size, 128) rows, each inside one page; lane i looks up and issues
-//               box i
+//   warp 0      K tiles into the ring by TMA, and query tiles where the group divides 128.  A tile is
+//               128 / box boxes of box = gcd(page_size, 128) rows, each inside one page; lane by lane
+//               they are looked up and issued
 //   warp 1      tensor products (one elected lane issues): S_X = Q_X K^T, O_X += P_X V with P
 //               read from tensor memory.  Rows of V that no box brought (past the sequence's keys,
 //               below every window) it sets to zero first, since 0 x NaN is not 0
-//               box i.  The next unit's query rows come by TMA too where the group divides 128
-//   warps 2-3   query rows by 16-byte asynchronous copies for the other groups
+//   warp 2      V tiles into the same ring
+//   warp 3      query rows by 16-byte asynchronous copies for the other groups
 //   warps 4-7   softmax of tile 0, one thread per row; warps 8-11 softmax of tile 1
 //
 // Running maxima move only when they grow by more than 2^8.  Every wait is bounded: on expiry the
@@ -38,8 +39,8 @@ using namespace ptx;
 
 constexpr int kBM = 128, kTM = 256, kTN = 128;
 constexpr int kThreads = 384;
-constexpr int kOV = 2;                // a unit's cost beside its tiles, in tiles
-constexpr int kMinShare = 6;
+constexpr int kOV = 4;                // a unit's cost beside its tiles, in tiles
+constexpr int kMinShare = 12;
 // Register split: the control warpgroup shrinks to kCtlRegs, the softmax warpgroups grow to
 // kSmxRegs; the sum stays within the launch's kThreads x kLaunchRegs, which the host checks.
 constexpr int kLaunchRegs = 168, kCtlRegs = 88, kSmxRegs = 208;
@@ -75,12 +76,6 @@ struct TcArgs {
   uint64_t wait_ns;
 };
 
-__device__ __forceinline__ void perm_coords(int ds, int dn, int db, int s, int n, int b, int* c) {
-  c[0] = ds == 1 ? s : (dn == 1 ? n : b);
-  c[1] = ds == 2 ? s : (dn == 2 ? n : b);
-  c[2] = ds == 3 ? s : (dn == 3 ? n : b);
-}
-
 // Keys outside [elo, ehi] of a 128-key segment take -inf: per 32 columns one bit set, then one
 // test and one select per key.
 __device__ __forceinline__ void clip(float (&s)[128], int elo, int ehi) {
@@ -94,11 +89,19 @@ __device__ __forceinline__ void clip(float (&s)[128], int elo, int ehi) {
   }
 }
 
-// Rows of key tile kt that the boxes bring: [first, last) of 128.
+// Rows of key tile kt that the boxes (a power of two rows) bring: [first, last) of 128.
 __device__ __forceinline__ void box_rows(const TcArgs& t, const SeqInfo& s, const RowBlock& r, int kt, int& first, int& last) {
-  first = max(0, min(kTN, r.lo - r.lo % t.box - kt * kTN));
+  first = max(0, min(kTN, (r.lo & -t.box) - kt * kTN));
   last = max(first, min(kTN, s.T - kt * kTN));
 }
+
+// Ring positions, from the unit's first, of the key and value tiles of a unit of n: in the order of
+// their first use.  With P in S's columns PV(j) comes before S(j + 1): K_0 V_0 K_1 V_1 ...; else S runs a
+// tile ahead: K_0 K_1 V_0 K_2 V_1 ... V_{n-1}.
+template <bool kAlias>
+__device__ __forceinline__ int k_at(int j) { return kAlias ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
+template <bool kAlias>
+__device__ __forceinline__ int v_at(int j, int n) { return kAlias ? 2 * j + 1 : j + 1 < n ? 2 * j + 2 : 2 * n - 1; }
 
 template <int H, bool BF, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -112,8 +115,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
   __shared__ __align__(8) uint64_t bar_qready, bar_qempty, bar_drain, bar_sfull[2], bar_sfree[2], bar_pfull[2], bar_odone[2];
+  __shared__ __align__(8) uint64_t bar_xfull[4], bar_xfree[4];      // joining the halves of a narrow unit
+  __shared__ float2 sm_ml[4][32];
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_flag;
+  __shared__ int issued[2][C::kStages];      // last tile + 1 that K's / V's producer put into a stage
   const PagedAttn& a = t.a;
   const Paged& g = a.g;
   const int ctas = gridDim.x, cta = blockIdx.x;
@@ -134,10 +140,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tv);
     if (t.q_tma) prefetch_tmap(&tq);
     abort_flag = 0;
-    for (int s = 0; s < C::kStages; ++s) { mbar_init(b_full(s), 1); mbar_init(b_empty(s), 1); }
-    mbar_init(b_qready, t.q_tma ? 1 : 2);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(b_full(s), 1);
+      mbar_init(b_empty(s), 1);
+      issued[0][s] = issued[1][s] = 0;
+    }
+    mbar_init(b_qready, 1);
     mbar_init(b_qempty, 1);
     mbar_init(b_drain, 1);
+    for (int x = 0; x < 4; ++x) { mbar_init(smem_u32(&bar_xfull[x]), 32); mbar_init(smem_u32(&bar_xfree[x]), 32); }
     for (int x = 0; x < 2; ++x) {
       mbar_init(b_sfull(x), 1);
       mbar_init(b_sfree(x), kBM);
@@ -165,84 +176,75 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
 
-  if (warp == 0) {
-    // ================================================================ producer
-    int seq = 0, it = 0;
+  if (warp == 0 || warp == 2) {
+    // ================================================================ producers: K and Q, V
+    // A lane's box: region = lane / 16, box = lane % 16.  The loads of a warp are issued one lane after
+    // the other (about 150 cycles each), so K and V have a warp each: with one for both, narrow units
+    // over pages of 16 waited for it.  Page ids are fetched a tile ahead.
+    const bool is_v = warp == 2;
+    const int region = lane >> 4, row = (lane & 15) * t.box;
+    const CUtensorMap* map = is_v ? &tv : &tk;
+    const int ds = is_v ? t.v_ds : t.k_ds, dn = is_v ? t.v_dn : t.k_dn;
+    int base = 0, it = 0;                // ring position of the unit's first tile, units
     bool ok = true;
     for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
       const int n = w.take(), kt0 = w.r.tile0 + w.tile;
       const int32_t* table = g.table + (int64_t)w.b * g.table_stride;
-      // page of this lane's box of tile kt (-1: the box is not brought)
-      auto page_of = [&](int j) -> int {
-        if (j >= n) return -1;
+      auto brought = [&](int j) -> bool {
         int first, last;
         box_rows(t, w.s, w.r, kt0 + j, first, last);
-        const int row = lane * t.box;
-        if (lane >= t.boxes || row < first || row >= last) return -1;
-        int id = table[page_div(g, (kt0 + j) * kTN + row)];
-        if (id < 0 || id >= g.num_pages) {
+        return j < n && region < C::kRegions && row < kTN && row >= first && row < last;
+      };
+      int id = 0;
+      auto look_up = [&](int j) {
+        if (brought(j)) id = table[page_div(g, (kt0 + j) * kTN + row)];
+      };
+      look_up(0);
+      for (int j = 0; j < n; ++j) {
+        const int sq = base + (is_v ? v_at<C::kAlias>(j, n) : k_at<C::kAlias>(j)), st = sq % C::kStages;
+        if (sq >= C::kStages && !(ok = wait_all(b_empty(st), ((sq / C::kStages) - 1) & 1))) break;
+        const bool take = brought(j);
+        if (take && (unsigned)id >= (unsigned)g.num_pages) {
           atomicOr(&g_paged_status, kPagedBadPage);
           id = g.num_pages;              // outside the map: the box is filled with zeros
         }
-        return id;
-      };
-      auto load = [&](bool is_v, int j, int id) -> bool {
-        const int st = seq % C::kStages;
-        if (seq >= C::kStages && !wait_all(b_empty(st), ((seq / C::kStages) - 1) & 1)) return false;
-        const unsigned brought = __ballot_sync(0xffffffffu, id >= 0);
-        if (lane == 0) mbar_arrive_expect_tx(b_full(st), __popc(brought) * t.box * H * 2);
-        __syncwarp();
-        if (id >= 0 && SDPA_IN_BOUNDS(st < C::kStages && lane * t.box < kTN && w.kvh < g.Nkv, 541)) {
-          const int row = lane * t.box, key = (kt0 + j) * kTN + row;
-          const int slot = key - page_div(g, key) * g.page_size;
-          int c[3];
-          if (is_v) perm_coords(t.v_ds, t.v_dn, t.v_db, slot, w.kvh, id, c);
-          else perm_coords(t.k_ds, t.k_dn, t.k_db, slot, w.kvh, id, c);
-#pragma unroll
-          for (int r = 0; r < C::kRegions; ++r)
-            tma_load_4d(sKV + st * C::kTile + r * C::kRegionBytes + row * 128, is_v ? &tv : &tk, b_full(st), 64 * r, c[0],
-                        c[1], c[2]);
-        }
-        __syncwarp();
-        ++seq;
-        return true;
-      };
-      int id = page_of(0);
-      ok = load(false, 0, id);
-      if (ok && t.q_tma) {
-        // the previous unit's last S products have read its query tiles; rows of the box behind the
-        // unit's belong to other rows and are masked
-        if (it > 0 && !(ok = wait_all(b_qempty, (it - 1) & 1))) break;
-        const int nx = w.r.rows > kBM ? 2 : 1;
+        const unsigned all = __ballot_sync(0xffffffffu, take);
         if (lane == 0) {
-          mbar_arrive_expect_tx(b_qready, nx * C::kTile);
-          for (int x = 0; x < nx; ++x)
-            for (int r = 0; r < C::kRegions; ++r)
-              tma_load_4d(sQ + x * C::kTile + r * C::kRegionBytes, &tq, b_qready, 64 * r, w.kvh * g.group,
-                          w.s.t0 + group_div(g, w.r.row0 + x * kBM), 0);
+          mbar_arrive_expect_tx(b_full(st), __popc(all) * t.box * 128);
+          issued[is_v][st] = sq + 1;
         }
         __syncwarp();
-        ++it;
-      }
-      for (int j = 0; j < n && ok; ++j) {
-        const int next = page_of(j + 1);
-        if constexpr (C::kAlias) {
-          ok = load(true, j, id);
-          if (ok && j + 1 < n) ok = load(false, j + 1, next);
-        } else {
-          if (j + 1 < n) ok = load(false, j + 1, next);
-          if (ok) ok = load(true, j, id);
+        if (take && SDPA_IN_BOUNDS(st < C::kStages && row + t.box <= kTN && w.kvh < g.Nkv, 541)) {
+          const int key = (kt0 + j) * kTN + row, slot = key - page_div(g, key) * g.page_size;
+          const int c1 = ds == 1 ? slot : dn == 1 ? w.kvh : id, c2 = ds == 2 ? slot : dn == 2 ? w.kvh : id,
+                    c3 = ds == 3 ? slot : dn == 3 ? w.kvh : id;
+          tma_load_4d(sKV + st * C::kTile + region * C::kRegionBytes + row * 128, map, b_full(st), 64 * region, c1, c2, c3);
         }
-        id = next;
+        __syncwarp();
+        look_up(j + 1);
+        if (j == 0 && !is_v && t.q_tma) {
+          // the previous unit's last S products have read its query tiles; rows of the box behind the
+          // unit's belong to other rows and go nowhere
+          if (it > 0 && !(ok = wait_all(b_qempty, (it - 1) & 1))) break;
+          const int nx = w.r.rows > kBM ? 2 : 1;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(b_qready, nx * C::kTile);
+            for (int x = 0; x < nx; ++x)
+              for (int r = 0; r < C::kRegions; ++r)
+                tma_load_4d(sQ + x * C::kTile + r * C::kRegionBytes, &tq, b_qready, 64 * r, w.kvh * g.group,
+                            w.s.t0 + group_div(g, w.r.row0 + x * kBM), 0);
+          }
+          __syncwarp();
+          ++it;
+        }
       }
+      base += 2 * n;
     }
     if (__any_sync(0xffffffffu, !ok || *abortp)) {
       // some role gave up: let every copy already issued land before the CTA can exit
       if (it > 0) mbar_wait_bounded(b_qready, (it - 1) & 1, nullptr, kDrainNs);
-      for (int s = 0; s < C::kStages && s < seq; ++s) {
-        const int last = s + ((seq - 1 - s) / C::kStages) * C::kStages;
-        mbar_wait_bounded(b_full(s), (last / C::kStages) & 1, nullptr, kDrainNs);
-      }
+      for (int s = 0; s < C::kStages; ++s)
+        if (issued[is_v][s]) mbar_wait_bounded(b_full(s), ((issued[is_v][s] - 1) / C::kStages) & 1, nullptr, kDrainNs);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -263,8 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return ok;
     };
-    auto issue_S = [&](int x, int st) {
-      const uint64_t dq = dQ0 + (uint64_t)((x * C::kTile) >> 4), dk = dK0 + (uint64_t)((st * C::kTile) >> 4);
+    // scores x of query tile q
+    auto issue_S = [&](int x, int q, int st) {
+      const uint64_t dq = dQ0 + (uint64_t)((q * C::kTile) >> 4), dk = dK0 + (uint64_t)((st * C::kTile) >> 4);
 #pragma unroll
       for (int kk = 0; kk < H / 16; ++kk) {
         const uint64_t off = (uint64_t)(((kk / 4) * C::kRegionBytes + (kk % 4) * 32) >> 4);
@@ -305,12 +308,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_all(b_qready, it & 1))) break;
       tc_fence_after();
       ++it;
+      if (nx == 1) {
+        // key tile j belongs to softmax group j & 1; S of the next tile runs before PV of this one
+        const int base = seq;
+        auto wait_at = [&](int sq) -> bool {
+          const bool ready = wait_all(b_full(sq % C::kStages), (sq / C::kStages) & 1);
+          tc_fence_after();
+          return ready;
+        };
+        auto scores = [&](int j) -> bool {
+          const int y = j & 1, st = (base + k_at<C::kAlias>(j)) % C::kStages;
+          if (!wait_at(base + k_at<C::kAlias>(j)) || !wait_sfree(y)) return false;
+          issue_S(y, 0, st);
+          commit(b_sfull(y));
+          ++ns[y];
+          if (j + 1 == n) commit(b_qempty);
+          commit(b_empty(st));
+          return true;
+        };
+        ok = scores(0);
+        for (int j = 0; j < n && ok; ++j) {
+          const int x = j & 1, vst = (base + v_at<C::kAlias>(j, n)) % C::kStages;
+          if (j + 1 < n && !(ok = scores(j + 1))) break;
+          if (!(ok = wait_at(base + v_at<C::kAlias>(j, n)))) break;
+          zero_v(j, vst);
+          if (!(ok = wait_all(b_pfull(x), np[x] & 1))) break;
+          tc_fence_after();
+          ++np[x];
+          issue_PV(x, vst, j > 1);
+          if (!C::kAlias || j + 2 >= n) commit(b_odone(x));
+          commit(b_empty(vst));
+        }
+        seq = base + 2 * n;
+        continue;
+      }
       if (!(ok = wait_full())) break;
       {
         const int st = seq % C::kStages;
         for (int x = 0; x < nx && ok; ++x) {
           if (!(ok = wait_sfree(x))) break;
-          issue_S(x, st);
+          issue_S(x, x, st);
           commit(b_sfull(x));
           ++ns[x];
         }
@@ -336,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             issue_PV(x, vst, j > 0);
             if (more) {
               if (x == 0 && !(ok = wait_full())) break;
-              issue_S(x, kst);
+              issue_S(x, x, kst);
               commit(b_sfull(x));
               ++ns[x];
             } else {
@@ -357,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++seq;
             for (int x = 0; x < nx && ok; ++x) {
               if (!(ok = wait_sfree(x))) break;
-              issue_S(x, kst);
+              issue_S(x, x, kst);
               commit(b_sfull(x));
               ++ns[x];
             }
@@ -385,9 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     commit(b_drain);
     mbar_wait_bounded(b_drain, 0, nullptr, kDrainNs);
     __syncwarp();
-  } else if (warp < 4) {
-    // ================================================================ query rows
-    const int x = warp - 2;
+  } else if (warp == 3) {
+    // ================================================================ query rows of groups that TMA does not box
     constexpr int CPR = H / 8;                       // 16-byte chunks of a row
     const int chunk = lane % CPR, rin = lane / CPR;
     int it = 0;
@@ -395,24 +431,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (Wk w(a, sh); ok && !t.q_tma && !w.done(); w.next(a)) {
       if (it > 0 && !(ok = wait_all(b_qempty, (it - 1) & 1))) break;
       ++it;
-      if (x * kBM < w.r.rows) {
-        const uint32_t dst = sQ + x * C::kTile + (chunk >> 3) * C::kRegionBytes;
+      const int rows = w.r.rows > kBM ? 2 * kBM : kBM;
 #pragma unroll 4
-        for (int r0 = 0; r0 < kBM; r0 += 32 / CPR) {
-          const int r = r0 + rin;
-          const bool take = x * kBM + r < w.r.rows;
-          const int pr = w.r.row0 + (take ? x * kBM + r : 0);
-          const int tok = group_div(g, pr);
-          const T* src = reinterpret_cast<const T*>(a.q.p) + a.q.off(0, w.kvh * g.group + pr - tok * g.group, w.s.t0 + tok) +
-                         chunk * 8;
-          const uint32_t d = dst + r * 128 + (((chunk & 7) ^ (r & 7)) << 4);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src),
-                       "r"(take && SDPA_IN_BOUNDS(w.s.t0 + tok < g.tokens, 542) ? 16 : 0) : "memory");
-        }
-        cp_async_commit();
-        cp_async_wait_all();
-        fence_proxy_async_smem();
+      for (int r0 = 0; r0 < rows; r0 += 32 / CPR) {
+        const int r = r0 + rin, x = r / kBM, xr = r % kBM;
+        const bool take = r < w.r.rows;
+        const int pr = w.r.row0 + (take ? r : 0), tok = group_div(g, pr);
+        const T* src = reinterpret_cast<const T*>(a.q.p) + a.q.off(0, w.kvh * g.group + pr - tok * g.group, w.s.t0 + tok) +
+                       chunk * 8;
+        const uint32_t d = sQ + x * C::kTile + (chunk >> 3) * C::kRegionBytes + xr * 128 + (((chunk & 7) ^ (xr & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src),
+                     "r"(take && SDPA_IN_BOUNDS(w.s.t0 + tok < g.tokens, 542) ? 16 : 0) : "memory");
       }
+      cp_async_commit();
+      cp_async_wait_all();
+      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_qready);
     }
@@ -425,17 +458,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = trow + 128 * x, tO = trow + (x ? C::kO1 : C::kO0), tP = trow + (x ? C::kP1 : C::kP0);
     const uint32_t sY = sQ + C::kYOff + (uint32_t)(x * 4 + sub) * C::kYWarp;
     const float kfac = CAP || t.pre ? 1.f : t.scale_log2;
-    int cs = 0, co = 0;                              // sfull / odone phases waited
+    int cs = 0, co = 0, xc = 0;                      // sfull / odone / joining phases waited
     bool ok = true;
     for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
-      if (x * kBM >= w.r.rows) continue;
       const int n = w.take(), kt0 = w.r.tile0 + w.tile;
-      const bool valid = x * kBM + row < w.r.rows;
-      const int pr = w.r.row0 + (valid ? x * kBM + row : 0);
-      int lo = 1, hi = 0;
+      const bool narrow = w.r.rows <= kBM;           // both groups have the rows, and every second tile
+      const int j0 = narrow ? x : 0, js = narrow ? 2 : 1, tile_row = narrow ? 0 : x * kBM;
+      if (j0 >= n) continue;
+      const bool valid = tile_row + row < w.r.rows;
+      const int pr = w.r.row0 + (valid ? tile_row + row : 0);
+      // rows past the unit's: every key, so that they cause no masking; their results go nowhere
+      int lo = 0, hi = 0x7fffffff;
       if (valid) row_keys(a, w.s, pr, lo, hi);
+      if (tile_row + sub * 32 >= w.r.rows) {
+        // no row of this warp: it keeps the barriers' counts, at the pace of the other warps
+        for (int j = j0; j < n && ok; j += js) {
+          if (!(ok = wait_all(b_sfull(x), cs & 1))) break;
+          ++cs;
+          if constexpr (!C::kAlias) {
+            mbar_arrive(b_sfree(x));
+            if (j != j0) {
+              if (!(ok = wait_all(b_odone(x), co & 1))) break;
+              ++co;
+            }
+          }
+          mbar_arrive(b_pfull(x));
+        }
+        if (!ok || !(ok = wait_all(b_odone(x), co & 1))) break;
+        ++co;
+        continue;
+      }
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j) {
+      for (int j = j0; j < n; j += js) {
         if (!(ok = wait_all(b_sfull(x), cs & 1))) break;
         ++cs;
         tc_fence_after();
@@ -496,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         f2_unpack(f2_add(acc[0], acc[1]), r0, r1);
         f2_unpack(f2_add(acc[2], acc[3]), r2, r3);
         l = l * corr + ((r0 + r1) + (r2 + r3));
-        if (j > 0) {
-          // PV_X(j-1) has read P_X and O_X holds it (with P in S's columns, sfull said so)
+        if (j != j0) {
+          // the previous PV_X has read P_X and O_X holds it (with P in S's columns, sfull said so)
           if constexpr (!C::kAlias) {
             if (!(ok = wait_all(b_odone(x), co & 1))) break;
             ++co;
@@ -534,17 +588,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_all(b_odone(x), co & 1))) break;
       ++co;
       tc_fence_after();
-      const bool whole = w.whole();
-      const int live = min(32, w.r.rows - x * kBM - sub * 32);       // rows of this warp
-      if (whole) {
-        const int tok = group_div(g, pr), h = w.kvh * g.group + pr - tok * g.group;
-        const float inv = row_scale<T>(a, h, m, l);
-        const long long yrow = (long long)(reinterpret_cast<uintptr_t>(a.y.p) + (uintptr_t)(a.y.off(0, h, w.s.t0 + tok) * 2));
-#pragma unroll
+      // a narrow unit's odd tiles: group 1 hands its rows to group 0, 32 columns at a time, through its
+      // staging (float4 q of lane i at [q][i])
+      const bool join = narrow && n > 1;
+      const uint32_t sX = sQ + C::kYOff + (uint32_t)(4 + sub) * C::kYWarp;
+      const uint32_t b_xfull = smem_u32(&bar_xfull[sub]), b_xfree = smem_u32(&bar_xfree[sub]);
+      if (join && x == 1) {
+        sm_ml[sub][lane] = make_float2(m, l);
+#pragma unroll 1
         for (int c = 0; c < H / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + c * 32, o);
           tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) st_shared_v4(sX + q * 512 + lane * 16, o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          mbar_arrive(b_xfull);
+          if (!(ok = wait_all(b_xfree, xc & 1))) break;
+          ++xc;
+        }
+        if (!ok) break;
+        continue;
+      }
+      float f0 = 1.f, f1 = 0.f;
+      // columns 32 c and on of this thread's row
+      auto read_o = [&](int c, uint32_t* o) {
+        tmem_ld32(tO + c * 32, o);
+        tmem_ld_wait();
+        if (!join) return;
+        ok = ok && wait_all(b_xfull, xc & 1);
+        if (c == 0) {
+          const float2 other = sm_ml[sub][lane];
+          const float M = fmaxf(m, other.x);
+          if (M != -INFINITY) {
+            f0 = ex2_approx(m - M);
+            f1 = ex2_approx(other.x - M);
+          }
+          l = l * f0 + other.y * f1;
+          m = M;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          uint32_t v[4];
+          ld_shared_v4(sX + q * 512 + lane * 16, v[0], v[1], v[2], v[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[4 * q + e] = __float_as_uint(fmaf(__uint_as_float(o[4 * q + e]), f0, __uint_as_float(v[e]) * f1));
+        }
+        mbar_arrive(b_xfree);
+        ++xc;
+      };
+      const bool whole = w.whole();
+      const int live = min(32, w.r.rows - tile_row - sub * 32);       // rows of this warp
+      if (whole) {
+        const int tok = group_div(g, pr), h = w.kvh * g.group + pr - tok * g.group;
+        float inv = 0.f;
+        const long long yrow = (long long)(reinterpret_cast<uintptr_t>(a.y.p) + (uintptr_t)(a.y.off(0, h, w.s.t0 + tok) * 2));
+#pragma unroll
+        for (int c = 0; c < H / 32; ++c) {
+          uint32_t o[32];
+          read_o(c, o);
+          if (c == 0) inv = row_scale<T>(a, h, m, l);      // m and l are the whole row's now
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t wv[4];
@@ -572,16 +675,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        const int64_t base = (2 * (int64_t)cta + (w.begins() ? 1 : 0)) * kTM + x * kBM + sub * 32;
-        if (lane < live && SDPA_IN_BOUNDS(base + lane < (int64_t)2 * ctas * kTM, 544)) {
-          t.ws.ml[(base + lane) * 2] = m;
-          t.ws.ml[(base + lane) * 2 + 1] = l;
-        }
+        const int64_t base = (2 * (int64_t)cta + (w.begins() ? 1 : 0)) * kTM + tile_row + sub * 32;
 #pragma unroll
         for (int c = 0; c < H / 32; ++c) {
           uint32_t o[32];
-          tmem_ld32(tO + c * 32, o);
-          tmem_ld_wait();
+          read_o(c, o);
+          if (c == 0 && lane < live && SDPA_IN_BOUNDS(base + lane < (int64_t)2 * ctas * kTM, 544)) {
+            t.ws.ml[(base + lane) * 2] = m;
+            t.ws.ml[(base + lane) * 2 + 1] = l;
+          }
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             st_shared_v4(sY + lane * 128 + ((q ^ (lane & 7)) << 4), o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
@@ -677,9 +779,11 @@ cudaError_t launch_paged_tc(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaSt
   t.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
   t.cap_log2 = a.softcap * kLog2e;
   t.wait_ns = wait_limit_ns();
+  // a head's row is one 128-byte line at H = 64: fetching 256 bytes would bring another head's
+  const CUtensorMapL2promotion promote = a.g.H == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   CUtensorMap tk, tv;
-  if (!tc_make_map(&tk, a.g.kp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, a.g.H, &t.k_ds, &t.k_dn, &t.k_db, t.box) ||
-      !tc_make_map(&tv, a.g.vp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, a.g.Hv, &t.v_ds, &t.v_dn, &t.v_db, t.box))
+  if (!tc_make_map(&tk, a.g.kp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, a.g.H, &t.k_ds, &t.k_dn, &t.k_db, t.box, promote) ||
+      !tc_make_map(&tv, a.g.vp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, a.g.Hv, &t.v_ds, &t.v_dn, &t.v_db, t.box, promote))
     return cudaErrorInvalidValue;
   const bool bf = dt == SDPA_BF16, cap = a.softcap > 0.f;
   CUtensorMap tq{};
