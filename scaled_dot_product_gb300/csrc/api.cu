@@ -1060,6 +1060,9 @@ int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* 
   if ((rc = check_aligned_view(q, "q", dt))) return rc;
   if ((rc = check_aligned_view(y, "y", dt))) return rc;
   const size_t need = paged_workspace(a, (sdpa_dtype)dt);
+  if (!workspace || workspace_bytes < need)
+    return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+  if ((uintptr_t)workspace & 255u) return fail(SDPA_ERR_ALIGNMENT, "workspace not 256-byte aligned");
   const Extent ws = flat(workspace, need, "workspace");
   paged_side_inputs(p, side);
   const Extent ins[] = {eq, pool[0], pool[1], side[0], side[1], side[2],
@@ -1069,9 +1072,6 @@ int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* 
     if (overlap(ws, in)) return fail(SDPA_ERR_ALIAS, "workspace overlaps input %s", in.name);
   }
   if (overlap(ws, ey)) return fail(SDPA_ERR_ALIAS, "workspace overlaps output y");
-  if (!workspace || workspace_bytes < need)
-    return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
-  if ((uintptr_t)workspace & 255u) return fail(SDPA_ERR_ALIGNMENT, "workspace not 256-byte aligned");
   g_error.clear();
   if (p->tokens == 0 || p->B == 0) return SDPA_OK;
   a.q = to_view(q);

@@ -19,7 +19,7 @@ static __device__ int g_append_status;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 2;        // units per thread
+constexpr int kUnits = 1;        // units per thread (two took 12.3 us against 11.9 on 12,000 ragged tokens)
 constexpr int kMaxTpb = 64;      // tokens per block
 
 struct Slot {                    // where one token goes; page < 0: nowhere

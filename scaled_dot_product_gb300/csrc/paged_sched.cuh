@@ -5,7 +5,7 @@
 // least one, so that rows with no key are written too) and OV more for its query rows and its
 // results, in tiles' time.  All units, laid end to end (sequence, row block, kv head, tile), are
 // dealt to the CTAs in equal contiguous shares of that cost (in units of 256 rows, a tile of more
-// than 128 rows counts twice), so ragged lengths, few rows over many
+// than 128 rows counts 4, one of fewer 3, and OV is in these), so ragged lengths, few rows over many
 // keys and many rows over few keys all fill the GPU alike, and a CTA meets at most two units that
 // it does not hold whole.  (Without OV, the CTA that gets the first, shortest row blocks of a
 // causal prompt had 40 units of one or two tiles and took twice as long as the others.)  Those leave partial results
@@ -71,7 +71,7 @@ __device__ __forceinline__ RowBlock row_block(const PagedAttn& a, const SeqInfo&
   r.lo = a.window > 0 ? max(0, s.T - s.n + i0 - a.window + 1) : 0;
   r.tile0 = r.lo / TN;
   r.tiles = r.hi >= r.lo ? r.hi / TN - r.tile0 + 1 : 1;
-  r.weight = TM > 128 && r.rows > 128 ? 2 : 1;
+  r.weight = TM > 128 ? (r.rows > 128 ? 4 : 3) : 1;
   return r;
 }
 __device__ __forceinline__ int row_blocks(const PagedAttn& a, const SeqInfo& s, int TM) {

@@ -39,8 +39,8 @@ using namespace ptx;
 
 constexpr int kBM = 128, kTM = 256, kTN = 128;
 constexpr int kThreads = 384;
-constexpr int kOV = 4;                // a unit's cost beside its tiles, in tiles
-constexpr int kMinShare = 12;
+constexpr int kOV = 8;                // a unit's cost beside its tiles (a tile costs 4, or 3 in a narrow unit)
+constexpr int kMinShare = 24;
 // Register split: the control warpgroup shrinks to kCtlRegs, the softmax warpgroups grow to
 // kSmxRegs; the sum stays within the launch's kThreads x kLaunchRegs, which the host checks.
 constexpr int kLaunchRegs = 168, kCtlRegs = 88, kSmxRegs = 208;
