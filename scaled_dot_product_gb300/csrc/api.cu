@@ -15,6 +15,7 @@
 #include "paged.h"
 #include "paged_sched.cuh"
 #include "prefill_tc.h"
+#include "qk_norm.h"
 
 namespace sdpa {
 

@@ -43,30 +43,6 @@ cudaError_t launch_rotary(sdpa_dtype dt, const RotaryJob* jobs, int njobs, int D
                           const void* sin_c, int R, int interleaved, cudaStream_t st);
 cudaError_t take_rotary_status(int* status);
 
-// RMS norm of query and key heads followed by the rotation, or its gradient.
-struct NormSide {
-  View x, dy, y;             // input, upstream gradient (backward), output (backward: dx)
-  const void* w;             // (D)
-  void* dw;                  // backward: (D)
-  int N;                     // heads
-};
-struct NormJob {
-  NormSide side[2];          // queries, keys
-  int B, S, tokens, D, R;    // tokens = B * S; R = 0: no rotation
-  int interleaved;
-  const void* cos_c;
-  const void* sin_c;
-  const int64_t* positions;  // (tokens), or nullptr: one cache row per token
-  int64_t max_pos;
-  float eps, inv_D;
-};
-// Most blocks of the backward: each leaves D partial sums of dw in the workspace.
-constexpr int kNormBwdMaxBlocks = 152 * 2;
-// part == nullptr: forward; else the backward with its partial sums there.
-cudaError_t launch_qk_norm(sdpa_dtype dt, const NormJob& j, float* part, cudaStream_t st);
-cudaError_t take_norm_status(int* status);
-cudaError_t take_bounds_norm(int* site);
-
 // Auxiliary qk output (B, Nq, S, T) fp32 at stage `mode` (0..3).  k_total: one view of all
 // T key rows when one exists (enables the tensor-core kernel), else nullptr.
 cudaError_t launch_qk(const Problem& p, const View* k_total, const View& out, int mode, sdpa_dtype dt,
@@ -98,10 +74,6 @@ cudaError_t take_bounds_prefill(int* site);
 cudaError_t take_bounds_decode(int* site);
 cudaError_t take_bounds_concat(int* site);
 cudaError_t take_bounds_simt(int* site);
-cudaError_t take_bounds_append(int* site);
-cudaError_t take_bounds_paged_simt(int* site);
-cudaError_t take_bounds_paged_mma(int* site);
-cudaError_t take_bounds_paged_tc(int* site);
 
 // Decode with the partials in the library's own device array (no workspace).
 size_t decode_static_scratch_bytes();

@@ -52,6 +52,10 @@ bool paged_mma_supported(const PagedAttn& a, sdpa_dtype dt);
 size_t paged_mma_workspace(const PagedAttn& a);
 cudaError_t launch_paged_mma(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
 
+cudaError_t take_bounds_append(int* site);
+cudaError_t take_bounds_paged_simt(int* site);
+cudaError_t take_bounds_paged_mma(int* site);
+cudaError_t take_bounds_paged_tc(int* site);
 cudaError_t take_paged_append_status(int* status);
 // Whether TMA boxes of at least eight rows tile the pages.
 bool paged_boxes(const PagedAttn& a);

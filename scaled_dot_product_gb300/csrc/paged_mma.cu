@@ -24,7 +24,6 @@
 #include <type_traits>
 
 #include "paged_sched.cuh"
-#include "prefill_tc.h"
 
 namespace sdpa {
 
@@ -539,10 +538,8 @@ cudaError_t launch_wm(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaStream_t
   if (paged_boxes(a)) {
     t.box = kTN;
     while (a.g.page_size % t.box) t.box >>= 1;
-    // a head's row is one 128-byte line at H = 64: fetching 256 bytes would bring another head's
-    const CUtensorMapL2promotion promote = H == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-    if (!tc_make_map(&tk, a.g.kp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, H, &t.k_ds, &t.k_dn, &t.k_db, t.box, promote) ||
-        !tc_make_map(&tv, a.g.vp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, H, &t.v_ds, &t.v_dn, &t.v_db, t.box, promote))
+    if (!paged_map(&tk, a.g, a.g.kp, H, dt, t.box, &t.k_ds, &t.k_dn, &t.k_db) ||
+        !paged_map(&tv, a.g, a.g.vp, H, dt, t.box, &t.v_ds, &t.v_dn, &t.v_db))
       return cudaErrorInvalidValue;
   }
   paged_mma_kernel<BF, H, WM><<<(unsigned)ctas, kThreads, C::kSmem, st>>>(tk, tv, t);

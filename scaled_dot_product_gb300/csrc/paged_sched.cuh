@@ -44,6 +44,8 @@ constexpr int kPagedMaxSms = 160;
 
 cudaError_t launch_paged_merge(const PagedAttn& a, sdpa_dtype dt, const PagedWs& ws, int ctas, int tm, cudaStream_t st);
 int paged_sms();
+// Tensor map over a page pool for boxes of box_rows slots.
+bool paged_map(CUtensorMap* map, const Paged& g, const View& v, int D, sdpa_dtype dt, int box_rows, int* ds, int* dn, int* db);
 // Fast division: the multiplier and shift of j / d for 0 <= j < 2^31.
 inline void paged_magic(int d, uint32_t* mul, uint32_t* shift) {
   int l = 0;

@@ -749,6 +749,36 @@ cudaError_t launch_h(bool bf, bool cap, const CUtensorMap& tq, const CUtensorMap
 
 }  // namespace
 
+// Dimension 0 is the head's channels; 1 to 3 are slot, head and page in the order of their strides
+// (ds, dn, db say where each went).  A box is 64 channels of box_rows slots.
+bool paged_map(CUtensorMap* map, const Paged& g, const View& v, int D, sdpa_dtype dt, int box_rows, int* ds, int* dn, int* db) {
+  auto enc = tc_encode_fn();
+  if (!enc) return false;
+  int order[3];
+  tc_axis_order(v, g.num_pages, g.Nkv, g.page_size, order);
+  const int64_t ext[3] = {g.page_size, g.Nkv, g.num_pages}, str[3] = {v.ss, v.sh, v.sb};
+  int* where[3] = {ds, dn, db};
+  cuuint64_t dims[4] = {(cuuint64_t)D, 1, 1, 1}, strides[3];
+  cuuint32_t box[4] = {64, 1, 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  int64_t span = D;                      // elements up to here: a legal stride for an axis of one entry
+  for (int k = 0; k < 3; ++k) {
+    const int id = order[k];
+    const int64_t st = ext[id] > 1 ? str[id] : (span + 7) / 8 * 8;
+    dims[k + 1] = (cuuint64_t)ext[id];
+    strides[k] = (cuuint64_t)(st * 2);
+    span = std::max(span, st * ext[id]);
+    if (id == 0) box[k + 1] = (cuuint32_t)box_rows;
+    *where[id] = k + 1;
+  }
+  // a head's row is one 128-byte line at D = 64: fetching 256 bytes would bring another head's (single
+  // tokens over 1.06 GB of such pages took 281 us against 203)
+  const CUtensorMapL2promotion promote = D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+  return enc(map, dt == SDPA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(v.p),
+             dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promote,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool paged_boxes(const PagedAttn& a) {
   if (a.g.page_size % 8 || a.g.num_pages < 1) return false;
   for (const View* v : {&a.g.kp, &a.g.vp})
@@ -779,11 +809,9 @@ cudaError_t launch_paged_tc(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaSt
   t.cap_in = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
   t.cap_log2 = a.softcap * kLog2e;
   t.wait_ns = wait_limit_ns();
-  // a head's row is one 128-byte line at H = 64: fetching 256 bytes would bring another head's
-  const CUtensorMapL2promotion promote = a.g.H == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   CUtensorMap tk, tv;
-  if (!tc_make_map(&tk, a.g.kp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, a.g.H, &t.k_ds, &t.k_dn, &t.k_db, t.box, promote) ||
-      !tc_make_map(&tv, a.g.vp, dt, a.g.num_pages, a.g.Nkv, a.g.page_size, a.g.Hv, &t.v_ds, &t.v_dn, &t.v_db, t.box, promote))
+  if (!paged_map(&tk, a.g, a.g.kp, a.g.H, dt, t.box, &t.k_ds, &t.k_dn, &t.k_db) ||
+      !paged_map(&tv, a.g, a.g.vp, a.g.Hv, dt, t.box, &t.v_ds, &t.v_dn, &t.v_db))
     return cudaErrorInvalidValue;
   const bool bf = dt == SDPA_BF16, cap = a.softcap > 0.f;
   CUtensorMap tq{};

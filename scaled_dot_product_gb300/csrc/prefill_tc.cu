@@ -1278,8 +1278,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // 4-D map over a (B, N, Seq, D) view: dim 0 = D (contiguous); dims 1..3 = the axes in
 // tc_axis_order.  Box: 64 x 128 rows.
 bool make_map(CUtensorMap* map, const View& v, sdpa_dtype dt, int64_t B, int64_t N, int64_t Sq, int D, int* ds,
-              int* dn, int* db, int box_rows = kBN,
-              CUtensorMapL2promotion promote = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+              int* dn, int* db, int box_rows = kBN) {
   auto enc = encode_fn();
   if (!enc) return false;
   const int64_t ext[3] = {Sq, N, B};
@@ -1305,7 +1304,7 @@ bool make_map(CUtensorMap* map, const View& v, sdpa_dtype dt, int64_t B, int64_t
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, dt == SDPA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                    const_cast<void*>(v.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -1521,8 +1520,8 @@ cudaError_t launch_prefill_tc_stats(const Problem& p, sdpa_dtype dt, float* lse2
 PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn() { return encode_fn(); }
 
 bool tc_make_map(CUtensorMap* map, const View& v, sdpa_dtype dt, int64_t B, int64_t N, int64_t Sq, int D, int* ds,
-                 int* dn, int* db, int box_rows, CUtensorMapL2promotion promote) {
-  return make_map(map, v, dt, B, N, Sq, D, ds, dn, db, box_rows, promote);
+                 int* dn, int* db, int box_rows) {
+  return make_map(map, v, dt, B, N, Sq, D, ds, dn, db, box_rows);
 }
 
 cudaError_t take_prefill_status(int* status) {

@@ -24,8 +24,7 @@ bool tc_same_axis_order(const View& k, const View& v, int64_t B, int64_t N, int6
 // swizzle); ds / dn / db receive the map dimension of seq / head / batch.
 PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn();
 bool tc_make_map(CUtensorMap* map, const View& v, sdpa_dtype dt, int64_t B, int64_t N, int64_t Sq, int D, int* ds,
-                 int* dn, int* db, int box_rows = 128,
-                 CUtensorMapL2promotion promote = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+                 int* dn, int* db, int box_rows = 128);
 
 // Launches the fused kernel; p.k / p.v must hold all T key rows (P == 0, no kv bias).
 cudaError_t launch_prefill_tc(const Problem& p, sdpa_dtype dt, cudaStream_t st, const char** name);

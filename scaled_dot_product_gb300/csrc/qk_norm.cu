@@ -15,7 +15,7 @@
 // row, the row in shared memory), as do fp32 heads of more than 128 channels.
 #include <algorithm>
 
-#include "internal.h"
+#include "qk_norm.h"
 #include "tc_ptx.cuh"
 
 namespace sdpa {
