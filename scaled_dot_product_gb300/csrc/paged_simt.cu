@@ -3,7 +3,9 @@
 //
 // LPK lanes read one key or value row as 16-byte vectors; the 128 / LPK lane groups of a block
 // take different keys and keep their own running maximum, sum and accumulator of TM query rows,
-// joined in shared memory at the end of a unit.  It serves fp32 (whose sums the 16-bit tensor
+// joined in shared memory at the end of a unit.  Bound by latency: eight float32 sequences of 500 to 4000
+// keys, 16/4 heads of 64, take 22 to 27 us (38.8 MB); 30.5 us with 64 full reductions a step instead of 15
+// exchanges, 34.6 with four CTAs an SM, 24.2 with two.  It serves fp32 (whose sums the 16-bit tensor
 // products cannot carry) and head sizes that the tensor-core kernels do not tile.
 #include <algorithm>
 
