@@ -357,8 +357,9 @@ SDPA_API int sdpa_paged_append(const sdpa_paged_params* p, sdpa_view k, sdpa_vie
  * cu_new[B] are left as they were; what lies in slots past a sequence's keys does not matter
  * (NaN included).  Lengths out of range are clamped and reported; a page id out of range is
  * reported and its keys and values read as zeros.
- * workspace: sdpa_paged_workspace_size(p) bytes (it depends on sizes, not on lengths), 256-byte
- * aligned.  Alignment as for sdpa_paged_append. */
+ * workspace: sdpa_paged_workspace_size(p) bytes (it depends on types, head sizes, page_size and the
+ * kernel that max_new picks, not on lengths), any contents, 256-byte aligned.  Alignment as for
+ * sdpa_paged_append. */
 SDPA_API int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace,
                              size_t workspace_bytes, sdpa_stream_t stream);
 SDPA_API size_t sdpa_paged_workspace_size(const sdpa_paged_params* p);

@@ -32,6 +32,13 @@ constexpr int kThreads = 256;
 constexpr int kFwdThreads = 128;
 constexpr int kMaxD = 256;
 
+// 16-byte asynchronous copy, or 16 zero bytes; waits until at most N groups are on their way.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Position of token tok, and its row in the caches: a position outside them is recorded and
 // clamped.
 __device__ __forceinline__ int64_t position(const NormJob& j, int tok) { return j.positions ? j.positions[tok] : tok; }
@@ -281,7 +288,8 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_scalar_kernel(const NormJob
 // block order, so results do not vary from run to run.  Bound by the latency of the two chained
 // sums at 16 warps an SM: one head at a time took 72 us on 8192 tokens x 40 heads, tasks of 16
 // heads 71, three blocks an SM (spills) 81, this 53.
-constexpr int kHeads = 8, kPair = 2;
+constexpr int kHeads = 8, kPair = 2, kRing = 4;
+constexpr int kRingBytes = kRing * kPair * 2 * kThreads * 16;
 constexpr int kBwdBlocks = 2;
 template <typename T, bool kInter, int LPR>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_bwd_kernel(const NormJob j, const int q_blocks,
@@ -289,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_bwd_kernel(const No
   constexpr int V = 16 / (int)sizeof(T), P = V / 2;
   constexpr int kGroups = kThreads / LPR;
   __shared__ float red[kGroups][LPR * V + 1];
+  extern __shared__ uint4 ring[];    // [kRing][kPair][x, dy][kThreads]
   const bool is_k = (int)blockIdx.x >= q_blocks;
   const NormSide& sd = j.side[is_k];
   const unsigned nblk = is_k ? gridDim.x - q_blocks : q_blocks;
@@ -303,73 +312,84 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_bwd_kernel(const No
   for (int e = 0; e < P; ++e) dw[e] = f2_zero();
 
   // Every group of a block runs kHeads / kPair steps per task (the shuffles need whole warps); heads
-  // past the task's nh, and tasks past the last (nh = 0), touch no memory.
-  const T *xr = nullptr, *gr = nullptr;
-  T* dr = nullptr;
-  int nh = 0;
-  unsigned tok = 0;
-  int64_t pos = 0;                   // of the task to come: on its way before place() needs it
-  auto look_ahead = [&](unsigned t0) {
+  // past the task's, and tasks past the last, touch no memory.  `ahead` brings the steps to come:
+  // every thread copies its own vectors into its own slots of the ring, so no barrier is needed.
+  const unsigned stride = nblk * kGroups;
+  struct Cursor { const T *x, *g; T* d; unsigned tok; int n; };
+  auto place = [&](unsigned t0, Cursor& c) {
     const unsigned task = t0 + grp;
+    c.n = 0;
     if (t0 >= tasks || task >= tasks) return;
-    tok = task / chunks;
-    if (j.R > 0) pos = position(j, (int)tok);
+    c.tok = task / chunks;
+    const int h0 = (int)(task - c.tok * chunks) * kHeads;
+    const int b = (int)(c.tok / (unsigned)j.S), s = (int)(c.tok - (unsigned)b * (unsigned)j.S);
+    c.n = min(kHeads, sd.N - h0);
+    c.x = reinterpret_cast<const T*>(sd.x.p) + sd.x.off(b, h0, s) + ln.c0;
+    c.g = reinterpret_cast<const T*>(sd.dy.p) + sd.dy.off(b, h0, s) + ln.c0;
+    c.d = reinterpret_cast<T*>(const_cast<void*>(sd.y.p)) + sd.y.off(b, h0, s);
+    if (!SDPA_IN_BOUNDS(b < j.B && h0 + c.n <= sd.N && s < j.S, 502)) c.n = 0;
   };
-  auto place = [&](unsigned t0) {
-    const unsigned task = t0 + grp;
-    nh = 0;
-    if (t0 >= tasks || task >= tasks) return;
-    const int h0 = (int)(task - tok * chunks) * kHeads;
-    const int b = (int)(tok / (unsigned)j.S), s = (int)(tok - (unsigned)b * (unsigned)j.S);
-    nh = min(kHeads, sd.N - h0);
-    xr = reinterpret_cast<const T*>(sd.x.p) + sd.x.off(b, h0, s);
-    gr = reinterpret_cast<const T*>(sd.dy.p) + sd.dy.off(b, h0, s);
-    dr = reinterpret_cast<T*>(const_cast<void*>(sd.y.p)) + sd.y.off(b, h0, s);
-    if (!SDPA_IN_BOUNDS(b < j.B && h0 + nh <= sd.N && s < j.S, 502)) nh = 0;
-    if (j.R > 0) {
-      const int64_t row = cache_row(j, pos) * (j.R / 2);
-      ln.load_cs(reinterpret_cast<const T*>(j.cos_c) + row, reinterpret_cast<const T*>(j.sin_c) + row);
-    }
-  };
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 x[kPair], g[kPair];
-  // the kPair heads from i on of the task that `place` set
-  auto fetch = [&](int i, uint4* xv, uint4* gv) {
+  unsigned at = blk * kGroups;       // task row of the copies
+  int ai = 0, put = 0;               // first head of the copies' step, its ring slot
+  Cursor fetch{};
+  auto ahead = [&]() {
+    if (at < tasks) {
+      if (ai == 0) place(at, fetch);
 #pragma unroll
-    for (int k = 0; k < kPair; ++k) {
-      xv[k] = gv[k] = zero;
-      if (i + k < nh) {
-        xv[k] = ln.load(xr);
-        gv[k] = ln.load(gr);
-        xr += sd.x.sh;
-        gr += sd.dy.sh;
+      for (int k = 0; k < kPair; ++k) {
+        const bool take = ai + k < fetch.n && ln.live;
+        const uint32_t slot = smem_u32(ring) + (uint32_t)(((put * kPair + k) * 2) * kThreads + threadIdx.x) * 16;
+        cp_async16_or_zero(slot, take ? fetch.x : reinterpret_cast<const T*>(sd.w), take);
+        cp_async16_or_zero(slot + kThreads * 16, take ? fetch.g : reinterpret_cast<const T*>(sd.w), take);
+        fetch.x += sd.x.sh;
+        fetch.g += sd.dy.sh;
+      }
+      ai += kPair;
+      if (ai == kHeads) {
+        ai = 0;
+        at += stride;
       }
     }
+    cp_async_commit();
+    put = put + 1 == kRing ? 0 : put + 1;
   };
-  look_ahead(blk * kGroups);
-  place(blk * kGroups);
-  fetch(0, x, g);
-  for (unsigned t0 = blk * kGroups; t0 < tasks; t0 += nblk * kGroups) {
+#pragma unroll 1
+  for (int i = 0; i < kRing - 1; ++i) ahead();
+  Cursor now{}, next{};
+  int64_t pos = 0;                   // position of the next task's token: on its way before it is needed
+  place(blk * kGroups, now);
+  auto load_cs = [&](const Cursor& c) {
+    if (j.R == 0 || c.n == 0) return;
+    const int64_t row = cache_row(j, pos) * (j.R / 2);
+    ln.load_cs(reinterpret_cast<const T*>(j.cos_c) + row, reinterpret_cast<const T*>(j.sin_c) + row);
+  };
+  if (j.R > 0 && now.n > 0) pos = position(j, (int)now.tok);
+  load_cs(now);
+  int get = 0;
+  for (unsigned t0 = blk * kGroups; t0 < tasks; t0 += stride) {
     ln.factors(C, S, -1.f);
-    const int n = nh;
-    T* d = dr;
-    look_ahead(t0 + nblk * kGroups);
+    T* d = now.d;
+    const int n = now.n;
+    place(t0 + stride, next);
+    if (j.R > 0 && next.n > 0) pos = position(j, (int)next.tok);
 #pragma unroll 1
     for (int i = 0; i < kHeads; i += kPair) {
-      uint4 xn[kPair], gn[kPair];
-      if (i + kPair < kHeads) {
-        fetch(i + kPair, xn, gn);
-      } else {
-        place(t0 + nblk * kGroups);
-        fetch(0, xn, gn);
-      }
+      cp_async_wait<kRing - 2>();
       f2_t f[kPair][P], q[kPair][P], m[kPair][P];
       float ss[kPair], dot[kPair];
 #pragma unroll
       for (int k = 0; k < kPair; ++k) {
-        to_pairs<T>(x[k], f[k]);
-        to_pairs<T>(g[k], q[k]);
-        ln.mates(g[k], q[k], m[k]);
+        const uint4 x = ring[((get * kPair + k) * 2) * kThreads + threadIdx.x];
+        const uint4 g = ring[((get * kPair + k) * 2 + 1) * kThreads + threadIdx.x];
+        to_pairs<T>(x, f[k]);
+        to_pairs<T>(g, q[k]);
+        ln.mates(g, q[k], m[k]);
+      }
+      get = get + 1 == kRing ? 0 : get + 1;
+      ahead();
+      if (i + kPair >= kHeads) load_cs(next);
+#pragma unroll
+      for (int k = 0; k < kPair; ++k) {
         f2_t s2 = f2_zero(), d2 = f2_zero();
 #pragma unroll
         for (int e = 0; e < P; ++e) {
@@ -403,11 +423,11 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_bwd_kernel(const No
           ln.store(d, f[k]);
           d += sd.y.sh;
         }
-        x[k] = xn[k];
-        g[k] = gn[k];
       }
     }
+    now = next;
   }
+  cp_async_wait_all();
 #pragma unroll
   for (int e = 0; e < P; ++e) f2_unpack(dw[e], red[grp][u * V + 2 * e], red[grp][u * V + 2 * e + 1]);
   __syncthreads();
@@ -569,9 +589,12 @@ template <typename T, bool kInter, int LPR>
 cudaError_t run_bwd(const NormJob& j, float* part, cudaStream_t st) {
   int qb, kb;
   bwd_blocks(j, side_blocks(j, 0, kThreads, LPR, kHeads), side_blocks(j, 1, kThreads, LPR, kHeads), &qb, &kb);
-  norm_bwd_kernel<T, kInter, LPR><<<(unsigned)(qb + kb), kThreads, 0, st>>>(j, qb, part);
+  // per device: set at every call (the attribute belongs to the current context)
+  cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<T, kInter, LPR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e != cudaSuccess) return e;
+  norm_bwd_kernel<T, kInter, LPR><<<(unsigned)(qb + kb), kThreads, kRingBytes, st>>>(j, qb, part);
   count_launch(1);
-  const cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   return e == cudaSuccess ? finish_dw<T>(j, part, qb, kb, st) : e;
 }
 
