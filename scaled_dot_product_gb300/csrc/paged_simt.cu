@@ -4,8 +4,8 @@
 // LPK lanes read one key or value row as 16-byte vectors; the 128 / LPK lane groups of a block
 // take different keys and keep their own running maximum, sum and accumulator of TM query rows,
 // joined in shared memory at the end of a unit.  Bound by latency: eight float32 sequences of 500 to 4000
-// keys, 16/4 heads of 64, take 22 to 27 us (38.8 MB); 30.5 us with 64 full reductions a step instead of 15
-// exchanges, 34.6 with four CTAs an SM, 24.2 with two.  It serves fp32 (whose sums the 16-bit tensor
+// keys, 16/4 heads of 64, take 20 to 21 us (38.8 MB); 30.5 us with 64 full reductions a step instead of 15
+// exchanges and one thread an item of the join, 34.6 with four CTAs an SM.  It serves fp32 (whose sums the 16-bit tensor
 // products cannot carry) and head sizes that the tensor-core kernels do not tile.
 #include <algorithm>
 
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kCtasPerSm : 2) paged_simt
 
 constexpr int kMergeThreads = 256;
 
-// How a joined unit is cut: a block takes `rows` rows (8, 16 or 32) and `cols` groups of four
+// How a joined unit is cut: a block takes `rows` rows (a power of two up to 32) and `cols` groups of four
 // columns; with fewer than 256 of these items, 256 / (rows * cols) threads share one, each taking
 // a part of the partial results.
 struct MergeCut { int rows, cols; };
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   auto slot_of = [&](int i) -> int64_t { return (i == 0 ? 2 * (int64_t)(c - 1) + 1 : 2 * (int64_t)(c + i - 1)) * TM; };
 
   const int items = cut.rows * cut.cols, share = max(1, kMergeThreads / items);      // threads of one item
-  if (n <= 4 && share == 1) {
+  if (n <= 4) {
     // Few partials: a thread reads all of an item's at once, beside the lengths, and finds the row's
     // maximum and sum by itself.  (Every slot of a joined unit holds TM rows; those past the unit's
     // rows are not used.)
@@ -337,10 +337,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   const RowBlock rbk = row_block<TM, TN>(a, s, at.rb);
   if (row0 >= rbk.rows) return;
 
-  // maximum and sum of each row, 256 / rows threads (8, 16 or 32) a row
+  // maximum and sum of each row, 256 / rows threads (8, 16 or 32 at most) a row
   {
-    const int tpr = kMergeThreads / cut.rows, r = threadIdx.x / tpr, sub = threadIdx.x % tpr;
-    const bool live = row0 + r < rbk.rows;
+    const int tpr = min(32, kMergeThreads / cut.rows), r = threadIdx.x / tpr, sub = threadIdx.x % tpr;
+    const bool live = r < cut.rows && row0 + r < rbk.rows;
     float M = -INFINITY, L = 0.f;
     for (int i = sub; i < n && live; i += tpr) {
       const float2 v = *reinterpret_cast<const float2*>(ws.ml + (slot_of(i) + row0 + r) * 2);
@@ -364,51 +364,59 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
   __syncthreads();
 
   const int per = kMergeThreads / share, g0 = threadIdx.x / per;
-  for (int x = threadIdx.x % per; x < items; x += per) {
+  // the sum of item x over partials g0, g0 + share, ...
+  auto sum_of = [&](int x) {
     const int r = x / cut.cols, d = (col0 + x % cut.cols) * 4;
-    const bool live = row0 + r < rbk.rows && d < cols_all * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-      const float M = sm_m[r];
+    if (row0 + r >= rbk.rows || d >= cols_all * 4) return v;
+    const float M = sm_m[r];
 #pragma unroll 4
-      for (int i = g0; i < n; i += share) {
-        const int64_t at_row = slot_of(i) + row0 + r;
-        const float mm = ws.ml[at_row * 2];
-        const float4 o = *reinterpret_cast<const float4*>(ws.o + at_row * g.Hv + d);
-        const float f = mm == -INFINITY ? 0.f : exp2f(mm - M);
-        v.x = fmaf(f, o.x, v.x);
-        v.y = fmaf(f, o.y, v.y);
-        v.z = fmaf(f, o.z, v.z);
-        v.w = fmaf(f, o.w, v.w);
-      }
+    for (int i = g0; i < n; i += share) {
+      const int64_t at_row = slot_of(i) + row0 + r;
+      const float mm = ws.ml[at_row * 2];
+      const float4 o = *reinterpret_cast<const float4*>(ws.o + at_row * g.Hv + d);
+      const float f = mm == -INFINITY ? 0.f : exp2f(mm - M);
+      v.x = fmaf(f, o.x, v.x);
+      v.y = fmaf(f, o.y, v.y);
+      v.z = fmaf(f, o.z, v.z);
+      v.w = fmaf(f, o.w, v.w);
     }
-    if (share > 1) {                           // one pass: items < 256
-      part[threadIdx.x] = v;
-      __syncthreads();
-      if (g0 > 0) return;
-      for (int k = 1; k < share; ++k) {
-        const float4 w = part[threadIdx.x + k * per];
-        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
-      }
-    }
-    if (live && SDPA_IN_BOUNDS(s.t0 + group_div(g, rbk.row0 + row0 + r) < g.tokens, 524)) {
-      const float inv = sm_inv[r];
-      T out[4] = {Elem<T>::from_f32(v.x * inv), Elem<T>::from_f32(v.y * inv), Elem<T>::from_f32(v.z * inv),
-                  Elem<T>::from_f32(v.w * inv)};
-      T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + sm_y[r] + d;
-      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(out);
-      else *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(out);
-    }
+    return v;
+  };
+  auto store = [&](int x, const float4& v) {
+    const int r = x / cut.cols, d = (col0 + x % cut.cols) * 4;
+    if (row0 + r >= rbk.rows || d >= cols_all * 4) return;
+    if (!SDPA_IN_BOUNDS(s.t0 + group_div(g, rbk.row0 + row0 + r) < g.tokens, 524)) return;
+    const float inv = sm_inv[r];
+    T out[4] = {Elem<T>::from_f32(v.x * inv), Elem<T>::from_f32(v.y * inv), Elem<T>::from_f32(v.z * inv),
+                Elem<T>::from_f32(v.w * inv)};
+    T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + sm_y[r] + d;
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(out);
+    else *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(out);
+  };
+  if (share == 1) {
+    for (int x = threadIdx.x; x < items; x += kMergeThreads) store(x, sum_of(x));
+    return;
   }
+  const int x = threadIdx.x % per;               // fewer items than threads: one each, every thread at the barrier
+  if (x < items) part[threadIdx.x] = sum_of(x);
+  __syncthreads();
+  if (g0 > 0 || x >= items) return;
+  float4 v = part[x];
+  for (int k = 1; k < share; ++k) {
+    const float4 w = part[x + k * per];
+    v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+  }
+  store(x, v);
 }
 
 template <typename T, int TM, int TN>
 cudaError_t merge_tn(const PagedAttn& a, const PagedWs& ws, int ctas, cudaStream_t st) {
   // Few units are cut into many partials each (16 and more): then 8 rows and 32 columns a block, four threads an
-  // item.  Otherwise whole rows, 16 (or 32 of a 256-row unit) a block.
+  // item.  Otherwise whole rows, at most 16 (or 32 of a 256-row unit) a block.
   const int cols = a.g.Hv / 4;
   const bool few = TM <= 64 && (int64_t)a.g.B * a.g.Nkv < ctas / 16;
-  const MergeCut cut = few ? MergeCut{8, 8} : MergeCut{TM == 256 ? 32 : 16, cols};
+  const MergeCut cut = few ? MergeCut{std::min(TM, 8), 8} : MergeCut{TM == 256 ? 32 : std::min(TM, 16), cols};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)std::max(1, ctas - 1), (unsigned)((TM + cut.rows - 1) / cut.rows),
                      (unsigned)((cols + cut.cols - 1) / cut.cols));

@@ -12,7 +12,7 @@
 // save those shuffles but took 118 registers forward and 174 backward, and the loads in flight
 // with them: 20.9 and 98.7 us on the first and last of these.)  On the device, bf16, heads of 128:
 // 4096 tokens x 40 heads forward 17.0 us (4.98 TB/s), 4503 tokens x 72 float16 heads of 64 15.0 us
-// (5.55 TB/s), backward of 8192 tokens x 40 heads 53.3 us (4.75 TB/s).
+// (5.55 TB/s), backward of 8192 tokens x 40 heads 50.7 us (5.0 TB/s).
 // Shapes or pointers that do not allow 16-byte vectors take the scalar kernels (one warp per
 // row, the row in shared memory), as do fp32 heads of more than 128 channels.
 #include <algorithm>
@@ -283,11 +283,12 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_scalar_kernel(const NormJob
 
 // Persistent: blocks [0, q_blocks) walk the query tasks, the others the key tasks, so a lane
 // accumulates dw for the one weight vector of its side.  A task is up to kHeads heads of one
-// token, taken kPair at a time, whose sums' shuffles overlap; the next pair's x and dy are on their
-// way meanwhile.  Each block leaves its D sums in part[blockIdx.x]; norm_dw_kernel adds them in
+// token, taken kPair at a time, whose sums' shuffles overlap; the next kRing - 1 pairs' x and dy are on
+// their way into shared memory meanwhile.  Each block leaves its D sums in part[blockIdx.x]; norm_dw_kernel adds them in
 // block order, so results do not vary from run to run.  Bound by the latency of the two chained
 // sums at 16 warps an SM: one head at a time took 72 us on 8192 tokens x 40 heads, tasks of 16
-// heads 71, three blocks an SM (spills) 81, this 53.
+// heads 71, three blocks an SM (spills) 90, the next pair in registers instead of the ring 53.3, equal
+// contiguous shares of the rows instead of tasks in turn 54.3, this 50.7.
 constexpr int kHeads = 8, kPair = 2, kRing = 4;
 constexpr int kRingBytes = kRing * kPair * 2 * kThreads * 16;
 constexpr int kBwdBlocks = 2;

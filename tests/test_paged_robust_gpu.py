@@ -67,6 +67,17 @@ def test_group_sizes(group):
         assert ((y.cpu().double() - want).abs() <= tol).all(), sdpa.sdpa_last_kernel_name()
 
 
+@pytest.mark.parametrize("dtype,H,Hv", [(HF, 96, 96), (FP, 64, 20), (FP, 128, 4), (BF, 128, 128), (HF, 64, 64), (BF, 256, 200)])
+@pytest.mark.parametrize("Nq,Nkv,new", [(1, 1, [1]), (5, 1, [1]), (2, 2, [1, 3]), (8, 8, [2, 1, 1])])
+def test_many_partial_results(dtype, H, Hv, Nq, Nkv, new):
+    """Long sequences in few units: each is cut over many CTAs, whose partial results are joined in
+    every way the joining kernel cuts its work (head sizes that are no power of two among them)."""
+    r = ragged(new, [9000, 700, 5000][:len(new)], dtype=dtype, H=H, Hv=Hv, page=32, Nq=Nq, Nkv=Nkv, seed=H + Hv)
+    want, tol = paged_attn64(r)
+    y = attn(r, max_new=max(new))
+    assert ((y.cpu().double() - want).abs() <= tol).all(), sdpa.sdpa_last_kernel_name()
+
+
 def test_keys_that_are_not_numbers_outside_the_window():
     """Pages below every row's window may be gone (their ids are not looked at), and what lies past
     a sequence's keys is not a number."""
