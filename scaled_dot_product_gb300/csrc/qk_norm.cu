@@ -11,7 +11,7 @@
 // pair layout the packed partners come from another lane.  (Two vectors a lane, pairs together,
 // save those shuffles but took 118 registers forward and 174 backward, and the loads in flight
 // with them: 20.9 and 98.7 us on the first and last of these.)  On the device, bf16, heads of 128:
-// 4096 tokens x 40 heads forward 17.0 us (4.98 TB/s), 4503 tokens x 72 float16 heads of 64 15.0 us
+// 4096 tokens x 40 heads forward 16.5 us (5.1 TB/s), 4503 tokens x 72 float16 heads of 64 15.0 us
 // (5.55 TB/s), backward of 8192 tokens x 40 heads 50.7 us (5.0 TB/s).
 // Shapes or pointers that do not allow 16-byte vectors take the scalar kernels (one warp per
 // row, the row in shared memory), as do fp32 heads of more than 128 channels.
@@ -186,7 +186,7 @@ struct Lane {
 // once for them and folded into two factors a channel, y = r (x (w C) + mate(x) (mate(w) S)), and
 // HPG x 16 bytes are in flight per lane.
 template <typename T, bool kInter, int LPR, int HPG>
-__global__ void __launch_bounds__(kFwdThreads) norm_fwd_kernel(const NormJob j, const int q_blocks) {
+__global__ void __launch_bounds__(kFwdThreads, 10) norm_fwd_kernel(const NormJob j, const int q_blocks) {
   constexpr int V = 16 / (int)sizeof(T), P = V / 2;
   const bool is_k = (int)blockIdx.x >= q_blocks;
   const NormSide& sd = j.side[is_k];
