@@ -101,19 +101,21 @@ struct Share {
 // least cost worth a CTA.
 template <int TM, int TN, int OV, int NT>
 __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int ctas, int min_share, int* status) {
-  constexpr int kW = NT / 32;
+  constexpr int kW = NT / 32, kChunks = 32;
   __shared__ long long sh_sum[kW + 1];
+  __shared__ long long sh_chunk[kChunks];      // costs of NT sequences each, the last of all that follow
   __shared__ ShareStart sh_at;
   __shared__ SeqInfo sh_s;
   __shared__ int sh_pos;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool bad = false;
 
-  // costs of the sequences, NT at a time; sequences of several row blocks are summed by a warp
-  auto cost_of = [&](int b, SeqInfo& s) -> long long {
+  if (threadIdx.x < kChunks) sh_chunk[threadIdx.x] = 0;
+  __syncthreads();
+  auto info_of = [&](int b) { return b < a.g.B ? seq_info(a.g, b, bad) : SeqInfo{0, 0, 0}; };
+  // cost of this thread's sequence; sequences of several row blocks are summed by the warp
+  auto cost_of = [&](const SeqInfo& s) -> long long {
     long long c = 0;
-    s = SeqInfo{0, 0, 0};
-    if (b < a.g.B) s = seq_info(a.g, b, bad);
     const int nrb = row_blocks(a, s, TM);
     if (nrb == 1) c = unit_cost(row_block<TM, TN>(a, s, 0), OV);
     unsigned many = __ballot_sync(0xffffffffu, nrb > 1);
@@ -134,20 +136,21 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
     return c * a.g.Nkv;
   };
 
-  long long total = 0;
-  SeqInfo s;
   long long mine = 0;
-  for (int base = 0; base < a.g.B; base += NT) {
-    mine = cost_of(base + (int)threadIdx.x, s);
+  SeqInfo s = info_of(threadIdx.x);
+  for (int base = 0, chunk = 0; base < a.g.B; base += NT, ++chunk) {
+    const SeqInfo next = base + NT < a.g.B ? info_of(base + NT + (int)threadIdx.x) : SeqInfo{0, 0, 0};
+    mine = cost_of(s);
     long long v = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) sh_sum[warp] = v;
-    __syncthreads();
-#pragma unroll 1
-    for (int w = 0; w < kW; ++w) total += sh_sum[w];
-    __syncthreads();
+    if (lane == 0 && v) atomicAdd(reinterpret_cast<unsigned long long*>(&sh_chunk[min(chunk, kChunks - 1)]), (unsigned long long)v);
+    if (base + NT < a.g.B) s = next;
   }
+  __syncthreads();
+  const int chunks = min(kChunks, (a.g.B + NT - 1) / NT);
+  long long total = 0;
+  for (int c = 0; c < chunks; ++c) total += sh_chunk[c];
   if (bad && cta == 0) atomicOr(status, kPagedBadLength);
 
   Share r;
@@ -171,10 +174,15 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
   const long long begin_at = cta * each + min((long long)cta, more);
   r.count = each + (cta < more ? 1 : 0);
 
-  // the sequence that holds begin_at
+  // the sequence that holds begin_at, from its chunk on
   long long before = 0;
-  for (int base = 0; base < a.g.B; base += NT) {
-    if (a.g.B > NT) mine = cost_of(base + (int)threadIdx.x, s);
+  int from = 0;
+  while (from + 1 < chunks && before + sh_chunk[from] <= begin_at) before += sh_chunk[from++];
+  for (int base = from * NT; base < a.g.B; base += NT) {
+    if (a.g.B > NT) {
+      s = info_of(base + (int)threadIdx.x);
+      mine = cost_of(s);
+    }
     long long v = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
