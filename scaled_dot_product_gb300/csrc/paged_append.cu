@@ -51,7 +51,7 @@ __device__ __forceinline__ Slot find_slot(const Paged& g, const PagedRot& rot, i
   bool bad = false;
   const SeqInfo q = seq_info(g, b, bad);
   const int pos = q.T - q.n + (t - q.t0);
-  if (t < q.t0 || pos < 0 || bad) {            // before the first sequence, or lengths that contradict
+  if (t < q.t0 || q.T < q.n || bad) {          // before the first sequence, or lengths that contradict
     atomicOr(&g_append_status, kPagedBadLength);
     return s;
   }

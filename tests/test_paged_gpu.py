@@ -105,8 +105,13 @@ def test_append_skips_and_reports_bad_data():
     for change in (lambda r: r.kv_lens.__setitem__(1, 10 ** 6), lambda r: r.kv_lens.__setitem__(1, -3),
                    lambda r: r.kv_lens.__setitem__(1, 2), lambda r: r.cu.__setitem__(3, 10 ** 6),
                    lambda r: r.cu.__setitem__(1, -9), lambda r: r.cu.__setitem__(0, 1)):
-        _, _, rc, msg = run(change)
+        r, d, rc, msg = run(change)
         assert rc == sdpa.SDPA_ERR_INVALID and "cu_new" in msg
+    # a sequence with fewer keys than new tokens is skipped as a whole, the others arrive
+    r, d, _, _ = run(lambda r: r.kv_lens.__setitem__(1, 2))
+    pages = r.table[1, :3].long()
+    assert torch.equal(bits(d.vp.cpu()[pages]), bits(r.vp[pages])) and torch.equal(bits(d.kp.cpu()[pages]), bits(r.kp[pages]))
+    assert torch.equal(d.vp.cpu()[r.table[0, 0], :, 4:6].transpose(0, 1), r.v[:2])
     cos, sin = (t.cuda() for t in rope_caches(22, 32, BF))
     _, _, rc, msg = run(lambda r: None, cos_cache=cos, sin_cache=sin)
     assert rc == sdpa.SDPA_ERR_INVALID and "position" in msg
