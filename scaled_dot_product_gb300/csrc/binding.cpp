@@ -390,7 +390,8 @@ PyObject* paged_attn(Args& a) {
   const int64_t shape[3] = {q.size(0), q.size(1), p.Hv};
   Tensor y = py ? *py : at::empty(shape, q.options().requires_grad(false));
   typed(pl, &y, "y", type, shape);
-  Tensor ws = pws ? *pws : at::empty({std::max<int64_t>(1, (int64_t)size(&p))}, q.options().dtype(at::kByte).requires_grad(false));
+  const auto bytes = q.options().dtype(at::kByte).requires_grad(false);
+  Tensor ws = pws ? *pws : at::empty({std::max<int64_t>(1, (int64_t)size(&p))}, bytes);
   typed(pl, &ws, "workspace", ws.scalar_type(), ws.sizes());
   const int rc = fn(&p, packed(q, "q"), packed(y, "y"), ws.data_ptr(), ws.nbytes(), st);
   return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(y);

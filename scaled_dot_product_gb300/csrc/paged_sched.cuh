@@ -26,7 +26,9 @@ struct PagedWs {
   float* ml;           // [2 * ctas][TM][2]: running maximum (log2 units) and sum
   float* o;            // [2 * ctas][TM][Hv]
 };
-__host__ __device__ inline size_t paged_ws_ml_off(int ctas) { return (((size_t)ctas + 1) * sizeof(ShareStart) + 255) & ~(size_t)255; }
+__host__ __device__ inline size_t paged_ws_ml_off(int ctas) {
+  return (((size_t)ctas + 1) * sizeof(ShareStart) + 255) & ~(size_t)255;
+}
 __host__ __device__ inline size_t paged_ws_o_off(int ctas, int tm) {
   return paged_ws_ml_off(ctas) + (((size_t)2 * ctas * tm * 2 * sizeof(float) + 255) & ~(size_t)255);
 }
@@ -144,7 +146,9 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
     long long v = mine;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0 && v) atomicAdd(reinterpret_cast<unsigned long long*>(&sh_chunk[min(chunk, kChunks - 1)]), (unsigned long long)v);
+    // integers: the order of the additions does not matter
+    auto* sum = reinterpret_cast<unsigned long long*>(&sh_chunk[min(chunk, kChunks - 1)]);
+    if (lane == 0 && v) atomicAdd(sum, (unsigned long long)v);
     if (base + NT < a.g.B) s = next;
   }
   __syncthreads();

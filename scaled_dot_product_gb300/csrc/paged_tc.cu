@@ -4,8 +4,8 @@
 // Bound by the tensor cores.  A unit is 256 packed rows (token x group head) of one (sequence,
 // kv head): two 128-row tiles that stream the same keys and values.  A unit of at most 128 rows (a
 // single token beside chunks) has one tile of rows; there the two softmax warpgroups take turns with
-// the keys, even tiles and odd ones with their own maximum, sum and accumulator, joined at its end.  One CTA per SM walks its share (paged_sched.cuh) of all units'
-// 128-key tiles:
+// the keys, even tiles and odd ones with their own maximum, sum and accumulator, joined at its end.
+// One CTA per SM walks its share (paged_sched.cuh) of all units' 128-key tiles:
 //
 //   warp 0      K tiles into the ring by TMA, and query tiles where the group divides 128.  A tile is
 //               128 / box boxes of box = gcd(page_size, 128) rows, each inside one page; lane by lane
@@ -19,12 +19,11 @@
 //
 // A chunk of 2048 tokens over 32000 keys, 32/8 heads of 128: 732 us, 1500 TFLOP/s (79 % of the
 // measured bf16 burst rate); a causal prompt of 4096 tokens 125 us, 1090 TFLOP/s; single tokens through
-// this kernel 6.4 TB/s.  Running maxima move only when they grow by more than 2^8.  Every wait is bounded: on expiry the
-// kernel raises an abort flag, lets its own copies and products finish, frees its tensor memory
-// and records SDPA_ERR_TIMEOUT.
+// this kernel 6.4 TB/s.  Running maxima move only when they grow by more than 2^8.  Every wait is
+// bounded: on expiry the kernel raises an abort flag, lets its own copies and products finish, frees
+// its tensor memory and records SDPA_ERR_TIMEOUT.
 #include <algorithm>
 #include <cstdlib>
-#include <mutex>
 #include <type_traits>
 
 #include "paged_sched.cuh"
@@ -60,7 +59,8 @@ struct Cfg {
   static constexpr int kStages = kFit < 10 ? kFit : 10;
   static constexpr int kYOff = kKVOff + kStages * kTile;
   static constexpr int kSmem = kYOff + 8 * kYWarp + 1024;
-  static_assert(kSmem <= 232448 && kStages >= 4, "shared memory");
+  // 227 KB per block, of which the barriers and the share take less than 2 KB
+  static_assert(kSmem + 2048 <= 232448 && kStages >= 4, "shared memory");
   // with H = 128 P_X overwrites S_X's first columns
   static constexpr bool kAlias = H == 128;
   static constexpr int kO0 = 256, kO1 = 256 + H;
@@ -727,7 +727,8 @@ uint64_t wait_limit_ns() {
 }
 
 template <int H, bool BF, bool CAP>
-cudaError_t launch_cap(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TcArgs& t, int ctas, cudaStream_t st) {
+cudaError_t launch_cap(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TcArgs& t, int ctas,
+                       cudaStream_t st) {
   using C = Cfg<H>;
   auto* kernel = paged_tc_kernel<H, BF, CAP>;
   // per device: set at every call (the attribute belongs to the current context)

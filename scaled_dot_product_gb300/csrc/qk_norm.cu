@@ -113,7 +113,8 @@ struct Lane {
   int c0, mate, ci;                // mate's lane, first cos / sin entry
   bool live, rot, second;          // has channels; is rotated; holds the second of its pairs
   uint4 cw, sw;                    // packed cos and sin (adjacent pairs: the first half)
-  __device__ __forceinline__ Lane(int u, int D, int R) : c0(u * V), mate(u), ci(0), live(u * V < D), rot(u * V < R), second(false) {
+  __device__ __forceinline__ Lane(int u, int D, int R)
+      : c0(u * V), mate(u), ci(0), live(u * V < D), rot(u * V < R), second(false) {
     cw = sw = make_uint4(0u, 0u, 0u, 0u);
     if (kInter) {
       ci = c0 / 2;

@@ -513,7 +513,7 @@ def _new(t: torch.Tensor) -> torch.Tensor:
     return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _direct_positions(position_ids, q, num_heads):
+def _direct_positions(position_ids, q):
     """position_ids as the kernels read them: (B, S) int64, contiguous."""
     if position_ids is None:
         return None
@@ -537,7 +537,7 @@ def sdpa_qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor
                                         sin_cache, position_ids, eps, rotary_dim, interleaved, num_heads or 0,
                                         kv_num_heads or 0, q_out, k_out))
     q_out, k_out = _new(q) if q_out is None else q_out, _new(k) if k_out is None else k_out
-    pos = _direct_positions(position_ids, q, num_heads)
+    pos = _direct_positions(position_ids, q)
     return _raised(_elsewhere(q, stream, lambda h: b.qk_norm_rotary(
         entry["sdpa_qk_norm_rotary"], h, q, k, q_weight, k_weight, cos_cache, sin_cache, pos, eps, rotary_dim, interleaved,
         num_heads or 0, kv_num_heads or 0, q_out, k_out), (q_out, k_out, pos)))
@@ -559,7 +559,7 @@ def sdpa_qk_norm_rotary_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tens
                                             position_ids, eps, rotary_dim, interleaved, num_heads or 0, kv_num_heads or 0,
                                             dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace))
     outs = [_new(like) if t is None else t for t, like in ((dq, q), (dk, k), (dq_weight, q_weight), (dk_weight, k_weight))]
-    pos = _direct_positions(position_ids, q, num_heads)
+    pos = _direct_positions(position_ids, q)
     if workspace is None:
         workspace = torch.empty(QK_NORM_WORKSPACE, dtype=torch.uint8, device=q.device)
     return _raised(_elsewhere(q, stream, lambda h: b.qk_norm_rotary_bwd(

@@ -144,7 +144,6 @@ def test_the_binding_refuses():
         with pytest.raises(ValueError):
             sdpa.sdpa_qk_norm_rotary(**{**dict(q=x, k=x.clone(), q_weight=w, k_weight=w), **bad})
     # the size the binding falls back on for a call on another stream
-    p = sdpa.sdpa_qk_norm_params()
     assert sdpa.QK_NORM_WORKSPACE >= 304 * 256 * 4
 
 
