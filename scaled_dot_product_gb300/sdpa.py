@@ -488,18 +488,21 @@ def _handle(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(d) if d >= 0 else 0
 
 
-def _elsewhere(first: torch.Tensor, stream, call, allocated) -> object:
-    """call(handle) with first's device current, on `stream` (default: that device's current one).
-    Tensors the binding allocated for it belong to that stream until its work is done."""
+def _elsewhere(first: torch.Tensor, stream, call) -> object:
+    """call(handle) with first's device current and `stream` (default: that device's current one) as
+    its stream: what the binding converts or allocates for the call is ordered with its kernels."""
     with torch.cuda.device(first.device):
-        here = _handle(first)
-        handle = here if stream is None else _stream(stream)
-        r = call(handle)
-        if handle != here:
-            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, device=first.device)
-            for t in allocated:
-                if t is not None and t.numel():
-                    t.record_stream(s)
+        here = torch.cuda.current_stream()
+        s = here if stream is None else stream
+        if not isinstance(s, torch.cuda.Stream):
+            handle = _stream(s)
+            s = torch.cuda.ExternalStream(handle, device=first.device) if handle else torch.cuda.default_stream()
+        with torch.cuda.stream(s):
+            r = call(s.cuda_stream)
+        if s.cuda_stream != here.cuda_stream:
+            for t in r if type(r) is tuple else (r,):    # allocated on s, the caller's from here on
+                if isinstance(t, torch.Tensor) and t.numel():
+                    t.record_stream(here)
     return r
 
 
@@ -507,18 +510,6 @@ def _raised(r):
     if type(r) is int:
         _check(r)
     return r
-
-
-def _new(t: torch.Tensor) -> torch.Tensor:
-    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
-
-
-def _direct_positions(position_ids, q):
-    """position_ids as the kernels read them: (B, S) int64, contiguous."""
-    if position_ids is None:
-        return None
-    B, S = q.shape[0], q.shape[2 if q.dim() == 4 else 1]
-    return position_ids.to(torch.int64).expand(B, S).contiguous()
 
 
 def sdpa_qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
@@ -532,15 +523,10 @@ def sdpa_qk_norm_rotary(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor
     given).  Caches as for sdpa_rotary; without caches there is no rotation.  Returns (q_out,
     k_out) in the inputs' shapes; an output may be its input."""
     b, entry = _native()
-    if _here(q, stream):
-        return _raised(b.qk_norm_rotary(entry["sdpa_qk_norm_rotary"], _handle(q), q, k, q_weight, k_weight, cos_cache,
-                                        sin_cache, position_ids, eps, rotary_dim, interleaved, num_heads or 0,
-                                        kv_num_heads or 0, q_out, k_out))
-    q_out, k_out = _new(q) if q_out is None else q_out, _new(k) if k_out is None else k_out
-    pos = _direct_positions(position_ids, q)
-    return _raised(_elsewhere(q, stream, lambda h: b.qk_norm_rotary(
-        entry["sdpa_qk_norm_rotary"], h, q, k, q_weight, k_weight, cos_cache, sin_cache, pos, eps, rotary_dim, interleaved,
-        num_heads or 0, kv_num_heads or 0, q_out, k_out), (q_out, k_out, pos)))
+    call = lambda h: b.qk_norm_rotary(entry["sdpa_qk_norm_rotary"], h, q, k, q_weight, k_weight, cos_cache, sin_cache,
+                                      position_ids, eps, rotary_dim, interleaved, num_heads or 0, kv_num_heads or 0, q_out,
+                                      k_out)
+    return _raised(call(_handle(q)) if _here(q, stream) else _elsewhere(q, stream, call))
 
 
 def sdpa_qk_norm_rotary_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch.Tensor,
@@ -554,21 +540,10 @@ def sdpa_qk_norm_rotary_bwd(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tens
     returns (dq, dk, dq_weight, dk_weight).  dq may be dq_out itself and dk dk_out."""
     b, entry = _native()
     fn, size = entry["sdpa_qk_norm_rotary_bwd"], entry["sdpa_qk_norm_workspace_size"]
-    if _here(q, stream):
-        return _raised(b.qk_norm_rotary_bwd(fn, size, _handle(q), q, k, q_weight, k_weight, cos_cache, sin_cache,
-                                            position_ids, eps, rotary_dim, interleaved, num_heads or 0, kv_num_heads or 0,
-                                            dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace))
-    outs = [_new(like) if t is None else t for t, like in ((dq, q), (dk, k), (dq_weight, q_weight), (dk_weight, k_weight))]
-    pos = _direct_positions(position_ids, q)
-    if workspace is None:
-        workspace = torch.empty(QK_NORM_WORKSPACE, dtype=torch.uint8, device=q.device)
-    return _raised(_elsewhere(q, stream, lambda h: b.qk_norm_rotary_bwd(
-        fn, size, h, q, k, q_weight, k_weight, cos_cache, sin_cache, pos, eps, rotary_dim, interleaved, num_heads or 0,
-        kv_num_heads or 0, dq_out, dk_out, *outs, workspace), (*outs, workspace, pos)))
-
-
-# Most bytes the backward's workspace takes (sdpa_qk_norm_workspace_size at D = 256).
-QK_NORM_WORKSPACE = 1 << 20
+    call = lambda h: b.qk_norm_rotary_bwd(fn, size, h, q, k, q_weight, k_weight, cos_cache, sin_cache, position_ids, eps,
+                                          rotary_dim, interleaved, num_heads or 0, kv_num_heads or 0, dq_out, dk_out, dq,
+                                          dk, dq_weight, dk_weight, workspace)
+    return _raised(call(_handle(q)) if _here(q, stream) else _elsewhere(q, stream, call))
 
 
 def _causal(causal) -> int:
@@ -600,7 +575,7 @@ def sdpa_paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v
     b, entry = _native()
     call = lambda h: b.paged_append(entry["sdpa_paged_append"], h, k, v, k_pages, v_pages, page_table, kv_lens, cu_new,
                                     cos_cache, sin_cache, rotary_dim, interleaved)
-    _raised(call(_handle(k)) if _here(k, stream) else _elsewhere(k, stream, call, ()))
+    _raised(call(_handle(k)) if _here(k, stream) else _elsewhere(k, stream, call))
     return k_pages, v_pages
 
 
@@ -618,15 +593,7 @@ def sdpa_paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     fn, size, mode = entry["sdpa_paged_attn"], entry["sdpa_paged_workspace_size"], _causal(causal)
     call = lambda h: b.paged_attn(fn, size, h, q, k_pages, v_pages, page_table, kv_lens, cu_new, scale, softcap, mode, window,
                                   head_sink, max_new or 0, y, workspace)
-    if _here(q, stream):
-        return _raised(call(_handle(q)))
-    if y is None:
-        y = torch.empty(*q.shape[:2], v_pages.shape[3], dtype=q.dtype, device=q.device)
-    if workspace is None:
-        p = make_paged_params(k_pages, v_pages, page_table, kv_lens, q.shape[0], q.shape[1], cu_new=cu_new, scale=scale,
-                              softcap=softcap, causal=causal, window=window, head_sink=head_sink, max_new=max_new)
-        workspace = torch.empty(max(1, lib().sdpa_paged_workspace_size(p)), dtype=torch.uint8, device=q.device)
-    return _raised(_elsewhere(q, stream, call, (y, workspace)))
+    return _raised(call(_handle(q)) if _here(q, stream) else _elsewhere(q, stream, call))
 
 
 def sdpa_query_status(stream=None) -> int:

@@ -207,6 +207,20 @@ def test_other_stream_and_graph_replay():
     got, gotb = sdpa.sdpa_qk_norm_rotary(**f, **kw, stream=st), sdpa.sdpa_qk_norm_rotary_bwd(**g, **kw, stream=st.cuda_stream)
     st.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got + gotb, want + wantb))
+    # positions of another type, written late on the call's stream, are converted behind that write
+    late = torch.zeros(2, 5, dtype=torch.int32, device="cuda")
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for handle in (st, st.cuda_stream):
+        late.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            for _ in range(20):
+                busy = (busy @ busy).clamp_(-1, 1)
+            late.copy_(g["position_ids"])
+        got = sdpa.sdpa_qk_norm_rotary(**{**f, "position_ids": late}, **kw, stream=handle)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         got, gotb = sdpa.sdpa_qk_norm_rotary(**f, **kw), sdpa.sdpa_qk_norm_rotary_bwd(**g, **kw)
