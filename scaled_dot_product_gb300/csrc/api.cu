@@ -995,6 +995,8 @@ int sdpa_qk_norm_rotary_bwd(const sdpa_qk_norm_params* p, sdpa_view dq_out, sdpa
     if (overlap(ws, o)) return fail(SDPA_ERR_ALIAS, "workspace overlaps output %s", o.name);
   for (const Extent& i : in)
     if (overlap(ws, i)) return fail(SDPA_ERR_ALIAS, "workspace overlaps input %s", i.name);
+  for (const Extent& i : side)
+    if (overlap(ws, i)) return fail(SDPA_ERR_ALIAS, "workspace overlaps input %s", i.name);
   g_error.clear();
   j.side[0].dy = to_view(dq_out);
   j.side[1].dy = to_view(dk_out);
@@ -1030,7 +1032,8 @@ int sdpa_paged_append(const sdpa_paged_params* p, sdpa_view k, sdpa_view v, sdpa
   for (const Extent& o : {pool[0], pool[1]})
     for (const Extent& in : ins)
       if (overlap(o, in)) return fail(SDPA_ERR_ALIAS, "output %s overlaps input %s", o.name, in.name);
-  if (!disjoint(pool_shape(p, p->k_pages, p->H, pool[0]), pool_shape(p, p->v_pages, p->Hv, pool[1]), esize(dt))) return fail(SDPA_ERR_ALIAS, "k_pages and v_pages overlap");
+  if (!disjoint(pool_shape(p, p->k_pages, p->H, pool[0]), pool_shape(p, p->v_pages, p->Hv, pool[1]), esize(dt)))
+    return fail(SDPA_ERR_ALIAS, "k_pages and v_pages overlap");
   g_error.clear();
   if (p->tokens == 0 || p->B == 0) return SDPA_OK;
   rot.cos_c = p->rotary_cos; rot.sin_c = p->rotary_sin; rot.max_pos = p->rotary_max_pos;

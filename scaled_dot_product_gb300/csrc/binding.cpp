@@ -259,7 +259,8 @@ PyObject* qk_norm_rotary_bwd(Args& a) {
   typed(n.place, &ws, "workspace", ws.scalar_type(), ws.sizes());
   const int64_t D = n.p.D;
   const int rc = fn(&n.p, head_view(gq, D, "dq_out"), head_view(gk, D, "dk_out"), head_view(dq, D, "dq"),
-                    head_view(dk, D, "dk"), flat(&dwq, "dq_weight"), flat(&dwk, "dk_weight"), ws.data_ptr(), ws.nbytes(), st);
+                    head_view(dk, D, "dk"), flat(&dwq, "dq_weight"), flat(&dwk, "dk_weight"), flat(&ws, "workspace"),
+                    ws.nbytes(), st);
   return rc ? PyLong_FromLong(rc) : pack({dq, dk, dwq, dwk});
 }
 
@@ -393,7 +394,7 @@ PyObject* paged_attn(Args& a) {
   const auto bytes = q.options().dtype(at::kByte).requires_grad(false);
   Tensor ws = pws ? *pws : at::empty({std::max<int64_t>(1, (int64_t)size(&p))}, bytes);
   typed(pl, &ws, "workspace", ws.scalar_type(), ws.sizes());
-  const int rc = fn(&p, packed(q, "q"), packed(y, "y"), ws.data_ptr(), ws.nbytes(), st);
+  const int rc = fn(&p, packed(q, "q"), packed(y, "y"), flat(&ws, "workspace"), ws.nbytes(), st);
   return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(y);
 }
 

@@ -107,6 +107,9 @@ def test_norm_backward_refusals():
     assert code(where=at + 16) == sdpa.SDPA_ERR_ALIGNMENT
     assert code(dq=q) == sdpa.SDPA_ERR_ALIAS
     assert code(dwq=w[0], dwk=w[0]) == sdpa.SDPA_ERR_ALIAS
+    p.q_weight, kept = at + 128, p.q_weight              # the sums of the weights' gradients would overwrite it
+    assert code() == sdpa.SDPA_ERR_ALIAS and "q_weight" in sdpa.sdpa_last_error()
+    p.q_weight = kept
     both = torch.zeros_like(q)
     assert accepted(lambda: code(dyq=both, dq=both))
     bad, _, _, keep2 = norm(dict(eps=-1.0))

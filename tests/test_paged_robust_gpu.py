@@ -143,8 +143,12 @@ def test_the_binding_refuses():
                 dict(cos_cache=x), dict(q_out=x.float()), dict(q=x[..., ::2], k=x[..., ::2]), dict(k_weight=w.cpu())):
         with pytest.raises(ValueError):
             sdpa.sdpa_qk_norm_rotary(**{**dict(q=x, k=x.clone(), q_weight=w, k_weight=w), **bad})
-    # the size the binding falls back on for a call on another stream
-    assert sdpa.QK_NORM_WORKSPACE >= 304 * 256 * 4
+    # one byte that claims to be many
+    many = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 27)
+    with pytest.raises(ValueError, match="workspace"):
+        sdpa.sdpa_paged_attn(**args, workspace=many)
+    with pytest.raises(ValueError, match="workspace"):
+        sdpa.sdpa_qk_norm_rotary_bwd(x, x.clone(), x.clone(), x.clone(), w, w, workspace=many)
 
 
 EXPIRED = textwrap.dedent("""
