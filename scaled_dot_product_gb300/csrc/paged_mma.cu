@@ -15,7 +15,7 @@
 // 64-column region of K or V; other pages by 16-byte asynchronous copies, row by row through the
 // page table.  (When the product warps issued the copies themselves, a third of their
 // instructions went into addresses, and a single-token batch of 4.48 GB took 851 us.)  Rows of V that
-// no copy brought (past the sequence's keys, below every window) are set to zero before they are
+// no row of the unit admits (past its keys, below every window) are set to zero before they are
 // multiplied, since 0 x NaN is not 0.  Single tokens of 64 sequences, 1000 to 32000 keys, 64/8 heads of
 // 128: 650 to 680 us, 6.6 to 6.9 TB/s (98 % of the measured copy rate and more); five drafted tokens of 16
 // sequences 95 us, 5.4 TB/s; four short sequences 11.4 us.  Every wait is bounded: on expiry the kernel raises an abort
@@ -325,9 +325,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(b_full(st), phase, abortp, args.wait_ns));
     {
       const int tile_key = (w.r.tile0 + w.tile + t) * kTN, key0 = tile_key + wk * KW;
-      if (args.box && (tile_key + kTN > w.s.T || tile_key < w.r.lo)) {
-        // this warp's rows of V that no box brought become zeros
-        const int first = (w.r.lo & -args.box) - tile_key, last = w.s.T - tile_key;
+      if (args.box && (tile_key + kTN > w.r.hi + 1 || tile_key < w.r.lo)) {
+        // this warp's rows of V that no row of the unit admits become zeros, brought or not
+        const int first = w.r.lo - tile_key, last = w.r.hi + 1 - tile_key;
         for (int i = lane; i < KW * 8; i += 32) {
           const int r = wk * KW + (i >> 3);
           if (r < first || r >= last) {

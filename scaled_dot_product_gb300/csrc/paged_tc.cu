@@ -291,10 +291,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
       const int n = w.take(), kt0 = w.r.tile0 + w.tile, nx = w.r.rows > kBM ? 2 : 1;
-      // rows of V tile j that no box brought become zeros
+      // rows of V tile j past the sequence's keys or below the unit's windows become zeros
       auto zero_v = [&](int j, int st) {
         int first, last;
         box_rows(t, w.s, w.r, kt0 + j, first, last);
+        first = max(first, min(kTN, w.r.lo - (kt0 + j) * kTN));
         if (first == 0 && last == kTN) return;
         for (int i = lane; i < kTN * 8; i += 32) {
           const int row = i >> 3;

@@ -298,6 +298,22 @@ def test_pools_beyond_32_bit_offsets():
         assert sdpa.sdpa_query_status() == 0
 
 
+@pytest.mark.parametrize("dtype,H,page", [(BF, 128, 16), (HF, 64, 64), (BF, 64, 7), (HF, 96, 16), (FP, 64, 24)])
+@pytest.mark.parametrize("new,hint", [([1, 1, 1], 1), ([1, 3, 1], 300), ([90, 1, 200], 200)])
+def test_keys_below_every_window_do_not_matter(dtype, H, page, new, hint):
+    r = ragged(new, [700, 75, 1000], dtype=dtype, H=H, page=page, Nq=4, Nkv=2, seed=23)
+    want, tol = paged_attn64(r, window=50)
+    for b, (n, T) in enumerate(zip(r.new, r.lens)):
+        j = torch.arange(max(0, T - n - 49))                   # the first new token admits T - n - 49 and on
+        ids = r.table[b, j // page].long()
+        for pool, x in ((r.kp, float("nan")), (r.vp, float("inf"))):
+            pool[ids, :, j % page] = x
+    d = r.to("cuda")
+    y = sdpa.sdpa_paged_attn(d.q, d.kp, d.vp, d.table, d.kv_lens, cu_new=d.cu, max_new=hint, window=50)
+    assert sdpa.sdpa_query_status() == 0
+    assert ((y.cpu().double() - want).abs() <= tol).all(), sdpa.sdpa_last_kernel_name()
+
+
 def test_streams_graphs_and_a_shared_workspace():
     """Two captured calls that share one workspace, replayed in turn, and a call on another stream."""
     probs = [ragged([1, 1, 1], [700, 30, 5], dtype=BF, H=128, Nq=8, Nkv=2, uniform=True, seed=19).to("cuda"),
