@@ -112,8 +112,6 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   bool bad = false;
 
-  if (threadIdx.x < kChunks) sh_chunk[threadIdx.x] = 0;
-  __syncthreads();
   auto info_of = [&](int b) { return b < a.g.B ? seq_info(a.g, b, bad) : SeqInfo{0, 0, 0}; };
   // cost of this thread's sequence; sequences of several row blocks are summed by the warp
   auto cost_of = [&](const SeqInfo& s) -> long long {
@@ -138,23 +136,42 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
     return c * a.g.Nkv;
   };
 
-  long long mine = 0;
-  SeqInfo s = info_of(threadIdx.x);
-  for (int base = 0, chunk = 0; base < a.g.B; base += NT, ++chunk) {
-    const SeqInfo next = base + NT < a.g.B ? info_of(base + NT + (int)threadIdx.x) : SeqInfo{0, 0, 0};
-    mine = cost_of(s);
-    long long v = mine;
+  // running sum of x over the warp; the warps' sums go to sh_sum
+  auto scan = [&](long long x) -> long long {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    // integers: the order of the additions does not matter
-    auto* sum = reinterpret_cast<unsigned long long*>(&sh_chunk[min(chunk, kChunks - 1)]);
-    if (lane == 0 && v) atomicAdd(sum, (unsigned long long)v);
-    if (base + NT < a.g.B) s = next;
-  }
-  __syncthreads();
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += u;
+    }
+    if (lane == 31) sh_sum[warp] = x;
+    return x;
+  };
+
+  const bool one = a.g.B <= NT;      // a sequence per thread: one pass, whose running sums also find the share
   const int chunks = min(kChunks, (a.g.B + NT - 1) / NT);
-  long long total = 0;
-  for (int c = 0; c < chunks; ++c) total += sh_chunk[c];
+  long long mine = 0, v = 0, total = 0;
+  SeqInfo s = info_of(threadIdx.x);
+  if (one) {
+    mine = cost_of(s);
+    v = scan(mine);
+    __syncthreads();
+    for (int i = 0; i < kW; ++i) total += sh_sum[i];
+  } else {
+    if (threadIdx.x < kChunks) sh_chunk[threadIdx.x] = 0;
+    __syncthreads();
+    for (int base = 0, chunk = 0; base < a.g.B; base += NT, ++chunk) {
+      const SeqInfo next = base + NT < a.g.B ? info_of(base + NT + (int)threadIdx.x) : SeqInfo{0, 0, 0};
+      long long c = cost_of(s);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      // integers: the order of the additions does not matter
+      auto* sum = reinterpret_cast<unsigned long long*>(&sh_chunk[min(chunk, kChunks - 1)]);
+      if (lane == 0 && c) atomicAdd(sum, (unsigned long long)c);
+      if (base + NT < a.g.B) s = next;
+    }
+    __syncthreads();
+    for (int c = 0; c < chunks; ++c) total += sh_chunk[c];
+  }
   if (bad && cta == 0) atomicOr(status, kPagedBadLength);
 
   Share r;
@@ -183,18 +200,12 @@ __device__ __forceinline__ Share find_share(const PagedAttn& a, int cta, int cta
   int from = 0;
   while (from + 1 < chunks && before + sh_chunk[from] <= begin_at) before += sh_chunk[from++];
   for (int base = from * NT; base < a.g.B; base += NT) {
-    if (a.g.B > NT) {
+    if (!one) {
       s = info_of(base + (int)threadIdx.x);
       mine = cost_of(s);
+      v = scan(mine);
+      __syncthreads();
     }
-    long long v = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) sh_sum[warp] = v;
-    __syncthreads();
     long long off = before, all = 0;
 #pragma unroll 1
     for (int w = 0; w < kW; ++w) {
