@@ -11,14 +11,14 @@
 //               128 / box boxes of box = gcd(page_size, 128) rows, each inside one page; lane by lane
 //               they are looked up and issued
 //   warp 1      tensor products (one elected lane issues): S_X = Q_X K^T, O_X += P_X V with P
-//               read from tensor memory.  Rows of V that no box brought (past the sequence's keys,
-//               below every window) it sets to zero first, since 0 x NaN is not 0
+//               read from tensor memory.  Rows of V past the sequence's keys or below every
+//               window of the unit it sets to zero first, since 0 x NaN is not 0
 //   warp 2      V tiles into the same ring
 //   warp 3      query rows by 16-byte asynchronous copies for the other groups
 //   warps 4-7   softmax of tile 0, one thread per row; warps 8-11 softmax of tile 1
 //
-// A chunk of 2048 tokens over 32000 keys, 32/8 heads of 128: 732 us, 1500 TFLOP/s (79 % of the
-// measured bf16 burst rate); a causal prompt of 4096 tokens 125 us, 1090 TFLOP/s; single tokens through
+// A chunk of 2048 tokens over 32000 keys, 32/8 heads of 128: 735 to 768 us, 1430 to 1495 TFLOP/s (76
+// to 79 % of the measured bf16 burst rate); a causal prompt of 4096 tokens 125 us, 1090 TFLOP/s; single tokens through
 // this kernel 6.4 TB/s.  Running maxima move only when they grow by more than 2^8.  Every wait is
 // bounded: on expiry the kernel raises an abort flag, lets its own copies and products finish, frees
 // its tensor memory and records SDPA_ERR_TIMEOUT.
