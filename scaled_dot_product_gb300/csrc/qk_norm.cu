@@ -570,17 +570,9 @@ cudaError_t run_fwd(const NormJob& j, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Blocks of the persistent backward, split between the sides by their rows.
-void bwd_blocks(const NormJob& j, int want_q, int want_k, int* qb, int* kb) {
-  const int total = std::min(want_q + want_k, kNormBwdMaxBlocks);
-  const double share = (double)j.side[1].N / (j.side[0].N + j.side[1].N);
-  *kb = std::max(1, std::min(want_k, (int)(share * total + 0.5)));
-  *qb = std::max(1, std::min(want_q, total - *kb));
-}
-
 template <typename T>
-cudaError_t finish_dw(const NormJob& j, float* part, int qb, int kb, cudaStream_t st) {
-  norm_dw_kernel<T><<<dim3((unsigned)(j.D + 31) / 32, 2), 1024, 0, st>>>(part, j.D, qb, qb + kb,
+cudaError_t finish_dw(const NormJob& j, float* part, const NormBwdBlocks& nb, cudaStream_t st) {
+  norm_dw_kernel<T><<<dim3((unsigned)(j.D + 31) / 32, 2), 1024, 0, st>>>(part, j.D, nb.q, nb.q + nb.k,
                                                                          reinterpret_cast<T*>(j.side[0].dw),
                                                                          reinterpret_cast<T*>(j.side[1].dw));
   count_launch(1);
@@ -589,15 +581,15 @@ cudaError_t finish_dw(const NormJob& j, float* part, int qb, int kb, cudaStream_
 
 template <typename T, bool kInter, int LPR>
 cudaError_t run_bwd(const NormJob& j, float* part, cudaStream_t st) {
-  int qb, kb;
-  bwd_blocks(j, side_blocks(j, 0, kThreads, LPR, kHeads), side_blocks(j, 1, kThreads, LPR, kHeads), &qb, &kb);
+  const NormBwdBlocks nb = norm_bwd_blocks(j.side[0].N, j.side[1].N, side_blocks(j, 0, kThreads, LPR, kHeads),
+                                           side_blocks(j, 1, kThreads, LPR, kHeads));
   // per device: set at every call (the attribute belongs to the current context)
   cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<T, kInter, LPR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
   if (e != cudaSuccess) return e;
-  norm_bwd_kernel<T, kInter, LPR><<<(unsigned)(qb + kb), kThreads, kRingBytes, st>>>(j, qb, part);
+  norm_bwd_kernel<T, kInter, LPR><<<(unsigned)(nb.q + nb.k), kThreads, kRingBytes, st>>>(j, nb.q, part);
   count_launch(1);
   e = cudaGetLastError();
-  return e == cudaSuccess ? finish_dw<T>(j, part, qb, kb, st) : e;
+  return e == cudaSuccess ? finish_dw<T>(j, part, nb, st) : e;
 }
 
 template <typename T, bool kInter, int LPR>
@@ -628,12 +620,11 @@ cudaError_t run_t(const NormJob& j, float* part, cudaStream_t st) {
     count_launch(1);
     return cudaGetLastError();
   }
-  int qb, kb;
-  bwd_blocks(j, want(0), want(1), &qb, &kb);
-  norm_bwd_scalar_kernel<T><<<(unsigned)(qb + kb), kThreads, 0, st>>>(j, qb, j.interleaved, part);
+  const NormBwdBlocks nb = norm_bwd_blocks(j.side[0].N, j.side[1].N, want(0), want(1));
+  norm_bwd_scalar_kernel<T><<<(unsigned)(nb.q + nb.k), kThreads, 0, st>>>(j, nb.q, j.interleaved, part);
   count_launch(1);
   const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? finish_dw<T>(j, part, qb, kb, st) : e;
+  return e == cudaSuccess ? finish_dw<T>(j, part, nb, st) : e;
 }
 
 }  // namespace

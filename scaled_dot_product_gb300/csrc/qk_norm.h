@@ -2,6 +2,7 @@
 #pragma once
 
 #include "internal.h"
+#include "norm_split.h"
 
 namespace sdpa {
 
@@ -22,8 +23,6 @@ struct NormJob {
   int64_t max_pos;
   float eps, inv_D;
 };
-// Most blocks of the backward: each leaves D partial sums of dw in the workspace.
-constexpr int kNormBwdMaxBlocks = 152 * 2;
 // part == nullptr: forward; else the backward with its partial sums there.
 cudaError_t launch_qk_norm(sdpa_dtype dt, const NormJob& j, float* part, cudaStream_t st);
 cudaError_t take_norm_status(int* status);

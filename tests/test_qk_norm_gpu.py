@@ -229,3 +229,24 @@ def test_other_stream_and_graph_replay():
     torch.cuda.synchronize()
     assert torch.equal(got[0], -want[0]) and torch.equal(got[1], want[1])
     assert torch.equal(gotb[0], wantb[0]) and torch.equal(gotb[2], -wantb[2]) and torch.equal(gotb[3], wantb[3])
+
+
+@pytest.mark.parametrize("Nq,Nkv,D,dtype,S", [(1, 700, 128, BF, 70), (700, 1, 64, HF, 40), (1, 2000, 50, BF, 3), (1, 900, 256, FP, 9)])
+def test_gradient_of_very_unequal_head_counts(Nq, Nkv, D, dtype, S):
+    """One side has nearly all the rows: the partial sums stay within a workspace of exactly the size
+    asked for."""
+    import ctypes
+    d = draw(1, S, Nq, Nkv, D, dtype, 4, 0, "ids", seed=5, grad=True)
+    g = {n: t.cuda() for n, t in d.items()}
+    p = sdpa.sdpa_qk_norm_params(struct_size=ctypes.sizeof(sdpa.sdpa_qk_norm_params), B=1, Nq=Nq, Nkv=Nkv, S=S, D=D,
+                                 dtype=sdpa._DTYPES[dtype], q=sdpa._view(g["q"], []), k=sdpa._view(g["k"], []),
+                                 q_weight=g["q_weight"].data_ptr(), k_weight=g["k_weight"].data_ptr(), eps=1e-5)
+    need = sdpa.lib().sdpa_qk_norm_workspace_size(ctypes.byref(p))
+    room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    dq, dk, dwq, dwk = sdpa.sdpa_qk_norm_rotary_bwd(**g, eps=1e-5, workspace=room[:need])
+    assert (room[need:] == 0xA5).all() and sdpa.sdpa_query_status() == 0
+    for t, N, dx, dw in (("q", Nq, dq, dwq), ("k", Nkv, dk, dwk)):
+        wx, ww, mag, wsum = norm_rotary_grad64(d[t].double(), d[t + "_weight"].double(), d["d" + t + "_out"].double(), None, None,
+                                               0, False, 1e-5)
+        assert ((dx.cpu().double() - wx).abs() <= HALF_STEP[dtype] * wx.abs() + 64 * U32 * mag + (2.0 ** -25 if dtype == HF else 0)).all()
+        assert ((dw.cpu().double() - ww).abs() <= HALF_STEP[dtype] * ww.abs() + (S * N + 64) * U32 * wsum).all()
