@@ -105,6 +105,9 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+// The product warps say that they are done; the producer waits until all of them have.
+__device__ __forceinline__ void ended_arrive() { asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void ended_sync() { named_bar_sync(2, kThreads); }
 
 template <bool BF, int H, int WM>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
@@ -256,8 +259,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (ok) w.next(a);
       }
     }
-    if (!ok || *abortp) {
-      // given up: copies already issued land before the CTA can exit
+    // Copies may still be on their way when a wait has expired, whichever role's it was and however
+    // early the last copy was issued: the CTA, whose shared memory they write, ends behind them.
+    ended_sync();
+    if (*abortp) {
       constexpr uint64_t kDrainNs = 2000000000ull;
       cp_async_wait_all();
       for (int s = 0; s < C::kStages; ++s) {
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     __syncwarp();
     if (lane == 0) mbar_arrive(b_empty(done_st));
   }
-  if (!ok && lane == 0) atomicExch(&g_paged_timeout, (int)SDPA_ERR_TIMEOUT);
+  ended_arrive();
 }
 
 // Rows per unit: the smallest of 16, 32 and 64 that holds all rows of a sequence with max_new

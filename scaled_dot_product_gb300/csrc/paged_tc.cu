@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_flag;
   __shared__ int issued[2][C::kStages];      // last tile + 1 that K's / V's producer put into a stage
+  __shared__ int issued_q;                   // units whose query tiles came by TMA
   const PagedAttn& a = t.a;
   const Paged& g = a.g;
   const int ctas = gridDim.x, cta = blockIdx.x;
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(b_empty(s), 1);
       issued[0][s] = issued[1][s] = 0;
     }
+    issued_q = 0;
     mbar_init(b_qready, 1);
     mbar_init(b_qempty, 1);
     mbar_init(b_drain, 1);
@@ -236,17 +238,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_4d(sQ + x * C::kTile + r * C::kRegionBytes, &tq, b_qready, 64 * r, w.kvh * g.group,
                             w.s.t0 + group_div(g, w.r.row0 + x * kBM), 0);
           }
-          __syncwarp();
           ++it;
+          if (lane == 0) issued_q = it;
+          __syncwarp();
         }
       }
       base += 2 * n;
-    }
-    if (__any_sync(0xffffffffu, !ok || *abortp)) {
-      // some role gave up: let every copy already issued land before the CTA can exit
-      if (it > 0) mbar_wait_bounded(b_qready, (it - 1) & 1, nullptr, kDrainNs);
-      for (int s = 0; s < C::kStages; ++s)
-        if (issued[is_v][s]) mbar_wait_bounded(b_full(s), ((issued[is_v][s] - 1) / C::kStages) & 1, nullptr, kDrainNs);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -710,6 +707,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- teardown
   tc_fence_before();
   __syncthreads();
+  if (warp == 0 && abort_flag) {
+    // Some role gave up, perhaps behind the producers' last copies: every copy lands before the CTA,
+    // whose shared memory it writes, ends.  A stage's and the query tiles' earlier copies landed
+    // before their space was filled again.
+    if (issued_q > 0) mbar_wait_bounded(b_qready, (issued_q - 1) & 1, nullptr, kDrainNs);
+    for (int s = 0; s < C::kStages; ++s) {
+      const int last = max(issued[0][s], issued[1][s]);
+      if (last > 0) mbar_wait_bounded(b_full(s), ((last - 1) / C::kStages) & 1, nullptr, kDrainNs);
+    }
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -212,3 +212,44 @@ def test_the_bounds_checking_build_runs_clean():
                        text=True, timeout=1800)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
     assert all(k in r.stdout for k in ("paged_mma", "paged_tc", "paged_simt")), r.stdout
+
+
+LATE = textwrap.dedent("""
+    import sys, torch
+    sys.path.insert(0, {root!r}); sys.path.insert(0, {tests!r})
+    from paged_reference import paged_attn64, ragged
+    from scaled_dot_product_gb300 import sdpa
+    probs = [ragged(new, past, dtype=dtype, H=H, page=page, Nq=4, Nkv=2).to("cuda") for dtype, H, page, new, past in
+             ((torch.bfloat16, 128, 16, [1], [100]), (torch.bfloat16, 128, 16, [1, 1, 2], [150, 60, 0]),
+              (torch.float16, 64, 7, [1, 3], [200, 90]), (torch.bfloat16, 128, 16, [40], [80]),
+              (torch.float16, 64, 8, [90, 1], [60, 30]), (torch.bfloat16, 64, 64, [150], [0]))]
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    x = torch.randn(512, 512, device="cuda")
+    want = x @ x
+    plain = ragged([2, 3], [70, 9], dtype=torch.float32, H=64)
+    y, tol = paged_attn64(plain)
+    d = plain.to("cuda")
+    for i in range(20):
+        for r in probs:
+            flush.zero_()                          # pages and tables come from memory: the copies take their time
+            sdpa.sdpa_paged_attn(r.q, r.kp, r.vp, r.table, r.kv_lens, cu_new=r.cu)
+            same = torch.equal(x @ x, want)        # the next kernel on those SMs has its shared memory to itself
+            got = sdpa.sdpa_paged_attn(d.q, d.kp, d.vp, d.table, d.kv_lens, cu_new=d.cu).cpu().double()
+            print("STATUS", int(same and bool(((got - y).abs() <= tol).all())), sdpa.sdpa_query_status())
+    print("AFTER", sdpa.sdpa_query_status())
+""")
+
+
+@pytest.mark.parametrize("limit", ["1", "300", "900", "2000"])
+def test_waits_that_expire_behind_the_last_copy(limit):
+    """Shares of few tiles, whose copies are all issued before the first is there: a wait that expires
+    then leaves no copy behind.  Whether it expires at all depends on the limit; the call ends, says
+    so, and what runs next on the GPU is right."""
+    out = subprocess.run([sys.executable, "-c", LATE.format(root=ROOT, tests=os.path.join(ROOT, "tests"))],
+                         env=dict(os.environ, SDPA_WAIT_LIMIT_NS=limit), capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr[-2000:]
+    lines = [line.split() for line in out.stdout.splitlines()]
+    got = [(int(line[1]), int(line[2])) for line in lines if line[0] == "STATUS"]
+    assert len(got) == 120 and all(right and status in (0, sdpa.SDPA_ERR_TIMEOUT) for right, status in got), got
+    assert limit != "1" or all(status == sdpa.SDPA_ERR_TIMEOUT for _, status in got)
+    assert lines[-1] == ["AFTER", "0"]
