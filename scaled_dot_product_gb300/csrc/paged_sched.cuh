@@ -303,10 +303,14 @@ struct Walk {
   }
 };
 
+// Whether a row, or a part of one, has no weight so far: no admitted key.  Scores that are not
+// numbers leave the maximum at -inf too (a maximum drops them), but not the sum.
+__device__ __forceinline__ bool no_key(float m, float l) { return m == -INFINITY && l == 0.f; }
+
 // Final scale of row (head h): 1 / (l + sink term), 0 for a row with no key; m, l in log2 units.
 template <typename T>
 __device__ __forceinline__ float row_scale(const PagedAttn& a, int h, float m, float l) {
-  if (m == -INFINITY) return 0.f;
+  if (no_key(m, l)) return 0.f;
   if (a.head_sink) l += exp2f(Elem<T>::to_f32(reinterpret_cast<const T*>(a.head_sink)[h]) * kLog2e - m);
   return l > 0.f ? 1.f / l : 0.f;
 }

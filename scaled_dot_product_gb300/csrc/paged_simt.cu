@@ -214,13 +214,11 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kCtasPerSm : 2) paged_simt
       float M = -INFINITY;
       for (int k = 0; k < KPI; ++k) M = fmaxf(M, sm_m[k][r]);
       float O = 0.f, L = 0.f;
-      if (M != -INFINITY) {
-        for (int k = 0; k < KPI; ++k) {
-          if (sm_m[k][r] == -INFINITY) continue;
-          const float f = exp2f(sm_m[k][r] - M);
-          O = fmaf(f, smem[(k * TM + r) * HM + d], O);
-          L = fmaf(f, sm_l[k][r], L);
-        }
+      for (int k = 0; k < KPI; ++k) {
+        if (no_key(sm_m[k][r], sm_l[k][r])) continue;
+        const float f = exp2f(sm_m[k][r] - M);
+        O = fmaf(f, smem[(k * TM + r) * HM + d], O);
+        L = fmaf(f, sm_l[k][r], L);
       }
       if (whole) {
         const int pr = w.r.row0 + r, h = w.kvh * g.group + pr - group_div(g, pr) * g.group;
@@ -316,7 +314,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (i >= n || ml[i].x == -INFINITY) continue;
+        if (no_key(ml[i].x, ml[i].y)) continue;
         const float f = exp2f(ml[i].x - M);
         L = fmaf(f, ml[i].y, L);
         v.x = fmaf(f, o[i].x, v.x);
@@ -345,13 +343,13 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     for (int i = sub; i < n && live; i += tpr) {
       const float2 v = *reinterpret_cast<const float2*>(ws.ml + (slot_of(i) + row0 + r) * 2);
       const float mn = fmaxf(M, v.x);
-      if (mn != -INFINITY) L = L * exp2f(M - mn) + v.y * exp2f(v.x - mn);
+      L = mn == -INFINITY ? L + v.y : L * exp2f(M - mn) + v.y * exp2f(v.x - mn);
       M = mn;
     }
     for (int o = tpr / 2; o > 0; o >>= 1) {
       const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o);
       const float mn = fmaxf(M, m2);
-      if (mn != -INFINITY) L = L * exp2f(M - mn) + l2 * exp2f(m2 - mn);
+      L = mn == -INFINITY ? L + l2 : L * exp2f(M - mn) + l2 * exp2f(m2 - mn);
       M = mn;
     }
     if (sub == 0 && live) {
@@ -373,9 +371,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
 #pragma unroll 4
     for (int i = g0; i < n; i += share) {
       const int64_t at_row = slot_of(i) + row0 + r;
-      const float mm = ws.ml[at_row * 2];
+      const float2 ml = *reinterpret_cast<const float2*>(ws.ml + at_row * 2);
       const float4 o = *reinterpret_cast<const float4*>(ws.o + at_row * g.Hv + d);
-      const float f = mm == -INFINITY ? 0.f : exp2f(mm - M);
+      if (no_key(ml.x, ml.y)) continue;
+      const float f = exp2f(ml.x - M);
       v.x = fmaf(f, o.x, v.x);
       v.y = fmaf(f, o.y, v.y);
       v.z = fmaf(f, o.z, v.z);
