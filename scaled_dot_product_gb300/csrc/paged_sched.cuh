@@ -312,7 +312,7 @@ template <typename T>
 __device__ __forceinline__ float row_scale(const PagedAttn& a, int h, float m, float l) {
   if (no_key(m, l)) return 0.f;
   if (a.head_sink) l += exp2f(Elem<T>::to_f32(reinterpret_cast<const T*>(a.head_sink)[h]) * kLog2e - m);
-  return l > 0.f ? 1.f / l : 0.f;
+  return 1.f / l;                        // about 1 or more where m is finite; NaN, also of a sink, stays NaN
 }
 
 // Lets the joining kernel be scheduled; it waits for this one's results itself.

@@ -1,4 +1,4 @@
-"""The attention over a paged cache where a query, a key or a value is not a number: rows that
+"""The attention over a paged cache where a query, a key, a value or a sink is not a number: rows that
 it enters are not numbers either, however the batch is cut, and the other rows are as ever."""
 import pytest
 import torch
@@ -31,11 +31,12 @@ def problem(dtype, H, page, new, past, seed=0):
     return ragged([1, new, 2], [20, past, 300], dtype=dtype, H=H, page=page, Nq=4, Nkv=2, seed=past + seed)
 
 
-def check(r, hint, **kw):
+def check(r, hint, sink=None, **kw):
     """NaN exactly where the definition has it, and the definition's values elsewhere."""
-    want, tol = paged_attn64(r, **kw)
+    want, tol = paged_attn64(r, sink=sink, **{n: x for n, x in kw.items() if n != "causal"})
     d = r.to("cuda")
-    y = sdpa.sdpa_paged_attn(d.q, d.kp, d.vp, d.table, d.kv_lens, cu_new=d.cu, max_new=hint, **kw).cpu().double()
+    y = sdpa.sdpa_paged_attn(d.q, d.kp, d.vp, d.table, d.kv_lens, cu_new=d.cu, max_new=hint,
+                             head_sink=None if sink is None else sink.cuda(), **kw).cpu().double()
     assert sdpa.sdpa_query_status() == 0
     bad = want.isnan()
     assert bad.any() and not bad.all()
@@ -83,13 +84,21 @@ def test_a_value(dtype, H, page, new, kernel, past):
 
 
 @pytest.mark.parametrize("dtype,H,page,new,kernel", KERNELS)
+@pytest.mark.parametrize("past", PAST)
+def test_a_sink(dtype, H, page, new, kernel, past):
+    r = problem(dtype, H, page, new, past)
+    check(r, new, sink=torch.tensor([0.5, NAN, -1.0, 2.0]).to(dtype))
+
+
+@pytest.mark.parametrize("dtype,H,page,new,kernel", KERNELS)
 def test_rows_without_keys_stay_zero(dtype, H, page, new, kernel):
-    """No admitted key: zeros, whatever the query holds."""
+    """No admitted key: zeros, whatever the query and the sink hold."""
     r = ragged([1, new, 2], [20, -new, 300], dtype=dtype, H=H, page=page, Nq=4, Nkv=2, seed=3)
     r.q[1] = NAN
+    sink = torch.tensor([0.5, NAN, -1.0, 2.0]).to(dtype)
     d = r.to("cuda")
-    y = sdpa.sdpa_paged_attn(d.q, d.kp, d.vp, d.table, d.kv_lens, cu_new=d.cu, max_new=new)
-    assert not y[1:1 + new].any() and not y.isnan().any()
+    y = sdpa.sdpa_paged_attn(d.q, d.kp, d.vp, d.table, d.kv_lens, cu_new=d.cu, max_new=new, head_sink=sink.cuda())
+    assert not y[1:1 + new].any() and y[0, 1].isnan().all()
 
 
 @pytest.mark.parametrize("dtype,H,page,new,kernel", KERNELS)
