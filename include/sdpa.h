@@ -360,9 +360,9 @@ SDPA_API int sdpa_paged_append(const sdpa_paged_params* p, sdpa_view k, sdpa_vie
  * not admitted.  A value that is not finite at a key that one new token admits may reach the
  * sequence's others.  Lengths out of range are clamped and reported; a page id out of range is
  * reported and its keys and values read as zeros.
- * workspace: sdpa_paged_workspace_size(p) bytes (it depends on types, head sizes, page_size and the
- * kernel that max_new picks, not on lengths), any contents, 256-byte aligned.  Alignment as for
- * sdpa_paged_append. */
+ * workspace: sdpa_paged_workspace_size(p) bytes, any contents, 256-byte aligned.  The size depends on
+ * dtype, H and Hv alone, so one workspace serves every call with these (on one stream at a time).
+ * Alignment as for sdpa_paged_append. */
 SDPA_API int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace,
                              size_t workspace_bytes, sdpa_stream_t stream);
 SDPA_API size_t sdpa_paged_workspace_size(const sdpa_paged_params* p);

@@ -1049,7 +1049,7 @@ size_t sdpa_paged_workspace_size(const sdpa_paged_params* p) {
   PagedAttn a;
   Extent pool[2];
   if (check_paged_attn(p, &a, pool) != SDPA_OK) return 0;
-  return paged_workspace(a, (sdpa_dtype)p->dtype);
+  return paged_workspace(p->H, p->Hv, (sdpa_dtype)p->dtype);
 }
 
 int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace, size_t workspace_bytes,
@@ -1063,7 +1063,7 @@ int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* 
   if ((rc = check_view(y, "y", dt, 1, p->Nq, p->tokens, p->Hv, true, false, &ey))) return rc;
   if ((rc = check_aligned_view(q, "q", dt))) return rc;
   if ((rc = check_aligned_view(y, "y", dt))) return rc;
-  const size_t need = paged_workspace(a, (sdpa_dtype)dt);
+  const size_t need = paged_workspace(p->H, p->Hv, (sdpa_dtype)dt);
   if (!workspace || workspace_bytes < need)
     return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
   if ((uintptr_t)workspace & 255u) return fail(SDPA_ERR_ALIGNMENT, "workspace not 256-byte aligned");

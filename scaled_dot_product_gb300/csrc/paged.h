@@ -43,13 +43,15 @@ struct PagedRot {                 // rotation of appended keys; R = 0: none
 cudaError_t launch_paged_append(sdpa_dtype dt, const Paged& g, const View& k, const View& v, const PagedRot& rot,
                                 cudaStream_t st);
 
-// Workspace of the attention: the same for every call of one kernel, whatever the lengths.
 enum PagedKernel { kPagedSimt = 0, kPagedMma = 1, kPagedTc = 2 };
 PagedKernel paged_kernel(const PagedAttn& a, sdpa_dtype dt);
-size_t paged_workspace(const PagedAttn& a, sdpa_dtype dt);
+// Workspace of the attention: enough for every kernel and tile that the type and the head sizes
+// admit, so that it changes with nothing else (rows, lengths, hints, pages, strides) and a caller
+// can keep one for all its calls.
+size_t paged_workspace(int H, int Hv, sdpa_dtype dt);
 cudaError_t launch_paged_attn(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
-bool paged_mma_supported(const PagedAttn& a, sdpa_dtype dt);
-size_t paged_mma_workspace(const PagedAttn& a);
+bool paged_mma_supported(int H, int Hv, sdpa_dtype dt);
+size_t paged_mma_workspace(int Hv);      // of its widest tile
 cudaError_t launch_paged_mma(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
 
 cudaError_t take_bounds_append(int* site);
@@ -60,7 +62,7 @@ cudaError_t take_paged_append_status(int* status);
 // Whether TMA boxes of at least eight rows tile the pages.
 bool paged_boxes(const PagedAttn& a);
 bool paged_tc_supported(const PagedAttn& a, sdpa_dtype dt);
-size_t paged_tc_workspace(const PagedAttn& a);
+size_t paged_tc_workspace(int Hv);
 cudaError_t launch_paged_tc(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
 cudaError_t take_paged_simt_status(int* status);
 cudaError_t take_paged_mma_status(int* status, int* timeout);

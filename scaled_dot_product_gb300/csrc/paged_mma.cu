@@ -566,13 +566,9 @@ cudaError_t launch_h(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t s
 
 }  // namespace
 
-bool paged_mma_supported(const PagedAttn& a, sdpa_dtype dt) {
-  return dt != SDPA_F32 && a.g.H == a.g.Hv && (a.g.H == 64 || a.g.H == 128);
-}
+bool paged_mma_supported(int H, int Hv, sdpa_dtype dt) { return dt != SDPA_F32 && H == Hv && (H == 64 || H == 128); }
 
-size_t paged_mma_workspace(const PagedAttn& a) {
-  return paged_ws_bytes(kPagedMaxSms * kCtasPerSm, mma_tm(a), a.g.Hv);
-}
+size_t paged_mma_workspace(int Hv) { return paged_ws_bytes(kPagedMaxSms * kCtasPerSm, 64, Hv); }
 
 cudaError_t launch_paged_mma(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name) {
   const bool bf = dt == SDPA_BF16;

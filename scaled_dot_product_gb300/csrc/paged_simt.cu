@@ -444,7 +444,8 @@ cudaError_t merge_t(const PagedAttn& a, const PagedWs& ws, int ctas, int tm, cud
 }
 
 // Rows per unit: the tokens of a uniform single-row batch need no more than one.
-int simt_tm(const PagedAttn& a) { return a.g.group == 1 && a.g.uniform == 1 ? 1 : 4; }
+constexpr int kMaxTM = 4;
+int simt_tm(const PagedAttn& a) { return a.g.group == 1 && a.g.uniform == 1 ? 1 : kMaxTM; }
 
 template <typename T, int LPK, int NV, int TM>
 cudaError_t launch_simt(const PagedAttn& a, sdpa_dtype dt, void* wsp, int ctas, cudaStream_t st) {
@@ -492,16 +493,12 @@ cudaError_t launch_paged_merge(const PagedAttn& a, sdpa_dtype dt, const PagedWs&
 
 PagedKernel paged_kernel(const PagedAttn& a, sdpa_dtype dt) {
   if (paged_tc_supported(a, dt)) return kPagedTc;
-  return paged_mma_supported(a, dt) ? kPagedMma : kPagedSimt;
+  return paged_mma_supported(a.g.H, a.g.Hv, dt) ? kPagedMma : kPagedSimt;
 }
 
-size_t paged_workspace(const PagedAttn& a, sdpa_dtype dt) {
-  switch (paged_kernel(a, dt)) {
-    case kPagedTc: return paged_tc_workspace(a);
-    case kPagedMma: return paged_mma_workspace(a);
-    default: break;
-  }
-  return paged_ws_bytes(kPagedMaxSms * kCtasPerSm, simt_tm(a), a.g.Hv);
+size_t paged_workspace(int H, int Hv, sdpa_dtype dt) {
+  if (paged_mma_supported(H, Hv, dt)) return std::max(paged_mma_workspace(Hv), paged_tc_workspace(Hv));
+  return paged_ws_bytes(kPagedMaxSms * kCtasPerSm, kMaxTM, Hv);
 }
 
 cudaError_t launch_paged_attn(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name) {

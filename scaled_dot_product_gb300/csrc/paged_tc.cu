@@ -800,11 +800,10 @@ bool paged_boxes(const PagedAttn& a) {
 
 // More rows of a sequence than paged_mma's widest unit holds.
 bool paged_tc_supported(const PagedAttn& a, sdpa_dtype dt) {
-  if (dt == SDPA_F32 || a.g.H != a.g.Hv || (a.g.H != 64 && a.g.H != 128)) return false;
-  return paged_boxes(a) && (int64_t)a.max_new * a.g.group > 64;
+  return paged_mma_supported(a.g.H, a.g.Hv, dt) && paged_boxes(a) && (int64_t)a.max_new * a.g.group > 64;
 }
 
-size_t paged_tc_workspace(const PagedAttn& a) { return paged_ws_bytes(kPagedMaxSms, kTM, a.g.Hv); }
+size_t paged_tc_workspace(int Hv) { return paged_ws_bytes(kPagedMaxSms, kTM, Hv); }
 
 cudaError_t launch_paged_tc(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaStream_t st, const char** name) {
   const int ctas = paged_sms();

@@ -266,3 +266,29 @@ def test_gradient_formula_against_differences(R, inter):
             e.view(-1)[i] = h
             d = (f(x + e, w) - f(x - e, w)) if t is x else (f(x, w + e) - f(x, w - e))
             assert abs(d / (2 * h) - grad.view(-1)[i]) < 1e-7
+
+
+@pytest.mark.parametrize("dtype,H,Hv", [(BF, 64, 64), (torch.float16, 128, 128), (BF, 96, 96), (torch.float32, 64, 64), (BF, 128, 64)])
+def test_one_workspace_serves_every_call(dtype, H, Hv):
+    """Its size depends on the type and the head sizes: not on the tokens, the hint, the head counts,
+    the pages or their strides, with offsets or without, whichever kernel and tile they pick."""
+    size = lambda p: sdpa.lib().sdpa_paged_workspace_size(ctypes.byref(p))
+    sizes = {}
+    for tokens in (2, 4, 8, 12, 16, 32, 40, 200):
+        for Nq, Nkv in ((1, 1), (4, 2), (16, 1)):
+            for page in (7, 16, 64):
+                for hint in (0, 1, 3, 17, 1000):
+                    for cu in (True, False):
+                        p, _, _ = paged(tokens=tokens, Nq=Nq, Nkv=Nkv, H=H, Hv=Hv, page=page, dtype=dtype)
+                        p.max_new = hint
+                        if not cu:
+                            p.cu_new = None
+                        sizes.setdefault(size(p), (tokens, Nq, Nkv, page, hint, cu))
+    far = paged(tokens=200, H=H, Hv=Hv, dtype=dtype)[0]
+    far.k_pages = sdpa.sdpa_view(far.k_pages.data, 1 << 39, 64 * H, H)         # strides that no TMA box takes
+    sizes.setdefault(size(far), "strides")
+    assert len(sizes) == 1 and 0 not in sizes, sizes
+    p, rows, keep = paged(tokens=200, H=H, Hv=Hv, dtype=dtype)
+    need = size(p)
+    assert attn_code(p, rows, keep, size=need - 1) == sdpa.SDPA_ERR_WORKSPACE
+    assert accepted(lambda: attn_code(p, rows, keep, where=1 << 60, size=need)), sdpa.sdpa_last_error()

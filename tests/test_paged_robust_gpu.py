@@ -253,3 +253,21 @@ def test_waits_that_expire_behind_the_last_copy(limit):
     assert len(got) == 120 and all(right and status in (0, sdpa.SDPA_ERR_TIMEOUT) for right, status in got), got
     assert limit != "1" or all(status == sdpa.SDPA_ERR_TIMEOUT for _, status in got)
     assert lines[-1] == ["AFTER", "0"]
+
+
+@pytest.mark.parametrize("dtype,H", [(BF, 128), (HF, 64), (FP, 64)])
+def test_a_serving_loop_keeps_one_workspace(dtype, H):
+    """Allocated once, for the first step's single tokens, it takes larger batches, drafts, prompts and
+    long sequences; nothing behind it is written."""
+    import ctypes
+    first = ragged([1, 1], [5, 9], dtype=dtype, H=H, page=16, Nq=8, Nkv=2, uniform=True).to("cuda")
+    p = sdpa.make_paged_params(first.kp, first.vp, first.table, first.kv_lens, 2, 8)
+    need = sdpa.lib().sdpa_paged_workspace_size(ctypes.byref(p))
+    room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    for new, past, page in (([1, 1], [5, 9], 16), ([1] * 30, [40] * 30, 16), ([1, 1], [9000, 20000], 16), ([4, 3], [100, 9], 16),
+                            ([9, 5, 6], [300, 0, 1000], 7), ([200, 1, 33], [0, 700, 90], 64)):
+        r = ragged(new, past, dtype=dtype, H=H, page=page, Nq=8, Nkv=2, seed=len(new))
+        want, tol = paged_attn64(r)
+        y = attn(r, workspace=room[:need])
+        assert ((y.cpu().double() - want).abs() <= tol).all(), sdpa.sdpa_last_kernel_name()
+    assert (room[need:] == 0xA5).all()
