@@ -436,9 +436,11 @@ int check_norm(const sdpa_qk_norm_params* p, NormJob* j, Extent ext[2]) {
   if (!p->q_weight || !p->k_weight) return fail(SDPA_ERR_NULL, "q_weight / k_weight is NULL");
   if (((uintptr_t)p->q_weight | (uintptr_t)p->k_weight) % esize(dt))
     return fail(SDPA_ERR_ALIGNMENT, "weights not aligned to the element size");
-  int R, rc;
-  if ((rc = check_rotation(dt, p->D, p->rotary_cos, p->rotary_sin, p->rotary_max_pos, p->rotary_dim,
-                           p->rotary_interleaved, &R)))
+  int R = 0, rc;
+  // caches of a row per token have none, and no address, for no tokens
+  const bool no_rows = (int64_t)p->B * p->S == 0 && p->rotary_max_pos == 0;
+  if (!no_rows && (rc = check_rotation(dt, p->D, p->rotary_cos, p->rotary_sin, p->rotary_max_pos, p->rotary_dim,
+                                       p->rotary_interleaved, &R)))
     return rc;
   if (R && !p->position_ids && p->rotary_max_pos != (int64_t)p->B * p->S && (int64_t)p->B * p->S > 0)
     return fail(SDPA_ERR_SHAPE, "without position_ids the caches are (B, S, R/2): rotary_max_pos must be B*S=%lld",

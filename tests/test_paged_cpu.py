@@ -292,3 +292,17 @@ def test_one_workspace_serves_every_call(dtype, H, Hv):
     need = size(p)
     assert attn_code(p, rows, keep, size=need - 1) == sdpa.SDPA_ERR_WORKSPACE
     assert accepted(lambda: attn_code(p, rows, keep, where=1 << 60, size=need)), sdpa.sdpa_last_error()
+
+
+@pytest.mark.parametrize("B,S", [(2, 0), (0, 3), (0, 0)])
+def test_empty_batches_with_a_cache_row_per_token(B, S):
+    """Caches (B, S, R/2) of no tokens have no elements and no address."""
+    p, q, k, keep = norm(B=B, S=S, ids=False)
+    assert p.rotary_max_pos == 0 and p.rotary_dim == 64
+    assert norm_code(p, q, k, keep) == sdpa.SDPA_OK, sdpa.sdpa_last_error()
+    for cos in (None, 4096):                        # a cache without rows may still have an address
+        p.rotary_cos = p.rotary_sin = cos
+        assert norm_code(p, q, k, keep) == sdpa.SDPA_OK, sdpa.sdpa_last_error()
+        assert sdpa.lib().sdpa_qk_norm_workspace_size(ctypes.byref(p)) > 0
+    p, q, k, keep = norm(dict(rotary_max_pos=0), ids=False)      # tokens without rows are refused as before
+    assert norm_code(p, q, k, keep) == sdpa.SDPA_ERR_SHAPE

@@ -250,3 +250,19 @@ def test_gradient_of_very_unequal_head_counts(Nq, Nkv, D, dtype, S):
                                                0, False, 1e-5)
         assert ((dx.cpu().double() - wx).abs() <= HALF_STEP[dtype] * wx.abs() + 64 * U32 * mag + (2.0 ** -25 if dtype == HF else 0)).all()
         assert ((dw.cpu().double() - ww).abs() <= HALF_STEP[dtype] * ww.abs() + (S * N + 64) * U32 * wsum).all()
+
+
+@pytest.mark.parametrize("rank", [3, 4])
+def test_empty_batches_with_a_cache_row_per_token(rank):
+    full = draw(2, 5, 4, 2, 64, BF, rank, 64, "token", grad=True)
+    no_token = lambda t: t if t.dim() == 1 else t[:, :, :0] if t.dim() == 4 else t[:, :0]
+    no_batch = lambda t: t if t.dim() == 1 else t[:0]
+    for cut in (no_token, no_batch):
+        g = {n: cut(t).cuda() for n, t in full.items()}
+        f = {n: t for n, t in g.items() if not n.startswith("d")}
+        kw = dict(num_heads=4, kv_num_heads=2, rotary_dim=64)
+        q, k = sdpa.sdpa_qk_norm_rotary(**f, **kw)
+        assert q.shape == g["q"].shape and k.shape == g["k"].shape
+        dq, dk, dwq, dwk = sdpa.sdpa_qk_norm_rotary_bwd(**g, **kw)
+        assert dq.shape == g["q"].shape and not dwq.any() and not dwk.any()      # sums over no rows
+        assert sdpa.sdpa_query_status() == 0
