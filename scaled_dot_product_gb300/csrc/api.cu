@@ -24,6 +24,16 @@ void count_launch(int n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
 namespace {
 
+// The norm and paged kernels that this process has launched, or captured into a graph that it may
+// replay at any time: sdpa_query_status reads the words of these alone (a blocking copy of about 10
+// us for each).
+std::atomic<unsigned> g_used{0};
+constexpr unsigned kUsedNorm = 1, kUsedAppend = 2, kUsedPaged = 4;      // kUsedPaged << PagedKernel
+constexpr unsigned kUsedSimt = kUsedPaged << kPagedSimt, kUsedMma = kUsedPaged << kPagedMma, kUsedTc = kUsedPaged << kPagedTc;
+void mark_used(unsigned what) {
+  if ((g_used.load(std::memory_order_relaxed) & what) != what) g_used.fetch_or(what, std::memory_order_relaxed);
+}
+
 thread_local std::string g_error;
 thread_local const char* g_kernel = "";
 
@@ -945,6 +955,7 @@ int sdpa_qk_norm_rotary(const sdpa_qk_norm_params* p, sdpa_view q_out, sdpa_view
   if (j.tokens == 0) return SDPA_OK;
   j.side[0].y = to_view(q_out);
   j.side[1].y = to_view(k_out);
+  mark_used(kUsedNorm);
   const cudaError_t e = launch_qk_norm((sdpa_dtype)dt, j, nullptr, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rotary launch");
   g_kernel = "qk_norm_rotary";
@@ -1006,6 +1017,7 @@ int sdpa_qk_norm_rotary_bwd(const sdpa_qk_norm_params* p, sdpa_view dq_out, sdpa
   j.side[1].y = to_view(dk);
   j.side[0].dw = dq_weight;
   j.side[1].dw = dk_weight;
+  mark_used(kUsedNorm);
   const cudaError_t e = launch_qk_norm((sdpa_dtype)dt, j, reinterpret_cast<float*>(workspace),
                                        reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "qk_norm_rotary backward launch");
@@ -1040,6 +1052,7 @@ int sdpa_paged_append(const sdpa_paged_params* p, sdpa_view k, sdpa_view v, sdpa
   if (p->tokens == 0 || p->B == 0) return SDPA_OK;
   rot.cos_c = p->rotary_cos; rot.sin_c = p->rotary_sin; rot.max_pos = p->rotary_max_pos;
   rot.interleaved = rot.R ? p->rotary_interleaved : 0;
+  mark_used(kUsedAppend);
   const cudaError_t e = launch_paged_append((sdpa_dtype)dt, g, to_view(k), to_view(v), rot,
                                             reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged_append launch");
@@ -1083,6 +1096,7 @@ int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* 
   a.q = to_view(q);
   a.y = to_view(y);
   const char* name = "";
+  mark_used(kUsedPaged << paged_kernel(a, (sdpa_dtype)dt));
   const cudaError_t e = launch_paged_attn(a, (sdpa_dtype)dt, workspace, reinterpret_cast<cudaStream_t>(stream), &name);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   g_kernel = name;
@@ -1097,29 +1111,37 @@ int sdpa_query_status(sdpa_stream_t stream) {
   if (e == cudaSuccess) e = take_rotary_status(&rot_status);
   if (e == cudaSuccess) e = take_qk_status(&qk_status);
   if (e == cudaSuccess) e = take_bwd_status(&bwd_status);
-  if (e == cudaSuccess) e = take_norm_status(&norm_status);
-  if (e == cudaSuccess) e = take_paged_append_status(&app_status);
-  if (e == cudaSuccess) e = take_paged_simt_status(&paged_status);
+  const unsigned used = g_used.load(std::memory_order_relaxed);
+  if (e == cudaSuccess && (used & kUsedNorm)) e = take_norm_status(&norm_status);
+  if (e == cudaSuccess && (used & kUsedAppend)) e = take_paged_append_status(&app_status);
+  if (e == cudaSuccess && (used & kUsedSimt)) e = take_paged_simt_status(&paged_status);
   int paged_timeout = 0;
-  for (auto take : {take_paged_mma_status, take_paged_tc_status}) {
+  auto take_paged = [&](unsigned kernel, cudaError_t (*take)(int*, int*)) {
     int v = 0, late = 0;
-    if (e == cudaSuccess) e = take(&v, &late);
+    if (e == cudaSuccess && (used & kernel)) e = take(&v, &late);
     paged_status |= v;
     paged_timeout |= late;
-  }
+  };
+  take_paged(kUsedMma, take_paged_mma_status);
+  take_paged(kUsedTc, take_paged_tc_status);
   if (e != cudaSuccess) return cuda_fail(e, "status read");
   if (!status) status = qk_status;
   if (!status) status = bwd_status;
   if (!status) status = paged_timeout;
   // the bounds-checking build: the first failing index check of each kernel family
   int site = 0;
-  for (auto take : {take_bounds_prefill, take_bounds_decode, take_bounds_concat, take_bounds_simt, take_bounds_norm,
-                    take_bounds_append, take_bounds_paged_simt, take_bounds_paged_mma,
-                    take_bounds_paged_tc}) {
+  auto take_site = [&](bool wanted, cudaError_t (*take)(int*)) {
     int v = 0;
-    if ((e = take(&v)) != cudaSuccess) return cuda_fail(e, "bounds status read");
+    if (e == cudaSuccess && wanted) e = take(&v);
     if (!site) site = v;
-  }
+  };
+  for (auto take : {take_bounds_prefill, take_bounds_decode, take_bounds_concat, take_bounds_simt}) take_site(true, take);
+  take_site(used & kUsedNorm, take_bounds_norm);
+  take_site(used & kUsedAppend, take_bounds_append);
+  take_site(used & (kUsedSimt | kUsedMma | kUsedTc), take_bounds_paged_simt);      // it holds the joining kernel of all three
+  take_site(used & kUsedMma, take_bounds_paged_mma);
+  take_site(used & kUsedTc, take_bounds_paged_tc);
+  if (e != cudaSuccess) return cuda_fail(e, "bounds status read");
   if (site) return fail(SDPA_ERR_BOUNDS, "an index check failed at site %d; the access was skipped", site);
   if (status) return fail(SDPA_ERR_TIMEOUT, "a bounded device wait expired (code %d)", status);
   if (rot_status || norm_status || (app_status & kPagedBadPosition))

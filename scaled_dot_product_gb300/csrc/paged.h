@@ -1,6 +1,7 @@
 // Paged caches: the problem as the kernels see it, and their launch functions.
 #pragma once
 
+#include "device_words.h"
 #include "internal.h"
 
 namespace sdpa {

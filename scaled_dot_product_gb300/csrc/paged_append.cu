@@ -15,7 +15,7 @@
 
 namespace sdpa {
 
-static __device__ int g_append_status;
+static __device__ int g_append_status[1];
 
 namespace {
 
@@ -52,13 +52,13 @@ __device__ __forceinline__ Slot find_slot(const Paged& g, const PagedRot& rot, i
   const SeqInfo q = seq_info(g, b, bad);
   const int pos = q.T - q.n + (t - q.t0);
   if (t < q.t0 || q.T < q.n || bad) {          // before the first sequence, or lengths that contradict
-    atomicOr(&g_append_status, kPagedBadLength);
+    atomicOr(g_append_status, kPagedBadLength);
     return s;
   }
   const int pg = page_div(g, pos);
   const int id = g.table[(int64_t)b * g.table_stride + pg];
   if (id < 0 || id >= g.num_pages) {
-    atomicOr(&g_append_status, kPagedBadPage);
+    atomicOr(g_append_status, kPagedBadPage);
     return s;
   }
   s.page = id;
@@ -66,7 +66,7 @@ __device__ __forceinline__ Slot find_slot(const Paged& g, const PagedRot& rot, i
   if (rot.R) {
     int64_t row = pos;
     if (row >= rot.max_pos) {
-      atomicOr(&g_append_status, kPagedBadPosition);
+      atomicOr(g_append_status, kPagedBadPosition);
       row = rot.max_pos - 1;
     }
     s.crow = row * (rot.R / 2);
@@ -236,17 +236,7 @@ cudaError_t launch_paged_append(sdpa_dtype dt, const Paged& g, const View& k, co
   }
 }
 
-cudaError_t take_paged_append_status(int* status) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_append_status, sizeof v);
-  if (e != cudaSuccess) return e;
-  *status = v;
-  if (v) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_append_status, &zero, sizeof zero);
-  }
-  return e;
-}
+cudaError_t take_paged_append_status(int* status) { return take_words(g_append_status, status); }
 
 SDPA_DEFINE_BOUNDS_TAKE(take_bounds_append)
 

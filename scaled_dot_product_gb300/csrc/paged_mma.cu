@@ -29,8 +29,7 @@
 
 namespace sdpa {
 
-static __device__ int g_paged_status;
-static __device__ int g_paged_timeout;
+static __device__ int g_paged_words[2];      // status bits, SDPA_ERR_TIMEOUT after an expired wait
 
 namespace {
 
@@ -142,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     fence_mbar_init();
   }
-  const Share sh = find_share<TM, kTN, kOV, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
+  const Share sh = find_share<TM, kTN, kOV, kThreads>(a, cta, ctas, kMinShare, &g_paged_words[0]);
   if (threadIdx.x == 0) {
     if (cta == 0) ws.start[ctas].b = sh.active;
     if (cta < sh.active) ws.start[cta] = sh.at;
@@ -189,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           const bool take = brought(t);
           const int key = (w.r.tile0 + w.tile + t) * kTN + row;
           if (take && (unsigned)id >= (unsigned)g.num_pages) {
-            atomicOr(&g_paged_status, kPagedBadPage);
+            atomicOr(&g_paged_words[0], kPagedBadPage);
             id = g.num_pages;          // outside the map: the box is filled with zeros
           }
           const unsigned all = __ballot_sync(0xffffffffu, take);
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const int id = i < 32 ? a0 : a1;
             bool take = key >= w.r.lo && key <= w.r.hi;      // other keys: zeros, their pages are not read
             if (take && (unsigned)id >= (unsigned)g.num_pages) {
-              atomicOr(&g_paged_status, kPagedBadPage);
+              atomicOr(&g_paged_words[0], kPagedBadPage);
               take = false;
             }
             take = take && SDPA_IN_BOUNDS(i >= 0 && i < 64 && key < g.cap, 532);
@@ -269,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int turns = it + (s < st ? 1 : 0);
         if (turns > 0) mbar_wait_bounded(b_full(s), (turns - 1) & 1, nullptr, kDrainNs);
       }
-      if (lane == 0) atomicExch(&g_paged_timeout, (int)SDPA_ERR_TIMEOUT);
+      if (lane == 0) atomicExch(&g_paged_words[1], (int)SDPA_ERR_TIMEOUT);
     }
     return;
   }
@@ -582,14 +581,9 @@ cudaError_t launch_paged_mma(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaSt
 
 cudaError_t take_paged_mma_status(int* status, int* timeout) {
   int v[2] = {0, 0};
-  cudaError_t e = cudaMemcpyFromSymbol(&v[0], g_paged_status, sizeof v[0]);
-  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v[1], g_paged_timeout, sizeof v[1]);
-  if (e != cudaSuccess) return e;
+  const cudaError_t e = take_words(g_paged_words, v);
   *status = v[0];
   *timeout = v[1];
-  const int zero = 0;
-  if (v[0]) e = cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero);
-  if (e == cudaSuccess && v[1]) e = cudaMemcpyToSymbol(g_paged_timeout, &zero, sizeof zero);
   return e;
 }
 

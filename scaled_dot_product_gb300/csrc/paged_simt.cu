@@ -13,7 +13,7 @@
 
 namespace sdpa {
 
-static __device__ int g_paged_status;
+static __device__ int g_paged_status[1];
 
 namespace {
 
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kCtasPerSm : 2) paged_simt
   __shared__ float sm_m[KPI][TM], sm_l[KPI][TM];
   const Paged& g = a.g;
   const int ctas = gridDim.x, cta = blockIdx.x;
-  const Share sh = find_share<TM, kTN, kOV, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
+  const Share sh = find_share<TM, kTN, kOV, kThreads>(a, cta, ctas, kMinShare, g_paged_status);
   if (threadIdx.x == 0) {
     if (cta == 0) ws.start[ctas].b = sh.active;
     if (cta < sh.active) ws.start[cta] = sh.at;
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, NV == 1 ? kCtasPerSm : 2) paged_simt
         const int key = (int)min(j, (int64_t)g.cap), slot = key - page_div(g, key) * g.page_size;
         bool take = j < j_end;
         if (take && (unsigned)id[u] >= (unsigned)g.num_pages) {
-          atomicOr(&g_paged_status, kPagedBadPage);
+          atomicOr(g_paged_status, kPagedBadPage);
           take = false;                    // read as zeros
         }
         take = take && SDPA_IN_BOUNDS(key < g.cap && slot < g.page_size, 521);
@@ -515,17 +515,7 @@ cudaError_t launch_paged_attn(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaS
   }
 }
 
-cudaError_t take_paged_simt_status(int* status) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_paged_status, sizeof v);
-  if (e != cudaSuccess) return e;
-  *status = v;
-  if (v) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero);
-  }
-  return e;
-}
+cudaError_t take_paged_simt_status(int* status) { return take_words(g_paged_status, status); }
 
 SDPA_DEFINE_BOUNDS_TAKE(take_bounds_paged_simt)
 

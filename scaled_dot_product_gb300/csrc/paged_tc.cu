@@ -31,8 +31,7 @@
 
 namespace sdpa {
 
-static __device__ int g_paged_status;
-static __device__ int g_paged_timeout;
+static __device__ int g_paged_words[2];      // status bits, SDPA_ERR_TIMEOUT after an expired wait
 
 namespace {
 
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&tmem_sh), 512);
     tmem_relinquish();
   }
-  const Share sh = find_share<kTM, kTN, kOV, kThreads>(a, cta, ctas, kMinShare, &g_paged_status);
+  const Share sh = find_share<kTM, kTN, kOV, kThreads>(a, cta, ctas, kMinShare, &g_paged_words[0]);
   if (threadIdx.x == 0) {
     if (cta == 0) t.ws.start[ctas].b = sh.active;
     if (cta < sh.active) t.ws.start[cta] = sh.at;
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sq >= C::kStages && !(ok = wait_all(b_empty(st), ((sq / C::kStages) - 1) & 1))) break;
         const bool take = brought(j);
         if (take && (unsigned)id >= (unsigned)g.num_pages) {
-          atomicOr(&g_paged_status, kPagedBadPage);
+          atomicOr(&g_paged_words[0], kPagedBadPage);
           id = g.num_pages;              // outside the map: the box is filled with zeros
         }
         const unsigned all = __ballot_sync(0xffffffffu, take);
@@ -721,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (threadIdx.x == 0 && abort_flag) atomicExch(&g_paged_timeout, (int)SDPA_ERR_TIMEOUT);
+  if (threadIdx.x == 0 && abort_flag) atomicExch(&g_paged_words[1], (int)SDPA_ERR_TIMEOUT);
 }
 
 // ---------------------------------------------------------------- host side
@@ -851,14 +850,9 @@ cudaError_t launch_paged_tc(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaSt
 
 cudaError_t take_paged_tc_status(int* status, int* timeout) {
   int v[2] = {0, 0};
-  cudaError_t e = cudaMemcpyFromSymbol(&v[0], g_paged_status, sizeof v[0]);
-  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v[1], g_paged_timeout, sizeof v[1]);
-  if (e != cudaSuccess) return e;
+  const cudaError_t e = take_words(g_paged_words, v);
   *status = v[0];
   *timeout = v[1];
-  const int zero = 0;
-  if (v[0]) e = cudaMemcpyToSymbol(g_paged_status, &zero, sizeof zero);
-  if (e == cudaSuccess && v[1]) e = cudaMemcpyToSymbol(g_paged_timeout, &zero, sizeof zero);
   return e;
 }
 

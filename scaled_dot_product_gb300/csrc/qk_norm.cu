@@ -22,7 +22,7 @@
 
 namespace sdpa {
 
-static __device__ int g_norm_status;
+static __device__ int g_norm_status[1];
 
 namespace {
 
@@ -44,7 +44,7 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 __device__ __forceinline__ int64_t position(const NormJob& j, int tok) { return j.positions ? j.positions[tok] : tok; }
 __device__ __forceinline__ int64_t cache_row(const NormJob& j, int64_t row) {
   if (row < 0 || row >= j.max_pos) {
-    atomicExch(&g_norm_status, 1);
+    atomicExch(g_norm_status, 1);
     row = row < 0 ? 0 : j.max_pos - 1;
   }
   return row;
@@ -637,17 +637,7 @@ cudaError_t launch_qk_norm(sdpa_dtype dt, const NormJob& j, float* part, cudaStr
   }
 }
 
-cudaError_t take_norm_status(int* status) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_status, sizeof v);
-  if (e != cudaSuccess) return e;
-  *status = v;
-  if (v) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbol(g_norm_status, &zero, sizeof zero);
-  }
-  return e;
-}
+cudaError_t take_norm_status(int* status) { return take_words(g_norm_status, status); }
 
 SDPA_DEFINE_BOUNDS_TAKE(take_bounds_norm)
 

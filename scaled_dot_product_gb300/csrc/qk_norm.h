@@ -1,6 +1,7 @@
 // The query/key norm: its problem and launch function.
 #pragma once
 
+#include "device_words.h"
 #include "internal.h"
 #include "norm_split.h"
 

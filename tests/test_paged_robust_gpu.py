@@ -271,3 +271,61 @@ def test_a_serving_loop_keeps_one_workspace(dtype, H):
         y = attn(r, workspace=room[:need])
         assert ((y.cpu().double() - want).abs() <= tol).all(), sdpa.sdpa_last_kernel_name()
     assert (room[need:] == 0xA5).all()
+
+
+QUERY = textwrap.dedent("""
+    import sys, time, torch
+    sys.path.insert(0, {root!r}); sys.path.insert(0, {tests!r})
+    from paged_reference import ragged
+    from scaled_dot_product_gb300 import sdpa
+
+    def median(n=300):
+        ts = []
+        for _ in range(n):
+            t = time.perf_counter()
+            sdpa.sdpa_query_status()
+            ts.append(time.perf_counter() - t)
+        return sorted(ts)[n // 2]
+
+    torch.zeros(1, device="cuda")
+    median(50)
+    alone = median()
+    # one call of each kind, each with one bad page or position: reported once by the query that follows
+    seen = []
+    for dtype, new in ((torch.bfloat16, [1, 1]), (torch.bfloat16, [90, 1]), (torch.float32, [1, 1])):
+        r = ragged(new, [300, 50], dtype=dtype)
+        r.table[1, 0] = -1
+        d = r.to("cuda")
+        sdpa.sdpa_paged_attn(d.q, d.kp, d.vp, d.table, d.kv_lens, cu_new=d.cu)
+        seen += [sdpa.sdpa_query_status(), sdpa.sdpa_query_status()]
+    r.table[1] = -1
+    d = r.to("cuda")
+    sdpa.sdpa_paged_append(d.k, d.v, d.kp, d.vp, d.table, d.kv_lens, cu_new=d.cu)
+    seen += [sdpa.sdpa_query_status(), sdpa.sdpa_query_status()]
+    x, w = torch.randn(1, 2, 3, 64, device="cuda"), torch.ones(64, device="cuda")
+    c = torch.ones(4, 32, device="cuda")
+    pos = torch.tensor([[0, 1, 9]], device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):                    # captured, not run: nothing to report yet
+        sdpa.sdpa_qk_norm_rotary(x, x, w, w, c, c, pos)
+    seen.append(sdpa.sdpa_query_status())
+    for _ in range(2):
+        graph.replay()
+        seen += [sdpa.sdpa_query_status(), sdpa.sdpa_query_status()]
+    print("SEEN", *seen)
+    print("TIMES", alone, median())
+""")
+
+
+def test_the_status_query_reads_what_the_process_has_used():
+    """In a process that made no norm or paged call the query takes no longer than before there were
+    any; what each of them reports still arrives, of replayed graphs too."""
+    out = subprocess.run([sys.executable, "-c", QUERY.format(root=ROOT, tests=os.path.join(ROOT, "tests"))], capture_output=True,
+                         text=True, timeout=300)
+    assert out.returncode == 0, out.stderr[-2000:]
+    lines = {line.split()[0]: line.split()[1:] for line in out.stdout.splitlines()}
+    bad = str(sdpa.SDPA_ERR_INVALID)
+    assert lines["SEEN"] == [bad, "0"] * 4 + ["0"] + [bad, "0"] * 2
+    alone, after = (float(x) for x in lines["TIMES"])
+    # four words are read by themselves, nine with all kernels used
+    assert alone < 0.7 * after, (alone, after)
