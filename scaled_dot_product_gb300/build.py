@@ -3,6 +3,7 @@
 Each translation unit under csrc/ is compiled in parallel to an object in _build/,
 then linked into scaled_dot_product_gb300/libsdpa.so; csrc/binding.cpp, the native part of the
 Python binding, becomes scaled_dot_product_gb300/_binding.so.  Up-to-date objects are reused.
+The library needs neither torch nor its headers: it is built where the binding cannot be.
 """
 from __future__ import annotations
 
@@ -50,6 +51,16 @@ BINDING = os.path.join(PKG, "_binding.so")
 
 
 def build_binding(verbose: bool = False) -> str:
+    """Builds the binding; raises if it cannot, and leaves no older one in its place."""
+    try:
+        return _build_binding(verbose)
+    except Exception:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        raise
+
+
+def _build_binding(verbose: bool) -> str:
     import torch
     root = os.path.dirname(torch.__file__)
     # built against one interpreter and one torch: a stamp names them
@@ -77,6 +88,8 @@ def build_binding(verbose: bool = False) -> str:
 
 
 def build(verbose: bool = False, extra_flags=None, bounds_check: bool = False) -> str:
+    """Builds the library and returns its path; the binding too, where it can be (what kept it from
+    that is printed, and the norm and paged calls of sdpa.py raise without it)."""
     nvcc = _nvcc()
     build_dir = BUILD + ("_bounds" if bounds_check else "")
     lib_path = LIB_BOUNDS if bounds_check else LIB
@@ -102,7 +115,6 @@ def build(verbose: bool = False, extra_flags=None, bounds_check: bool = False) -
     with ThreadPoolExecutor(max_workers=max(1, min(len(sources) + 1, os.cpu_count() or 4))) as ex:
         binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(compile_one, sources))
-        binding.result()
     if _stale(lib_path, objs):
         tmp = lib_path + f".tmp{os.getpid()}"
         cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart"]
@@ -110,6 +122,8 @@ def build(verbose: bool = False, extra_flags=None, bounds_check: bool = False) -
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, lib_path)
+    if binding.exception() is not None:
+        print(f"{lib_path} is built, {BINDING} is not: {binding.exception()}", file=sys.stderr)
     return lib_path
 
 
