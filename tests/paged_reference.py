@@ -185,3 +185,37 @@ def paged_attn64(r: Ragged, *, scale=None, softcap=0.0, causal=True, window=-1, 
                     tol[t0 + i, h] += 2.0 ** -25      # half of the smallest subnormal step
         t0 += n
     return y, tol
+
+
+# ------------------------------------------------------------------ gradients by differences
+
+def slope64(f, h):
+    """f'(0) of a smooth float64 function by central differences at h, h/2 and h/4, extrapolated twice
+    over (their h^2 terms cancel), and a bound of its error: what the finer extrapolation still changed,
+    which is about 16 times the error left, beside the rounding of the differences."""
+    d = [(f(s) - f(-s)) / (2 * s) for s in (h, h / 2, h / 4)]
+    coarse, fine = (4 * d[1] - d[0]) / 3, (4 * d[2] - d[1]) / 3
+    return fine, abs(fine - coarse) + 2.0 ** -44 * max(abs(f(h)), abs(f(-h))) / h
+
+
+def norm_slope_check(d, name, grads, cos, sin, R, interleaved, eps, seed):
+    """The gradient of sum(q_out dq_out) + sum(k_out dk_out) along a direction of -1, 0 and 1 in
+    d[name] against differences of the float64 forward: -> (error, tolerance).  d: rank-4 problem;
+    grads[name]: the gradient in question.  The tolerance takes nothing from it: the slope's own
+    bound, and fp32 arithmetic's error of each element (the sums of test_backward's bounds)."""
+    gen = torch.Generator().manual_seed(seed)
+    t = name[0]
+    direction = torch.randint(-1, 2, d[name].shape, generator=gen).double()
+    x, w, dy = d[t].double(), d[t + "_weight"].double(), d["d" + t + "_out"].double()
+
+    def loss(step):
+        at = {name: d[name].double() + step * direction}
+        y, _ = norm_rotary64(at.get(t, x), at.get(t + "_weight", w), cos, sin, R, interleaved, eps)
+        return (y * dy).sum().item()
+
+    truth, tol = slope64(loss, 2.0 ** -6)
+    dx, dw, mag, wsum = norm_rotary_grad64(x, w, dy, cos, sin, R, interleaved, eps)
+    hs = HALF_STEP[d[name].dtype]
+    each = hs * dx.abs() + 64 * U32 * mag if name == t else hs * dw.abs() + (x[..., 0].numel() + 64) * U32 * wsum
+    inner = (grads[name].cpu().double() * direction).sum().item()
+    return abs(inner - truth), tol + (each * direction.abs()).sum().item()

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 import torch
 
-from paged_reference import norm_rotary64, norm_rotary_grad64
+from paged_reference import norm_rotary64, norm_rotary_grad64, norm_slope_check, rotate64
 from scaled_dot_product_gb300 import sdpa
 
 BF = torch.bfloat16
@@ -306,3 +306,50 @@ def test_empty_batches_with_a_cache_row_per_token(B, S):
         assert sdpa.lib().sdpa_qk_norm_workspace_size(ctypes.byref(p)) > 0
     p, q, k, keep = norm(dict(rotary_max_pos=0), ids=False)      # tokens without rows are refused as before
     assert norm_code(p, q, k, keep) == sdpa.SDPA_ERR_SHAPE
+
+
+def grad_problem(R, inter, dtype=torch.float32, D=64):
+    g = torch.Generator().manual_seed(3)
+    rn = lambda *s: torch.randn(*s, generator=g).to(dtype)
+    d = dict(q=rn(1, 2, 4, D), k=rn(1, 1, 4, D), q_weight=(1 + 0.3 * torch.randn(D, generator=g)).to(dtype),
+             k_weight=(1 + 0.3 * torch.randn(D, generator=g)).to(dtype), dq_out=rn(1, 2, 4, D), dk_out=rn(1, 1, 4, D))
+    ang = torch.rand(1, 4, max(R, 2) // 2, generator=g) * 6
+    return d, torch.cos(ang).to(dtype), torch.sin(ang).to(dtype)
+
+
+def formula_grads(d, cos, sin, R, inter):
+    out = {}
+    for t in "qk":
+        dx, dw, _, _ = norm_rotary_grad64(d[t].double(), d[t + "_weight"].double(), d["d" + t + "_out"].double(), cos.double(),
+                                          sin.double(), R, inter, 1e-5)
+        out[t], out[t + "_weight"] = dx, dw
+    return out
+
+
+@pytest.mark.parametrize("R,inter", [(64, False), (32, True), (0, False)])
+def test_the_check_by_differences_tells_wrong_gradients(R, inter):
+    """The formula's gradient passes with room; one without its mean term, one with 0.9 of the weights'
+    sums and one turned the wrong way do not."""
+    d, cos, sin = grad_problem(R, inter)
+    good = formula_grads(d, cos, sin, R, inter)
+    autograd = {}
+    for t in "qk":
+        x, w = d[t].double().requires_grad_(), d[t + "_weight"].double().requires_grad_()
+        (norm_rotary64(x, w, cos.double(), sin.double(), R, inter, 1e-5)[0] * d["d" + t + "_out"].double()).sum().backward()
+        autograd[t], autograd[t + "_weight"] = x.grad, w.grad
+    no_mean, short, turned = {}, {}, formula_grads(d, cos, -sin, R, inter)
+    for t in "qk":
+        x, w = d[t].double(), d[t + "_weight"].double()
+        dy = d["d" + t + "_out"].double()
+        g = rotate64(dy, cos.double()[:, None], -sin.double()[:, None], R, inter) if R else dy
+        no_mean[t] = g * w / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-5)
+        short[t + "_weight"] = 0.9 * good[t + "_weight"]
+    for i, name in enumerate(("q", "k", "q_weight", "k_weight")):
+        check = lambda grads: norm_slope_check(d, name, grads, cos.double(), sin.double(), R, inter, 1e-5, 9 + i)
+        assert torch.allclose(good[name], autograd[name], rtol=1e-10, atol=1e-12)
+        err, tol = check(good)
+        assert err < 0.2 * tol
+        for wrong in (no_mean, short) + ((turned,) if R else ()):
+            if name in wrong:
+                err, tol = check(wrong)
+                assert err > 3 * tol, (name, err, tol)

@@ -10,7 +10,7 @@ sum of the terms' magnitudes.
 import pytest
 import torch
 
-from paged_reference import HALF_STEP, U32, norm_rotary64, norm_rotary_grad64
+from paged_reference import HALF_STEP, U32, norm_rotary64, norm_rotary_grad64, norm_slope_check
 from scaled_dot_product_gb300 import sdpa
 from scaled_dot_product_gb300.workloads import rope_caches
 
@@ -266,3 +266,18 @@ def test_empty_batches_with_a_cache_row_per_token(rank):
         dq, dk, dwq, dwk = sdpa.sdpa_qk_norm_rotary_bwd(**g, **kw)
         assert dq.shape == g["q"].shape and not dwq.any() and not dwk.any()      # sums over no rows
         assert sdpa.sdpa_query_status() == 0
+
+
+@pytest.mark.parametrize("dtype,D,R,inter", [(FP, 64, 64, False), (FP, 128, 32, True), (FP, 50, 50, False), (FP, 256, 0, False),
+                                             (BF, 128, 128, False), (HF, 64, 64, True)])
+def test_gradient_against_differences_of_the_definition(dtype, D, R, inter):
+    """Along random directions, within a bound that takes nothing from the gradient under test (the CPU
+    tests show that a gradient without its mean term is well outside it)."""
+    d = draw(1, 4, 2, 1, D, dtype, 4, R, "ids", seed=3, grad=True)
+    out = sdpa.sdpa_qk_norm_rotary_bwd(**{n: t.cuda() for n, t in d.items()}, rotary_dim=R, interleaved=inter, eps=1e-5)
+    grads = dict(zip(("q", "k", "q_weight", "k_weight"), out))
+    cos, sin = tables(d)
+    for name in grads:
+        for seed in range(4):
+            err, tol = norm_slope_check(d, name, grads, cos, sin, R, inter, 1e-5, seed)
+            assert err <= tol, (name, err, tol)
