@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (whole) {
         const int pr = row0 + r, tok = group_div(g, pr), h = head0 + pr - tok * g.group;
         T* y = reinterpret_cast<T*>(const_cast<void*>(a.y.p)) + a.y.off(0, h, t0 + tok);
-        if (SDPA_IN_BOUNDS(t0 + tok < g.tokens && h < g.Nq, 532))
+        if (SDPA_IN_BOUNDS(t0 + tok < g.tokens && h < g.Nq, 535))
           *reinterpret_cast<uint2*>(y + c) = make_uint2(pack2<BF>(v.x, v.y), pack2<BF>(v.z, v.w));
       } else if (SDPA_IN_BOUNDS(slot < 2 * ctas, 534)) {
         *reinterpret_cast<float4*>(ws.o + (slot * TM + r) * H + c) = v;

@@ -39,3 +39,21 @@ def test_the_library_is_built_without_torch():
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == build.LIB, r.stderr[-2000:]
     assert "torch" in r.stderr
+
+
+def test_a_bounds_site_names_one_check():
+    """The checking build reports a number: it stands for one place in the sources."""
+    sites = {}
+    for name in sorted(os.listdir(build.CSRC)):
+        src = open(os.path.join(build.CSRC, name)).read()
+        at = src.find("SDPA_IN_BOUNDS(")
+        while at >= 0:
+            end, depth = at + len("SDPA_IN_BOUNDS("), 1
+            while depth:
+                depth += {"(": 1, ")": -1}.get(src[end], 0)
+                end += 1
+            last = src[at:end - 1].rsplit(",", 1)[1].strip()
+            if last.isdigit():                            # not the macro itself
+                sites.setdefault(int(last), []).append((name, src.count("\n", 0, at) + 1))
+            at = src.find("SDPA_IN_BOUNDS(", end)
+    assert len(sites) > 20 and all(len(v) == 1 for v in sites.values()), {k: v for k, v in sites.items() if len(v) > 1}
