@@ -356,8 +356,10 @@ SDPA_API int sdpa_paged_append(const sdpa_paged_params* p, sdpa_view k, sdpa_vie
  * a few, chunks and any mixture.  A row with no admitted key is written as zeros; rows behind
  * cu_new[B] are left as they were; what lies in slots past a sequence's keys, or of keys below
  * the windows of all its new tokens, does not matter (NaN included).  A NaN in a row's query, in a
- * key or value that it admits or in its head's sink makes the row NaN; a score of -inf counts as
- * not admitted.  A value that is not finite at a key that one new token admits may reach the
+ * key that it admits or in its head's sink makes the row NaN, one in a value that channel; a score
+ * of -inf counts as not admitted.  In 16-bit types with H = Hv in {64, 128} the weights enter the
+ * value product rounded to the type (half a step each; sdpa_attn_decode keeps them in fp32); every
+ * other sum is fp32.  A value that is not finite at a key that one new token admits may reach the
  * sequence's others.  Lengths out of range are clamped and reported; a page id out of range is
  * reported and its keys and values read as zeros.
  * workspace: sdpa_paged_workspace_size(p) bytes, any contents, 256-byte aligned.  The size depends on

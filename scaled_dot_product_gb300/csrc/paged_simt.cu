@@ -6,7 +6,10 @@
 // joined in shared memory at the end of a unit.  Bound by latency: eight float32 sequences of 500 to 4000
 // keys, 16/4 heads of 64, take 20 to 21 us (38.8 MB); 30.5 us with 64 full reductions a step instead of 15
 // exchanges and one thread an item of the join, 34.6 with four CTAs an SM.  It serves fp32 (whose sums the 16-bit tensor
-// products cannot carry) and head sizes that the tensor-core kernels do not tile.
+// products cannot carry) and head sizes that the tensor-core kernels do not tile, for single tokens and a
+// few: 16 sequences of 2000 to 16000 keys, 32/8 heads, float32 of 128 334 us (4.5 TB/s), bfloat16 of 96 428 us
+// (1.3 TB/s), of 256 830 us (1.8 TB/s).  Chunks read their keys again for every four rows: 200 tokens
+// over 4000 keys, 16/4 float32 heads of 64, 296 us; 512 over 4000, 32/8 heads of 96, 2.96 ms (9 TFLOP/s).
 #include <algorithm>
 
 #include "paged_sched.cuh"
@@ -412,7 +415,11 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
 template <typename T, int TM, int TN>
 cudaError_t merge_tn(const PagedAttn& a, const PagedWs& ws, int ctas, cudaStream_t st) {
   // Few units are cut into many partials each (16 and more): then 8 rows and 32 columns a block, four threads an
-  // item.  Otherwise whole rows, at most 16 (or 32 of a 256-row unit) a block.
+  // item.  Otherwise whole rows, at most 16 (or 32 of a 256-row unit) a block.  Both sides, 16000 keys a
+  // sequence, units of 16 / 32 / 64 rows (304 CTAs): 1 unit 29 / 29 / 49 us in whole rows, 15 / 15 / 24 cut; 8
+  // units 25 / 26 / 49 and 19 / 20 / 38; 16 units 35 / 26 / 56 and 32 / 24 / 56; 24 units 43 / 30 / 67 and 42 / 30 / 70;
+  // 64 units 89 / 61 / 133 and 90 / 63 / 144.  Of 4 rows (456 CTAs): 1 unit 17.9 and 16.3, 24 units 54.0 and
+  // 54.6.  At 2000 keys they are within 2 us of each other up to 16 units.
   const int cols = a.g.Hv / 4;
   const bool few = TM <= 64 && (int64_t)a.g.B * a.g.Nkv < ctas / 16;
   const MergeCut cut = few ? MergeCut{std::min(TM, 8), 8} : MergeCut{TM == 256 ? 32 : std::min(TM, 16), cols};

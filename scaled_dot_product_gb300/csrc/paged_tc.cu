@@ -17,11 +17,14 @@
 //   warp 3      query rows by 16-byte asynchronous copies for the other groups
 //   warps 4-7   softmax of tile 0, one thread per row; warps 8-11 softmax of tile 1
 //
-// A chunk of 2048 tokens over 32000 keys, 32/8 heads of 128: 735 to 768 us, 1430 to 1495 TFLOP/s (76
-// to 79 % of the measured bf16 burst rate); a causal prompt of 4096 tokens 125 us, 1090 TFLOP/s; single tokens through
-// this kernel 6.4 TB/s.  Running maxima move only when they grow by more than 2^8.  Every wait is
-// bounded: on expiry the kernel raises an abort flag, lets its own copies and products finish, frees
-// its tensor memory and records SDPA_ERR_TIMEOUT.
+// A chunk of 2048 tokens over 32000 keys, 32/8 heads of 128: 717 to 768 us, 1430 to 1530 TFLOP/s (76
+// to 81 % of the measured bf16 burst rate); a causal prompt of 4096 tokens 125 to 138 us, up to 1090
+// TFLOP/s (64/8 heads of 64: 194 us, 709); single tokens through this kernel 6.4 TB/s.  Running maxima
+// move only when they grow by more than 2^8.  The weights enter the second product rounded to the
+// element type (half a step each), since its operands are 16-bit; their sum takes them unrounded.
+// 168 registers at launch, 252 bytes of spills a thread.  Every wait is bounded: on expiry the kernel
+// raises an abort flag, lets its own copies and products finish, frees its tensor memory and records
+// SDPA_ERR_TIMEOUT.
 #include <algorithm>
 #include <cstdlib>
 #include <type_traits>
@@ -39,7 +42,11 @@ using namespace ptx;
 
 constexpr int kBM = 128, kTM = 256, kTN = 128;
 constexpr int kThreads = 384;
-constexpr int kOV = 8;                // a unit's cost beside its tiles (a tile costs 4, or 3 in a narrow unit)
+// A unit's cost beside its tiles (a tile costs 4, or 3 in a narrow unit).  Measured: 4 chunks and 24
+// tokens with a window of 1024 81 us (with 4: 84, with 16: 87), a causal prompt of 4096 137 us on the
+// same GPU (166, 137).
+constexpr int kOV = 8;
+// Least cost worth a CTA: 12, 24 and 48 measure alike, down to four prompts of 1000 (61 to 67 us each).
 constexpr int kMinShare = 24;
 // Register split: the control warpgroup shrinks to kCtlRegs, the softmax warpgroups grow to
 // kSmxRegs; the sum stays within the launch's kThreads x kLaunchRegs, which the host checks.
@@ -797,7 +804,9 @@ bool paged_boxes(const PagedAttn& a) {
   return true;
 }
 
-// More rows of a sequence than paged_mma's widest unit holds.
+// More rows of a sequence than paged_mma's widest unit holds.  16 sequences of 2000 to 8000 keys, 8
+// query heads a key head, H = 64 / 128: 72 rows 54 / 79 us here, 93 / 166 there; 64 rows 54 / 78 here, 54
+// / 96 there; 32 rows 52 / 77 here, 42 / 70 there.
 bool paged_tc_supported(const PagedAttn& a, sdpa_dtype dt) {
   return paged_mma_supported(a.g.H, a.g.Hv, dt) && paged_boxes(a) && (int64_t)a.max_new * a.g.group > 64;
 }

@@ -12,9 +12,11 @@
 // save those shuffles but took 118 registers forward and 174 backward, and the loads in flight
 // with them: 20.9 and 98.7 us on the first and last of these.)  On the device, bf16, heads of 128:
 // 4096 tokens x 40 heads forward 16.5 us (5.1 TB/s), 4503 tokens x 72 float16 heads of 64 15.0 us
-// (5.55 TB/s), backward of 8192 tokens x 40 heads 50.7 us (5.0 TB/s).
+// (5.55 TB/s), backward of 8192 tokens x 40 heads 50.7 us (5.0 TB/s); in fp32 29.1 us (5.8 TB/s) and 79.5
+// us (6.4 TB/s) for the first and the last.
 // Shapes or pointers that do not allow 16-byte vectors take the scalar kernels (one warp per
-// row, the row in shared memory), as do fp32 heads of more than 128 channels.
+// row, the row in shared memory), as do fp32 heads of more than 128 channels: 63.0 and 196 us for as
+// many bytes as those two fp32 cases, 76.6 us for the first case with 20 of 128 channels rotated.
 #include <algorithm>
 
 #include "qk_norm.h"
@@ -286,8 +288,10 @@ __global__ void __launch_bounds__(kThreads) norm_fwd_scalar_kernel(const NormJob
 // accumulates dw for the one weight vector of its side.  A task is up to kHeads heads of one
 // token, taken kPair at a time, whose sums' shuffles overlap; the next kRing - 1 pairs' x and dy are on
 // their way into shared memory meanwhile.  Each block leaves its D sums in part[blockIdx.x]; norm_dw_kernel adds them in
-// block order, so results do not vary from run to run.  Bound by the latency of the two chained
-// sums at 16 warps an SM: one head at a time took 72 us on 8192 tokens x 40 heads, tasks of 16
+// block order, so results do not vary from run to run.  Bound by instructions in 16-bit types: 68 % of
+// the issue slots are busy (DRAM 57 %), and a scheduler's four warps wait for their turn (1.2 of them
+// per issued instruction) and for fixed latencies (1.2) more than for memory (0.5) or shuffles (0.4).
+// One head at a time took 72 us on 8192 tokens x 40 heads, tasks of 16
 // heads 71, three blocks an SM (spills) 90, the next pair in registers instead of the ring 53.3, equal
 // contiguous shares of the rows instead of tasks in turn 54.3, this 50.7.
 constexpr int kHeads = 8, kPair = 2, kRing = 4;
