@@ -17,13 +17,13 @@
 // instructions went into addresses, and a single-token batch of 4.48 GB took 851 us.)  Rows of V that
 // no row of the unit admits (past its keys, below every window) are set to zero before they are
 // multiplied, since 0 x NaN is not 0.  Single tokens of 64 sequences, 1000 to 32000 keys, 64/8 heads of
-// 128: 650 to 680 us, 6.6 to 6.9 TB/s (98 % of the measured copy rate and more); five drafted tokens of 16
+// 128: 650 to 682 us, 6.6 to 6.9 TB/s (97 % of the measured copy rate and more); five drafted tokens of 16
 // sequences 95 us, 5.4 TB/s; four short sequences 11.3 us.  The weights enter the second product rounded
 // to the element type (half a step each; their sum takes them unrounded), since that product's
-// operands are 16-bit (the dense decode's one row a step keeps them in fp32).  With H = 128 the tiles of 32 and 64 rows spill 12 and 78 bytes a thread (168 registers at
-// two CTAs an SM).  Every wait is bounded: on expiry the kernel raises an abort
-// flag, goes through its loops without waiting, lets its own copies finish and records
-// SDPA_ERR_TIMEOUT.
+// operands are 16-bit (the dense decode's one row a step keeps them in fp32).  With H = 128 the tiles of
+// 32 and 64 rows spill 12 and 78 bytes a thread (168 registers at two CTAs an SM).  Every wait is
+// bounded: on expiry the kernel raises an abort flag, goes through its loops without waiting, lets its
+// own copies finish and records SDPA_ERR_TIMEOUT.
 #include <algorithm>
 #include <cstdlib>
 #include <type_traits>
