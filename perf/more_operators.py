@@ -190,7 +190,11 @@ def prepare(case, seed):
         st["count"] = torch.tensor([spare.numel()], dtype=torch.int32, device="cuda")
         st["past"] = torch.tensor(past, dtype=torch.int32, device="cuda")
         st["new"] = torch.tensor(new, dtype=torch.int32, device="cuda")
-        st["tokens"] = sum(max(n, 0) for n in new) + 3          # rows of the program's buffers, a few more than used
+        tokens = st["tokens"] = sum(max(n, 0) for n in new) + 3      # rows of the program's buffers, a few more than used
+        st["out"] = dict(kv_lens=torch.empty_like(st["past"]), free_count_out=torch.empty_like(st["count"]),
+                         cu_new=torch.empty(case["B"] + 1, dtype=torch.int32, device="cuda"),
+                         positions=torch.empty(tokens, dtype=torch.int64, device="cuda"),
+                         slots=torch.empty(tokens, dtype=torch.int64, device="cuda"))
         return st
     dt = _DT[case["dtype"]]
     B, Nkv, D = (case[x] for x in ("B", "Nkv", "D"))
@@ -209,6 +213,7 @@ def prepare(case, seed):
         size = torch.exp(0.5 * torch.randn(D, generator=gen, device="cuda"))
         st["k"] = (torch.randn(tokens, Nkv, D, generator=gen, device="cuda") * size).to(dt)
         st["v"] = _randn(gen, (tokens, Nkv, D), dt)
+        st["k_held"], st["v_held"] = torch.empty_like(st["k"]), torch.empty_like(st["v"])
         seq = torch.repeat_interleave(torch.arange(B, device="cuda"), torch.tensor(new, device="cuda"))
         first = torch.tensor([p - c for p, c in zip(past, cu)], device="cuda")
         st["positions"] = first[seq] + torch.arange(tokens, device="cuda")
@@ -375,14 +380,14 @@ def run(state):
     if op == "tables":
         lens, cu, pos, slots, count = sdpa.sdpa_paged_tables(state["table"], state["past"], state["new"], state["free"],
                                                              state["count"], page_size=case["page"],
-                                                             tokens=state["tokens"])
+                                                             tokens=state["tokens"], **state["out"])
         return lens, cu, pos, slots, state["table"], state["free"], count
     if op == "append":
         rot = {}
         if case["R"]:
             rot = dict(positions=state["positions"], cos_cache=state["cos"], sin_cache=state["sin"],
                        rotary_dim=case["R"], interleaved=case["interleaved"])
-        kh, vh = torch.empty_like(state["k"]), torch.empty_like(state["v"])
+        kh, vh = state["k_held"], state["v_held"]
         kp, vp = sdpa.sdpa_paged4_append(state["k"], state["v"], state["k_pages"], state["v_pages"], state["slots"],
                                          k_held=kh, v_held=vh, **rot)
         return kh, vh, kp, vp
