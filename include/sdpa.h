@@ -369,6 +369,91 @@ SDPA_API int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view 
                              size_t workspace_bytes, sdpa_stream_t stream);
 SDPA_API size_t sdpa_paged_workspace_size(const sdpa_paged_params* p);
 
+/* The tables of a step over a paged cache, made on the device: from past_lens (keys of each sequence
+ * before the step) and new_lens (its new tokens; negative: the sequence has ended) the call gives back the pages of ended
+ * sequences, takes pages for the grown ones, and writes
+ *   page_table[b]    entries ceil(past / page_size) .. ceil(T / page_size) - 1, T = past + new; others stay
+ *   kv_lens[b]       T (0 where the sequence has ended)
+ *   cu_new           running sum of the new tokens, B + 1 entries: first packed row of each sequence
+ *   positions[t]     key position of packed row t, for t < tokens; 0 behind the last sequence's rows
+ *   slots[t]         page * page_size + slot of that position; -1 behind the last row, or without a page
+ *   free_pages       a stack of num_pages entries, the first free_count of them free pages.  Ended
+ *                    sequences' pages (their first ceil(past / page_size) entries) go on top, in the order
+ *                    of sequences and entries; then the pages taken come off it, in the order of
+ *                    sequences and entries, from the top.  Entries above the top keep their contents
+ *   free_count_out   free pages afterwards; negative: so many were missing
+ * Every page belongs to one sequence.  All values are device data and checked there; what is out
+ * of range is reported by sdpa_query_status as SDPA_ERR_INVALID and nothing outside the given
+ * buffers is touched: a length beyond the table's width, or more new tokens than `tokens` rows, is cut
+ * off; a missing page or a page id outside [0, num_pages) makes its tokens' slots -1 (a missing one
+ * its table entry too), and such ids are not given back.
+ * kv_lens may be past_lens, and free_count_out free_count (in place); other arrays share nothing.
+ * Without in-place arguments a call repeated on the same inputs writes the same outputs.  B <= 8192. */
+typedef struct {
+  int32_t struct_size;          /* must be sizeof(sdpa_paged_tables_params)                  */
+  int32_t B, tokens;
+  int32_t page_size, max_pages, num_pages;
+  int32_t* page_table;          /* (B, max_pages), rows page_table_stride apart              */
+  int64_t page_table_stride;
+  const int32_t* past_lens;     /* (B)                                                       */
+  const int32_t* new_lens;      /* (B)                                                       */
+  int32_t* free_pages;          /* (num_pages)                                               */
+  const int32_t* free_count;    /* (1)                                                       */
+  int32_t* kv_lens;             /* (B)                                                       */
+  int32_t* cu_new;              /* (B + 1)                                                   */
+  int64_t* positions;           /* (tokens)                                                  */
+  int64_t* slots;               /* (tokens)                                                  */
+  int32_t* free_count_out;      /* (1)                                                       */
+} sdpa_paged_tables_params;
+SDPA_API int sdpa_paged_tables(const sdpa_paged_tables_params* p, sdpa_stream_t stream);
+
+/* A paged cache of 4 bits a value.  A head row of D channels (D a multiple of 32, at most 256) is a
+ * record of sdpa_paged4_row_bytes(D, dtype) bytes: D/2 bytes of codes, channel 2j in the low half of
+ * byte j and channel 2j + 1 in the high half; then for each 32 channels their minimum and their scale
+ * in dtype.  A value is minimum + scale * code.  A pool is (num_pages, Nkv, page_size, record) bytes
+ * whose last two axes are contiguous: views have strides in bytes, stride_s the record's, stride_b and
+ * stride_n multiples of 16; page_size * record must be a multiple of 16 (so page_size is even for 64
+ * channels of 16-bit types), pointers 16-byte aligned. */
+SDPA_API int64_t sdpa_paged4_row_bytes(int32_t D, sdpa_dtype dtype);      /* -1: no such record */
+
+typedef struct {
+  int32_t struct_size;          /* must be sizeof(sdpa_paged4_append_params)                 */
+  int32_t tokens;               /* packed rows                                               */
+  int32_t Nkv, H, Hv;
+  sdpa_dtype dtype;             /* element type of the rows, the caches and the records' sides */
+  int32_t num_pages, page_size;
+  sdpa_view k_pages, v_pages;   /* pools of records                                          */
+  const int64_t* slots;         /* (tokens): page * page_size + slot; negative: not stored   */
+  const int64_t* positions;     /* (tokens): needed for the rotation alone                   */
+  const void* rotary_cos;       /* as in sdpa_paged_params                                   */
+  const void* rotary_sin;
+  int64_t rotary_max_pos;
+  int32_t rotary_dim;
+  int32_t rotary_interleaved;
+} sdpa_paged4_append_params;
+
+/* Writes the records of the new keys k (packed, (tokens, Nkv, H)), turned by the angle of their
+ * positions and rounded to dtype, and values v (packed, (tokens, Nkv, Hv)) into their slots.  Per 32 channels, in
+ * fp32: scale = (max - min) / 15 rounded to dtype (down where min + 15 * scale would leave its range), code = (x - min) / scale rounded to the nearest integer,
+ * ties to even, and at most 15 (0 where the scale is 0).  A group whose spread is not finite (with a value
+ * that is not, or wider than fp32) takes NaN for both and reads as NaN.  The slots of different tokens must
+ * differ; every other slot keeps its contents.  A slot behind the pool is skipped and reported by
+ * sdpa_query_status (SDPA_ERR_INVALID), a position outside the rotary cache reported and clamped.
+ * k_held, v_held (packed as k and v, or data NULL): the rows as the cache holds them, minimum + scale *
+ * code rounded to dtype, for calls that attend to the new tokens from their rows; rows without a
+ * slot are left as they were.  Alignment of rows as for sdpa_paged_append. */
+SDPA_API int sdpa_paged4_append(const sdpa_paged4_append_params* p, sdpa_view k, sdpa_view v, sdpa_view k_held,
+                                sdpa_view v_held, sdpa_stream_t stream);
+
+/* sdpa_paged_attn over pools of records: k_pages and v_pages of p are those (strides in bytes), H and
+ * Hv multiples of 32, everything else as there, the rotary fields unused.  The products take the codes as they are; with H = Hv in {64,
+ * 128} and a 16-bit type the weights enter the value product rounded to 16 bits.  workspace:
+ * sdpa_paged4_workspace_size(p) bytes, any contents, 256-byte aligned; the size depends on dtype, H and Hv
+ * alone. */
+SDPA_API int sdpa_paged4_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace, size_t workspace_bytes,
+                              sdpa_stream_t stream);
+SDPA_API size_t sdpa_paged4_workspace_size(const sdpa_paged_params* p);
+
 /* present[b, n, 0:P] = past[b, n, :]; present[b, n, P:P+L] = cur[b, n, :] (+ bias[n*D:(n+1)*D]
  * rounded once to dtype when bias is non-NULL).  (class Attention, past_key/past_value
  * and Result.present_key; MHA: present holds P+L positions; GQA: present holds the whole
@@ -381,7 +466,8 @@ SDPA_API int sdpa_kv_concat(sdpa_dtype dtype, int32_t B, int32_t N, int32_t P, i
 
 /* Synchronises `stream`, then reads and clears the current device's status words: set when
  * a bounded wait of a kernel expires (SDPA_ERR_TIMEOUT), or a rotary position falls outside its
- * cache or a page id, length or offset of a paged call outside its range (SDPA_ERR_INVALID).
+ * cache or a page id, length, offset or slot of a paged call outside its range, or a list of free
+ * pages runs out (SDPA_ERR_INVALID).
  * Returns SDPA_OK, one of those codes, or SDPA_ERR_CUDA when the synchronisation itself failed. */
 SDPA_API int sdpa_query_status(sdpa_stream_t stream);
 

@@ -13,6 +13,7 @@
 
 #include "internal.h"
 #include "paged.h"
+#include "paged4.h"
 #include "paged_sched.cuh"
 #include "prefill_tc.h"
 #include "qk_norm.h"
@@ -29,7 +30,9 @@ namespace {
 // us for each).
 std::atomic<unsigned> g_used{0};
 constexpr unsigned kUsedNorm = 1, kUsedAppend = 2, kUsedPaged = 4;      // kUsedPaged << PagedKernel
+constexpr unsigned kUsedTables = 32, kUsedAppend4 = 64, kUsedPaged4 = 128;      // kUsedPaged4 << PagedKernel
 constexpr unsigned kUsedSimt = kUsedPaged << kPagedSimt, kUsedMma = kUsedPaged << kPagedMma, kUsedTc = kUsedPaged << kPagedTc;
+constexpr unsigned kUsedAttn4 = (kUsedPaged4 << kPagedSimt) | (kUsedPaged4 << kPagedMma) | (kUsedPaged4 << kPagedTc);
 void mark_used(unsigned what) {
   if ((g_used.load(std::memory_order_relaxed) & what) != what) g_used.fetch_or(what, std::memory_order_relaxed);
 }
@@ -47,7 +50,8 @@ int fail(int code, const char* fmt, ...) {
   return code;
 }
 
-int esize(int dt) { return dt == SDPA_F32 ? 4 : 2; }
+constexpr int kBytes = -1;      // "element type" of pools of records
+int esize(int dt) { return dt == SDPA_F32 ? 4 : dt == kBytes ? 1 : 2; }
 int vec_elems(int dt) { return 16 / esize(dt); }
 
 struct Extent {
@@ -488,8 +492,31 @@ void norm_side_inputs(const sdpa_qk_norm_params* p, const NormJob& j, Extent out
   out[4] = flat(j.positions, (size_t)j.tokens * 8, "position_ids");
 }
 
-// The paged cache and the ragged batch, as both paged entry points check them.
-int check_paged(const sdpa_paged_params* p, Paged* g, Extent ext[2]) {
+// A pool of records of D channels.
+int check_pool4(const sdpa_view& v, const char* name, int64_t pages, int64_t heads, int64_t slots, int D, int dt, Extent* ext) {
+  const int64_t rb = q4_row_bytes(D, esize(dt));
+  int rc;
+  if ((rc = check_view(v, name, kBytes, pages, heads, slots, rb, true, false, ext))) return rc;
+  if (!v.data) return SDPA_OK;
+  if (slots > 1 && v.stride_s != rb)
+    return fail(SDPA_ERR_INVALID, "%s: records of %lld bytes must lie one after another (stride %lld)", name, (long long)rb,
+                (long long)v.stride_s);
+  if (((uintptr_t)v.data & 15u) != 0) return fail(SDPA_ERR_ALIGNMENT, "%s: pointer not 16-byte aligned", name);
+  if (v.stride_b % 16 || v.stride_n % 16) return fail(SDPA_ERR_ALIGNMENT, "%s: strides must be multiples of 16 bytes", name);
+  if (slots * rb % 16)
+    return fail(SDPA_ERR_ALIGNMENT, "%s: %lld slots of %lld bytes are no multiple of 16 bytes", name, (long long)slots, (long long)rb);
+  return SDPA_OK;
+}
+
+int check_heads4(int H, int Hv) {
+  if (H < 1 || Hv < 1 || H > 256 || Hv > 256 || H % kQ4Group || Hv % kQ4Group)
+    return fail(SDPA_ERR_UNSUPPORTED, "head sizes must be multiples of %d and at most 256 (H=%d Hv=%d)", kQ4Group, H, Hv);
+  return SDPA_OK;
+}
+
+// The paged cache and the ragged batch, as the paged entry points check them.  four: pools of records
+// of 4 bits a value.
+int check_paged(const sdpa_paged_params* p, Paged* g, Extent ext[2], bool four = false) {
   if (!p) return fail(SDPA_ERR_NULL, "params is NULL");
   if (p->struct_size != (int32_t)sizeof(sdpa_paged_params))
     return fail(SDPA_ERR_INVALID, "struct_size %d != sizeof(sdpa_paged_params) %d", p->struct_size,
@@ -504,8 +531,12 @@ int check_paged(const sdpa_paged_params* p, Paged* g, Extent ext[2]) {
   if (p->Nq % p->Nkv != 0)
     return fail(SDPA_ERR_SHAPE, "q heads (%d) must be a multiple of kv heads (%d)", p->Nq, p->Nkv);
   const int ve = vec_elems(dt);
-  if (p->H > 256 || p->Hv > 256 || p->H % ve || p->Hv % ve)
+  int rc;
+  if (four) {
+    if ((rc = check_heads4(p->H, p->Hv))) return rc;
+  } else if (p->H > 256 || p->Hv > 256 || p->H % ve || p->Hv % ve) {
     return fail(SDPA_ERR_UNSUPPORTED, "head sizes must be multiples of %d and at most 256 (H=%d Hv=%d)", ve, p->H, p->Hv);
+  }
   if ((int64_t)p->max_pages * p->page_size > ((int64_t)1 << 30))
     return fail(SDPA_ERR_OVERFLOW, "max_pages * page_size exceeds 2^30 keys");
   if ((int64_t)p->max_pages * p->page_size * p->Nkv > ((int64_t)1 << 36))
@@ -526,11 +557,15 @@ int check_paged(const sdpa_paged_params* p, Paged* g, Extent ext[2]) {
                 p->max_pages);
   if (p->page_table_stride < 0 || p->page_table_stride > ((int64_t)1 << 40))
     return fail(SDPA_ERR_OVERFLOW, "page_table_stride %lld out of range", (long long)p->page_table_stride);
-  int rc;
-  if ((rc = check_view(p->k_pages, "k_pages", dt, p->num_pages, p->Nkv, p->page_size, p->H, true, false, &ext[0]))) return rc;
-  if ((rc = check_view(p->v_pages, "v_pages", dt, p->num_pages, p->Nkv, p->page_size, p->Hv, true, false, &ext[1]))) return rc;
-  if ((rc = check_aligned_view(p->k_pages, "k_pages", dt))) return rc;
-  if ((rc = check_aligned_view(p->v_pages, "v_pages", dt))) return rc;
+  if (four) {
+    if ((rc = check_pool4(p->k_pages, "k_pages", p->num_pages, p->Nkv, p->page_size, p->H, dt, &ext[0]))) return rc;
+    if ((rc = check_pool4(p->v_pages, "v_pages", p->num_pages, p->Nkv, p->page_size, p->Hv, dt, &ext[1]))) return rc;
+  } else {
+    if ((rc = check_view(p->k_pages, "k_pages", dt, p->num_pages, p->Nkv, p->page_size, p->H, true, false, &ext[0]))) return rc;
+    if ((rc = check_view(p->v_pages, "v_pages", dt, p->num_pages, p->Nkv, p->page_size, p->Hv, true, false, &ext[1]))) return rc;
+    if ((rc = check_aligned_view(p->k_pages, "k_pages", dt))) return rc;
+    if ((rc = check_aligned_view(p->v_pages, "v_pages", dt))) return rc;
+  }
   *g = Paged{};
   g->B = p->B; g->tokens = p->tokens; g->Nq = p->Nq; g->Nkv = p->Nkv; g->H = p->H; g->Hv = p->Hv;
   g->group = p->Nq / p->Nkv;
@@ -539,6 +574,10 @@ int check_paged(const sdpa_paged_params* p, Paged* g, Extent ext[2]) {
   paged_magic(p->page_size, &g->page_mul, &g->page_shift);
   paged_magic(g->group, &g->group_mul, &g->group_shift);
   g->kp = to_view(p->k_pages); g->vp = to_view(p->v_pages);
+  if (four) {                     // a page of one slot may come with any stride
+    g->kp.ss = q4_row_bytes(p->H, esize(dt));
+    g->vp.ss = q4_row_bytes(p->Hv, esize(dt));
+  }
   g->table = p->page_table; g->table_stride = p->page_table_stride;
   g->lens = p->kv_lens; g->cu = p->cu_new;
   g->uniform = p->cu_new || !p->B ? 0 : p->tokens / p->B;
@@ -599,9 +638,9 @@ Shaped head_shape(const sdpa_qk_norm_params* p, const sdpa_view& v, int N, const
   return Shaped{v, {p->B, N, p->S}, p->D, e};
 }
 
-int check_paged_attn(const sdpa_paged_params* p, PagedAttn* a, Extent ext[2]) {
+int check_paged_attn(const sdpa_paged_params* p, PagedAttn* a, Extent ext[2], bool four = false) {
   int rc;
-  if ((rc = check_paged(p, &a->g, ext))) return rc;
+  if ((rc = check_paged(p, &a->g, ext, four))) return rc;
   if (p->causal != SDPA_CAUSAL_NONE && p->causal != SDPA_CAUSAL_LOWER_RIGHT)
     return fail(SDPA_ERR_INVALID, "causal mode %d: the new tokens are the last ones of their sequence (none or lower right)",
                 p->causal);
@@ -620,6 +659,45 @@ int check_paged_attn(const sdpa_paged_params* p, PagedAttn* a, Extent ext[2]) {
   a->window = p->window > 0 && p->window < (int64_t)a->g.cap ? (int)p->window : 0;
   a->head_sink = p->head_sink;
   a->max_new = a->g.uniform ? a->g.uniform : (p->max_new ? std::min(p->max_new, p->tokens) : p->tokens);
+  return SDPA_OK;
+}
+
+// Both attention entry points over pages.
+int run_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace, size_t workspace_bytes,
+                   sdpa_stream_t stream, bool four) {
+  PagedAttn a;
+  Extent pool[2], eq, ey, side[3];
+  int rc;
+  if ((rc = check_paged_attn(p, &a, pool, four))) return rc;
+  const int dt = p->dtype;
+  if ((rc = check_view(q, "q", dt, 1, p->Nq, p->tokens, p->H, true, false, &eq))) return rc;
+  if ((rc = check_view(y, "y", dt, 1, p->Nq, p->tokens, p->Hv, true, false, &ey))) return rc;
+  if ((rc = check_aligned_view(q, "q", dt))) return rc;
+  if ((rc = check_aligned_view(y, "y", dt))) return rc;
+  const size_t need = four ? paged4_workspace(p->H, p->Hv, (sdpa_dtype)dt) : paged_workspace(p->H, p->Hv, (sdpa_dtype)dt);
+  if (!workspace || workspace_bytes < need)
+    return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+  if ((uintptr_t)workspace & 255u) return fail(SDPA_ERR_ALIGNMENT, "workspace not 256-byte aligned");
+  const Extent ws = flat(workspace, need, "workspace");
+  paged_side_inputs(p, side);
+  const Extent ins[] = {eq, pool[0], pool[1], side[0], side[1], side[2],
+                        flat(p->head_sink, (size_t)p->Nq * esize(dt), "head_sink")};
+  for (const Extent& in : ins) {
+    if (overlap(ey, in)) return fail(SDPA_ERR_ALIAS, "output y overlaps input %s", in.name);
+    if (overlap(ws, in)) return fail(SDPA_ERR_ALIAS, "workspace overlaps input %s", in.name);
+  }
+  if (overlap(ws, ey)) return fail(SDPA_ERR_ALIAS, "workspace overlaps output y");
+  g_error.clear();
+  if (p->tokens == 0 || p->B == 0) return SDPA_OK;
+  a.q = to_view(q);
+  a.y = to_view(y);
+  const char* name = "";
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  mark_used(four ? kUsedPaged4 << paged4_kernel(a, (sdpa_dtype)dt) : kUsedPaged << paged_kernel(a, (sdpa_dtype)dt));
+  const cudaError_t e = four ? launch_paged4_attn(a, (sdpa_dtype)dt, workspace, st, &name)
+                             : launch_paged_attn(a, (sdpa_dtype)dt, workspace, st, &name);
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+  g_kernel = name;
   return SDPA_OK;
 }
 
@@ -1069,37 +1147,153 @@ size_t sdpa_paged_workspace_size(const sdpa_paged_params* p) {
 
 int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace, size_t workspace_bytes,
                     sdpa_stream_t stream) {
+  return run_paged_attn(p, q, y, workspace, workspace_bytes, stream, false);
+}
+
+size_t sdpa_paged4_workspace_size(const sdpa_paged_params* p) {
   PagedAttn a;
-  Extent pool[2], eq, ey, side[3];
-  int rc;
-  if ((rc = check_paged_attn(p, &a, pool))) return rc;
+  Extent pool[2];
+  if (check_paged_attn(p, &a, pool, true) != SDPA_OK) return 0;
+  return paged4_workspace(p->H, p->Hv, (sdpa_dtype)p->dtype);
+}
+
+int sdpa_paged4_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace, size_t workspace_bytes,
+                     sdpa_stream_t stream) {
+  return run_paged_attn(p, q, y, workspace, workspace_bytes, stream, true);
+}
+
+int64_t sdpa_paged4_row_bytes(int32_t D, sdpa_dtype dtype) {
+  if ((dtype != SDPA_F32 && dtype != SDPA_F16 && dtype != SDPA_BF16) || D < 1 || D > 256 || D % kQ4Group) return -1;
+  return q4_row_bytes(D, esize(dtype));
+}
+
+int sdpa_paged4_append(const sdpa_paged4_append_params* p, sdpa_view k, sdpa_view v, sdpa_view k_held, sdpa_view v_held,
+                       sdpa_stream_t stream) {
+  if (!p) return fail(SDPA_ERR_NULL, "params is NULL");
+  if (p->struct_size != (int32_t)sizeof(sdpa_paged4_append_params))
+    return fail(SDPA_ERR_INVALID, "struct_size %d != sizeof(sdpa_paged4_append_params) %d", p->struct_size,
+                (int)sizeof(sdpa_paged4_append_params));
   const int dt = p->dtype;
-  if ((rc = check_view(q, "q", dt, 1, p->Nq, p->tokens, p->H, true, false, &eq))) return rc;
-  if ((rc = check_view(y, "y", dt, 1, p->Nq, p->tokens, p->Hv, true, false, &ey))) return rc;
-  if ((rc = check_aligned_view(q, "q", dt))) return rc;
-  if ((rc = check_aligned_view(y, "y", dt))) return rc;
-  const size_t need = paged_workspace(p->H, p->Hv, (sdpa_dtype)dt);
-  if (!workspace || workspace_bytes < need)
-    return fail(SDPA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
-  if ((uintptr_t)workspace & 255u) return fail(SDPA_ERR_ALIGNMENT, "workspace not 256-byte aligned");
-  const Extent ws = flat(workspace, need, "workspace");
-  paged_side_inputs(p, side);
-  const Extent ins[] = {eq, pool[0], pool[1], side[0], side[1], side[2],
-                        flat(p->head_sink, (size_t)p->Nq * esize(dt), "head_sink")};
-  for (const Extent& in : ins) {
-    if (overlap(ey, in)) return fail(SDPA_ERR_ALIAS, "output y overlaps input %s", in.name);
-    if (overlap(ws, in)) return fail(SDPA_ERR_ALIAS, "workspace overlaps input %s", in.name);
+  if (dt != SDPA_F32 && dt != SDPA_F16 && dt != SDPA_BF16) return fail(SDPA_ERR_INVALID, "dtype %d", dt);
+  if (p->tokens < 0 || p->num_pages < 0) return fail(SDPA_ERR_SHAPE, "negative size (tokens=%d num_pages=%d)", p->tokens, p->num_pages);
+  if (p->Nkv < 1 || p->page_size < 1) return fail(SDPA_ERR_SHAPE, "Nkv and page_size must be >= 1");
+  if (p->Nkv > 65536 || (int64_t)p->tokens * p->Nkv > ((int64_t)1 << 30))
+    return fail(SDPA_ERR_OVERFLOW, "Nkv exceeds 2^16 or tokens * Nkv 2^30");
+  int rc;
+  if ((rc = check_heads4(p->H, p->Hv))) return rc;
+  Extent pool[2], ek, ev, held[2];
+  if ((rc = check_pool4(p->k_pages, "k_pages", p->num_pages, p->Nkv, p->page_size, p->H, dt, &pool[0]))) return rc;
+  if ((rc = check_pool4(p->v_pages, "v_pages", p->num_pages, p->Nkv, p->page_size, p->Hv, dt, &pool[1]))) return rc;
+  Paged4Append a{};
+  if ((rc = check_rotation(dt, p->H, p->rotary_cos, p->rotary_sin, p->rotary_max_pos, p->rotary_dim, p->rotary_interleaved, &a.R)))
+    return rc;
+  if (p->tokens > 0 && !p->slots) return fail(SDPA_ERR_NULL, "slots is NULL");
+  if (p->tokens > 0 && a.R && !p->positions) return fail(SDPA_ERR_NULL, "the rotation needs positions");
+  if (((uintptr_t)p->slots | (uintptr_t)p->positions) & 7u)
+    return fail(SDPA_ERR_ALIGNMENT, "slots and positions must be 8-byte aligned");
+  const struct { const sdpa_view* v; const char* name; int D; bool required; Extent* e; } rows[] = {
+      {&k, "k", p->H, true, &ek}, {&v, "v", p->Hv, true, &ev}, {&k_held, "k_held", p->H, false, &held[0]},
+      {&v_held, "v_held", p->Hv, false, &held[1]}};
+  for (const auto& r : rows) {
+    if ((rc = check_view(*r.v, r.name, dt, 1, p->Nkv, p->tokens, r.D, r.required, false, r.e))) return rc;
+    if ((rc = check_aligned_view(*r.v, r.name, dt))) return rc;
   }
-  if (overlap(ws, ey)) return fail(SDPA_ERR_ALIAS, "workspace overlaps output y");
+  const size_t cache = a.R ? (size_t)p->rotary_max_pos * (a.R / 2) * esize(dt) : 0;
+  const Extent ins[] = {ek, ev, flat(p->slots, (size_t)p->tokens * 8, "slots"),
+                        flat(a.R ? p->positions : nullptr, (size_t)p->tokens * 8, "positions"), flat(p->rotary_cos, cache, "rotary_cos"),
+                        flat(p->rotary_sin, cache, "rotary_sin")};
+  const Extent outs[] = {pool[0], pool[1], held[0], held[1]};
+  for (const Extent& o : outs)
+    for (const Extent& in : ins)
+      if (overlap(o, in)) return fail(SDPA_ERR_ALIAS, "output %s overlaps input %s", o.name, in.name);
+  const int64_t rk = q4_row_bytes(p->H, esize(dt)), rv = q4_row_bytes(p->Hv, esize(dt));
+  auto pool4 = [&](sdpa_view w, int64_t rb, const Extent& e) {
+    w.stride_s = rb;
+    return Shaped{w, {p->num_pages, p->Nkv, p->page_size}, rb, e};
+  };
+  if (!disjoint(pool4(p->k_pages, rk, pool[0]), pool4(p->v_pages, rv, pool[1]), 1))
+    return fail(SDPA_ERR_ALIAS, "k_pages and v_pages overlap");
+  for (int h = 0; h < 2; ++h)
+    for (int q = 0; q < 2; ++q)
+      if (overlap(held[h], pool[q])) return fail(SDPA_ERR_ALIAS, "output %s overlaps output %s", held[h].name, pool[q].name);
+  if (!disjoint(Shaped{k_held, {1, p->Nkv, p->tokens}, p->H, held[0]}, Shaped{v_held, {1, p->Nkv, p->tokens}, p->Hv, held[1]}, esize(dt)))
+    return fail(SDPA_ERR_ALIAS, "k_held and v_held overlap");
   g_error.clear();
-  if (p->tokens == 0 || p->B == 0) return SDPA_OK;
-  a.q = to_view(q);
-  a.y = to_view(y);
-  const char* name = "";
-  mark_used(kUsedPaged << paged_kernel(a, (sdpa_dtype)dt));
-  const cudaError_t e = launch_paged_attn(a, (sdpa_dtype)dt, workspace, reinterpret_cast<cudaStream_t>(stream), &name);
-  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
-  g_kernel = name;
+  if (p->tokens == 0) return SDPA_OK;
+  a.tokens = p->tokens; a.Nkv = p->Nkv; a.H = p->H; a.Hv = p->Hv;
+  a.num_pages = p->num_pages; a.page_size = p->page_size;
+  a.k = to_view(k); a.v = to_view(v); a.k_held = to_view(k_held); a.v_held = to_view(v_held);
+  a.kp = to_view(p->k_pages); a.vp = to_view(p->v_pages);
+  a.kp.ss = rk; a.vp.ss = rv;
+  a.slots = p->slots; a.positions = p->positions;
+  a.cos_c = p->rotary_cos; a.sin_c = p->rotary_sin; a.max_pos = p->rotary_max_pos;
+  a.interleaved = a.R ? p->rotary_interleaved : 0;
+  a.vec_rot = a.R % 16 == 0 && (((uintptr_t)p->rotary_cos | (uintptr_t)p->rotary_sin) & 15u) == 0;
+  mark_used(kUsedAppend4);
+  const cudaError_t e = launch_paged4_append((sdpa_dtype)dt, a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged4_append launch");
+  g_kernel = "paged4_append";
+  return SDPA_OK;
+}
+
+int sdpa_paged_tables(const sdpa_paged_tables_params* p, sdpa_stream_t stream) {
+  if (!p) return fail(SDPA_ERR_NULL, "params is NULL");
+  if (p->struct_size != (int32_t)sizeof(sdpa_paged_tables_params))
+    return fail(SDPA_ERR_INVALID, "struct_size %d != sizeof(sdpa_paged_tables_params) %d", p->struct_size,
+                (int)sizeof(sdpa_paged_tables_params));
+  if (p->B < 0 || p->tokens < 0 || p->num_pages < 0 || p->max_pages < 0)
+    return fail(SDPA_ERR_SHAPE, "negative size (B=%d tokens=%d num_pages=%d max_pages=%d)", p->B, p->tokens, p->num_pages,
+                p->max_pages);
+  if (p->page_size < 1) return fail(SDPA_ERR_SHAPE, "page_size must be >= 1");
+  if (p->B > kTablesMaxB) return fail(SDPA_ERR_UNSUPPORTED, "B exceeds %d", kTablesMaxB);
+  if (p->tokens > (1 << 30) || p->page_size > (1 << 30) || (int64_t)p->max_pages * p->page_size > ((int64_t)1 << 30))
+    return fail(SDPA_ERR_OVERFLOW, "tokens, page_size or max_pages * page_size exceeds 2^30");
+  if (!p->cu_new || !p->free_count || !p->free_count_out) return fail(SDPA_ERR_NULL, "cu_new, free_count or free_count_out is NULL");
+  if (p->B > 0 && (!p->past_lens || !p->new_lens || !p->kv_lens)) return fail(SDPA_ERR_NULL, "past_lens, new_lens or kv_lens is NULL");
+  if (p->B > 0 && p->max_pages > 0 && !p->page_table) return fail(SDPA_ERR_NULL, "page_table is NULL");
+  if (p->num_pages > 0 && !p->free_pages) return fail(SDPA_ERR_NULL, "free_pages is NULL");
+  if (p->tokens > 0 && (!p->positions || !p->slots)) return fail(SDPA_ERR_NULL, "positions or slots is NULL");
+  if (((uintptr_t)p->page_table | (uintptr_t)p->past_lens | (uintptr_t)p->new_lens | (uintptr_t)p->free_pages |
+       (uintptr_t)p->free_count | (uintptr_t)p->kv_lens | (uintptr_t)p->cu_new | (uintptr_t)p->free_count_out) & 3u)
+    return fail(SDPA_ERR_ALIGNMENT, "32-bit arrays must be 4-byte aligned");
+  if (((uintptr_t)p->positions | (uintptr_t)p->slots) & 7u)
+    return fail(SDPA_ERR_ALIGNMENT, "positions and slots must be 8-byte aligned");
+  if (p->B > 1 && p->page_table_stride < p->max_pages)
+    return fail(SDPA_ERR_INVALID, "page_table_stride %lld is smaller than max_pages %d", (long long)p->page_table_stride,
+                p->max_pages);
+  if (p->page_table_stride < 0 || p->page_table_stride > ((int64_t)1 << 40))
+    return fail(SDPA_ERR_OVERFLOW, "page_table_stride %lld out of range", (long long)p->page_table_stride);
+  const size_t rows = (size_t)p->B * 4, toks = (size_t)p->tokens * 8;
+  const Extent table = p->B && p->max_pages
+                           ? flat(p->page_table, ((size_t)(p->B - 1) * (size_t)p->page_table_stride + p->max_pages) * 4, "page_table")
+                           : Extent{};
+  const Extent outs[] = {table, flat(p->free_pages, (size_t)p->num_pages * 4, "free_pages"), flat(p->kv_lens, rows, "kv_lens"),
+                         flat(p->cu_new, rows + 4, "cu_new"), flat(p->positions, toks, "positions"), flat(p->slots, toks, "slots"),
+                         flat(p->free_count_out, 4, "free_count_out")};
+  const Extent ins[] = {flat(p->past_lens, rows, "past_lens"), flat(p->new_lens, rows, "new_lens"), flat(p->free_count, 4, "free_count")};
+  for (const Extent& o : outs)
+    for (const Extent& in : ins) {
+      const bool in_place = (p->kv_lens == p->past_lens && o.lo == (uintptr_t)p->kv_lens && in.lo == (uintptr_t)p->past_lens) ||
+                            (p->free_count_out == p->free_count && o.lo == (uintptr_t)p->free_count_out && in.lo == (uintptr_t)p->free_count);
+      if (!in_place && overlap(o, in)) return fail(SDPA_ERR_ALIAS, "output %s overlaps input %s", o.name, in.name);
+    }
+  for (size_t i = 0; i < sizeof outs / sizeof outs[0]; ++i)
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return fail(SDPA_ERR_ALIAS, "outputs %s and %s overlap", outs[j].name, outs[i].name);
+  g_error.clear();
+  PagedTables a{};
+  a.B = p->B; a.tokens = p->tokens; a.page_size = p->page_size; a.max_pages = p->max_pages; a.num_pages = p->num_pages;
+  a.cap = p->max_pages * p->page_size;
+  paged_magic(p->page_size, &a.page_mul, &a.page_shift);
+  a.table = p->page_table; a.table_stride = p->page_table_stride;
+  a.past = p->past_lens; a.fresh = p->new_lens;
+  a.free_pages = p->free_pages; a.free_count = p->free_count;
+  a.kv_lens = p->kv_lens; a.cu = p->cu_new; a.positions = p->positions; a.slots = p->slots;
+  a.free_count_out = p->free_count_out;
+  mark_used(kUsedTables);
+  const cudaError_t e = launch_paged_tables(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "paged_tables launch");
+  g_kernel = "paged_tables";
   return SDPA_OK;
 }
 
@@ -1115,6 +1309,12 @@ int sdpa_query_status(sdpa_stream_t stream) {
   if (e == cudaSuccess && (used & kUsedNorm)) e = take_norm_status(&norm_status);
   if (e == cudaSuccess && (used & kUsedAppend)) e = take_paged_append_status(&app_status);
   if (e == cudaSuccess && (used & kUsedSimt)) e = take_paged_simt_status(&paged_status);
+  int tables_status = 0, app4_status = 0, simt4_status = 0;
+  if (e == cudaSuccess && (used & kUsedTables)) e = take_paged_tables_status(&tables_status);
+  if (e == cudaSuccess && (used & kUsedAppend4)) e = take_paged4_append_status(&app4_status);
+  if (e == cudaSuccess && (used & (kUsedPaged4 << kPagedSimt))) e = take_paged4_simt_status(&simt4_status);
+  app_status |= app4_status | tables_status;
+  paged_status |= simt4_status;
   int paged_timeout = 0;
   auto take_paged = [&](unsigned kernel, cudaError_t (*take)(int*, int*)) {
     int v = 0, late = 0;
@@ -1138,7 +1338,11 @@ int sdpa_query_status(sdpa_stream_t stream) {
   for (auto take : {take_bounds_prefill, take_bounds_decode, take_bounds_concat, take_bounds_simt}) take_site(true, take);
   take_site(used & kUsedNorm, take_bounds_norm);
   take_site(used & kUsedAppend, take_bounds_append);
-  take_site(used & (kUsedSimt | kUsedMma | kUsedTc), take_bounds_paged_simt);      // it holds the joining kernel of all three
+  // it holds the joining kernel of all attention kernels
+  take_site(used & (kUsedSimt | kUsedMma | kUsedTc | kUsedAttn4), take_bounds_paged_simt);
+  take_site(used & kUsedTables, take_bounds_paged_tables);
+  take_site(used & kUsedAppend4, take_bounds_paged4_append);
+  take_site(used & (kUsedPaged4 << kPagedSimt), take_bounds_paged4_simt);
   take_site(used & kUsedMma, take_bounds_paged_mma);
   take_site(used & kUsedTc, take_bounds_paged_tc);
   if (e != cudaSuccess) return cuda_fail(e, "bounds status read");
@@ -1149,6 +1353,8 @@ int sdpa_query_status(sdpa_stream_t stream) {
   if ((app_status | paged_status) & kPagedBadPage) return fail(SDPA_ERR_INVALID, "a page id fell outside [0, num_pages)");
   if ((app_status | paged_status) & kPagedBadLength)
     return fail(SDPA_ERR_INVALID, "kv_lens or cu_new contradict the batch or the page table's width");
+  if (app_status & kPagedNoPages) return fail(SDPA_ERR_INVALID, "the list of free pages ran out");
+  if (app_status & kPagedBadSlot) return fail(SDPA_ERR_INVALID, "a slot fell behind the pool");
   return SDPA_OK;
 }
 

@@ -266,8 +266,17 @@ PyObject* qk_norm_rotary_bwd(Args& a) {
 
 // ------------------------------------------------------------------ paged cache
 
-// k_pages, v_pages, page_table, kv_lens, cu_new, then by the caller: tokens and Nq
-void read_pages(Args& a, const Place& pl, sdpa_paged_params& p, const Tensor*& kp, const Tensor*& vp) {
+// Channels of a record of `bytes` bytes: 32 of them are 16 bytes of codes and two values of their side.
+int64_t record_channels(int64_t bytes, sdpa_dtype dt, const char* name) {
+  const int64_t part = dt == SDPA_F32 ? 24 : 20;
+  if (bytes < part || bytes % part) bad(name, ": ", bytes, " bytes are no record of whole groups of ", part, " bytes");
+  return bytes / part * 32;
+}
+
+// k_pages, v_pages, page_table, kv_lens, cu_new, then by the caller: tokens and Nq.  records: the type of
+// the rows beside pools of records (bytes), or nullptr for pools in that type.
+void read_pages(Args& a, const Place& pl, sdpa_paged_params& p, const Tensor*& kp, const Tensor*& vp,
+                const Tensor* records = nullptr) {
   std::memset(&p, 0, sizeof p);
   p.struct_size = sizeof p;
   kp = &a.needed("k_pages");
@@ -275,8 +284,8 @@ void read_pages(Args& a, const Place& pl, sdpa_paged_params& p, const Tensor*& k
   const Tensor &table = a.needed("page_table"), &lens = a.needed("kv_lens");
   const Tensor* cu = a.tensor("cu_new");
   if (kp->dim() != 4 || vp->dim() != 4) bad("k_pages and v_pages are (pages, heads, slots, dim) views");
-  const auto type = kp->scalar_type();
-  p.dtype = element_type(*kp);
+  const auto type = records ? at::kByte : kp->scalar_type();
+  p.dtype = element_type(records ? *records : *kp);
   typed(pl, kp, "k_pages", type, kp->sizes());
   typed(pl, vp, "v_pages", type, {kp->size(0), kp->size(1), kp->size(2), vp->size(3)});
   if (table.dim() != 2) bad("page_table must be (B, max_pages)");
@@ -287,7 +296,9 @@ void read_pages(Args& a, const Place& pl, sdpa_paged_params& p, const Tensor*& k
   typed(pl, cu, "cu_new", at::kInt, {B + 1});
   p.B = small(B, "B");
   p.num_pages = small(kp->size(0), "num_pages"); p.Nkv = small(kp->size(1), "Nkv");
-  p.page_size = small(kp->size(2), "page_size"); p.H = small(kp->size(3), "H"); p.Hv = small(vp->size(3), "Hv");
+  p.page_size = small(kp->size(2), "page_size");
+  p.H = small(records ? record_channels(kp->size(3), p.dtype, "k_pages") : kp->size(3), "H");
+  p.Hv = small(records ? record_channels(vp->size(3), p.dtype, "v_pages") : vp->size(3), "Hv");
   p.max_pages = small(table.size(1), "max_pages");
   p.k_pages = pool_view(*kp, "k_pages");
   p.v_pages = pool_view(*vp, "v_pages");
@@ -371,6 +382,7 @@ PyObject* paged_append(Args& a) {
 }
 
 // entry point, size query, stream, q, read_pages' and read_rules' arguments, y, workspace -> y or a status
+template <bool kRecords>
 PyObject* paged_attn(Args& a) {
   const auto fn = reinterpret_cast<AttnFn>(a.address("entry"));
   const auto size = reinterpret_cast<PagedSize>(a.address("size"));
@@ -381,8 +393,8 @@ PyObject* paged_attn(Args& a) {
   if (q.dim() != 3) bad("q must be packed rows (tokens, heads, dim)");
   sdpa_paged_params p;
   const Tensor *kp, *vp;
-  read_pages(a, pl, p, kp, vp);
-  const auto type = kp->scalar_type();
+  read_pages(a, pl, p, kp, vp, kRecords ? &q : nullptr);
+  const auto type = kRecords ? q.scalar_type() : kp->scalar_type();
   typed(pl, &q, "q", type, {q.size(0), q.size(1), p.H});
   p.tokens = small(q.size(0), "tokens");
   p.Nq = small(q.size(1), "Nq");
@@ -396,6 +408,112 @@ PyObject* paged_attn(Args& a) {
   typed(pl, &ws, "workspace", ws.scalar_type(), ws.sizes());
   const int rc = fn(&p, packed(q, "q"), packed(y, "y"), flat(&ws, "workspace"), ws.nbytes(), st);
   return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(y);
+}
+
+// entry point, stream, k, v, k_pages, v_pages, slots, positions, cos_cache, sin_cache, rotary_dim, interleaved, k_held,
+// v_held -> None or a status
+PyObject* paged4_append(Args& a) {
+  using Fn = int (*)(const sdpa_paged4_append_params*, sdpa_view, sdpa_view, sdpa_view, sdpa_view, sdpa_stream_t);
+  const auto fn = reinterpret_cast<Fn>(a.address("entry"));
+  const auto st = static_cast<sdpa_stream_t>(a.address("stream"));
+  const Tensor &k = a.needed("k"), &v = a.needed("v"), &kp = a.needed("k_pages"), &vp = a.needed("v_pages");
+  const Tensor &slots = a.needed("slots"), *pos = a.tensor("positions");
+  const Tensor *cos = a.tensor("cos_cache"), *sin = a.tensor("sin_cache");
+  sdpa_paged4_append_params p;
+  std::memset(&p, 0, sizeof p);
+  p.struct_size = sizeof p;
+  p.rotary_dim = a.i32("rotary_dim");
+  p.rotary_interleaved = a.i32("interleaved");
+  const Tensor *kh = a.tensor("k_held"), *vh = a.tensor("v_held");
+  Place pl;
+  pl.start(k, "k");
+  const auto type = k.scalar_type();
+  p.dtype = element_type(k);
+  if (k.dim() != 3 || v.dim() != 3) bad("k and v must be packed rows (tokens, heads, dim)");
+  const int64_t tokens = k.size(0), heads = k.size(1), H = k.size(2), Hv = v.size(2);
+  typed(pl, &v, "v", type, {tokens, heads, Hv});
+  if (kp.dim() != 4 || vp.dim() != 4) bad("k_pages and v_pages are (pages, heads, slots, record) views");
+  typed(pl, &kp, "k_pages", at::kByte, {kp.size(0), heads, kp.size(2), kp.size(3)});
+  typed(pl, &vp, "v_pages", at::kByte, {kp.size(0), heads, kp.size(2), vp.size(3)});
+  if (record_channels(kp.size(3), p.dtype, "k_pages") != H) bad("k_pages: records of ", kp.size(3), " bytes do not hold ", H, " channels");
+  if (record_channels(vp.size(3), p.dtype, "v_pages") != Hv) bad("v_pages: records of ", vp.size(3), " bytes do not hold ", Hv, " channels");
+  typed(pl, &slots, "slots", at::kLong, {tokens});
+  typed(pl, pos, "positions", at::kLong, {tokens});
+  p.tokens = small(tokens, "tokens"); p.Nkv = small(heads, "Nkv"); p.H = small(H, "H"); p.Hv = small(Hv, "Hv");
+  p.num_pages = small(kp.size(0), "num_pages"); p.page_size = small(kp.size(2), "page_size");
+  p.k_pages = pool_view(kp, "k_pages");
+  p.v_pages = pool_view(vp, "v_pages");
+  p.slots = static_cast<const int64_t*>(flat(&slots, "slots"));
+  p.positions = static_cast<const int64_t*>(flat(pos, "positions"));
+  if (!cos != !sin) bad("cos_cache and sin_cache must be given together");
+  if (cos) {
+    const int64_t half = (p.rotary_dim ? p.rotary_dim : H) / 2;
+    typed(pl, cos, "cos_cache", type, {cos->dim() ? cos->size(0) : 0, half});
+    typed(pl, sin, "sin_cache", type, cos->sizes());
+    p.rotary_max_pos = cos->size(0);
+    p.rotary_cos = flat(cos, "cos_cache");
+    p.rotary_sin = flat(sin, "sin_cache");
+  }
+  typed(pl, kh, "k_held", type, {tokens, heads, H});
+  typed(pl, vh, "v_held", type, {tokens, heads, Hv});
+  const sdpa_view none{nullptr, 0, 0, 0};
+  const int rc = fn(&p, packed(k, "k"), packed(v, "v"), kh ? packed(*kh, "k_held") : none, vh ? packed(*vh, "v_held") : none, st);
+  if (rc) return PyLong_FromLong(rc);
+  Py_RETURN_NONE;
+}
+
+// entry point, stream, page_table, past_lens, new_lens, free_pages, free_count, page_size, tokens, kv_lens, cu_new, positions,
+// slots, free_count_out -> (kv_lens, cu_new, positions, slots, free_count_out) or a status
+PyObject* paged_tables(Args& a) {
+  using Fn = int (*)(const sdpa_paged_tables_params*, sdpa_stream_t);
+  const auto fn = reinterpret_cast<Fn>(a.address("entry"));
+  const auto st = static_cast<sdpa_stream_t>(a.address("stream"));
+  const Tensor &table = a.needed("page_table"), &past = a.needed("past_lens"), &fresh = a.needed("new_lens");
+  const Tensor &pages = a.needed("free_pages"), &count = a.needed("free_count");
+  sdpa_paged_tables_params p;
+  std::memset(&p, 0, sizeof p);
+  p.struct_size = sizeof p;
+  p.page_size = a.i32("page_size");
+  p.tokens = a.i32("tokens");
+  const Tensor *lens = a.tensor("kv_lens"), *cu = a.tensor("cu_new"), *pos = a.tensor("positions"), *slots = a.tensor("slots");
+  const Tensor* left = a.tensor("free_count_out");
+  Place pl;
+  pl.start(table, "page_table");
+  if (table.dim() != 2) bad("page_table must be (B, max_pages)");
+  if (table.stride(1) != 1 && table.size(1) > 1) bad("the rows of page_table must be contiguous");
+  if (p.tokens < 0) bad("tokens ", p.tokens, " is negative");
+  const int64_t B = table.size(0);
+  typed(pl, &table, "page_table", at::kInt, table.sizes());
+  typed(pl, &past, "past_lens", at::kInt, {B});
+  typed(pl, &fresh, "new_lens", at::kInt, {B});
+  if (pages.dim() != 1) bad("free_pages must be (num_pages,)");
+  typed(pl, &pages, "free_pages", at::kInt, pages.sizes());
+  typed(pl, &count, "free_count", at::kInt, {1});
+  typed(pl, lens, "kv_lens", at::kInt, {B});
+  typed(pl, cu, "cu_new", at::kInt, {B + 1});
+  typed(pl, pos, "positions", at::kLong, {p.tokens});
+  typed(pl, slots, "slots", at::kLong, {p.tokens});
+  typed(pl, left, "free_count_out", at::kInt, {1});
+  const auto ints = past.options().requires_grad(false), longs = ints.dtype(at::kLong);
+  Tensor o_lens = lens ? *lens : at::empty({B}, ints), o_cu = cu ? *cu : at::empty({B + 1}, ints);
+  Tensor o_pos = pos ? *pos : at::empty({p.tokens}, longs), o_slots = slots ? *slots : at::empty({p.tokens}, longs);
+  Tensor o_left = left ? *left : at::empty({1}, ints);
+  p.B = small(B, "B");
+  p.max_pages = small(table.size(1), "max_pages");
+  p.num_pages = small(pages.size(0), "num_pages");
+  p.page_table = table.data_ptr<int32_t>();
+  p.page_table_stride = table.stride(0);
+  p.past_lens = static_cast<const int32_t*>(flat(&past, "past_lens"));
+  p.new_lens = static_cast<const int32_t*>(flat(&fresh, "new_lens"));
+  p.free_pages = static_cast<int32_t*>(flat(&pages, "free_pages"));
+  p.free_count = static_cast<const int32_t*>(flat(&count, "free_count"));
+  p.kv_lens = static_cast<int32_t*>(flat(&o_lens, "kv_lens"));
+  p.cu_new = static_cast<int32_t*>(flat(&o_cu, "cu_new"));
+  p.positions = static_cast<int64_t*>(flat(&o_pos, "positions"));
+  p.slots = static_cast<int64_t*>(flat(&o_slots, "slots"));
+  p.free_count_out = static_cast<int32_t*>(flat(&o_left, "free_count_out"));
+  const int rc = fn(&p, st);
+  return rc ? PyLong_FromLong(rc) : pack({o_lens, o_cu, o_pos, o_slots, o_left});
 }
 
 // Runs one of the above; a C++ exception becomes a Python one.
@@ -422,7 +540,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<qk_norm_rotary>("qk_norm_rotary"), method<qk_norm_rotary_bwd>("qk_norm_rotary_bwd"),
                          method<paged_params>("paged_params"), method<paged_append>("paged_append"),
-                         method<paged_attn>("paged_attn"), PyMethodDef{nullptr, nullptr, 0, nullptr}};
+                         method<paged_attn<false>>("paged_attn"), method<paged_attn<true>>("paged4_attn"),
+                         method<paged4_append>("paged4_append"), method<paged_tables>("paged_tables"), PyMethodDef{nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

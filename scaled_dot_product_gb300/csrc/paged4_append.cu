@@ -1,0 +1,215 @@
+// Appends new keys and values to a paged cache of 4 bits a value, the keys turned by the angle of
+// their position on the way (the pairs of class RotaryEmbedding) and rounded to their type.
+//
+// Per 32 channels: m = min, s = (max - min) / 15 rounded to the type, code = round((x - m) / s) to the
+// nearest, ties to even, at most 15; s and m are what the cache holds, so a code makes up for their
+// rounding.  All in fp32 with one rounding an operation (no contracted products), which makes the
+// record a function of the input alone.  A group with a value that is not finite, or whose spread
+// is not, takes a scale and a minimum that are no numbers: it reads as NaN.
+//
+// Every element is read once and written once at 5/8 byte (and once more, as the cache holds it,
+// where the caller wants that).  A thread has 8 channels, four lanes a group: its minimum and
+// maximum take two exchanges.  The slot and the position of a token are one load each.
+#include <algorithm>
+#include <type_traits>
+
+#include "paged4.h"
+
+namespace sdpa {
+
+static __device__ int g_append4_status[1];
+
+namespace {
+
+constexpr int kThreads = 128;
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* f) {
+  unpack16<T>(*reinterpret_cast<const uint4*>(p), f);
+  if constexpr (sizeof(T) == 4) unpack16<T>(*reinterpret_cast<const uint4*>(p + 4), f + 4);
+}
+
+// The next smaller value of the type below x > 0.
+template <typename T>
+__device__ __forceinline__ float step_down(float x) {
+  if constexpr (sizeof(T) == 4) return __int_as_float(__float_as_int(x) - 1);
+  else {
+    T v = Elem<T>::from_f32(x);
+    *reinterpret_cast<uint16_t*>(&v) -= 1;
+    return Elem<T>::to_f32(v);
+  }
+}
+template <typename T>
+__device__ __forceinline__ float largest() {
+  if constexpr (std::is_same<T, __half>::value) return 65504.f;
+  else if constexpr (sizeof(T) == 2) return __int_as_float(0x7f7f0000);
+  else return __int_as_float(0x7f7fffff);
+}
+
+template <typename T>
+__device__ __forceinline__ float rounded(float x) { return Elem<T>::to_f32(Elem<T>::from_f32(x)); }
+
+// Channels [c0, c0 + 8) of a key turned.  Whole vectors of pairs (vec_rot), or pair by pair.
+template <typename T, bool kInter>
+__device__ __forceinline__ void turn8(const Paged4Append& a, const T* row, int c0, int64_t crow, float* x) {
+  const int half = a.R / 2;
+  const T* cr = reinterpret_cast<const T*>(a.cos_c) + crow;
+  const T* sr = reinterpret_cast<const T*>(a.sin_c) + crow;
+  if constexpr (kInter) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const int i = (c0 + e) / 2;
+      if (c0 + e >= a.R) break;
+      const float c = Elem<T>::to_f32(cr[i]), s = Elem<T>::to_f32(sr[i]);
+      const float x1 = x[e], x2 = x[e + 1];
+      x[e] = rounded<T>(__fsub_rn(__fmul_rn(x1, c), __fmul_rn(x2, s)));
+      x[e + 1] = rounded<T>(__fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s)));
+    }
+  } else if (a.vec_rot) {
+    const bool low = c0 < half;
+    const int i0 = low ? c0 : c0 - half;
+    float o[8], c[8], s[8];
+    load8<T>(row + (low ? c0 + half : i0), o);
+    load8<T>(cr + i0, c);
+    load8<T>(sr + i0, s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float p = __fmul_rn(x[e], c[e]), q = __fmul_rn(o[e], s[e]);
+      x[e] = rounded<T>(low ? __fsub_rn(p, q) : __fadd_rn(p, q));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int ch = c0 + e;
+      if (ch >= a.R) break;
+      const bool low = ch < half;
+      const int i = low ? ch : ch - half;
+      const float p = __fmul_rn(x[e], Elem<T>::to_f32(cr[i]));
+      const float q = __fmul_rn(Elem<T>::to_f32(row[low ? ch + half : i]), Elem<T>::to_f32(sr[i]));
+      x[e] = rounded<T>(low ? __fsub_rn(p, q) : __fadd_rn(p, q));
+    }
+  }
+}
+
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4Append a, const int tpb) {
+  const int ku = a.Nkv * (a.H / 8), per_tok = ku + a.Nkv * (a.Hv / 8);
+  const int x0 = (int)blockIdx.y * kThreads + (int)threadIdx.x;
+  const int t = (int)blockIdx.x * tpb + x0 / per_tok;
+  // four lanes of a group have the same token, tensor and head
+  const bool live = x0 / per_tok < tpb && t < a.tokens;
+  int u = x0 % per_tok;
+  const bool isk = u < ku;
+  if (!isk) u -= ku;
+  const int D = isk ? a.H : a.Hv, head = u / (D / 8), c0 = (u - head * (D / 8)) * 8;
+  const int64_t slots = (int64_t)a.num_pages * a.page_size;
+  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  int64_t slot = -1;
+  const T* row = nullptr;
+  if (live) {
+    const View& src = isk ? a.k : a.v;
+    row = reinterpret_cast<const T*>(src.p) + src.off(0, head, t);
+    slot = a.slots[t];
+    if (SDPA_IN_BOUNDS(head < a.Nkv && c0 + 8 <= D, 571)) load8<T>(row + c0, x);
+    if (isk && c0 < a.R) {
+      int64_t pos = a.positions[t];
+      // the place of a token that goes nowhere is not looked at
+      if (slot >= 0 && (pos < 0 || pos >= a.max_pos)) atomicOr(g_append4_status, kPagedBadPosition);
+      pos = min(max(pos, (int64_t)0), a.max_pos - 1);
+      turn8<T, kInter>(a, row, c0, pos * (a.R / 2), x);
+    }
+  }
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) {
+    lo = min_nan(lo, x[e]);
+    hi = max_nan(hi, x[e]);
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  }
+  if (!live || slot < 0) return;
+  if (slot >= slots) {
+    atomicOr(g_append4_status, kPagedBadSlot);
+    return;
+  }
+  const float spread = hi - lo;
+  float s = rounded<T>(__fdiv_rn(spread, 15.f));
+  // a scale rounded up at the end of the type's range: code 15 would have no value
+  if (fmaf(15.f, s, lo) > largest<T>()) s = step_down<T>(s);
+  if (!(spread < INFINITY)) s = lo = __int_as_float(0x7fffffff);
+  float code[8];
+  uint32_t word = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float q = s > 0.f ? __fdiv_rn(x[e] - lo, s) : 0.f;
+    code[e] = fminf(rintf(q), 15.f);
+    word |= (uint32_t)code[e] << (4 * e);
+  }
+  const uint64_t page = slots <= 0xffffffffll ? (uint32_t)slot / (uint32_t)a.page_size : (uint64_t)slot / (uint32_t)a.page_size;
+  const int at = (int)(slot - (int64_t)page * a.page_size);
+  const View& dst = isk ? a.kp : a.vp;
+  unsigned char* rec = reinterpret_cast<unsigned char*>(const_cast<void*>(dst.p)) + dst.off((int64_t)page, head, at);
+  if (SDPA_IN_BOUNDS((int64_t)page < a.num_pages && at >= 0 && at < a.page_size, 572)) {
+    *reinterpret_cast<uint32_t*>(rec + c0 / 2) = word;
+    if (c0 % kQ4Group == 0) {
+      T* side = reinterpret_cast<T*>(rec + D / 2) + c0 / kQ4Group * 2;
+      if constexpr (sizeof(T) == 4) {
+        side[0] = lo;
+        side[1] = s;
+      } else {
+        T pair[2] = {Elem<T>::from_f32(lo), Elem<T>::from_f32(s)};
+        *reinterpret_cast<uint32_t*>(side) = *reinterpret_cast<const uint32_t*>(pair);
+      }
+    }
+  }
+  const View& held = isk ? a.k_held : a.v_held;
+  if (held.p) {
+    T out[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = Elem<T>::from_f32(__fadd_rn(__fmul_rn(code[e], s), lo));
+    T* h = reinterpret_cast<T*>(const_cast<void*>(held.p)) + held.off(0, head, t) + c0;
+    *reinterpret_cast<uint4*>(h) = *reinterpret_cast<const uint4*>(out);
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(h + 4) = *reinterpret_cast<const uint4*>(out + 4);
+  }
+}
+
+template <typename T>
+cudaError_t launch_t(const Paged4Append& a, cudaStream_t st) {
+  const int64_t per_tok = (int64_t)a.Nkv * ((a.H + a.Hv) / 8);
+  const int tpb = (int)std::max<int64_t>(1, std::min<int64_t>(64, kThreads / per_tok));
+  const dim3 grid((unsigned)((a.tokens + tpb - 1) / tpb), (unsigned)((per_tok * tpb + kThreads - 1) / kThreads));
+  if (a.R && a.interleaved) paged4_append_kernel<T, true><<<grid, kThreads, 0, st>>>(a, tpb);
+  else paged4_append_kernel<T, false><<<grid, kThreads, 0, st>>>(a, tpb);
+  count_launch(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged4_append(sdpa_dtype dt, const Paged4Append& a, cudaStream_t st) {
+  switch (dt) {
+    case SDPA_F32: return launch_t<float>(a, st);
+    case SDPA_F16: return launch_t<__half>(a, st);
+    default: return launch_t<__nv_bfloat16>(a, st);
+  }
+}
+
+cudaError_t take_paged4_append_status(int* status) { return take_words(g_append4_status, status); }
+
+SDPA_DEFINE_BOUNDS_TAKE(take_bounds_paged4_append)
+
+}  // namespace sdpa

@@ -1,0 +1,260 @@
+// The page tables of a step, made on the device from past and new lengths: pages of ended sequences
+// go back to the list of free pages, grown sequences take theirs from it, and every new token gets its
+// row offset, position and cache slot.
+//
+// One launch of one cluster.  Every CTA scans all sequences for itself (a running sum of the rows,
+// of the pages given back and of the pages taken, kept in shared memory), so nothing but the list of
+// free pages passes between CTAs; tokens and pages are then dealt to the threads of the whole
+// cluster, each finding its sequence by bisection in shared memory.  A thread per sequence would
+// leave a long prompt's tokens to one thread.  A page taken is the list's entry from the top down, in
+// the order of sequences, whatever the number of threads: results do not vary.  The cluster's barrier
+// orders the entries given back before those taken, and the inputs' reads before the outputs that may
+// be the inputs themselves.  Bound by latency (a chain of lengths, scans, barrier, list or table,
+// slot).
+#include <algorithm>
+
+#include "paged4.h"
+
+namespace sdpa {
+
+static __device__ int g_tables_status[1];
+
+namespace {
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int cluster_size() {
+  int r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+// Last i in [0, n) with at[i] <= x, for at[0] <= x, at not decreasing.
+__device__ __forceinline__ int last_not_above(const int* at, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(NT) paged_tables_kernel(const PagedTables a) {
+  constexpr int kW = NT / 32;
+  extern __shared__ int smem[];
+  int* cu = smem;                        // [B + 1]: rows before a sequence
+  int* taken = cu + a.B + 1;             // [B + 1]: pages taken before it
+  int* given = taken + a.B + 1;          // [B]: pages given back before it
+  int* past = given + a.B;               // [B]: keys before the step; -1 - keys where the sequence has ended
+  __shared__ long long sum_n[kW], sum_g[kW];
+  __shared__ int sum_t[kW];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = cluster_rank(), ctas = cluster_size();
+  int bad = 0;
+  auto div = [&](int j) { return (int)(((uint64_t)(uint32_t)j * a.page_mul) >> a.page_shift); };
+  auto pages_of = [&](int keys) { return div(keys + a.page_size - 1); };
+  const int count0 = a.free_count[0];
+  const int c0 = min(max(count0, 0), a.num_pages);
+  if (count0 > a.num_pages) bad |= kPagedBadLength;
+
+  // running sum over the block of x, before this thread's own; total: of all
+  auto scan = [&](long long x, long long* sums, long long& total) -> long long {
+    long long v = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    return before + v - x;
+  };
+
+  long long rows = 0, back = 0;
+  int pages = 0;
+  for (int base = 0; base < a.B; base += NT) {
+    const int b = base + tid;
+    const bool in = b < a.B;
+    const int p_in = in ? a.past[b] : 0, n_in = in ? a.fresh[b] : 0;
+    const int p = min(max(p_in, 0), a.cap);
+    const bool ended = n_in < 0;
+    const int have = pages_of(p);
+    const int n1 = ended ? 0 : min(n_in, a.cap - p);
+    if (p != p_in || (!ended && n1 != n_in)) bad |= kPagedBadLength;
+    // pages that this thread's sequence gives back: entries in range, counted by the warp
+    int g = 0;
+    unsigned who = __ballot_sync(0xffffffffu, ended && have > 0);
+    while (who) {
+      const int src = __ffs(who) - 1;
+      who &= who - 1;
+      const int32_t* row = a.table + (int64_t)(base + warp * 32 + src) * a.table_stride;
+      const int h = __shfl_sync(0xffffffffu, have, src);
+      int c = 0;
+      for (int j = lane; j < h; j += 32) c += (unsigned)row[j] < (unsigned)a.num_pages;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      if (lane == src) {
+        g = c;
+        if (c != h) bad |= kPagedBadPage;
+      }
+    }
+    long long all_n, all_g = 0;
+    const long long e = rows + scan(n1, sum_n, all_n);
+    long long eg = 0;
+    if (__syncthreads_or(ended)) eg = scan(g, sum_g, all_g);
+    const int n = (int)max(0ll, min((long long)n1, a.tokens - e));
+    if (n != n1) bad |= kPagedBadLength;
+    const int need = ended ? 0 : pages_of(p + n) - have;
+    // pages taken: no more than tokens
+    int v = need;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) sum_t[warp] = v;
+    __syncthreads();
+    int before = pages, all_t = 0;
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) before += sum_t[w];
+      all_t += sum_t[w];
+    }
+    if (in) {
+      cu[b] = (int)min(e, (long long)a.tokens);
+      taken[b] = before + v - need;
+      given[b] = (int)min(back + eg, 1ll << 30);
+      past[b] = ended ? -1 - p : p;
+    }
+    rows += all_n;
+    back += all_g;
+    pages += all_t;
+    __syncthreads();                     // the sums are used again
+  }
+  if (tid == 0) {
+    cu[a.B] = (int)min(rows, (long long)a.tokens);
+    taken[a.B] = pages;
+  }
+  __syncthreads();
+  const int64_t top = min((long long)c0 + back, (long long)a.num_pages);
+  if ((int64_t)c0 + back > a.num_pages) bad |= kPagedBadLength;
+
+  // ---- pages given back, in the order of sequences and entries: a warp a sequence
+  if (back > 0) {
+    for (int b = rank * kW + warp; b < a.B; b += ctas * kW) {
+      if (past[b] >= 0) continue;
+      const int h = pages_of(-1 - past[b]);
+      const int32_t* row = a.table + (int64_t)b * a.table_stride;
+      int64_t at = (int64_t)c0 + given[b];
+      for (int j0 = 0; j0 < h; j0 += 32) {
+        const int id = j0 + lane < h ? row[j0 + lane] : -1;
+        const bool ok = (unsigned)id < (unsigned)a.num_pages;
+        const unsigned m = __ballot_sync(0xffffffffu, ok);
+        const int64_t to = at + __popc(m & ((1u << lane) - 1));
+        if (ok && to < a.num_pages) a.free_pages[to] = id;
+        at += __popc(m);
+      }
+    }
+  }
+  cluster_sync();
+
+  // the i-th page taken
+  auto take = [&](int i) -> int {
+    const int64_t at = top - 1 - i;
+    if (at < 0) {
+      bad |= kPagedNoPages;
+      return -1;
+    }
+    const int id = SDPA_IN_BOUNDS(at < a.num_pages, 561) ? __ldcg(a.free_pages + at) : -1;
+    if ((unsigned)id >= (unsigned)a.num_pages) {
+      bad |= kPagedBadPage;
+      return -1;
+    }
+    return id;
+  };
+  const int step = ctas * NT, first = rank * NT + tid;
+  for (int i = first; i < pages; i += step) {
+    const int b = last_not_above(taken, a.B, i);
+    const int pg = pages_of(past[b]) + i - taken[b];
+    if (SDPA_IN_BOUNDS(b < a.B && past[b] >= 0 && pg < a.max_pages, 562)) a.table[(int64_t)b * a.table_stride + pg] = take(i);
+  }
+  const int live = cu[a.B];
+  for (int t = first; t < a.tokens; t += step) {
+    if (t >= live) {
+      a.positions[t] = 0;
+      a.slots[t] = -1;
+      continue;
+    }
+    const int b = last_not_above(cu, a.B, t);
+    const int pos = past[b] + t - cu[b], pg = div(pos), have = pages_of(past[b]);
+    int id = -1;
+    if (pg >= have) {
+      id = take(taken[b] + pg - have);
+    } else if (SDPA_IN_BOUNDS(b < a.B && pg >= 0 && pg < a.max_pages, 563)) {
+      id = a.table[(int64_t)b * a.table_stride + pg];
+      if ((unsigned)id >= (unsigned)a.num_pages) {
+        bad |= kPagedBadPage;
+        id = -1;
+      }
+    }
+    a.positions[t] = pos;
+    a.slots[t] = id < 0 ? -1 : (int64_t)id * a.page_size + (pos - pg * a.page_size);
+  }
+  for (int b = first; b <= a.B; b += step) {
+    a.cu[b] = cu[b];
+    if (b < a.B) a.kv_lens[b] = past[b] < 0 ? 0 : past[b] + cu[b + 1] - cu[b];
+  }
+  if (first == 0) a.free_count_out[0] = (int)(top - pages);
+  if (bad) atomicOr(g_tables_status, bad);
+}
+
+template <int NT>
+cudaError_t launch_nt(const PagedTables& a, int ctas, cudaStream_t st) {
+  const size_t smem = ((size_t)4 * a.B + 2) * sizeof(int);
+  auto* kernel = paged_tables_kernel<NT>;
+  // per device: set at every call that needs it (the attribute belongs to the current context)
+  if (smem > 48 * 1024 - 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)ctas;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  if (e == cudaSuccess) count_launch(1);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tables(const PagedTables& a, cudaStream_t st) {
+  if (a.B <= 256 && a.tokens <= 1024) return launch_nt<256>(a, 1, st);
+  return launch_nt<1024>(a, a.tokens <= 4096 ? 1 : 8, st);
+}
+
+cudaError_t take_paged_tables_status(int* status) { return take_words(g_tables_status, status); }
+
+SDPA_DEFINE_BOUNDS_TAKE(take_bounds_paged_tables)
+
+}  // namespace sdpa

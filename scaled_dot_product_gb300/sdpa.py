@@ -116,11 +116,37 @@ class sdpa_paged_params(ctypes.Structure):
     ]
 
 
+class sdpa_paged_tables_params(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_int32), ("B", ctypes.c_int32), ("tokens", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+        ("page_table", ctypes.c_void_p), ("page_table_stride", ctypes.c_int64),
+        ("past_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
+        ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p), ("cu_new", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p), ("free_count_out", ctypes.c_void_p),
+    ]
+
+
+class sdpa_paged4_append_params(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_int32), ("tokens", ctypes.c_int32),
+        ("Nkv", ctypes.c_int32), ("H", ctypes.c_int32), ("Hv", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("k_pages", sdpa_view), ("v_pages", sdpa_view),
+        ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("rotary_cos", ctypes.c_void_p), ("rotary_sin", ctypes.c_void_p),
+        ("rotary_max_pos", ctypes.c_int64), ("rotary_dim", ctypes.c_int32),
+        ("rotary_interleaved", ctypes.c_int32),
+    ]
+
+
 EXPORTED = ("sdpa_attn_fwd", "sdpa_attn_decode", "sdpa_workspace_size", "sdpa_validate",
             "sdpa_kv_concat", "sdpa_query_status", "sdpa_last_error", "sdpa_last_kernel_name",
             "sdpa_version", "sdpa_launch_count", "sdpa_attn_decode_static", "sdpa_rotary",
             "sdpa_attn_bwd", "sdpa_qk_norm_rotary", "sdpa_qk_norm_rotary_bwd", "sdpa_qk_norm_workspace_size",
-            "sdpa_paged_append", "sdpa_paged_attn", "sdpa_paged_workspace_size")
+            "sdpa_paged_append", "sdpa_paged_attn", "sdpa_paged_workspace_size", "sdpa_paged_tables",
+            "sdpa_paged4_append", "sdpa_paged4_attn", "sdpa_paged4_workspace_size", "sdpa_paged4_row_bytes")
 
 _lib = None
 
@@ -168,6 +194,16 @@ def lib() -> ctypes.CDLL:
         L.sdpa_paged_attn.restype = ctypes.c_int
         L.sdpa_paged_workspace_size.argtypes = [GP]
         L.sdpa_paged_workspace_size.restype = ctypes.c_size_t
+        L.sdpa_paged_tables.argtypes = [ctypes.POINTER(sdpa_paged_tables_params), ctypes.c_void_p]
+        L.sdpa_paged_tables.restype = ctypes.c_int
+        L.sdpa_paged4_append.argtypes = [ctypes.POINTER(sdpa_paged4_append_params)] + [sdpa_view] * 4 + [ctypes.c_void_p]
+        L.sdpa_paged4_append.restype = ctypes.c_int
+        L.sdpa_paged4_attn.argtypes = L.sdpa_paged_attn.argtypes
+        L.sdpa_paged4_attn.restype = ctypes.c_int
+        L.sdpa_paged4_workspace_size.argtypes = [GP]
+        L.sdpa_paged4_workspace_size.restype = ctypes.c_size_t
+        L.sdpa_paged4_row_bytes.argtypes = [ctypes.c_int32, ctypes.c_int]
+        L.sdpa_paged4_row_bytes.restype = ctypes.c_int64
         L.sdpa_query_status.argtypes = [ctypes.c_void_p]
         L.sdpa_query_status.restype = ctypes.c_int
         for f in ("sdpa_last_error", "sdpa_last_kernel_name", "sdpa_version"):
@@ -593,6 +629,66 @@ def sdpa_paged_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     fn, size, mode = entry["sdpa_paged_attn"], entry["sdpa_paged_workspace_size"], _causal(causal)
     call = lambda h: b.paged_attn(fn, size, h, q, k_pages, v_pages, page_table, kv_lens, cu_new, scale, softcap, mode, window,
                                   head_sink, max_new or 0, y, workspace)
+    return _raised(call(_handle(q)) if _here(q, stream) else _elsewhere(q, stream, call))
+
+
+def sdpa_paged_tables(page_table: torch.Tensor, past_lens: torch.Tensor, new_lens: torch.Tensor,
+                      free_pages: torch.Tensor, free_count: torch.Tensor, *, page_size: int, tokens: int,
+                      kv_lens: Optional[torch.Tensor] = None, cu_new: Optional[torch.Tensor] = None,
+                      positions: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                      free_count_out: Optional[torch.Tensor] = None, stream=None):
+    """The tables of a step's batch, made on the device: takes pages off the stack free_pages
+    (num_pages,) for the new tokens, gives those of ended sequences (new_lens[b] < 0) back, and returns (kv_lens,
+    cu_new, positions, slots, free_count_out).
+
+    page_table (B, max_pages), past_lens (B,), new_lens (B,), free_pages and free_count (1,) are int32;
+    page_table and free_pages are updated in place.  kv_lens (B,) and cu_new (B + 1,) int32 are what
+    sdpa_paged_append and the paged attention calls take; positions (tokens,) int64 is position_ids of a packed
+    row (sdpa_qk_norm_rotary) and slots (tokens,) int64 its place in the cache (sdpa_paged4_append), -1 behind the
+    last row.  kv_lens may be past_lens and free_count_out free_count.  A list that runs out leaves table
+    entries and slots of -1, a negative free_count_out and a status (sdpa_query_status)."""
+    b, entry = _native()
+    call = lambda h: b.paged_tables(entry["sdpa_paged_tables"], h, page_table, past_lens, new_lens, free_pages, free_count,
+                                    page_size, tokens, kv_lens, cu_new, positions, slots, free_count_out)
+    return _raised(call(_handle(page_table)) if _here(page_table, stream) else _elsewhere(page_table, stream, call))
+
+
+def sdpa_paged4_row_bytes(D: int, dtype: torch.dtype) -> int:
+    """Bytes of a head row of D channels in a cache of 4 bits a value: a pool is a uint8 tensor
+    (pages, Nkv, slots, sdpa_paged4_row_bytes(D, dtype))."""
+    n = int(lib().sdpa_paged4_row_bytes(D, _DTYPES[dtype]))
+    if n < 0:
+        raise ValueError(f"head sizes are multiples of 32 and at most 256, got {D}")
+    return n
+
+
+def sdpa_paged4_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                       slots: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                       cos_cache: Optional[torch.Tensor] = None, sin_cache: Optional[torch.Tensor] = None, *,
+                       rotary_dim: int = 0, interleaved: bool = False, k_held: Optional[torch.Tensor] = None,
+                       v_held: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Writes new keys k and values v (packed rows (tokens, Nkv, H / Hv)) in 4 bits a value into the pools of records
+    k_pages, v_pages (uint8 (pages, Nkv, slots, sdpa_paged4_row_bytes), the last two axes contiguous) at
+    slots (tokens,) int64 (page * page_size + slot; negative: not stored), the keys rotated at positions
+    (tokens,) int64 when caches (positions, R/2) are given.  k_held, v_held: filled with the rows as the cache holds
+    them.  Returns the pools."""
+    b, entry = _native()
+    call = lambda h: b.paged4_append(entry["sdpa_paged4_append"], h, k, v, k_pages, v_pages, slots, positions, cos_cache,
+                                     sin_cache, rotary_dim, interleaved, k_held, v_held)
+    _raised(call(_handle(k)) if _here(k, stream) else _elsewhere(k, stream, call))
+    return k_pages, v_pages
+
+
+def sdpa_paged4_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                     kv_lens: torch.Tensor, *, cu_new: Optional[torch.Tensor] = None, max_new: Optional[int] = None,
+                     scale: Optional[float] = None, softcap: float = 0.0, causal="lower_right", window: int = -1,
+                     head_sink: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, workspace=None,
+                     stream=None) -> torch.Tensor:
+    """sdpa_paged_attn over pools of records of 4 bits a value (sdpa_paged4_append), with the same arguments."""
+    b, entry = _native()
+    fn, size, mode = entry["sdpa_paged4_attn"], entry["sdpa_paged4_workspace_size"], _causal(causal)
+    call = lambda h: b.paged4_attn(fn, size, h, q, k_pages, v_pages, page_table, kv_lens, cu_new, scale, softcap, mode, window,
+                                   head_sink, max_new or 0, y, workspace)
     return _raised(call(_handle(q)) if _here(q, stream) else _elsewhere(q, stream, call))
 
 
