@@ -443,6 +443,7 @@ cudaError_t merge_t(const PagedAttn& a, const PagedWs& ws, int ctas, int tm, cud
   switch (tm) {
     case 1: return merge_tn<T, 1, kTN>(a, ws, ctas, st);
     case 4: return merge_tn<T, 4, kTN>(a, ws, ctas, st);
+    case 8: return merge_tn<T, 8, kTN>(a, ws, ctas, st);
     case 16: return merge_tn<T, 16, kTN>(a, ws, ctas, st);
     case 32: return merge_tn<T, 32, kTN>(a, ws, ctas, st);
     case 64: return merge_tn<T, 64, kTN>(a, ws, ctas, st);
