@@ -49,6 +49,7 @@ constexpr int kMinShare = 2;
 constexpr float kRescale = 8.f;       // log2 units a maximum may grow before the state is rescaled
 constexpr int kScaleRoom = 6;         // and a scale
 constexpr int kLeastL = -24, kMostL = 100;
+constexpr float kNone = -1e30f;       // the maximum of a row that has admitted no key: finite, so that differences are numbers
 
 template <int H, int NT, int WM>
 struct Cfg {
@@ -76,6 +77,12 @@ __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with accumulators that start at zero.
+__device__ __forceinline__ void mma_first(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // 8 x 8 matrix of 16-bit values, a row in four lanes, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -189,16 +196,24 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         last = min(k0 + kTN, w.r.hi + 1);
       }
     };
-    // page of part `part` of the t-th tile of w's unit
-    auto page_of = [&](int t, int part) -> int {
-      if (w.done() || t >= w.take()) return -1;
+    // The ids of 64 pages are at hand, two in a lane; the further 32 are on their way while the nearer
+    // ones are used.
+    int wbase = 0, near_id = -1, far_id = -1;
+    const int32_t* table = nullptr;
+    int end = -1;                     // last page that some row of the unit admits
+    auto fetch = [&](int page) { return page <= end ? table[page] : -1; };
+    auto start_unit = [&]() {
+      if (w.done()) return;
       int k0, first, last;
-      keys_of(t, k0, first, last);
-      if (first >= last) return -1;
-      const int pg = page_div(g, first) + part;
-      return pg <= page_div(g, last - 1) ? g.table[(int64_t)w.b * g.table_stride + pg] : -1;
+      table = g.table + (int64_t)w.b * g.table_stride;
+      keys_of(0, k0, first, last);
+      wbase = page_div(g, max(first, 0));
+      keys_of(w.take() - 1, k0, first, last);
+      end = first < last ? page_div(g, last - 1) : -1;
+      near_id = fetch(wbase + lane);
+      far_id = fetch(wbase + 32 + lane);
     };
-    int id = page_of(0, lane);
+    start_unit();
     while (!w.done() && wait_free()) {
       const int n = w.take();
       for (int t = 0; t < n && wait_free(); ++t) {
@@ -206,6 +221,15 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         keys_of(t, k0, first, last);
         const int p0 = page_div(g, max(first, 0)), parts = first < last ? page_div(g, last - 1) - p0 + 1 : 0;
         const uint32_t at = sb + st * 2 * C::kTile;
+        while (p0 >= wbase + 32) {
+          wbase += 32;
+          near_id = far_id;
+          far_id = fetch(wbase + 32 + lane);
+        }
+        // page of this lane's first part
+        const int x = p0 - wbase + lane;
+        const int from_near = __shfl_sync(0xffffffffu, near_id, x & 31), from_far = __shfl_sync(0xffffffffu, far_id, x & 31);
+        const int id = x < 32 ? from_near : from_far;
         // this lane's parts are announced before any of them is copied
         uint32_t bytes = 0;
         auto span = [&](int part, int& from, int& to) {
@@ -214,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         };
         int pid = id;
         for (int part = lane; part < parts; part += 32) {
-          if (part >= 32) pid = g.table[(int64_t)w.b * g.table_stride + p0 + part];
+          if (part >= 32) pid = table[p0 + part];
           int from, to;
           span(part, from, to);
           if ((unsigned)pid < (unsigned)g.num_pages) {
@@ -232,7 +256,7 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         mbar_arrive_expect_tx(b_full(st), bytes);
         pid = id;
         for (int part = lane; part < parts; part += 32) {
-          if (part >= 32) pid = g.table[(int64_t)w.b * g.table_stride + p0 + part];
+          if (part >= 32) pid = table[p0 + part];
           int from, to;
           span(part, from, to);
           if ((unsigned)pid < (unsigned)g.num_pages &&
@@ -247,11 +271,10 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         }
         __syncwarp();
         if (++st == C::kStages) { st = 0; ++it; }
-        if (t + 1 < n) id = page_of(t + 1, lane);      // arrives while the ring is waited for
       }
       if (!ok) break;
       w.next(a);
-      id = page_of(0, lane);
+      start_unit();
     }
     // Copies may still be on their way when a wait has expired, whichever role's it was and however
     // early the last copy was issued: the CTA, whose shared memory they write, ends behind them.
@@ -352,7 +375,7 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          m[n][x] = -INFINITY;
+          m[n][x] = kNone;
           l[n][x] = 0.f;
 #pragma unroll
           for (int y = 0; y < G; ++y) {
@@ -389,8 +412,8 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
           const float m0 = low_half<T>(sd[0][y]), m1 = low_half<T>(sd[1][y]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma(d, k0 & kLow, k1 & kLow, k0 & kHigh, k1 & kHigh, qf[n][y][0], qf[n][y][1]);
+            float d[4];
+            mma_first(d, k0 & kLow, k1 & kLow, k0 & kHigh, k1 & kHigh, qf[n][y][0], qf[n][y][1]);
             mma(d, (k0 >> 8) & kLow, (k1 >> 8) & kLow, (k0 >> 8) & kHigh, (k1 >> 8) & kHigh, qf[n][y][2], qf[n][y][3]);
             s[n][0] = fmaf(c0, d[0], fmaf(m0, qs[n][0][y], s[n][0]));
             s[n][1] = fmaf(c0, d[1], fmaf(m0, qs[n][1][y], s[n][1]));
@@ -460,10 +483,10 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
           for (int x = 0; x < 2; ++x) {
             const float mx = rows_max(fmaxf(s[n][x], s[n][2 + x]));
             const float was = m[n][x];
-            float top = was - old_L;                     // -inf stays
-            if (mx > top + kRescale || (top == -INFINITY && mx != -INFINITY)) top = mx;
+            float top = was - old_L;                     // kNone stays
+            if (mx > top + kRescale) top = mx;
             m[n][x] = top + new_L;
-            const float corr = m[n][x] == -INFINITY ? 1.f : ex2_approx(was - m[n][x]);
+            const float corr = ex2_approx(was - m[n][x]);
             l[n][x] *= corr;
 #pragma unroll
             for (int y = 0; y < G; ++y) {
@@ -480,13 +503,12 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         if constexpr (std::is_same<T, __nv_bfloat16>::value) s_most = __float_as_uint(most_s) >> 16;
         else s_most = L + kScaleRoom > 15 ? 0x7bffu : (uint32_t)__half_as_ushort(__float2half_rn(most_s));
       }
-      // ---- weights; rows with nothing admitted so far: exponent -inf, weight 0
+      // ---- weights
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float nm = m[n][e & 1] == -INFINITY ? -INFINITY : -m[n][e & 1];
-          s[n][e] = ex2_approx(s[n][e] + nm);
+          s[n][e] = ex2_approx(s[n][e] - m[n][e & 1]);
           l[n][e & 1] += s[n][e];
         }
       // ---- values
@@ -543,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         }
         const float sum = rows_sum(l[n][x]);
         if (r8 == 0) {
-          sm_m[wk][prow + n * 8 + 2 * j4 + x] = m[n][x];
+          sm_m[wk][prow + n * 8 + 2 * j4 + x] = m[n][x] <= 0.5f * kNone ? -INFINITY : m[n][x];
           sm_l[wk][prow + n * 8 + 2 * j4 + x] = sum;
         }
       }
