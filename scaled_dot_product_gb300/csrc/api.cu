@@ -1325,6 +1325,7 @@ int sdpa_query_status(sdpa_stream_t stream) {
   take_paged(kUsedMma, take_paged_mma_status);
   take_paged(kUsedTc, take_paged_tc_status);
   take_paged(kUsedPaged4 << kPagedMma, take_paged4_mma_status);
+  take_paged(kUsedPaged4 << kPagedTc, take_paged4_tc_status);
   if (e != cudaSuccess) return cuda_fail(e, "status read");
   if (!status) status = qk_status;
   if (!status) status = bwd_status;
@@ -1345,6 +1346,7 @@ int sdpa_query_status(sdpa_stream_t stream) {
   take_site(used & kUsedAppend4, take_bounds_paged4_append);
   take_site(used & (kUsedPaged4 << kPagedSimt), take_bounds_paged4_simt);
   take_site(used & (kUsedPaged4 << kPagedMma), take_bounds_paged4_mma);
+  take_site(used & (kUsedPaged4 << kPagedTc), take_bounds_paged4_tc);
   take_site(used & kUsedMma, take_bounds_paged_mma);
   take_site(used & kUsedTc, take_bounds_paged_tc);
   if (e != cudaSuccess) return cuda_fail(e, "bounds status read");

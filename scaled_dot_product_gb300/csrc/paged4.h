@@ -37,6 +37,11 @@ size_t paged4_workspace(int H, int Hv, sdpa_dtype dt);
 bool paged4_mma_supported(int H, int Hv, sdpa_dtype dt);
 size_t paged4_mma_workspace(int Hv);     // of its widest tile
 cudaError_t launch_paged4_mma(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
+bool paged4_tc_supported(const PagedAttn& a, sdpa_dtype dt);
+size_t paged4_tc_workspace(int Hv);
+cudaError_t launch_paged4_tc(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
+cudaError_t take_paged4_tc_status(int* status, int* timeout);
+cudaError_t take_bounds_paged4_tc(int* site);
 cudaError_t take_paged4_simt_status(int* status);
 cudaError_t take_paged4_mma_status(int* status, int* timeout);
 cudaError_t take_bounds_paged4_mma(int* site);

@@ -306,16 +306,21 @@ cudaError_t launch_t(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t s
 }  // namespace
 
 PagedKernel paged4_kernel(const PagedAttn& a, sdpa_dtype dt) {
+  if (paged4_tc_supported(a, dt)) return kPagedTc;
   return paged4_mma_supported(a.g.H, a.g.Hv, dt) ? kPagedMma : kPagedSimt;
 }
 
 size_t paged4_workspace(int H, int Hv, sdpa_dtype dt) {
-  if (paged4_mma_supported(H, Hv, dt)) return paged4_mma_workspace(Hv);
+  if (paged4_mma_supported(H, Hv, dt)) return std::max(paged4_mma_workspace(Hv), paged4_tc_workspace(Hv));
   return paged_ws_bytes(kPagedMaxSms * ctas_per_sm(1), kMaxTM, Hv);
 }
 
 cudaError_t launch_paged4_attn(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name) {
-  if (paged4_kernel(a, dt) == kPagedMma) return launch_paged4_mma(a, dt, ws, st, name);
+  switch (paged4_kernel(a, dt)) {
+    case kPagedTc: return launch_paged4_tc(a, dt, ws, st, name);
+    case kPagedMma: return launch_paged4_mma(a, dt, ws, st, name);
+    default: break;
+  }
   *name = dt == SDPA_F32 ? "paged4_simt_f32" : dt == SDPA_F16 ? "paged4_simt_f16" : "paged4_simt_bf16";
   switch (dt) {
     case SDPA_F32: return launch_t<float>(a, dt, ws, st);
