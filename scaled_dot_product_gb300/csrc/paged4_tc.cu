@@ -18,10 +18,9 @@
 // 1024 (fp16) or 128 (bf16), less that number, times the scale, plus the minimum: exact up to the one
 // rounding to the type, as the tensor cores' operands are 16-bit (half a step, like the keys and values of a
 // cache in the type).  Weights are rounded to the type too; their sum takes them unrounded.  Records of
-// keys that no row of the unit admits become zeros, since 0 x NaN is not 0.  The softmax reads its
-// scores twice from tensor memory, 32 columns at a time, once for the maximum and once for the weights,
-// which fits the registers that 16 warps leave.  Running maxima move only when they grow by more
-// than 2^8.  Every wait is bounded: on expiry the kernel raises an abort flag, lets its own copies and
+// keys that no row of the unit admits become zeros, since 0 x NaN is not 0.  The softmax takes 32 columns
+// of its scores at a time, which fits the registers that 16 warps leave: a running maximum is passed by at most 2^8,
+// and where it has to move, the weights and products made with it are rescaled by a power of two.  Every wait is bounded: on expiry the kernel raises an abort flag, lets its own copies and
 // products finish, frees its tensor memory and records SDPA_ERR_TIMEOUT.
 #include <algorithm>
 #include <cstdlib>
@@ -45,10 +44,16 @@ constexpr int kThreads = 512;
 // caches in the type.
 constexpr int kOV = 8, kMinShare = 24;
 // Register split: control, softmax and record warps; the sum stays within the launch's kThreads x
-// kLaunchRegs, which the host checks.
-constexpr int kLaunchRegs = 128, kCtlRegs = 80, kSmxRegs = 168, kRecRegs = 96;
-static_assert(kCtlRegs * 128 + kSmxRegs * 256 + kRecRegs * 128 <= kLaunchRegs * kThreads, "register split");
+// kLaunchRegs, which the host checks.  Local memory is far away here (the first-level cache is all shared
+// memory), so the splits are ones that spill nothing.
+constexpr int kLaunchRegs = 128;
+template <int H>
+struct Regs {
+  static constexpr int kCtl = 104, kSmx = H == 128 ? 144 : 152, kRec = H == 128 ? 120 : 104;
+  static_assert(kCtl * 128 + kSmx * 256 + kRec * 128 <= kLaunchRegs * kThreads, "register split");
+};
 constexpr float kRescale = 8.f;      // log2 units
+constexpr float kNone = -1e30f;      // the maximum of a row that has admitted no key: finite, so that differences are numbers
 
 template <int H>
 struct Cfg {
@@ -83,6 +88,24 @@ __device__ __forceinline__ uint32_t key_bits(int key, int lo, int hi) {
   const int a = max(lo - key, 0), b = min(hi - key, 31);
   const uint32_t up = 0xffffffffu >> (31 - max(b, 0));
   return a <= b ? up & (0xffffffffu << min(a, 31)) : 0u;
+}
+
+// 32 lanes x 8 columns, for the seldom paths: few registers.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t times2(uint32_t a, uint32_t b) {
+  using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+  const T2 y = __hmul2(*reinterpret_cast<const T2*>(&a), *reinterpret_cast<const T2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&y);
 }
 
 // A word's eight codes as four pairs of values, minimum + scale * code rounded once.
@@ -176,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abortp, t.wait_ns));
   };
-  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<H>::kCtl));
 
   if (warp == 0) {
     // ================================================================ query tiles by TMA
@@ -201,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 12) {
     // ================================================================ keys and values
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRecRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<H>::kRec));
     constexpr int kRow = q4_row_bytes(H, 2), kVecs = kRow / 8, G = H / kQ4Group;
     const int row = threadIdx.x - 384;               // this thread's key of a tile
     int base = 0;                                    // ring position of the unit's first tile
@@ -481,13 +504,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ================================================================ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSmxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<H>::kSmx));
     const int x = (warp - 4) >> 2, sub = warp & 3;
     const int row = sub * 32 + lane;                 // row of the tile == tensor-memory lane
     const uint32_t trow = tmem + ((uint32_t)(sub * 32) << 16);
     const uint32_t tS = trow + 128 * x, tO = trow + (x ? C::kO1 : C::kO0), tP = trow + (x ? C::kP1 : C::kP0);
     const uint32_t sY = sQ + C::kYOff + (uint32_t)(x * 4 + sub) * C::kYWarp;
     const float fac = CAP ? t.cap_in : t.scale_log2;      // of the scores, or of the cap's argument
+    const float kfac = CAP || t.pre ? 1.f : fac;
     int cs = 0, co = 0, xc = 0;                      // sfull / odone / joining phases waited
     bool ok = true;
     for (Wk w(a, sh); ok && !w.done(); w.next(a)) {
@@ -518,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++co;
         continue;
       }
-      float m = -INFINITY, l = 0.f;
+      float m = kNone, l = 0.f;
       for (int j = j0; j < n; j += js) {
         if (!(ok = wait_all(b_sfull(x), cs & 1))) break;
         ++cs;
@@ -526,114 +550,105 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key0 = (kt0 + j) * kTN;
         // one answer for the warp: the loads from tensor memory below are the whole warp's
         const bool edge = __any_sync(0xffffffffu, !(lo <= key0 && key0 + kTN - 1 <= hi));
-        // ---- maximum, 32 columns at a time, the next ones on their way
-        float mx = -INFINITY;
-        {
-          uint32_t u[2][32];
-          tmem_ld32(tS, u[0]);
+        // ---- 32 columns at a time, the next ones on their way.  The weights refer to the maximum so far; columns
+        // that pass it by more than 2^8 move it, and what has been made with the old one is rescaled.
+        float sum = 0.f;
+        bool free_p = C::kAlias || j == j0;          // P_X has been read, O_X holds the product
+        // the previous PV_X has read P_X and O_X holds it (with P in S's columns, sfull said so)
+        auto wait_p = [&]() {
+          if (free_p || !ok) return;
+          ok = wait_all(b_odone(x), co & 1);
+          ++co;
+          tc_fence_after();
+          free_p = true;
+        };
+        uint32_t u[2][32], pw[32];
+        tmem_ld32(tS, u[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld_wait();
-            if (c < 3) tmem_ld32(tS + (c + 1) * 32, u[(c + 1) & 1]);
-            float v[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              v[e] = __uint_as_float(u[c & 1][e]);
-              if (t.pre) v[e] *= fac;
-            }
-            if (edge) {
-              const uint32_t bits = key_bits(key0 + c * 32, lo, hi);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = (bits >> e) & 1u ? v[e] : -INFINITY;
-            }
-            float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], v[e], v[e + 1]);
-            mx = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait();
+          if (c < 3) tmem_ld32(tS + (c + 1) * 32, u[(c + 1) & 1]);
+          else if constexpr (!C::kAlias) {
+            tc_fence_before();
+            mbar_arrive(b_sfree(x));
           }
-        }
-        if (!t.pre) mx *= fac;
-        // the cap rises with its argument
-        if (CAP && mx != -INFINITY) mx = t.cap_log2 * (1.f - __fdividef(2.f, ex2_approx(2.f * kLog2e * mx) + 1.f));
-        const float m_new = fmaxf(m, mx);
-        const bool need = m_new > m + kRescale;      // true for a row's first keys: m = -inf
-        float corr = 1.f;
-        if (need) {
-          corr = ex2_approx(m - m_new);
-          m = m_new;
-        }
-        // rows with nothing admitted yet: exponent -inf, weight 0
-        const float negm = (m == -INFINITY) ? -INFINITY : -m;
-        if (j != j0) {
-          // the previous PV_X has read P_X and O_X holds it (with P in S's columns, sfull said so)
-          if constexpr (!C::kAlias) {
-            if (!(ok = wait_all(b_odone(x), co & 1))) break;
-            ++co;
-            tc_fence_after();
+          float z[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) z[e] = __uint_as_float(u[c & 1][e]);
+          if constexpr (CAP) {
+            // cap tanh(u) in log2 units: 1 - 2 / (e^2u + 1), absolute error about 2^-23 of the cap
+            const float c2 = 2.f * kLog2e * fac;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) z[e] = t.cap_log2 * (1.f - __fdividef(2.f, ex2_approx(z[e] * c2) + 1.f));
+          } else if (t.pre) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) z[e] *= fac;
           }
+          if (edge) {
+            const uint32_t bits = key_bits(key0 + c * 32, lo, hi);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) z[e] = (bits >> e) & 1u ? z[e] : -INFINITY;
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) top[(e >> 1) & 3] = fmax3(top[(e >> 1) & 3], z[e], z[e + 1]);
+          const float mx = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * kfac;
+          const bool need = mx > m + kRescale;       // true for a row's first keys
           if (__any_sync(0xffffffffu, need)) {
-            const f2_t c2 = f2_pack(corr, corr);
+            const float m_new = need ? ceilf(mx) : m;
+            const float corr = ex2_approx(m - m_new);      // a power of two: rescaled weights keep their bits
+            m = m_new;
+            l *= corr;
+            sum *= corr;
+            const uint32_t corr2 = BF ? pack_bf16x2(corr, corr) : pack_f16x2(corr, corr);
+            if (c & 1) {
 #pragma unroll
-            for (int c = 0; c < H / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO + c * 32, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float v0, v1;
-                f2_unpack(f2_mul(f2_pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), c2), v0, v1);
-                o[e] = __float_as_uint(v0);
-                o[e + 1] = __float_as_uint(v1);
-              }
-              tmem_st32(tO + c * 32, o);
+              for (int e = 0; e < 16; ++e) pw[e] = times2<T>(pw[e], corr2);
             }
-            tmem_st_wait();
+            if (c >= 2) {
+              tmem_st_wait();
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) {
+                uint32_t o[8];
+                tmem_ld8(tP + i * 8, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = times2<T>(o[e], corr2);
+                tmem_st8(tP + i * 8, o);
+              }
+            }
+            if (j != j0) {
+              wait_p();
+              if (ok) {
+#pragma unroll 1
+                for (int i = 0; i < H / 8; ++i) {
+                  uint32_t o[8];
+                  tmem_ld8(tO + i * 8, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                  tmem_st8(tO + i * 8, o);
+                }
+                tmem_st_wait();
+              }
+            }
+          }
+          float part[2] = {0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float p0 = ex2_approx(fmaf(z[e], kfac, -m)), p1 = ex2_approx(fmaf(z[e + 1], kfac, -m));
+            part[(e >> 1) & 1] += p0 + p1;
+            pw[(c & 1) * 16 + (e >> 1)] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+          }
+          sum += part[0] + part[1];
+          if (c & 1) {
+            wait_p();
+            if (!ok) break;
+            tmem_st32(tP + (c >> 1) * 32, pw);
           }
         }
-        // ---- weights, again 32 columns at a time.  P's columns lie in front of those of S still to be read.
-        f2_t acc[2] = {f2_zero(), f2_zero()};
-        {
-          uint32_t u[2][32], pw[32];
-          tmem_ld32(tS, u[0]);
-          const f2_t kf2 = f2_pack(fac, fac), nm2 = f2_pack(negm, negm);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld_wait();
-            if (c < 3) tmem_ld32(tS + (c + 1) * 32, u[(c + 1) & 1]);
-            uint32_t bits = 0xffffffffu;
-            if (edge) bits = key_bits(key0 + c * 32, lo, hi);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float z0, z1;
-              const float s0 = __uint_as_float(u[c & 1][e]), s1 = __uint_as_float(u[c & 1][e + 1]);
-              if constexpr (CAP) {
-                // cap tanh(u) in log2 units: 1 - 2 / (e^2u + 1), absolute error about 2^-23 of the cap
-                const float c2 = 2.f * kLog2e * fac;
-                z0 = fmaf(t.cap_log2, 1.f - __fdividef(2.f, ex2_approx(s0 * c2) + 1.f), negm);
-                z1 = fmaf(t.cap_log2, 1.f - __fdividef(2.f, ex2_approx(s1 * c2) + 1.f), negm);
-              } else {
-                f2_unpack(f2_fma(f2_pack(s0, s1), kf2, nm2), z0, z1);
-              }
-              if (edge) {
-                z0 = (bits >> e) & 1u ? z0 : -INFINITY;
-                z1 = (bits >> (e + 1)) & 1u ? z1 : -INFINITY;
-              }
-              const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
-              acc[(e >> 1) & 1] = f2_add(acc[(e >> 1) & 1], f2_pack(p0, p1));
-              pw[(c & 1) * 16 + (e >> 1)] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
-            }
-            if (c & 1) tmem_st32(tP + (c >> 1) * 32, pw);
-          }
-        }
-        if constexpr (!C::kAlias) {
-          tc_fence_before();
-          mbar_arrive(b_sfree(x));
-        }
-        {
-          float r0, r1;
-          f2_unpack(f2_add(acc[0], acc[1]), r0, r1);
-          l = l * corr + (r0 + r1);
-        }
+        if (!ok) break;
+        l += sum;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(b_pfull(x));
@@ -641,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
 
       // ---- the unit's rows, or their partial results
+      if (m <= 0.5f * kNone) m = -INFINITY;
       if (!(ok = wait_all(b_odone(x), co & 1))) break;
       ++co;
       tc_fence_after();
@@ -699,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = group_div(g, pr), h = w.kvh * g.group + pr - tok * g.group;
         float inv = 0.f;
         const long long yrow = (long long)(reinterpret_cast<uintptr_t>(a.y.p) + (uintptr_t)(a.y.off(0, h, w.s.t0 + tok) * 2));
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < H / 32; ++c) {
           uint32_t o[32];
           read_o(c, o);
@@ -732,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         const int64_t base = (2 * (int64_t)cta + (w.begins() ? 1 : 0)) * kTM + tile_row + sub * 32;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < H / 32; ++c) {
           uint32_t o[32];
           read_o(c, o);
