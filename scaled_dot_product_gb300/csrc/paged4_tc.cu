@@ -18,7 +18,7 @@
 // 1024 (fp16) or 128 (bf16), less that number, times the scale, plus the minimum: exact up to the one
 // rounding to the type, as the tensor cores' operands are 16-bit (half a step, like the keys and values of a
 // cache in the type).  Weights are rounded to the type too; their sum takes them unrounded.  Records of
-// keys that no row of the unit admits become zeros, since 0 x NaN is not 0.  The softmax takes 32 columns
+// keys that no row of the unit admits become zeros, since 0 x NaN is not 0.  The softmax takes 64 columns
 // of its scores at a time, which fits the registers that 16 warps leave: a running maximum is passed by at most 2^8,
 // and where it has to move, the weights and products made with it are rescaled by a power of two.  Every wait is bounded: on expiry the kernel raises an abort flag, lets its own copies and
 // products finish, frees its tensor memory and records SDPA_ERR_TIMEOUT.
@@ -44,14 +44,10 @@ constexpr int kThreads = 512;
 // caches in the type.
 constexpr int kOV = 8, kMinShare = 24;
 // Register split: control, softmax and record warps; the sum stays within the launch's kThreads x
-// kLaunchRegs, which the host checks.  Local memory is far away here (the first-level cache is all shared
-// memory), so the splits are ones that spill nothing.
-constexpr int kLaunchRegs = 128;
-template <int H>
-struct Regs {
-  static constexpr int kCtl = 104, kSmx = H == 128 ? 144 : 152, kRec = H == 128 ? 120 : 104;
-  static_assert(kCtl * 128 + kSmx * 256 + kRec * 128 <= kLaunchRegs * kThreads, "register split");
-};
+// kLaunchRegs, which the host checks.  A chunk of 2048 over 32000 keys, H = 128 / 64: 876 / 750 us; with 96, 160
+// and 96 registers 905 / 743, with 120, 152 and 88 880 / 793.
+constexpr int kLaunchRegs = 128, kCtlRegs = 104, kSmxRegs = 152, kRecRegs = 104;
+static_assert(kCtlRegs * 128 + kSmxRegs * 256 + kRecRegs * 128 <= kLaunchRegs * kThreads, "register split");
 constexpr float kRescale = 8.f;      // log2 units
 constexpr float kNone = -1e30f;      // the maximum of a row that has admitted no key: finite, so that differences are numbers
 
@@ -199,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abortp, t.wait_ns));
   };
-  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<H>::kCtl));
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
 
   if (warp == 0) {
     // ================================================================ query tiles by TMA
@@ -224,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 12) {
     // ================================================================ keys and values
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<H>::kRec));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRecRegs));
     constexpr int kRow = q4_row_bytes(H, 2), kVecs = kRow / 8, G = H / kQ4Group;
     const int row = threadIdx.x - 384;               // this thread's key of a tile
     int base = 0;                                    // ring position of the unit's first tile
@@ -504,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ================================================================ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<H>::kSmx));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSmxRegs));
     const int x = (warp - 4) >> 2, sub = warp & 3;
     const int row = sub * 32 + lane;                 // row of the tile == tensor-memory lane
     const uint32_t trow = tmem + ((uint32_t)(sub * 32) << 16);
@@ -550,8 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key0 = (kt0 + j) * kTN;
         // one answer for the warp: the loads from tensor memory below are the whole warp's
         const bool edge = __any_sync(0xffffffffu, !(lo <= key0 && key0 + kTN - 1 <= hi));
-        // ---- 32 columns at a time, the next ones on their way.  The weights refer to the maximum so far; columns
-        // that pass it by more than 2^8 move it, and what has been made with the old one is rescaled.
+        // ---- 64 columns at a time (32 took 1578 us where these take 876: each step waits for its scores and
+        // for the warp's vote; all 128 at once 995).  The weights refer to the maximum so far; columns that pass it by more than 2^8 move it, and what has been made with the old one is rescaled.
         float sum = 0.f;
         bool free_p = C::kAlias || j == j0;          // P_X has been read, O_X holds the product
         // the previous PV_X has read P_X and O_X holds it (with P in S's columns, sfull said so)
@@ -562,36 +558,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           free_p = true;
         };
-        uint32_t u[2][32], pw[32];
-        tmem_ld32(tS, u[0]);
+        constexpr int kCols = 64;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait();
-          if (c < 3) tmem_ld32(tS + (c + 1) * 32, u[(c + 1) & 1]);
-          else if constexpr (!C::kAlias) {
-            tc_fence_before();
-            mbar_arrive(b_sfree(x));
+        for (int c = 0; c < kTN / kCols; ++c) {
+          uint32_t pw[32];
+          float z[kCols];
+          {
+            uint32_t u[kCols];
+            tmem_ld32(tS + c * kCols, u);
+            tmem_ld32(tS + c * kCols + 32, u + 32);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) z[e] = __uint_as_float(u[e]);
           }
-          float z[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) z[e] = __uint_as_float(u[c & 1][e]);
+          if constexpr (!C::kAlias) {
+            if (c == 1) {
+              tc_fence_before();
+              mbar_arrive(b_sfree(x));
+            }
+          }
           if constexpr (CAP) {
             // cap tanh(u) in log2 units: 1 - 2 / (e^2u + 1), absolute error about 2^-23 of the cap
             const float c2 = 2.f * kLog2e * fac;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) z[e] = t.cap_log2 * (1.f - __fdividef(2.f, ex2_approx(z[e] * c2) + 1.f));
+            for (int e = 0; e < kCols; ++e) z[e] = t.cap_log2 * (1.f - __fdividef(2.f, ex2_approx(z[e] * c2) + 1.f));
           } else if (t.pre) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) z[e] *= fac;
+            for (int e = 0; e < kCols; ++e) z[e] *= fac;
           }
           if (edge) {
-            const uint32_t bits = key_bits(key0 + c * 32, lo, hi);
+            const uint32_t b0 = key_bits(key0 + c * kCols, lo, hi), b1 = key_bits(key0 + c * kCols + 32, lo, hi);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) z[e] = (bits >> e) & 1u ? z[e] : -INFINITY;
+            for (int e = 0; e < kCols; ++e) z[e] = ((e < 32 ? b0 : b1) >> (e & 31)) & 1u ? z[e] : -INFINITY;
           }
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) top[(e >> 1) & 3] = fmax3(top[(e >> 1) & 3], z[e], z[e + 1]);
+          for (int e = 0; e < kCols; e += 2) top[(e >> 1) & 3] = fmax3(top[(e >> 1) & 3], z[e], z[e + 1]);
           const float mx = fmaxf(fmax3(top[0], top[1], top[2]), top[3]) * kfac;
           const bool need = mx > m + kRescale;       // true for a row's first keys
           if (__any_sync(0xffffffffu, need)) {
@@ -601,11 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             l *= corr;
             sum *= corr;
             const uint32_t corr2 = BF ? pack_bf16x2(corr, corr) : pack_f16x2(corr, corr);
-            if (c & 1) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) pw[e] = times2<T>(pw[e], corr2);
-            }
-            if (c >= 2) {
+            if (c == 1) {
               tmem_st_wait();
 #pragma unroll 1
               for (int i = 0; i < 4; ++i) {
@@ -633,19 +631,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          float part[2] = {0.f, 0.f};
+          f2_t part[2] = {f2_zero(), f2_zero()};
+          const f2_t kf2 = f2_pack(kfac, kfac), nm2 = f2_pack(-m, -m);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float p0 = ex2_approx(fmaf(z[e], kfac, -m)), p1 = ex2_approx(fmaf(z[e + 1], kfac, -m));
-            part[(e >> 1) & 1] += p0 + p1;
-            pw[(c & 1) * 16 + (e >> 1)] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+          for (int e = 0; e < kCols; e += 2) {
+            float z0, z1;
+            f2_unpack(f2_fma(f2_pack(z[e], z[e + 1]), kf2, nm2), z0, z1);
+            const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
+            part[(e >> 1) & 1] = f2_add(part[(e >> 1) & 1], f2_pack(p0, p1));
+            pw[e >> 1] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
           }
-          sum += part[0] + part[1];
-          if (c & 1) {
-            wait_p();
-            if (!ok) break;
-            tmem_st32(tP + (c >> 1) * 32, pw);
+          {
+            float r0, r1;
+            f2_unpack(f2_add(part[0], part[1]), r0, r1);
+            sum += r0 + r1;
           }
+          wait_p();
+          if (!ok) break;
+          tmem_st32(tP + c * 32, pw);
         }
         if (!ok) break;
         l += sum;
