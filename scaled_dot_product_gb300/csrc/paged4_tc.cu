@@ -547,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // one answer for the warp: the loads from tensor memory below are the whole warp's
         const bool edge = __any_sync(0xffffffffu, !(lo <= key0 && key0 + kTN - 1 <= hi));
         // ---- 64 columns at a time (32 took 1578 us where these take 876: each step waits for its scores and
-        // for the warp's vote; all 128 at once 995).  The weights refer to the maximum so far; columns that pass it by more than 2^8 move it, and what has been made with the old one is rescaled.
+        // for the warp's vote; all 128 at once 995).  The weights refer to the maximum so far; columns that pass it by
+        // more than 2^8 move it, and what has been made with the old one is rescaled.
         float sum = 0.f;
         bool free_p = C::kAlias || j == j0;          // P_X has been read, O_X holds the product
         // the previous PV_X has read P_X and O_X holds it (with P in S's columns, sfull said so)
