@@ -25,6 +25,7 @@ struct Paged4Append {
   int64_t max_pos;
   int R, interleaved;
   int vec_rot;                    // pairs and caches in whole 16-byte vectors
+  uint32_t tok_mul, tok_shift, k_mul, k_shift, v_mul, v_shift, page_mul, page_shift;      // divisions (paged_magic)
 };
 cudaError_t launch_paged4_append(sdpa_dtype dt, const Paged4Append& a, cudaStream_t st);
 cudaError_t take_paged4_append_status(int* status);

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "paged4.h"
+#include "paged_sched.cuh"
 
 namespace sdpa {
 
@@ -32,6 +33,10 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   float d;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
+}
+
+__device__ __forceinline__ int fast_div(int x, uint32_t mul, uint32_t shift) {
+  return (int)(((uint64_t)(uint32_t)x * mul) >> shift);
 }
 
 template <typename T>
@@ -106,24 +111,24 @@ template <typename T, bool kInter>
 __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4Append a, const int tpb) {
   const int ku = a.Nkv * (a.H / 8), per_tok = ku + a.Nkv * (a.Hv / 8);
   const int x0 = (int)blockIdx.y * kThreads + (int)threadIdx.x;
-  const int t = (int)blockIdx.x * tpb + x0 / per_tok;
+  const int lt = fast_div(x0, a.tok_mul, a.tok_shift), t = (int)blockIdx.x * tpb + lt;
   // four lanes of a group have the same token, tensor and head
-  const bool live = x0 / per_tok < tpb && t < a.tokens;
-  int u = x0 % per_tok;
+  const bool live = lt < tpb && t < a.tokens;
+  int u = x0 - lt * per_tok;
   const bool isk = u < ku;
   if (!isk) u -= ku;
-  const int D = isk ? a.H : a.Hv, head = u / (D / 8), c0 = (u - head * (D / 8)) * 8;
-  const int64_t slots = (int64_t)a.num_pages * a.page_size;
+  const int D = isk ? a.H : a.Hv;
+  const int head = isk ? fast_div(u, a.k_mul, a.k_shift) : fast_div(u, a.v_mul, a.v_shift), c0 = (u - head * (D / 8)) * 8;
   float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   int64_t slot = -1;
-  const T* row = nullptr;
   if (live) {
     const View& src = isk ? a.k : a.v;
-    row = reinterpret_cast<const T*>(src.p) + src.off(0, head, t);
+    const T* row = reinterpret_cast<const T*>(src.p) + src.off(0, head, t);
     slot = a.slots[t];
+    const bool turned = isk && c0 < a.R;
+    int64_t pos = turned ? a.positions[t] : 0;
     if (SDPA_IN_BOUNDS(head < a.Nkv && c0 + 8 <= D, 571)) load8<T>(row + c0, x);
-    if (isk && c0 < a.R) {
-      int64_t pos = a.positions[t];
+    if (turned) {
       // the place of a token that goes nowhere is not looked at
       if (slot >= 0 && (pos < 0 || pos >= a.max_pos)) atomicOr(g_append4_status, kPagedBadPosition);
       pos = min(max(pos, (int64_t)0), a.max_pos - 1);
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   if (!live || slot < 0) return;
-  if (slot >= slots) {
+  if (slot >= (int64_t)a.num_pages * a.page_size) {
     atomicOr(g_append4_status, kPagedBadSlot);
     return;
   }
@@ -151,15 +156,27 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
   // a scale rounded up at the end of the type's range: code 15 would have no value
   if (fmaf(15.f, s, lo) > largest<T>()) s = step_down<T>(s);
   if (!(spread < INFINITY)) s = lo = __int_as_float(0x7fffffff);
+  const bool ordinary = s > 1e-30f && s < 1e30f;      // the reciprocal is an ordinary number too
+  const float inv = ordinary ? __frcp_rn(s) : 0.f;
   float code[8];
   uint32_t word = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float q = s > 0.f ? __fdiv_rn(x[e] - lo, s) : 0.f;
-    code[e] = fminf(rintf(q), 15.f);
-    word |= (uint32_t)code[e] << (4 * e);
+    // The quotient by the reciprocal is off by 2^-22 of itself at most: only near a tie can its integer be
+    // another one, and there the division decides.
+    const float d = x[e] - lo;
+    float q = fminf(d * inv, 15.f);
+    constexpr float kInt = 12582912.f;       // 1.5 2^23: a sum with it is rounded to an integer, the even one at a tie
+    float i = (q + kInt) - kInt;
+    if ((!ordinary || fabsf(fabsf(q - i) - 0.5f) < 1e-4f) && s > 0.f) {
+      q = fminf(__fdiv_rn(d, s), 15.f);
+      i = (q + kInt) - kInt;
+    }
+    if (!(s > 0.f)) i = 0.f;                 // a constant group, or one that is not a number
+    code[e] = i;
+    word |= (__float_as_uint(i + kInt) & 15u) << (4 * e);
   }
-  const uint64_t page = slots <= 0xffffffffll ? (uint32_t)slot / (uint32_t)a.page_size : (uint64_t)slot / (uint32_t)a.page_size;
+  const uint64_t page = slot < (1ll << 31) ? (uint64_t)fast_div((int)slot, a.page_mul, a.page_shift) : (uint64_t)slot / (uint32_t)a.page_size;
   const int at = (int)(slot - (int64_t)page * a.page_size);
   const View& dst = isk ? a.kp : a.vp;
   unsigned char* rec = reinterpret_cast<unsigned char*>(const_cast<void*>(dst.p)) + dst.off((int64_t)page, head, at);
@@ -188,10 +205,14 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
 }
 
 template <typename T>
-cudaError_t launch_t(const Paged4Append& a, cudaStream_t st) {
+cudaError_t launch_t(Paged4Append a, cudaStream_t st) {
   const int64_t per_tok = (int64_t)a.Nkv * ((a.H + a.Hv) / 8);
   const int tpb = (int)std::max<int64_t>(1, std::min<int64_t>(64, kThreads / per_tok));
   const dim3 grid((unsigned)((a.tokens + tpb - 1) / tpb), (unsigned)((per_tok * tpb + kThreads - 1) / kThreads));
+  paged_magic((int)per_tok, &a.tok_mul, &a.tok_shift);
+  paged_magic(a.H / 8, &a.k_mul, &a.k_shift);
+  paged_magic(a.Hv / 8, &a.v_mul, &a.v_shift);
+  paged_magic(a.page_size, &a.page_mul, &a.page_shift);
   if (a.R && a.interleaved) paged4_append_kernel<T, true><<<grid, kThreads, 0, st>>>(a, tpb);
   else paged4_append_kernel<T, false><<<grid, kThreads, 0, st>>>(a, tpb);
   count_launch(1);
