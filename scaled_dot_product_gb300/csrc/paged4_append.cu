@@ -8,8 +8,7 @@
 // is not, takes a scale and a minimum that are no numbers: it reads as NaN.
 //
 // Every element is read once and written once at 5/8 byte (and once more, as the cache holds it,
-// where the caller wants that).  A thread has 8 channels, four lanes a group: its minimum and
-// maximum take two exchanges.  The slot and the position of a token are one load each.
+// where the caller wants that).  A thread has 16 channels, two lanes a group.  The slot and the position of a token are one load each.
 #include <algorithm>
 #include <type_traits>
 
@@ -39,10 +38,13 @@ __device__ __forceinline__ int fast_div(int x, uint32_t mul, uint32_t shift) {
   return (int)(((uint64_t)(uint32_t)x * mul) >> shift);
 }
 
+constexpr int kCh = 16;          // channels of a thread: two threads a group
+
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* f) {
-  unpack16<T>(*reinterpret_cast<const uint4*>(p), f);
-  if constexpr (sizeof(T) == 4) unpack16<T>(*reinterpret_cast<const uint4*>(p + 4), f + 4);
+__device__ __forceinline__ void load_ch(const T* p, float* f) {
+  constexpr int V = Elem<T>::kVec;
+#pragma unroll
+  for (int i = 0; i < kCh / V; ++i) unpack16<T>(reinterpret_cast<const uint4*>(p)[i], f + i * V);
 }
 
 // The next smaller value of the type below x > 0.
@@ -65,15 +67,15 @@ __device__ __forceinline__ float largest() {
 template <typename T>
 __device__ __forceinline__ float rounded(float x) { return Elem<T>::to_f32(Elem<T>::from_f32(x)); }
 
-// Channels [c0, c0 + 8) of a key turned.  Whole vectors of pairs (vec_rot), or pair by pair.
+// Channels [c0, c0 + 16) of a key turned.  Whole vectors of pairs (vec_rot), or pair by pair.
 template <typename T, bool kInter>
-__device__ __forceinline__ void turn8(const Paged4Append& a, const T* row, int c0, int64_t crow, float* x) {
+__device__ __forceinline__ void turn(const Paged4Append& a, const T* row, int c0, int64_t crow, float* x) {
   const int half = a.R / 2;
   const T* cr = reinterpret_cast<const T*>(a.cos_c) + crow;
   const T* sr = reinterpret_cast<const T*>(a.sin_c) + crow;
   if constexpr (kInter) {
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
+    for (int e = 0; e < kCh; e += 2) {
       const int i = (c0 + e) / 2;
       if (c0 + e >= a.R) break;
       const float c = Elem<T>::to_f32(cr[i]), s = Elem<T>::to_f32(sr[i]);
@@ -84,18 +86,19 @@ __device__ __forceinline__ void turn8(const Paged4Append& a, const T* row, int c
   } else if (a.vec_rot) {
     const bool low = c0 < half;
     const int i0 = low ? c0 : c0 - half;
-    float o[8], c[8], s[8];
-    load8<T>(row + (low ? c0 + half : i0), o);
-    load8<T>(cr + i0, c);
-    load8<T>(sr + i0, s);
+    float o[kCh], c[kCh], s[kCh];
+    load_ch<T>(row + (low ? c0 + half : i0), o);
+    load_ch<T>(cr + i0, c);
+    load_ch<T>(sr + i0, s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float p = __fmul_rn(x[e], c[e]), q = __fmul_rn(o[e], s[e]);
-      x[e] = rounded<T>(low ? __fsub_rn(p, q) : __fadd_rn(p, q));
+    for (int e = 0; e < kCh; ++e) {
+      // x cos - o sin in the lower half, x cos + o sin in the upper
+      const float q = __fmul_rn(o[e], s[e]);
+      x[e] = rounded<T>(__fadd_rn(__fmul_rn(x[e], c[e]), low ? -q : q));
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < kCh; ++e) {
       const int ch = c0 + e;
       if (ch >= a.R) break;
       const bool low = ch < half;
@@ -109,17 +112,19 @@ __device__ __forceinline__ void turn8(const Paged4Append& a, const T* row, int c
 
 template <typename T, bool kInter>
 __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4Append a, const int tpb) {
-  const int ku = a.Nkv * (a.H / 8), per_tok = ku + a.Nkv * (a.Hv / 8);
+  const int ku = a.Nkv * (a.H / kCh), per_tok = ku + a.Nkv * (a.Hv / kCh);
   const int x0 = (int)blockIdx.y * kThreads + (int)threadIdx.x;
   const int lt = fast_div(x0, a.tok_mul, a.tok_shift), t = (int)blockIdx.x * tpb + lt;
-  // four lanes of a group have the same token, tensor and head
+  // the two lanes of a group have the same token, tensor and head
   const bool live = lt < tpb && t < a.tokens;
   int u = x0 - lt * per_tok;
   const bool isk = u < ku;
   if (!isk) u -= ku;
   const int D = isk ? a.H : a.Hv;
-  const int head = isk ? fast_div(u, a.k_mul, a.k_shift) : fast_div(u, a.v_mul, a.v_shift), c0 = (u - head * (D / 8)) * 8;
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const int head = isk ? fast_div(u, a.k_mul, a.k_shift) : fast_div(u, a.v_mul, a.v_shift), c0 = (u - head * (D / kCh)) * kCh;
+  float x[kCh];
+#pragma unroll
+  for (int e = 0; e < kCh; ++e) x[e] = 0.f;
   int64_t slot = -1;
   if (live) {
     const View& src = isk ? a.k : a.v;
@@ -127,25 +132,22 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
     slot = a.slots[t];
     const bool turned = isk && c0 < a.R;
     int64_t pos = turned ? a.positions[t] : 0;
-    if (SDPA_IN_BOUNDS(head < a.Nkv && c0 + 8 <= D, 571)) load8<T>(row + c0, x);
+    if (SDPA_IN_BOUNDS(head < a.Nkv && c0 + kCh <= D, 571)) load_ch<T>(row + c0, x);
     if (turned) {
       // the place of a token that goes nowhere is not looked at
       if (slot >= 0 && (pos < 0 || pos >= a.max_pos)) atomicOr(g_append4_status, kPagedBadPosition);
       pos = min(max(pos, (int64_t)0), a.max_pos - 1);
-      turn8<T, kInter>(a, row, c0, pos * (a.R / 2), x);
+      turn<T, kInter>(a, row, c0, pos * (a.R / 2), x);
     }
   }
   float lo = x[0], hi = x[0];
 #pragma unroll
-  for (int e = 1; e < 8; ++e) {
+  for (int e = 1; e < kCh; ++e) {
     lo = min_nan(lo, x[e]);
     hi = max_nan(hi, x[e]);
   }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
+  lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+  hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
   if (!live || slot < 0) return;
   if (slot >= (int64_t)a.num_pages * a.page_size) {
     atomicOr(g_append4_status, kPagedBadSlot);
@@ -156,32 +158,48 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
   // a scale rounded up at the end of the type's range: code 15 would have no value
   if (fmaf(15.f, s, lo) > largest<T>()) s = step_down<T>(s);
   if (!(spread < INFINITY)) s = lo = __int_as_float(0x7fffffff);
-  const bool ordinary = s > 1e-30f && s < 1e30f;      // the reciprocal is an ordinary number too
+  // An integer q is the code where (q - 1/2) s < x - lo < (q + 1/2) s.  The quotient by the reciprocal finds the
+  // nearest half-integer h, and the sign of (x - lo) - h s, which a fused multiply-add has right, the side; zero is a
+  // tie, and the even neighbour.  A remainder that is neither zero nor clear of the quotient's own rounding leaves it
+  // to the division, as do scales whose reciprocal is no ordinary number.
+  const bool ordinary = s > 1e-30f && s < 1e30f;
   const float inv = ordinary ? __frcp_rn(s) : 0.f;
-  float code[8];
-  uint32_t word = 0;
+  constexpr float kInt = 12582912.f;         // 1.5 2^23: a sum with it is rounded to an integer, the even one at a tie
+  const float clear = s * 0x1p-18f;
+  float code[kCh];
+  bool divide = !ordinary;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    // The quotient by the reciprocal is off by 2^-22 of itself at most: only near a tie can its integer be
-    // another one, and there the division decides.
+  for (int e = 0; e < kCh; ++e) {
     const float d = x[e] - lo;
-    float q = fminf(d * inv, 15.f);
-    constexpr float kInt = 12582912.f;       // 1.5 2^23: a sum with it is rounded to an integer, the even one at a tie
-    float i = (q + kInt) - kInt;
-    if ((!ordinary || fabsf(fabsf(q - i) - 0.5f) < 1e-4f) && s > 0.f) {
-      q = fminf(__fdiv_rn(d, s), 15.f);
-      i = (q + kInt) - kInt;
+    const float low = (fmaf(d, inv, -0.5f) + kInt) - kInt;         // h - 1/2
+    const float rest = fmaf(-(low + 0.5f), s, d);
+    // a tie goes to the even one of low and low + 1: (low + 1/2) rounded so
+    const float up = rest > 0.f ? low + 1.f : low;
+    code[e] = rest == 0.f ? ((low + 0.5f) + kInt) - kInt : up;
+    divide = divide || (rest != 0.f && fabsf(rest) < clear);
+  }
+  if (divide) {
+#pragma unroll
+    for (int e = 0; e < kCh; ++e) code[e] = s > 0.f ? (__fdiv_rn(x[e] - lo, s) + kInt) - kInt : 0.f;
+  }
+  uint32_t word[kCh / 8];
+#pragma unroll
+  for (int w = 0; w < kCh / 8; ++w) {
+    word[w] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      code[8 * w + e] = fminf(code[8 * w + e], 15.f);
+      word[w] |= (__float_as_uint(code[8 * w + e] + kInt) & 15u) << (4 * e);
     }
-    if (!(s > 0.f)) i = 0.f;                 // a constant group, or one that is not a number
-    code[e] = i;
-    word |= (__float_as_uint(i + kInt) & 15u) << (4 * e);
   }
   const uint64_t page = slot < (1ll << 31) ? (uint64_t)fast_div((int)slot, a.page_mul, a.page_shift) : (uint64_t)slot / (uint32_t)a.page_size;
   const int at = (int)(slot - (int64_t)page * a.page_size);
   const View& dst = isk ? a.kp : a.vp;
   unsigned char* rec = reinterpret_cast<unsigned char*>(const_cast<void*>(dst.p)) + dst.off((int64_t)page, head, at);
   if (SDPA_IN_BOUNDS((int64_t)page < a.num_pages && at >= 0 && at < a.page_size, 572)) {
-    *reinterpret_cast<uint32_t*>(rec + c0 / 2) = word;
+    // records of 20 and 60 bytes are aligned to four alone
+    reinterpret_cast<uint32_t*>(rec + c0 / 2)[0] = word[0];
+    reinterpret_cast<uint32_t*>(rec + c0 / 2)[1] = word[1];
     if (c0 % kQ4Group == 0) {
       T* side = reinterpret_cast<T*>(rec + D / 2) + c0 / kQ4Group * 2;
       if constexpr (sizeof(T) == 4) {
@@ -195,23 +213,23 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
   }
   const View& held = isk ? a.k_held : a.v_held;
   if (held.p) {
-    T out[8];
+    T out[kCh];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = Elem<T>::from_f32(__fadd_rn(__fmul_rn(code[e], s), lo));
-    T* h = reinterpret_cast<T*>(const_cast<void*>(held.p)) + held.off(0, head, t) + c0;
-    *reinterpret_cast<uint4*>(h) = *reinterpret_cast<const uint4*>(out);
-    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(h + 4) = *reinterpret_cast<const uint4*>(out + 4);
+    for (int e = 0; e < kCh; ++e) out[e] = Elem<T>::from_f32(__fadd_rn(__fmul_rn(code[e], s), lo));
+    uint4* h = reinterpret_cast<uint4*>(reinterpret_cast<T*>(const_cast<void*>(held.p)) + held.off(0, head, t) + c0);
+#pragma unroll
+    for (int i = 0; i < kCh / Elem<T>::kVec; ++i) h[i] = reinterpret_cast<const uint4*>(out)[i];
   }
 }
 
 template <typename T>
 cudaError_t launch_t(Paged4Append a, cudaStream_t st) {
-  const int64_t per_tok = (int64_t)a.Nkv * ((a.H + a.Hv) / 8);
+  const int64_t per_tok = (int64_t)a.Nkv * ((a.H + a.Hv) / kCh);
   const int tpb = (int)std::max<int64_t>(1, std::min<int64_t>(64, kThreads / per_tok));
   const dim3 grid((unsigned)((a.tokens + tpb - 1) / tpb), (unsigned)((per_tok * tpb + kThreads - 1) / kThreads));
   paged_magic((int)per_tok, &a.tok_mul, &a.tok_shift);
-  paged_magic(a.H / 8, &a.k_mul, &a.k_shift);
-  paged_magic(a.Hv / 8, &a.v_mul, &a.v_shift);
+  paged_magic(a.H / kCh, &a.k_mul, &a.k_shift);
+  paged_magic(a.Hv / kCh, &a.v_mul, &a.v_shift);
   paged_magic(a.page_size, &a.page_mul, &a.page_shift);
   if (a.R && a.interleaved) paged4_append_kernel<T, true><<<grid, kThreads, 0, st>>>(a, tpb);
   else paged4_append_kernel<T, false><<<grid, kThreads, 0, st>>>(a, tpb);

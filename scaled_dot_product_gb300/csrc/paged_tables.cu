@@ -72,22 +72,25 @@ __global__ void __launch_bounds__(NT) paged_tables_kernel(const PagedTables a) {
   if (count0 > a.num_pages) bad |= kPagedBadLength;
 
   // running sum over the block of x, before this thread's own; total: of all
-  auto scan = [&](long long x, long long* sums, long long& total) -> long long {
-    long long v = x;
+  auto scan = [&](auto x, auto* sums, auto& total) {
+    auto v = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      const auto u = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += u;
     }
     if (lane == 31) sums[warp] = v;
     __syncthreads();
-    long long before = 0;
-    total = 0;
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
+    // every warp sums the warps' sums for itself
+    auto w = lane < kW ? sums[lane] : decltype(x)(0);
+#pragma unroll
+    for (int o = 1; o < kW; o <<= 1) {
+      const auto u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
     }
-    return before + v - x;
+    total = __shfl_sync(0xffffffffu, w, kW - 1);
+    const auto upto = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0);
+    return (warp ? upto : decltype(x)(0)) + v - x;
   };
 
   long long rows = 0, back = 0;
@@ -126,29 +129,18 @@ __global__ void __launch_bounds__(NT) paged_tables_kernel(const PagedTables a) {
       }
     }
     long long all_n, all_g = 0;
-    const long long e = rows + scan(n1, sum_n, all_n);
+    const long long e = rows + scan((long long)n1, sum_n, all_n);
     long long eg = 0;
-    if (__syncthreads_or(ended)) eg = scan(g, sum_g, all_g);
+    if (__syncthreads_or(ended)) eg = scan((long long)g, sum_g, all_g);
     const int n = (int)max(0ll, min((long long)n1, a.tokens - e));
     if (n != n1) bad |= kPagedBadLength;
     const int need = ended ? 0 : pages_of(p + n) - have;
     // pages taken: no more than tokens
-    int v = need;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 31) sum_t[warp] = v;
-    __syncthreads();
-    int before = pages, all_t = 0;
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) before += sum_t[w];
-      all_t += sum_t[w];
-    }
+    int all_t;
+    const int before = pages + scan(need, sum_t, all_t);
     if (in) {
       cu[b] = (int)min(e, (long long)a.tokens);
-      taken[b] = before + v - need;
+      taken[b] = before;
       given[b] = (int)min(back + eg, 1ll << 30);
       past[b] = ended ? -1 - p : p;
     }
