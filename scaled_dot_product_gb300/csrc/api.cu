@@ -1228,7 +1228,7 @@ int sdpa_paged4_append(const sdpa_paged4_append_params* p, sdpa_view k, sdpa_vie
   a.slots = p->slots; a.positions = p->positions;
   a.cos_c = p->rotary_cos; a.sin_c = p->rotary_sin; a.max_pos = p->rotary_max_pos;
   a.interleaved = a.R ? p->rotary_interleaved : 0;
-  a.vec_rot = a.R % 32 == 0 && (((uintptr_t)p->rotary_cos | (uintptr_t)p->rotary_sin) & 15u) == 0;
+  a.vec_rot = a.R % 16 == 0 && (((uintptr_t)p->rotary_cos | (uintptr_t)p->rotary_sin) & 15u) == 0;
   mark_used(kUsedAppend4);
   const cudaError_t e = launch_paged4_append((sdpa_dtype)dt, a, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "paged4_append launch");

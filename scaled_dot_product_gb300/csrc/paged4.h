@@ -37,6 +37,7 @@ PagedKernel paged4_kernel(const PagedAttn& a, sdpa_dtype dt);
 size_t paged4_workspace(int H, int Hv, sdpa_dtype dt);
 bool paged4_mma_supported(int H, int Hv, sdpa_dtype dt);
 size_t paged4_mma_workspace(int Hv);     // of its widest tile
+int paged4_mma_rows(int H);              // its rows
 cudaError_t launch_paged4_mma(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name);
 bool paged4_tc_supported(const PagedAttn& a, sdpa_dtype dt);
 size_t paged4_tc_workspace(int Hv);

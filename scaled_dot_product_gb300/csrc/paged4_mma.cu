@@ -54,10 +54,10 @@ constexpr float kNone = -1e30f;       // the maximum of a row that has admitted 
 template <int H, int NT, int WM>
 struct Cfg {
   // Product warps.  With the producer eight warps leave 128 registers a thread at two CTAs an SM, which
-  // eight rows take; five leave 168.
+  // eight rows take; five leave 168 for 16 rows.
   static constexpr int NW = NT == 1 ? 7 : 4;
   static constexpr int kProducts = NW * 32, kThreads = kProducts + 32;
-  static constexpr int WK = NW / WM, TN = NT == 1 ? 16 * NW : 128, TM = 8 * NT * WM, KW = TN / WK, G = H / kQ4Group;
+  static constexpr int WK = NW / WM, TN = NT == 1 ? 16 * NW : 128, KW = TN / WK, TM = 8 * NT * WM, G = H / kQ4Group;
   static constexpr int kRow = q4_row_bytes(H, 2);
   static constexpr int kTile = TN * kRow;
   static constexpr int kPitch = H + 4;                     // floats of a row of the joining buffer
@@ -626,11 +626,12 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
   asm volatile("bar.arrive 2, %0;" ::"n"(C::kThreads) : "memory");
 }
 
-// Rows per unit: the smallest of 8, 16, 32 and 64 that holds all rows of a sequence with max_new
-// tokens, at most 64.
+// Rows per unit: the smallest of 8, 16 and, of 64 channels, 32 that holds all rows of a sequence with max_new
+// tokens, at most the widest.  16 sequences of 2000 to 30000 keys, 8 key heads: 8 / 16 rows of 128 channels 89 / 166 us (340
+// bytes of spills at 16; two warps of eight rows each, without spills, 188), 8 / 16 / 32 rows of 64 75 / 88 / 142.
 int mma4_tm(const PagedAttn& a) {
   const int64_t rows = (int64_t)a.max_new * a.g.group;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : paged4_mma_rows(a.g.H);
 }
 
 uint64_t wait_limit_ns() {
@@ -666,16 +667,19 @@ cudaError_t launch_h(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t s
   switch (mma4_tm(a)) {
     case 8: return launch_wm<T, H, 1, 1>(a, dt, ws, st);
     case 16: return launch_wm<T, H, 2, 1>(a, dt, ws, st);
-    case 32: return launch_wm<T, H, 2, 2>(a, dt, ws, st);
-    default: return launch_wm<T, H, 2, 4>(a, dt, ws, st);
+    default: break;
   }
+  if constexpr (H == 64) return launch_wm<T, H, 2, 2>(a, dt, ws, st);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 bool paged4_mma_supported(int H, int Hv, sdpa_dtype dt) { return dt != SDPA_F32 && H == Hv && (H == 64 || H == 128); }
 
-size_t paged4_mma_workspace(int Hv) { return paged_ws_bytes(kPagedMaxSms * kCtasPerSm, 64, Hv); }
+size_t paged4_mma_workspace(int Hv) { return paged_ws_bytes(kPagedMaxSms * kCtasPerSm, 32, Hv); }
+
+int paged4_mma_rows(int H) { return H == 128 ? 16 : 32; }
 
 cudaError_t launch_paged4_mma(const PagedAttn& a, sdpa_dtype dt, void* ws, cudaStream_t st, const char** name) {
   const bool bf = dt == SDPA_BF16;
