@@ -57,12 +57,14 @@ struct Cfg {
   // eight rows take; five leave 168 for 16 rows.
   static constexpr int NW = NT == 1 ? 7 : 4;
   static constexpr int kProducts = NW * 32, kThreads = kProducts + 32;
-  static constexpr int WK = NW / WM, TN = NT == 1 ? 16 * NW : 128, KW = TN / WK, TM = 8 * NT * WM, G = H / kQ4Group;
+  // Keys of a tile: 32 a warp, 64 where records are half as long (with 16 a warp's waits and loops took 585 us
+  // where these take 535, and with 64 channels 469 where these take 299).
+  static constexpr int WK = NW / WM, TN = NT == 1 ? (H == 64 ? 64 : 32) * NW : 128, KW = TN / WK, TM = 8 * NT * WM, G = H / kQ4Group;
   static constexpr int kRow = q4_row_bytes(H, 2);
   static constexpr int kTile = TN * kRow;
   static constexpr int kPitch = H + 4;                     // floats of a row of the joining buffer
   static constexpr int kAcc = NW * 8 * NT * kPitch * 4;
-  static constexpr int kStages = H == 64 ? 8 : NT == 1 ? 4 : 3;
+  static constexpr int kStages = H == 64 ? (NT == 1 ? 2 : 8) : NT == 1 ? 2 : 3;
   static constexpr int kSmem = kStages * 2 * kTile + kAcc + 128;
   static_assert(KW % 16 == 0, "a warp takes whole blocks of 16 keys");
 };
@@ -83,6 +85,18 @@ __device__ __forceinline__ void mma_first(float* d, uint32_t a0, uint32_t a1, ui
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Minima times sums of queries: the first operand holds numbers of the cache's type.
+template <typename T>
+__device__ __forceinline__ void mma_minima(float* d, uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%4,%5}, {%6,%7}, {%8,%8,%8,%8};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%4,%5}, {%6,%7}, {%8,%8,%8,%8};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(b0), "r"(b1), "f"(0.f));
 }
 // 8 x 8 matrix of 16-bit values, a row in four lanes, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -298,7 +312,9 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
   // (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16.  For rows 2 j4 and + 1 of each eight: sums of each group and
   // the factor of the scores.
   uint32_t qf[NT][G][4];
-  float qs[NT][2][G], kf[NT][2];
+  // qm: the sum of group j4 of row r8 in three parts of the type (in fp16 times 2^-6), for the minima
+  uint32_t qm[NT][2];
+  float kf[NT][2];
   auto load_q = [&]() {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -336,13 +352,26 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         qf[n][x][3] = pack_f16x2(f[3] * 0.0625f, f[7] * 0.0625f);
         sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
         sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-        sum[x] *= pow2(-24);
+      }
+      {
+        float part = sum[0];
+#pragma unroll
+        for (int y = 1; y < G; ++y) part = j4 == y ? sum[y] : part;
+        part = j4 < G ? part * pow2(std::is_same<T, __half>::value ? -6 : -24) : 0.f;
+        const float hi = Elem<T>::to_f32(Elem<T>::from_f32(part));
+        const float mid = Elem<T>::to_f32(Elem<T>::from_f32(part - hi));
+        const float lo = part - hi - mid;
+        if constexpr (std::is_same<T, __half>::value) {
+          qm[n][0] = pack_f16x2(hi, mid);
+          qm[n][1] = pack_f16x2(lo, 0.f);
+        } else {
+          qm[n][0] = pack_bf16x2(hi, mid);
+          qm[n][1] = pack_bf16x2(lo, 0.f);
+        }
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int from = (2 * j4 + x) * 4;
-#pragma unroll
-        for (int y = 0; y < G; ++y) qs[n][x][y] = __shfl_sync(0xffffffffu, sum[y], from);
         const int sf = __shfl_sync(0xffffffffu, shift, from);
         // 24 - sf lies in -76 .. 127
         kf[n][x] = (a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e) * pow2(24) * pow2(-sf);
@@ -388,7 +417,7 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
     const unsigned char* tile_k = smem + st * 2 * C::kTile;
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(b_full(st), phase, abortp, args.wait_ns));
     const int tile_key = (w.r.tile0 + w.tile + t) * kTN;
-#pragma unroll 1
+#pragma unroll(NT == 1 ? 4 : 2)
     for (int kb = 0; kb < KW / 16; ++kb) {
       const int blk = wk * KW + kb * 16, key0 = tile_key + blk;
       const unsigned char* kp = tile_k + blk * kRow;
@@ -400,25 +429,30 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         uint32_t sd[2][G];
         load_sides<G>(kp + soff, sd[0]);
         load_sides<G>(kp + soff + 8 * kRow, sd[1]);
+        const unsigned char* own = kp + soff + 4 * (j4 & (G - 1));
+        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(own), w1 = *reinterpret_cast<const uint32_t*>(own + 8 * kRow);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+          mma_minima<T>(s[n], __byte_perm(w0, w0, 0x1010), __byte_perm(w1, w1, 0x1010), qm[n][0], qm[n][1]);
+          if (kCentre) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[n][e] *= pow2(-18);
+          }
+        }
 #pragma unroll
         for (int y = 0; y < G; ++y) {
           const uint32_t k0 = *reinterpret_cast<const uint32_t*>(kp + koff + 16 * y);
           const uint32_t k1 = *reinterpret_cast<const uint32_t*>(kp + koff + 8 * kRow + 16 * y);
           const float c0 = high_half<T>(sd[0][y]), c1 = high_half<T>(sd[1][y]);
-          const float m0 = low_half<T>(sd[0][y]), m1 = low_half<T>(sd[1][y]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float d[4];
             mma_first(d, k0 & kLow, k1 & kLow, k0 & kHigh, k1 & kHigh, qf[n][y][0], qf[n][y][1]);
             mma(d, (k0 >> 8) & kLow, (k1 >> 8) & kLow, (k0 >> 8) & kHigh, (k1 >> 8) & kHigh, qf[n][y][2], qf[n][y][3]);
-            s[n][0] = fmaf(c0, d[0], fmaf(m0, qs[n][0][y], s[n][0]));
-            s[n][1] = fmaf(c0, d[1], fmaf(m0, qs[n][1][y], s[n][1]));
-            s[n][2] = fmaf(c1, d[2], fmaf(m1, qs[n][0][y], s[n][2]));
-            s[n][3] = fmaf(c1, d[3], fmaf(m1, qs[n][1][y], s[n][3]));
+            s[n][0] = fmaf(c0, d[0], s[n][0]);
+            s[n][1] = fmaf(c0, d[1], s[n][1]);
+            s[n][2] = fmaf(c1, d[2], s[n][2]);
+            s[n][3] = fmaf(c1, d[3], s[n][3]);
           }
         }
       }
@@ -452,10 +486,14 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         }
       }
       // ---- running maximum and size of the scales
-      uint32_t most = 0;
+      // (a lane looks at one group of its two keys, the four lanes of a key at all of them)
+      const unsigned char* own = vp + soff + 4 * (j4 & (G - 1));
+      const uint32_t most = max(*reinterpret_cast<const uint32_t*>(own), *reinterpret_cast<const uint32_t*>(own + 8 * kRow));
+      bool need = (most >> 16) > s_most && !edge;
+      if (edge) {
 #pragma unroll
-      for (int y = 0; y < G; ++y) most = max(most, max(vd[0][y], vd[1][y]));
-      bool need = (most >> 16) > s_most;
+        for (int y = 0; y < G; ++y) need = need || (max(vd[0][y], vd[1][y]) >> 16) > s_most;
+      }
       const float room = kRescale - (float)L;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
