@@ -445,11 +445,15 @@ typedef struct {
 SDPA_API int sdpa_paged4_append(const sdpa_paged4_append_params* p, sdpa_view k, sdpa_view v, sdpa_view k_held,
                                 sdpa_view v_held, sdpa_stream_t stream);
 
-/* sdpa_paged_attn over pools of records: k_pages and v_pages of p are those (strides in bytes), H and
- * Hv multiples of 32, everything else as there, the rotary fields unused.  The products take the codes as they are; with H = Hv in {64,
- * 128} and a 16-bit type the weights enter the value product rounded to 16 bits.  workspace:
- * sdpa_paged4_workspace_size(p) bytes, any contents, 256-byte aligned; the size depends on dtype, H and Hv
- * alone. */
+/* sdpa_paged_attn over pools of records: k_pages and v_pages of p are those (strides in bytes), H and Hv
+ * multiples of 32, the rotary fields unused, everything else as there.  Sums are fp32.  With H = Hv in {64, 128} and a
+ * 16-bit type, for at most 16 rows of a sequence (H = 64: 32; max_new x query heads of a key head) the codes
+ * enter the products as they are, and a weight times its key's scale rounded to fp16 (half a step each; of a
+ * value's distance from the middle of its range in fp16, from its minimum in bf16); for more rows the weights, keys
+ * and values enter rounded to dtype.  Queries beyond 2^110, and values that grow by more than 2^80 along a
+ * sequence, may come out as infinities or NaN; an infinity in a query counts as NaN.
+ * workspace: sdpa_paged4_workspace_size(p) bytes, any contents, 256-byte aligned; the size depends on dtype, H
+ * and Hv alone. */
 SDPA_API int sdpa_paged4_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace, size_t workspace_bytes,
                               sdpa_stream_t stream);
 SDPA_API size_t sdpa_paged4_workspace_size(const sdpa_paged_params* p);

@@ -8,7 +8,10 @@
 // is not, takes a scale and a minimum that are no numbers: it reads as NaN.
 //
 // Every element is read once and written once at 5/8 byte (and once more, as the cache holds it,
-// where the caller wants that).  A thread has 8 channels, four lanes a group.  The slot and the position of a token are one load each.
+// where the caller wants that).  A thread has 8 channels, four lanes a group.  The slot and the position of a token are one load each: they
+// are made once a step and serve every layer.  Bound by instructions (50 a value and lane group): two prompts of
+// 2048 tokens, 8 bfloat16 heads of 128, rows as held wanted, 18.8 us (2.1 TB/s; 15.6 without rotation, float32 19.5),
+// 12,000 ragged tokens of float16 heads of 64 24.5 us, 64 single tokens 2.8 us.
 #include <algorithm>
 #include <type_traits>
 

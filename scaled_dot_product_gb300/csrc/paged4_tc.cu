@@ -20,7 +20,9 @@
 // cache in the type).  Weights are rounded to the type too; their sum takes them unrounded.  Records of
 // keys that no row of the unit admits become zeros, since 0 x NaN is not 0.  The softmax takes 64 columns
 // of its scores at a time, which fits the registers that 16 warps leave: a running maximum is passed by at most 2^8,
-// and where it has to move, the weights and products made with it are rescaled by a power of two.  Every wait is bounded: on expiry the kernel raises an abort flag, lets its own copies and
+// and where it has to move, the weights and products made with it are rescaled by a power of two.  A chunk of 2048 tokens over 32000 keys,
+// 32/8 heads of 128: 868 us, 1224 TFLOP/s (64 % of the measured rate); of 64: 742 us; softmax and record warps wait for one
+// another's issue slots (without the codes' arithmetic 697).  Every wait is bounded: on expiry the kernel raises an abort flag, lets its own copies and
 // products finish, frees its tensor memory and records SDPA_ERR_TIMEOUT.
 #include <algorithm>
 #include <cstdlib>

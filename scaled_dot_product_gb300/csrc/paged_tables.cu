@@ -10,7 +10,7 @@
 // the order of sequences, whatever the number of threads: results do not vary.  The cluster's barrier
 // orders the entries given back before those taken, and the inputs' reads before the outputs that may
 // be the inputs themselves.  Bound by latency (a chain of lengths, scans, barrier, list or table,
-// slot).
+// slot): 64 sequences of a token 8.6 us, 2000 sequences with 17,000 tokens 16.4, 48 prompts of 190,000 tokens 7.7.
 #include <algorithm>
 
 #include "paged4.h"
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(NT) paged_tables_kernel(const PagedTables a) {
 }
 
 // Positions and slots of many tokens, from the offsets, lengths and table entries of the first kernel: a
-// cluster's threads would take them in many turns (190,000 tokens 26.6 us, 13.9 this way).
+// cluster's threads would take them in many turns (190,000 tokens 26.6 us, 7.7 this way).
 constexpr int kSlotThreads = 256, kSlotTokens = 4;      // per thread
 __global__ void __launch_bounds__(kSlotThreads) paged_slots_kernel(const PagedTables a) {
   pdl_wait();

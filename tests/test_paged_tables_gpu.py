@@ -152,6 +152,34 @@ def test_calls_in_turn_in_a_graph():
     assert sdpa.sdpa_query_status() == 0
 
 
+def test_many_tokens_captured():
+    """A step of more tokens than one cluster takes (two kernels), captured and replayed in place."""
+    p = problem([5, 0, 77] * 20, [900, 700, 800] * 20, 16, spare=9000, width_extra=60)
+    table, past, new, free, count = ints(p["table"]), ints(p["past"]), ints(p["new"]), ints(p["free"]), ints([p["count"]])
+    T = p["tokens"]
+    assert T > 45000
+    out = dict(cu_new=ints([0] * 61), positions=ints([0] * T, torch.int64), slots=ints([0] * T, torch.int64))
+    step = lambda: sdpa.sdpa_paged_tables(table, past, new, free, count, page_size=16, tokens=T, kv_lens=past, free_count_out=count, **out)
+    start = [t.clone() for t in (table, past, free, count)]
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for t, s in zip((table, past, free, count), start):
+        t.copy_(s)
+    for k in range(2):
+        want, _ = tables_of(table.tolist(), past.tolist(), new.tolist(), free.tolist(), count.item(), 16, T)
+        graph.replay()
+        got = dict(kv_lens=past, free_count_out=count, page_table=table, free_pages=free, **out)
+        assert {n: t.tolist() for n, t in got.items()} == want
+        new.copy_(ints([-1, 300, 1] * 20))
+    assert sdpa.sdpa_query_status() == 0
+    check(problem([10, 40000, 16], [1, 60000, 20], 16, spare=30))          # pages run out in the second kernel's tokens
+    p = problem([20, 5], [3, 50000], 16)
+    p["table"][1][0] = -1
+    check(p)                                                               # a begun page that is none
+
+
 def test_another_stream():
     p = problem([20, 5, 33], [3, 100, -1], 16)
     s = torch.cuda.Stream()
