@@ -41,6 +41,13 @@ __device__ __forceinline__ int fast_div(int x, uint32_t mul, uint32_t shift) {
   return (int)(((uint64_t)(uint32_t)x * mul) >> shift);
 }
 
+// A row's place: strides below 2^31, as nearly all are, take one multiplication each.
+template <bool kWide>
+__device__ __forceinline__ int64_t place(const View& v, int head, int at) {
+  if constexpr (kWide) return v.off(0, head, at);
+  else return (int64_t)head * (int)v.sh + (int64_t)at * (int)v.ss;
+}
+
 constexpr int kCh = 8;           // channels of a thread, four threads a group (with 16, two prompts of 2048 took 22.5 us against 19.3)
 
 template <typename T>
@@ -60,6 +67,14 @@ __device__ __forceinline__ float step_down(float x) {
     return Elem<T>::to_f32(v);
   }
 }
+template <typename T>
+__device__ __forceinline__ auto pair_of(float a, float b) {
+  if constexpr (std::is_same<T, __half>::value) return __floats2half2_rn(a, b);
+  else return __floats2bfloat162_rn(a, b);
+}
+// Scales from here on are as exact as the type's normal numbers.
+template <typename T>
+__device__ __forceinline__ float least_scale() { return std::is_same<T, __half>::value ? 0x1p-14f : 1e-30f; }
 template <typename T>
 __device__ __forceinline__ float largest() {
   if constexpr (std::is_same<T, __half>::value) return 65504.f;
@@ -113,7 +128,7 @@ __device__ __forceinline__ void turn(const Paged4Append& a, const T* row, int c0
   }
 }
 
-template <typename T, bool kInter>
+template <typename T, bool kInter, bool kWide>
 __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4Append a, const int tpb) {
   const int ku = a.Nkv * (a.H / kCh), per_tok = ku + a.Nkv * (a.Hv / kCh);
   const int x0 = (int)blockIdx.y * kThreads + (int)threadIdx.x;
@@ -131,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
   int64_t slot = -1;
   if (live) {
     const View& src = isk ? a.k : a.v;
-    const T* row = reinterpret_cast<const T*>(src.p) + src.off(0, head, t);
+    const T* row = reinterpret_cast<const T*>(src.p) + place<kWide>(src, head, t);
     slot = a.slots[t];
     const bool turned = isk && c0 < a.R;
     int64_t pos = turned ? a.positions[t] : 0;
@@ -143,11 +158,28 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
       turn<T, kInter>(a, row, c0, pos * (a.R / 2), x);
     }
   }
-  float lo = x[0], hi = x[0];
+  float lo, hi;
+  if constexpr (sizeof(T) == 2) {
+    // the values are numbers of the type: two at a time
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    T2 v[kCh / 2], l, h;
 #pragma unroll
-  for (int e = 1; e < kCh; ++e) {
-    lo = min_nan(lo, x[e]);
-    hi = max_nan(hi, x[e]);
+    for (int e = 0; e < kCh / 2; ++e) v[e] = pair_of<T>(x[2 * e], x[2 * e + 1]);
+    l = h = v[0];
+#pragma unroll
+    for (int e = 1; e < kCh / 2; ++e) {
+      l = __hmin2_nan(l, v[e]);
+      h = __hmax2_nan(h, v[e]);
+    }
+    lo = min_nan(Elem<T>::to_f32(l.x), Elem<T>::to_f32(l.y));
+    hi = max_nan(Elem<T>::to_f32(h.x), Elem<T>::to_f32(h.y));
+  } else {
+    lo = hi = x[0];
+#pragma unroll
+    for (int e = 1; e < kCh; ++e) {
+      lo = min_nan(lo, x[e]);
+      hi = max_nan(hi, x[e]);
+    }
   }
 #pragma unroll
   for (int o = 1; o < kQ4Group / kCh; o <<= 1) {
@@ -164,40 +196,38 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
   // a scale rounded up at the end of the type's range: code 15 would have no value
   if (fmaf(15.f, s, lo) > largest<T>()) s = step_down<T>(s);
   if (!(spread < INFINITY)) s = lo = __int_as_float(0x7fffffff);
-  // An integer q is the code where (q - 1/2) s < x - lo < (q + 1/2) s.  The quotient by the reciprocal finds the
-  // nearest half-integer h, and the sign of (x - lo) - h s, which a fused multiply-add has right, the side; zero is a
-  // tie, and the even neighbour.  A remainder that is neither zero nor clear of the quotient's own rounding leaves it
-  // to the division, as do scales whose reciprocal is no ordinary number.
-  const bool ordinary = s > 1e-30f && s < 1e30f;
-  const float inv = ordinary ? __frcp_rn(s) : 0.f;
+  // The quotient by the reciprocal is off by 2^-22 of itself at most, and its integer is the code unless the
+  // remainder is half a scale but for that much.  There the remainder, which is exact, decides: more than half a scale is the
+  // next code's, half a scale the even one's.  A remainder within 2^-18 of a half but no half leaves it to the
+  // division's rounding; so do scales that are no ordinary numbers of the type (whose quotients may pass 15).
   constexpr float kInt = 12582912.f;         // 1.5 2^23: a sum with it is rounded to an integer, the even one at a tie
-  const float clear = s * 0x1p-18f;
+  const bool ordinary = s >= least_scale<T>() && s < 1e30f;
+  const float inv = ordinary ? __frcp_rn(s) : 0.f, near = ordinary ? 0.4999f * s : -1.f;
   float code[kCh];
-  bool divide = !ordinary;
-#pragma unroll
-  for (int e = 0; e < kCh; ++e) {
-    const float d = x[e] - lo;
-    const float low = (fmaf(d, inv, -0.5f) + kInt) - kInt;         // h - 1/2
-    const float rest = fmaf(-(low + 0.5f), s, d);
-    // a tie goes to the even one of low and low + 1: (low + 1/2) rounded so
-    const float up = rest > 0.f ? low + 1.f : low;
-    code[e] = rest == 0.f ? ((low + 0.5f) + kInt) - kInt : up;
-    divide = divide || (rest != 0.f && fabsf(rest) < clear);
-  }
-  if (divide) {
-#pragma unroll
-    for (int e = 0; e < kCh; ++e) code[e] = s > 0.f ? (__fdiv_rn(x[e] - lo, s) + kInt) - kInt : 0.f;
-  }
   uint32_t word = 0;
 #pragma unroll
   for (int e = 0; e < kCh; ++e) {
-    code[e] = fminf(code[e], 15.f);
-    word |= (__float_as_uint(code[e] + kInt) & 15u) << (4 * e);
+    const float d = x[e] - lo;
+    float i = fmaf(d, inv, kInt);
+    code[e] = i - kInt;
+    const float r = fmaf(-code[e], s, d);
+    if (!(fabsf(r) < near)) {
+      const float over = fabsf(r) - 0.5f * s;
+      if (ordinary && (over == 0.f || fabsf(over) > 0x1p-18f * s)) {
+        if (over > 0.f || (over == 0.f && (__float_as_uint(i) & 1u))) i += r > 0.f ? 1.f : -1.f;
+      } else {
+        i = (s > 0.f ? fminf(__fdiv_rn(d, s), 15.f) : 0.f) + kInt;      // 0: a constant group, or one that is not a number
+      }
+      code[e] = i - kInt;
+    }
+    // the integer is in i's last bits: those above belong to 1.5 2^23
+    word += __float_as_uint(i) << (4 * e);
   }
+  word -= 0x4b400000u * 0x11111111u;
   const uint64_t page = slot < (1ll << 31) ? (uint64_t)fast_div((int)slot, a.page_mul, a.page_shift) : (uint64_t)slot / (uint32_t)a.page_size;
   const int at = (int)(slot - (int64_t)page * a.page_size);
   const View& dst = isk ? a.kp : a.vp;
-  unsigned char* rec = reinterpret_cast<unsigned char*>(const_cast<void*>(dst.p)) + dst.off((int64_t)page, head, at);
+  unsigned char* rec = reinterpret_cast<unsigned char*>(const_cast<void*>(dst.p)) + (int64_t)page * dst.sb + place<kWide>(dst, head, at);
   if (SDPA_IN_BOUNDS((int64_t)page < a.num_pages && at >= 0 && at < a.page_size, 572)) {
     *reinterpret_cast<uint32_t*>(rec + c0 / 2) = word;
     if (c0 % kQ4Group == 0) {
@@ -216,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
     T out[kCh];
 #pragma unroll
     for (int e = 0; e < kCh; ++e) out[e] = Elem<T>::from_f32(__fadd_rn(__fmul_rn(code[e], s), lo));
-    uint4* h = reinterpret_cast<uint4*>(reinterpret_cast<T*>(const_cast<void*>(held.p)) + held.off(0, head, t) + c0);
+    uint4* h = reinterpret_cast<uint4*>(reinterpret_cast<T*>(const_cast<void*>(held.p)) + place<kWide>(held, head, t) + c0);
 #pragma unroll
     for (int i = 0; i < kCh / Elem<T>::kVec; ++i) h[i] = reinterpret_cast<const uint4*>(out)[i];
   }
@@ -231,8 +261,12 @@ cudaError_t launch_t(Paged4Append a, cudaStream_t st) {
   paged_magic(a.H / kCh, &a.k_mul, &a.k_shift);
   paged_magic(a.Hv / kCh, &a.v_mul, &a.v_shift);
   paged_magic(a.page_size, &a.page_mul, &a.page_shift);
-  if (a.R && a.interleaved) paged4_append_kernel<T, true><<<grid, kThreads, 0, st>>>(a, tpb);
-  else paged4_append_kernel<T, false><<<grid, kThreads, 0, st>>>(a, tpb);
+  bool wide = false;
+  for (const View* v : {&a.k, &a.v, &a.k_held, &a.v_held, &a.kp, &a.vp}) wide = wide || v->sh >= (1ll << 31) || v->ss >= (1ll << 31);
+  const bool inter = a.R && a.interleaved;
+  auto* kernel = wide ? (inter ? paged4_append_kernel<T, true, true> : paged4_append_kernel<T, false, true>)
+                      : (inter ? paged4_append_kernel<T, true, false> : paged4_append_kernel<T, false, false>);
+  kernel<<<grid, kThreads, 0, st>>>(a, tpb);
   count_launch(1);
   return cudaGetLastError();
 }

@@ -276,6 +276,24 @@ def test_pools_beyond_32_bits():
         del kp, vp
 
 
+def test_rows_far_apart():
+    """Token strides of 2^31 elements and more."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GiB")
+    base = torch.empty((1 << 31) + 8192, dtype=HF, device="cuda")
+    k = base.as_strided((2, 2, 64), (1 << 31, 64, 1))
+    held = base.as_strided((2, 2, 64), (1 << 31, 64, 1), 1024)
+    x = torch.randn(2, 2, 64, generator=torch.Generator().manual_seed(1)).to(HF)
+    k.copy_(x)
+    kp = torch.zeros(1, 2, 4, row_bytes(64, HF), dtype=torch.uint8, device="cuda")
+    vp = torch.zeros_like(kp)
+    with pytest.raises(sdpa.SdpaError):            # ranges that interleave: refused, whatever their elements
+        sdpa.sdpa_paged4_append(k, k, kp, vp, torch.tensor([1, 3], device="cuda"), v_held=held)
+    sdpa.sdpa_paged4_append(k, k, kp, vp, torch.tensor([1, 3], device="cuda"))
+    assert sdpa.sdpa_query_status() == 0 and torch.equal(kp, vp)
+    assert torch.equal(kp[0, :, [1, 3]].cpu().transpose(0, 1), pack(x, HF))
+
+
 def test_slots_beyond_31_bits():
     """More than 2^31 slots in a pool."""
     if torch.cuda.mem_get_info()[0] < 100 << 30:
