@@ -370,8 +370,8 @@ SDPA_API int sdpa_paged_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view 
 SDPA_API size_t sdpa_paged_workspace_size(const sdpa_paged_params* p);
 
 /* The tables of a step over a paged cache, made on the device: from past_lens (keys of each sequence
- * before the step) and new_lens (its new tokens; negative: the sequence has ended) the call gives back the pages of ended
- * sequences, takes pages for the grown ones, and writes
+ * before the step) and new_lens (its new tokens; negative: the sequence has ended) the call gives
+ * back the pages of ended sequences, takes pages for the grown ones, and writes
  *   page_table[b]    entries ceil(past / page_size) .. ceil(T / page_size) - 1, T = past + new; others stay
  *   kv_lens[b]       T (0 where the sequence has ended)
  *   cu_new           running sum of the new tokens, B + 1 entries: first packed row of each sequence
@@ -433,15 +433,16 @@ typedef struct {
 } sdpa_paged4_append_params;
 
 /* Writes the records of the new keys k (packed, (tokens, Nkv, H)), turned by the angle of their
- * positions and rounded to dtype, and values v (packed, (tokens, Nkv, Hv)) into their slots.  Per 32 channels, in
- * fp32: scale = (max - min) / 15 rounded to dtype (down where min + 15 * scale would leave its range), code = (x - min) / scale rounded to the nearest integer,
- * ties to even, and at most 15 (0 where the scale is 0).  A group whose spread is not finite (with a value
- * that is not, or wider than fp32) takes NaN for both and reads as NaN.  The slots of different tokens must
- * differ; every other slot keeps its contents.  A slot behind the pool is skipped and reported by
+ * positions and rounded to dtype, and values v (packed, (tokens, Nkv, Hv)) into their slots. Per 32
+ * channels, in fp32: scale = (max - min) / 15 rounded to dtype (down where min + 15 * scale would
+ * leave its range), code = (x - min) / scale rounded to the nearest integer, ties to even, and at
+ * most 15 (0 where the scale is 0). A group whose spread is not finite (with a value that is not,
+ * or wider than fp32) takes NaN for both and reads as NaN. The slots of different tokens must
+ * differ; every other slot keeps its contents. A slot behind the pool is skipped and reported by
  * sdpa_query_status (SDPA_ERR_INVALID), a position outside the rotary cache reported and clamped.
- * k_held, v_held (packed as k and v, or data NULL): the rows as the cache holds them, minimum + scale *
- * code rounded to dtype, for calls that attend to the new tokens from their rows; rows without a
- * slot are left as they were.  Alignment of rows as for sdpa_paged_append. */
+ * k_held, v_held (packed as k and v, or data NULL): the rows as the cache holds them, minimum +
+ * scale * code rounded to dtype, for calls that attend to the new tokens from their rows; rows
+ * without a slot are left as they were. Alignment of rows as for sdpa_paged_append. */
 SDPA_API int sdpa_paged4_append(const sdpa_paged4_append_params* p, sdpa_view k, sdpa_view v, sdpa_view k_held,
                                 sdpa_view v_held, sdpa_stream_t stream);
 

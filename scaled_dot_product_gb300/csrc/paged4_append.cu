@@ -7,11 +7,11 @@
 // record a function of the input alone.  A group with a value that is not finite, or whose spread
 // is not, takes a scale and a minimum that are no numbers: it reads as NaN.
 //
-// Every element is read once and written once at 5/8 byte (and once more, as the cache holds it,
-// where the caller wants that).  A thread has 8 channels, four lanes a group.  The slot and the position of a token are one load each: they
-// are made once a step and serve every layer.  Bound by instructions (50 a value and lane group): two prompts of
-// 2048 tokens, 8 bfloat16 heads of 128, rows as held wanted, 18.8 us (2.1 TB/s; 15.6 without rotation, float32 19.5),
-// 12,000 ragged tokens of float16 heads of 64 24.5 us, 64 single tokens 2.8 us.
+// Every element is read once and written once at 5/8 byte (and once more, as the cache holds it, where the
+// caller wants that). A thread has 8 channels, four lanes a group. The slot and the position of a token are one
+// load each: they are made once a step and serve every layer. Bound by instructions (400 a warp of 256 values):
+// two prompts of 2048 tokens, 8 bfloat16 heads of 128, rows as held wanted, 17.1 us (2.3 TB/s; 14.4 without
+// rotation, float32 17.8), 12,000 ragged tokens of float16 heads of 64 21.6 us, 64 single tokens 2.8 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -48,7 +48,8 @@ __device__ __forceinline__ int64_t place(const View& v, int head, int at) {
   else return (int64_t)head * (int)v.sh + (int64_t)at * (int)v.ss;
 }
 
-constexpr int kCh = 8;           // channels of a thread, four threads a group (with 16, two prompts of 2048 took 22.5 us against 19.3)
+// Channels of a thread, four threads a group (with 16, two prompts of 2048 took 22.5 us against 19.3).
+constexpr int kCh = 8;
 
 template <typename T>
 __device__ __forceinline__ void load_ch(const T* p, float* f) {

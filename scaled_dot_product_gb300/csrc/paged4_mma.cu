@@ -22,14 +22,14 @@
 // A unit's rows are dealt to WM warps (8 NT each), the keys of a tile to WK; each warp keeps its own m, L, sum and
 // accumulator, joined through shared memory at the end of a unit.
 //
-// One producer warp keeps a ring of tiles of keys full across unit boundaries.  A page's records of a head lie
-// one after another, so whatever part of a page falls into a tile is one bulk copy.  Rows of 80 (40)
-// bytes put the words that a warp reads at a time into different banks.  About 400 instructions a block of 16 keys of
-// 128 channels, half of them on the half-rate integer pipe, bound it: 128 single tokens, 1000 to 32000 keys, 64/8 heads
-// of 128: 530 us, 4.9 TB/s of records (floor 383); fp16 573; 64 channels 295 (floor 191); four short sequences 11.0 us.  Keys that no row of the unit
-// admits take a scale and a minimum of zero, since 0 x NaN is not 0.  Every wait is bounded: on expiry the
-// kernel raises an abort flag, goes through its loops without waiting, lets its own copies finish
-// and records SDPA_ERR_TIMEOUT.
+// One producer warp keeps a ring of tiles of keys full across unit boundaries. A page's records of a head lie
+// one after another, so whatever part of a page falls into a tile is one bulk copy. Rows of 80 (40) bytes put
+// the words that a warp reads at a time into different banks. About 400 instructions a block of 16 keys of 128
+// channels, half of them on the half-rate integer pipe, bound it: 128 single tokens, 1000 to 32000 keys, 64/8
+// heads of 128: 530 us, 4.9 TB/s of records (floor 383); fp16 573; 64 channels 295 (floor 191); four short
+// sequences 11.0 us. Keys that no row of the unit admits take a scale and a minimum of zero, since 0 x NaN is
+// not 0. Every wait is bounded: on expiry the kernel raises an abort flag, goes through its loops without
+// waiting, lets its own copies finish and records SDPA_ERR_TIMEOUT.
 #include <algorithm>
 #include <cstdlib>
 #include <type_traits>

@@ -14,16 +14,17 @@
 //   warps 12-15   keys and values: a thread has one record of each tile, loads it a tile ahead and writes
 //                 its values, rounded to the type, into the ring in the operands' layout
 //
-// Every unit makes its operands anew from the codes, which 256 rows share.  A code becomes the last bits of
-// 1024 (fp16) or 128 (bf16), less that number, times the scale, plus the minimum: exact up to the one
-// rounding to the type, as the tensor cores' operands are 16-bit (half a step, like the keys and values of a
-// cache in the type).  Weights are rounded to the type too; their sum takes them unrounded.  Records of
-// keys that no row of the unit admits become zeros, since 0 x NaN is not 0.  The softmax takes 64 columns
-// of its scores at a time, which fits the registers that 16 warps leave: a running maximum is passed by at most 2^8,
-// and where it has to move, the weights and products made with it are rescaled by a power of two.  A chunk of 2048 tokens over 32000 keys,
-// 32/8 heads of 128: 868 us, 1224 TFLOP/s (64 % of the measured rate); of 64: 742 us; softmax and record warps wait for one
-// another's issue slots (without the codes' arithmetic 697).  Every wait is bounded: on expiry the kernel raises an abort flag, lets its own copies and
-// products finish, frees its tensor memory and records SDPA_ERR_TIMEOUT.
+// Every unit makes its operands anew from the codes, which 256 rows share. A code becomes the last bits of 1024
+// (fp16) or 128 (bf16), less that number, times the scale, plus the minimum: exact up to the one rounding to
+// the type, as the tensor cores' operands are 16-bit (half a step, like the keys and values of a cache in the
+// type). Weights are rounded to the type too; their sum takes them unrounded. Records of keys that no row of
+// the unit admits become zeros, since 0 x NaN is not 0. The softmax takes 64 columns of its scores at a time,
+// which fits the registers that 16 warps leave: a running maximum is passed by at most 2^8, and where it has to
+// move, the weights and products made with it are rescaled by a power of two. A chunk of 2048 tokens over 32000
+// keys, 32/8 heads of 128: 868 us, 1224 TFLOP/s (64 % of the measured rate); of 64: 742 us; softmax and record
+// warps wait for one another's issue slots (without the softmax 697). Every wait is bounded: on expiry the
+// kernel raises an abort flag, lets its own copies and products finish, frees its tensor memory and records
+// SDPA_ERR_TIMEOUT.
 #include <algorithm>
 #include <cstdlib>
 #include <type_traits>

@@ -1,4 +1,5 @@
-// How the attention over a paged cache is cut up, shared by its three kernels.
+// How the attention over a paged cache is cut up, shared by its three kernels and by the three over
+// records of 4 bits a value.
 //
 // A unit is TM consecutive packed rows (row r = token * group + head of the group) of one
 // (sequence, kv head); its cost is the number of TN-key tiles that some of its rows admits (at
