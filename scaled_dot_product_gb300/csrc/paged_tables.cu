@@ -10,7 +10,7 @@
 // the order of sequences, whatever the number of threads: results do not vary.  The cluster's barrier
 // orders the entries given back before those taken, and the inputs' reads before the outputs that may
 // be the inputs themselves.  Bound by latency (a chain of lengths, scans, barrier, list or table,
-// slot): 64 sequences of a token 8.6 us, 2000 sequences with 17,000 tokens 16.4, 48 prompts of 190,000 tokens 7.7.
+// slot): 64 sequences of a token, four ended, 7.6 us, 2000 sequences with 17,000 tokens 16.4, 48 prompts of 190,000 tokens 7.7.
 #include <algorithm>
 
 #include "paged4.h"
@@ -48,6 +48,44 @@ __device__ __forceinline__ int last_not_above(const int* at, int n, int x) {
 }
 
 constexpr int kAhead = 4;        // loads of a lane in flight
+
+// Ids of a row's first h entries that are in range, counted by the warp; 32 U of them are on their way together.
+template <int U>
+__device__ __forceinline__ int count_ids(const int32_t* row, int h, int num_pages, int lane) {
+  int c = 0;
+#pragma unroll 1
+  for (int j0 = 0; j0 < h; j0 += 32 * U) {
+    int id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = j0 + u * 32 + lane < h ? row[j0 + u * 32 + lane] : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) c += (unsigned)id[u] < (unsigned)num_pages;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+  return c;
+}
+// The same ids onto the list, in order, from entry `at` on.
+template <int U>
+__device__ __forceinline__ void give_back(const int32_t* row, int h, int32_t* list, int64_t at, int num_pages, int lane) {
+#pragma unroll 1
+  for (int j0 = 0; j0 < h; j0 += 32 * U) {
+    int id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = j0 + u * 32 + lane < h ? row[j0 + u * 32 + lane] : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool ok = (unsigned)id[u] < (unsigned)num_pages;
+      const unsigned m = __ballot_sync(0xffffffffu, ok);
+      const int64_t to = at + __popc(m & ((1u << lane) - 1));
+      if (ok && to < num_pages) list[to] = id[u];
+      at += __popc(m);
+    }
+  }
+}
+// Rows of more entries than this take 16 loads a lane at a time (four ended sequences of up to 2000 pages: 7.6 us
+// against 8.6), shorter ones four (200 of 63 pages: 16.4 against 20.0).
+constexpr int kLongRow = 256;
 constexpr int kClusterTokens = 40000;      // most tokens that one cluster takes
 
 // kRows: positions and slots too; else paged_slots_kernel writes them.
@@ -112,17 +150,7 @@ __global__ void __launch_bounds__(NT) paged_tables_kernel(const PagedTables a) {
       who &= who - 1;
       const int32_t* row = a.table + (int64_t)(base + warp * 32 + src) * a.table_stride;
       const int h = __shfl_sync(0xffffffffu, have, src);
-      int c = 0;
-#pragma unroll 1
-      for (int j0 = 0; j0 < h; j0 += 32 * kAhead) {
-        int id[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) id[u] = j0 + u * 32 + lane < h ? row[j0 + u * 32 + lane] : -1;
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) c += (unsigned)id[u] < (unsigned)a.num_pages;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      const int c = h > kLongRow ? count_ids<16>(row, h, a.num_pages, lane) : count_ids<kAhead>(row, h, a.num_pages, lane);
       if (lane == src) {
         g = c;
         if (c != h) bad |= kPagedBadPage;
@@ -163,21 +191,9 @@ __global__ void __launch_bounds__(NT) paged_tables_kernel(const PagedTables a) {
       if (past[b] >= 0) continue;
       const int h = pages_of(-1 - past[b]);
       const int32_t* row = a.table + (int64_t)b * a.table_stride;
-      int64_t at = (int64_t)c0 + given[b];
-#pragma unroll 1
-      for (int j0 = 0; j0 < h; j0 += 32 * kAhead) {
-        int id[kAhead];
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) id[u] = j0 + u * 32 + lane < h ? row[j0 + u * 32 + lane] : -1;
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const bool ok = (unsigned)id[u] < (unsigned)a.num_pages;
-          const unsigned m = __ballot_sync(0xffffffffu, ok);
-          const int64_t to = at + __popc(m & ((1u << lane) - 1));
-          if (ok && to < a.num_pages) a.free_pages[to] = id[u];
-          at += __popc(m);
-        }
-      }
+      const int64_t at = (int64_t)c0 + given[b];
+      if (h > kLongRow) give_back<16>(row, h, a.free_pages, at, a.num_pages, lane);
+      else give_back<kAhead>(row, h, a.free_pages, at, a.num_pages, lane);
     }
   }
   cluster_sync();
