@@ -10,7 +10,7 @@
 // the order of sequences, whatever the number of threads: results do not vary.  The cluster's barrier
 // orders the entries given back before those taken, and the inputs' reads before the outputs that may
 // be the inputs themselves.  Bound by latency (a chain of lengths, scans, barrier, list or table,
-// slot): 64 sequences of a token, four ended, 7.6 us, 2000 sequences with 17,000 tokens 16.4, 48 prompts of 190,000 tokens 7.7.
+// slot): 64 sequences of a token, one ended, 7.6 us, 2000 sequences with 15,000 tokens 16.4, 48 prompts of 184,000 tokens 7.7.
 #include <algorithm>
 
 #include "paged4.h"
@@ -83,8 +83,8 @@ __device__ __forceinline__ void give_back(const int32_t* row, int h, int32_t* li
     }
   }
 }
-// Rows of more entries than this take 16 loads a lane at a time (four ended sequences of up to 2000 pages: 7.6 us
-// against 8.6), shorter ones four (200 of 63 pages: 16.4 against 20.0).
+// Rows of more entries than this take 16 loads a lane at a time (one ended sequence of 1259 pages: 7.6 us
+// against 8.6), shorter ones four (198 of up to 125 pages: 16.4 against 20.0).
 constexpr int kLongRow = 256;
 constexpr int kClusterTokens = 40000;      // most tokens that one cluster takes
 
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(NT) paged_tables_kernel(const PagedTables a) {
 }
 
 // Positions and slots of many tokens, from the offsets, lengths and table entries of the first kernel: a
-// cluster's threads would take them in many turns (190,000 tokens 26.6 us, 7.7 this way).
+// cluster's threads would take them in many turns (184,000 tokens 26.6 us, 7.7 this way).
 constexpr int kSlotThreads = 256, kSlotTokens = 4;      // per thread
 __global__ void __launch_bounds__(kSlotThreads) paged_slots_kernel(const PagedTables a) {
   pdl_wait();
