@@ -450,9 +450,10 @@ SDPA_API int sdpa_paged4_append(const sdpa_paged4_append_params* p, sdpa_view k,
  * multiples of 32, the rotary fields unused, everything else as there.  Sums are fp32.  With H = Hv in {64, 128} and a
  * 16-bit type, for at most 16 rows of a sequence (H = 64: 32; max_new x query heads of a key head) the codes
  * enter the products as they are, and a weight times its key's scale rounded to fp16 (half a step each; of a
- * value's distance from the middle of its range in fp16, from its minimum in bf16); for more rows the weights, keys
- * and values enter rounded to dtype.  Queries beyond 2^110, and values that grow by more than 2^80 along a
- * sequence, may come out as infinities or NaN; an infinity in a query counts as NaN.
+ * value's distance from the middle of its range in fp16, from its minimum in bf16; products far below the largest of
+ * their row and 32 channels 2^-24 of that instead); for more rows the weights, keys and values enter rounded to dtype.
+ * Queries beyond 2^110, and values whose sum over the keys, with weights of up to 2^8, passes fp32's range, may come out as
+ * infinities or NaN; an infinity in a query counts as NaN.
  * workspace: sdpa_paged4_workspace_size(p) bytes, any contents, 256-byte aligned; the size depends on dtype, H
  * and Hv alone. */
 SDPA_API int sdpa_paged4_attn(const sdpa_paged_params* p, sdpa_view q, sdpa_view y, void* workspace, size_t workspace_bytes,

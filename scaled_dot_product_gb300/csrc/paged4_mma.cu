@@ -16,18 +16,22 @@
 //    the minima are summed in fp32.  In fp16 caches 8 is taken off every code by a further product with the same
 //    rounded operand (and 8 scales added to the minimum), so that the rounding touches a value's distance from the
 //    middle of its range and not from the minimum; in bf16 the output's rounding is far larger.
-//  - fp16's range: a warp's weights are exp2(score - m - L), m its row's running maximum (it may be
-//    passed by 2^8) and L the size of the scales it has seen (in log2, from -24 on; passed by 2^6): products
-//    stay below 2^15, and what is lost lies 2^-39 below the largest.
-// A unit's rows are dealt to WM warps (8 NT each), the keys of a tile to WK; each warp keeps its own m, L, sum and
+//  - fp16's range: a power of two for each row and group of channels, the factor, brings the largest product of weight and
+//    scale that the warp has seen there to [1/2, 1) whenever it is set.  That is anew where a score passes the running
+//    maximum by 2^4, or a scale times some row's factor 2^11: operands stay within 2^15, and one far below the largest
+//    of its row and group is off by 2^-24 of that at most.  It has to follow the products themselves: with one factor a
+//    warp, of the largest weight and the largest scale, a large value of no weight took the others' bits away.  Packed
+//    products keep its cost small (single tokens 536 us, 531 with one factor; 16 rows 132, 121); a sequence whose weight lies
+//    on values 2^-11 and less of all others takes up to 1.3 times as long, as every block asks for new factors.
+// A unit's rows are dealt to WM warps (8 NT each), the keys of a tile to WK; each warp keeps its own m, factors, sum and
 // accumulator, joined through shared memory at the end of a unit.
 //
 // One producer warp keeps a ring of tiles of keys full across unit boundaries. A page's records of a head lie
 // one after another, so whatever part of a page falls into a tile is one bulk copy. Rows of 80 (40) bytes put
 // the words that a warp reads at a time into different banks. About 400 instructions a block of 16 keys of 128
 // channels, half of them on the half-rate integer pipe, bound it: 128 single tokens, 1000 to 32000 keys, 64/8
-// heads of 128: 530 us, 4.9 TB/s of records (floor 383); fp16 573; 64 channels 295 (floor 191); four short
-// sequences 11.0 us. Keys that no row of the unit admits take a scale and a minimum of zero, since 0 x NaN is
+// heads of 128: 536 us, 4.9 TB/s of records (floor 383); fp16 588; 64 channels 296 (floor 191); four short
+// sequences 11.9 us. Keys that no row of the unit admits take a scale and a minimum of zero, since 0 x NaN is
 // not 0. Every wait is bounded: on expiry the kernel raises an abort flag, goes through its loops without
 // waiting, lets its own copies finish and records SDPA_ERR_TIMEOUT.
 #include <algorithm>
@@ -48,9 +52,10 @@ using namespace ptx;
 constexpr int kCtasPerSm = 2;
 constexpr int kOV = 1;                // a unit's cost beside its tiles, in tiles
 constexpr int kMinShare = 2;
-constexpr float kRescale = 8.f;       // log2 units a maximum may grow before the state is rescaled
-constexpr int kScaleRoom = 6;         // and a scale
-constexpr int kLeastL = -24, kMostL = 100;
+constexpr float kRescale = 4.f;       // log2 units a maximum may grow before the state is rescaled
+// An operand is at most 2^(kRescale + kScaleRoom) = 2^15: a scale times its row's factor stays within 2^kScaleRoom.
+constexpr int kScaleRoom = 11;
+constexpr int kMostF = 120;           // log2 of the largest factor, where a row has no product yet
 constexpr float kNone = -1e30f;       // the maximum of a row that has admitted no key: finite, so that differences are numbers
 
 template <int H, int NT, int WM>
@@ -67,6 +72,7 @@ struct Cfg {
   static constexpr int kPitch = H + 4;                     // floats of a row of the joining buffer
   static constexpr int kAcc = NW * 8 * NT * kPitch * 4;
   static constexpr int kStages = H == 64 ? (NT == 1 ? 2 : 8) : NT == 1 ? 2 : 3;
+  static constexpr bool kSharedFac = NT == 2 && H == 128;
   static constexpr int kSmem = kStages * 2 * kTile + kAcc + 128;
   static_assert(KW % 16 == 0, "a warp takes whole blocks of 16 keys");
 };
@@ -164,6 +170,7 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
   __shared__ float sm_m[WK][TM], sm_l[WK][TM], sm_f[WK][TM];
+  __shared__ __align__(8) float sm_fac[C::kSharedFac ? C::NW : 1][NT][G][8];
   __shared__ int abort_flag;
   const PagedAttn& a = args.a;
   const PagedWs& ws = args.ws;
@@ -387,9 +394,20 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
   const uint32_t vsel = r8 & 1 ? 0x7632u : 0x5410u;
 
   int full_lo = 0, full_hi = 0;                // keys that every row admits
-  float o[NT][G][2][4], mt[NT][2][G], m[NT][2], l[NT][2];      // m: maximum + L
-  int L = -1000;                               // unset
-  uint32_t s_most = 0;                         // 16-bit pattern of the largest scale that L has room for
+  float o[NT][G][2][4], mt[NT][2][G], m[NT][2], l[NT][2];
+  // Factors of a row's products of weight and scale, powers of two, which o holds too; in shared memory where registers are full
+  // (16 rows of 128 channels: 132 us, in registers 162).
+  float fac[C::kSharedFac ? 1 : NT][2][G];
+  float* my_fac = &sm_fac[C::kSharedFac ? warp : 0][0][0][2 * j4];
+  auto factors = [&](int n, int y) -> float2 {
+    if constexpr (C::kSharedFac) return *reinterpret_cast<const float2*>(my_fac + (n * G + y) * 8);
+    else return make_float2(fac[n][0][y], fac[n][1][y]);
+  };
+  auto set_factor = [&](int n, int x, int y, float f) {
+    if constexpr (C::kSharedFac) my_fac[(n * G + y) * 8 + x] = f;      // the same in the eight lanes of a row
+    else fac[n][x][y] = f;
+  };
+  uint32_t s_most = 0;                         // largest scale (its bits) of group j4 that every row's factor has room for
   int t = 0, st = 0, phase = 0;                // tile of w's unit, stage and its phase
   bool ok = true;
   // One loop for the products and the units' ends: straight-line code runs once per call from a
@@ -400,7 +418,6 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
       int tmp;
       row_keys(a, w.s, w.r.row0, tmp, full_hi);
       row_keys(a, w.s, w.r.row0 + w.r.rows - 1, full_lo, tmp);
-      L = -1000;
       s_most = 0;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -411,6 +428,7 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
 #pragma unroll
           for (int y = 0; y < G; ++y) {
             mt[n][x][y] = 0.f;
+            set_factor(n, x, y, pow2(kMostF));
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][y][x][e] = 0.f;
           }
@@ -487,61 +505,64 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
           }
         }
       }
-      // ---- running maximum and size of the scales
+      // ---- running maximum and factors
       // (a lane looks at one group of its two keys, the four lanes of a key at all of them)
       const unsigned char* own = vp + soff + 4 * (j4 & (G - 1));
-      const uint32_t most = max(*reinterpret_cast<const uint32_t*>(own), *reinterpret_cast<const uint32_t*>(own + 8 * kRow));
-      bool need = (most >> 16) > s_most && !edge;
+      uint32_t own0 = *reinterpret_cast<const uint32_t*>(own), own1 = *reinterpret_cast<const uint32_t*>(own + 8 * kRow);
       if (edge) {
-#pragma unroll
-        for (int y = 0; y < G; ++y) need = need || (max(vd[0][y], vd[1][y]) >> 16) > s_most;
+        if (key0 + r8 < w.r.lo || key0 + r8 > w.r.hi) own0 = 0u;
+        if (key0 + r8 + 8 < w.r.lo || key0 + r8 + 8 > w.r.hi) own1 = 0u;
       }
-      const float room = kRescale - (float)L;
+      bool need = (max(own0, own1) >> 16) > s_most;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) need = need || fmaxf(s[n][x], s[n][2 + x]) > m[n][x] + room;
+        for (int x = 0; x < 2; ++x) need = need || fmaxf(s[n][x], s[n][2 + x]) > m[n][x] + kRescale;
       if (__any_sync(0xffffffffu, need)) {
-        // sizes of the finite scales, and of minima 2^20 beyond them
-        float big = 0.f;
+        int most_f[G];                         // largest exponents of the factors, of rows with a key
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int y = 0; y < G; ++y) {
-            const float c = fabsf(high_half<T>(vd[x][y])), f = fabsf(low_half<T>(vd[x][y]));
-            if (c < INFINITY) big = fmaxf(big, c);
-            if (f < INFINITY) big = fmaxf(big, f * pow2(-20));
-          }
-#pragma unroll
-        for (int x = 1; x < 32; x <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
-        int L2 = max(kLeastL, min(log2_floor(big) + 1, kMostL));      // scales < 2^L2
-        if (L2 <= L + kScaleRoom && L > -1000) L2 = L;
-        const float old_L = (float)L, new_L = (float)L2;
+        for (int y = 0; y < G; ++y) most_f[y] = -126;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const float mx = rows_max(fmaxf(s[n][x], s[n][2 + x]));
             const float was = m[n][x];
-            float top = was - old_L;                     // kNone stays
-            if (mx > top + kRescale) top = mx;
-            m[n][x] = top + new_L;
+            if (mx > was + kRescale) m[n][x] = mx;
             const float corr = ex2_approx(was - m[n][x]);
+            const float p0 = ex2_approx(s[n][x] - m[n][x]), p1 = ex2_approx(s[n][2 + x] - m[n][x]);
             l[n][x] *= corr;
 #pragma unroll
             for (int y = 0; y < G; ++y) {
               mt[n][x][y] *= corr;
+              // The factor brings the largest product so far to [1/2, 1).  Of those before this block the old factor tells
+              // a lower bound, half its reciprocal.
+              const float c0 = fabsf(high_half<T>(vd[0][y])), c1 = fabsf(high_half<T>(vd[1][y]));
+              const float old = x ? factors(n, y).y : factors(n, y).x, had = corr * pow2(-log2_floor(old));
+              const float top = rows_max(fmaxf(c0 < INFINITY ? p0 * c0 : 0.f, c1 < INFINITY ? p1 * c1 : 0.f));
+              const int e = max(-126, min(-1 - log2_floor(fmaxf(0.5f * had, top)), kMostF));
+              const float f = had * pow2(e);
+              if (C::kSharedFac) __syncwarp();
+              set_factor(n, x, y, pow2(e));
+              if (m[n][x] > kNone) most_f[y] = max(most_f[y], e);
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                o[n][y][q][x] *= corr;
-                o[n][y][q][2 + x] *= corr;
+                o[n][y][q][x] *= f;
+                o[n][y][q][2 + x] *= f;
               }
             }
           }
-        L = L2;
-        const float most_s = pow2(min(L + kScaleRoom, 127));
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) s_most = __float_as_uint(most_s) >> 16;
-        else s_most = L + kScaleRoom > 15 ? 0x7bffu : (uint32_t)__half_as_ushort(__float2half_rn(most_s));
+        int e = most_f[0];
+#pragma unroll
+        for (int y = 0; y < G; ++y) {
+          most_f[y] = max(most_f[y], __shfl_xor_sync(0xffffffffu, most_f[y], 1));
+          most_f[y] = max(most_f[y], __shfl_xor_sync(0xffffffffu, most_f[y], 2));
+          if (y == 0 || (j4 & (G - 1)) == y) e = most_f[y];
+        }
+        if (C::kSharedFac) __syncwarp();
+        e = kScaleRoom - e;                    // a scale beyond 2^e asks again
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) s_most = e < -126 ? 0u : (uint32_t)(min(e, 127) + 127) << 7;
+        else s_most = e > 15 ? 0x7bffu : e < -126 ? 0u : (uint32_t)__half_as_ushort(__float2half_rn(pow2(e)));
       }
       // ---- weights
 #pragma unroll
@@ -566,8 +587,12 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint32_t b0 = transposed(pack_f16x2(s[n][0] * c0, s[n][1] * c0));
-          const uint32_t b1 = transposed(pack_f16x2(s[n][2] * c1, s[n][3] * c1));
+          const float2 fr = factors(n, y);
+          const f2_t f = f2_pack(fr.x, fr.y);
+          float v0, v1, v2, v3;
+          f2_unpack(f2_mul(f2_mul(f2_pack(s[n][0], s[n][1]), f), f2_pack(c0, c0)), v0, v1);
+          f2_unpack(f2_mul(f2_mul(f2_pack(s[n][2], s[n][3]), f), f2_pack(c1, c1)), v2, v3);
+          const uint32_t b0 = transposed(pack_f16x2(v0, v1)), b1 = transposed(pack_f16x2(v2, v3));
           mt[n][0][y] = fmaf(s[n][0], m0, fmaf(s[n][2], m1, mt[n][0][y]));
           mt[n][1][y] = fmaf(s[n][1], m0, fmaf(s[n][3], m1, mt[n][1][y]));
           mma(o[n][y][0], xa & kLow, xa & kHigh, xb & kLow, xb & kHigh, b0, b1);
@@ -599,9 +624,12 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
 #pragma unroll
         for (int y = 0; y < G; ++y) {
           const float base = rows_sum(mt[n][x][y]);
+          // 2^24 (16-fold codes: 2^20) over the factor, in two steps that stay within fp32
+          const int e = 24 - log2_floor(x ? factors(n, y).y : factors(n, y).x);
+          const float h0 = pow2(e / 2), h1 = pow2(e - e / 2), h2 = pow2(e - e / 2 - 4);
           *reinterpret_cast<float4*>(dst + 32 * y) =
-              make_float4(fmaf(o[n][y][0][x], pow2(24), base), fmaf(o[n][y][0][2 + x], pow2(20), base),
-                          fmaf(o[n][y][1][x], pow2(24), base), fmaf(o[n][y][1][2 + x], pow2(20), base));
+              make_float4(fmaf(o[n][y][0][x] * h0, h1, base), fmaf(o[n][y][0][2 + x] * h0, h2, base),
+                          fmaf(o[n][y][1][x] * h0, h1, base), fmaf(o[n][y][1][2 + x] * h0, h2, base));
         }
         const float sum = rows_sum(l[n][x]);
         if (r8 == 0) {
@@ -667,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
 }
 
 // Rows per unit: the smallest of 8, 16 and, of 64 channels, 32 that holds all rows of a sequence with max_new
-// tokens, at most the widest.  16 sequences of 2000 to 30000 keys, 8 key heads: 8 / 16 rows of 128 channels 89 / 166 us (340
+// tokens, at most the widest.  16 sequences of 2000 to 30000 keys, 8 key heads: 8 / 16 rows of 128 channels 89 / 166 us (400
 // bytes of spills at 16; two warps of eight rows each, without spills, 188), 8 / 16 / 32 rows of 64 75 / 88 / 142.
 int mma4_tm(const PagedAttn& a) {
   const int64_t rows = (int64_t)a.max_new * a.g.group;
@@ -686,7 +714,7 @@ template <typename T, int H, int NT, int WM>
 cudaError_t launch_wm(const PagedAttn& a, sdpa_dtype dt, void* wsp, cudaStream_t st) {
   using C = Cfg<H, NT, WM>;
   // 228 KB per SM, of which each CTA takes 1 KB for itself
-  static_assert(C::kSmem + 3 * C::WK * C::TM * 4 + 2048 + 1024 <= 233472 / kCtasPerSm, "shared memory");
+  static_assert(C::kSmem + 3 * C::WK * C::TM * 4 + C::NW * NT * C::G * 32 + 2048 + 1024 <= 233472 / kCtasPerSm, "shared memory");
   const int ctas = paged_sms() * kCtasPerSm;
   if (ctas <= 0) return cudaErrorInvalidDevice;
   // per device: set at every call (the attribute belongs to the current context)
