@@ -100,11 +100,13 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
 }
 
+// Two weights times a power of two, in fp32: in fp16 the factor itself may lie below the type's range while the
+// products do not.
 template <typename T>
-__device__ __forceinline__ uint32_t times2(uint32_t a, uint32_t b) {
-  using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
-  const T2 y = __hmul2(*reinterpret_cast<const T2*>(&a), *reinterpret_cast<const T2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&y);
+__device__ __forceinline__ uint32_t times2(uint32_t w, float f) {
+  const T* e = reinterpret_cast<const T*>(&w);
+  const float a = Elem<T>::to_f32(e[0]) * f, b = Elem<T>::to_f32(e[1]) * f;
+  return std::is_same<T, __half>::value ? pack_f16x2(a, b) : pack_bf16x2(a, b);
 }
 
 // A word's eight codes as four pairs of values, minimum + scale * code rounded once.
@@ -606,7 +608,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = m_new;
             l *= corr;
             sum *= corr;
-            const uint32_t corr2 = BF ? pack_bf16x2(corr, corr) : pack_f16x2(corr, corr);
             if (c == 1) {
               tmem_st_wait();
 #pragma unroll 1
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld8(tP + i * 8, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = times2<T>(o[e], corr2);
+                for (int e = 0; e < 8; ++e) o[e] = times2<T>(o[e], corr);
                 tmem_st8(tP + i * 8, o);
               }
             }

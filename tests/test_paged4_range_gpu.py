@@ -141,3 +141,27 @@ def test_weights_fall_as_scales_grow(dtype, H):
         k = (-e * 0.6931 / H ** 0.5).view(-1, 1).repeat(1, H) * (0.0 if kind == 3 else 1.0)
         v = torch.randn(1500, H, generator=g) * 2.0 ** (e - (8 if dtype == HF else 30)).view(-1, 1)
         check(*problem(dtype, H, q, k, v))
+
+
+@pytest.mark.parametrize("octaves", [18, 24, 25, 26, 28])
+@pytest.mark.parametrize("H", [64, 128])
+def test_a_maximum_that_moves_far_within_a_tile(H, octaves):
+    """Chunks in fp16: scores of the first half of a tile of 128 keys lie 7 octaves above the maximum so far and those of the second
+    half `octaves` above it, whose values are zero: the output is what the first half's weights, made anew for the larger
+    maximum, are worth.  Such a weight is rounded to fp16 twice, by 2^-25 of the maximum's power of two each where it is
+    subnormal, which is at most 2^-23 of the largest weight, and not by more than itself."""
+    q = torch.ones(40, 4, H)                   # 160 rows: each has every tile
+    k, v = torch.zeros(300, H), torch.zeros(300, H)
+    v[:192] = 1000 + 300 * torch.randn(192, H, generator=torch.Generator().manual_seed(1))
+    score = torch.zeros(300)
+    score[128:192], score[192:200] = 7.0, octaves
+    k += (score * 0.6931 / H ** 0.5).view(-1, 1)
+    r, k4, v4, vs = problem(HF, H, q, k, v, 40)
+    want, tol = paged4_attn64(r, vs, operands="values")
+    p = 2.0 ** (score.double() - octaves)
+    far = torch.minimum(1.01 * p, torch.tensor(2.0 ** -23, dtype=torch.float64))
+    tol = tol + (far @ v.abs().double() * 1.01 / p.sum()).view(1, 1, H)
+    y = sdpa.sdpa_paged4_attn(r.q.cuda(), k4.cuda(), v4.cuda(), r.table.cuda(), r.kv_lens.cuda(), cu_new=r.cu.cuda(), max_new=40)
+    assert sdpa.sdpa_last_kernel_name().startswith("paged4_tc_f16") and sdpa.sdpa_query_status() == 0
+    err = (y.cpu().double() - want).abs()
+    assert (err <= tol).all(), (err / tol).max()
