@@ -386,7 +386,7 @@ SDPA_API size_t sdpa_paged_workspace_size(const sdpa_paged_params* p);
  * of range is reported by sdpa_query_status as SDPA_ERR_INVALID and nothing outside the given
  * buffers is touched: a length beyond the table's width, or more new tokens than `tokens` rows, is cut
  * off; a missing page or a page id outside [0, num_pages) makes its tokens' slots -1 (a missing one
- * its table entry too), and such ids are not given back.
+ * its table entry too), and such ids are not given back; nor are pages for which the list has no room.
  * kv_lens may be past_lens, and free_count_out free_count (in place); other arrays share nothing.
  * Without in-place arguments a call repeated on the same inputs writes the same outputs.  B <= 8192. */
 typedef struct {

@@ -1354,6 +1354,13 @@ int sdpa_query_status(sdpa_stream_t stream) {
   if (status) return fail(SDPA_ERR_TIMEOUT, "a bounded device wait expired (code %d)", status);
   if (rot_status || norm_status || (app_status & kPagedBadPosition))
     return fail(SDPA_ERR_INVALID, "a rotary position fell outside its cos/sin cache");
+  // of the tables, what also makes entries that are no pages comes first
+  if (tables_status & kPagedBadLength)
+    return fail(SDPA_ERR_INVALID, "past_lens is negative, or past_lens or new_lens pass the page table's width or the rows: kv_lens and "
+                                  "cu_new are cut off");
+  if (tables_status & kPagedFullList)
+    return fail(SDPA_ERR_INVALID, "the list of free pages would hold more than num_pages: free_count is too large or pages are given "
+                                  "back twice (kv_lens and cu_new hold)");
   if ((app_status | paged_status) & kPagedBadPage) return fail(SDPA_ERR_INVALID, "a page id fell outside [0, num_pages)");
   if ((app_status | paged_status) & kPagedBadLength)
     return fail(SDPA_ERR_INVALID, "kv_lens or cu_new contradict the batch or the page table's width");

@@ -70,6 +70,6 @@ cudaError_t take_paged_tables_status(int* status);
 cudaError_t take_bounds_paged_tables(int* site);
 
 // Status bits beside those of paged.h.
-enum { kPagedNoPages = 8, kPagedBadSlot = 16 };
+enum { kPagedNoPages = 8, kPagedBadSlot = 16, kPagedFullList = 32 };
 
 }  // namespace sdpa

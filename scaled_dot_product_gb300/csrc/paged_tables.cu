@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(NT) paged_tables_kernel(const PagedTables a) {
   auto pages_of = [&](int keys) { return div(keys + a.page_size - 1); };
   const int count0 = a.free_count[0];
   const int c0 = min(max(count0, 0), a.num_pages);
-  if (count0 > a.num_pages) bad |= kPagedBadLength;
+  if (count0 > a.num_pages) bad |= kPagedFullList;
 
   // running sum over the block of x, before this thread's own; total: of all
   auto scan = [&](auto x, auto* sums, auto& total) {
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(NT) paged_tables_kernel(const PagedTables a) {
   }
   __syncthreads();
   const int64_t top = min((long long)c0 + back, (long long)a.num_pages);
-  if ((int64_t)c0 + back > a.num_pages) bad |= kPagedBadLength;
+  if ((int64_t)c0 + back > a.num_pages) bad |= kPagedFullList;
 
   // ---- pages given back, in the order of sequences and entries: a warp a sequence
   if (back > 0) {

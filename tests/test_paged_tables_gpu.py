@@ -108,6 +108,18 @@ def test_data_out_of_range_is_cut_off_and_reported():
     check(p)
 
 
+def test_what_is_reported_names_its_cause():
+    """Lengths that do not fit, and a list that would be fuller than the pool: a count beyond it, or pages given back that
+    were free already."""
+    base = problem([20, 5, 33], [3, 10, -4], 16, spare=20)
+    full = dict(count=len(base["free"]))
+    for change, says in ((dict(past=[20, 5, 10 ** 9]), "past_lens"), (dict(tokens=5), "new_lens"), (dict(count=10 ** 9), "num_pages"),
+                         (full, "given back twice"), (dict(full, new=[0, 0, -1]), "free pages")):
+        check({**base, **change})
+        _, status, text = call({**base, **change})
+        assert status == sdpa.SDPA_ERR_INVALID and says in text, (change, text)
+
+
 def test_random_steps():
     rng = random.Random(7)
     for seed in range(40):
