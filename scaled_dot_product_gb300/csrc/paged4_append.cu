@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4App
   if (held.p) {
     T out[kCh];
 #pragma unroll
-    for (int e = 0; e < kCh; ++e) out[e] = Elem<T>::from_f32(__fadd_rn(__fmul_rn(code[e], s), lo));
+    for (int e = 0; e < kCh; ++e) out[e] = Elem<T>::from_f32(fmaf(code[e], s, lo));      // the product alone may pass fp32
     uint4* h = reinterpret_cast<uint4*>(reinterpret_cast<T*>(const_cast<void*>(held.p)) + place<kWide>(held, head, t) + c0);
 #pragma unroll
     for (int i = 0; i < kCh / Elem<T>::kVec; ++i) h[i] = reinterpret_cast<const uint4*>(out)[i];

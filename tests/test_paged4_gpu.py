@@ -138,6 +138,22 @@ def test_append_groups_at_the_edges():
         assert torch.isfinite(h[[0, 1, 2, 3, 4, 8, 9]]).all()
 
 
+def test_append_held_rows_near_the_end_of_fp32():
+    """bf16 groups whose 15 scales pass fp32's largest number while minimum + 15 scales does not: the value is held as
+    defined, not as an infinity."""
+    u = 2.0 ** 120
+    x = torch.zeros(4, 1, 32, dtype=BF)
+    for i, (hi, lo) in enumerate(((252.0, -3.953125), (251.0, -4.96875), (253.0, -2.984375), (3.953125, -252.0))):
+        x[i, 0, 0], x[i, 0, 1] = hi * u, lo * u
+    value, scale = unpack64(pack(x, BF), 32, BF)
+    assert torch.isfinite(value).all() and (15 * scale >= 2.0 ** 128).all()
+    kp = torch.zeros(1, 1, 4, row_bytes(32, BF), dtype=torch.uint8, device="cuda")
+    vp, held = torch.zeros_like(kp), torch.zeros_like(x).cuda()
+    sdpa.sdpa_paged4_append(x.cuda(), x.cuda(), kp, vp, torch.arange(4, device="cuda"), v_held=held)
+    # rounded once to the type, from an fp32 number
+    assert ((held.cpu().double() - value).abs() <= (HALF_STEP[BF] + 2.0 ** -24) * value.abs()).all()
+
+
 def test_append_bad_slots_and_positions():
     k = rows(4, 2, 64, BF, 5)
     cos, sin = (t.cuda() for t in rope_caches(10, 32, BF))
