@@ -448,10 +448,15 @@ SDPA_API int sdpa_paged4_append(const sdpa_paged4_append_params* p, sdpa_view k,
 
 /* sdpa_paged_attn over pools of records: k_pages and v_pages of p are those (strides in bytes), H and Hv
  * multiples of 32, the rotary fields unused, everything else as there.  Sums are fp32.  With H = Hv in {64, 128} and a
- * 16-bit type, for at most 16 rows of a sequence (H = 64: 32; max_new x query heads of a key head) the codes
- * enter the products as they are, and a weight times its key's scale rounded to fp16 (half a step each; of a
- * value's distance from the middle of its range in fp16, from its minimum in bf16; products far below the largest of
- * their row and 32 channels 2^-24 of that instead); for more rows the weights, keys and values enter rounded to dtype.
+ * 16-bit type the products have 16-bit operands:
+ *   - at most 16 rows of a sequence (H = 64: 32; rows are max_new x query heads of a key head): codes, scales and minima as
+ *     they are; queries as fp16 numbers times a power of two (bf16 keeps its bits down to 2^-27 of the row's largest); a
+ *     weight times its key's scale rounded to fp16 (half a step each; of a value's distance from the middle of its range
+ *     in fp16, from its minimum in bf16; products far below the largest of their row and 32 channels 2^-24 of that instead);
+ *   - more rows: keys and values, minimum + scale * code, and weights rounded to dtype (half a step each; in fp16 weights below
+ *     2^-14 of the largest 2^-24 of that or, where a maximum moved behind them, 2^-23).
+ * max_new chooses between the two, and with it the rounding and the time: with cu_new and max_new = 0 all packed rows count
+ * as one sequence's, so give it for batches of single tokens.  One chunk in a batch takes its single tokens along.
  * Queries beyond 2^110, and values whose sum over the keys, with weights of up to 2^8, passes fp32's range, may come out as
  * infinities or NaN; an infinity in a query counts as NaN.
  * workspace: sdpa_paged4_workspace_size(p) bytes, any contents, 256-byte aligned; the size depends on dtype, H

@@ -9,9 +9,10 @@
 //
 // Every element is read once and written once at 5/8 byte (and once more, as the cache holds it, where the
 // caller wants that). A thread has 8 channels, four lanes a group. The slot and the position of a token are one
-// load each: they are made once a step and serve every layer. Bound by instructions (400 a warp of 256 values):
-// two prompts of 2048 tokens, 8 bfloat16 heads of 128, rows as held wanted, 17.1 us (2.3 TB/s; 14.4 without
-// rotation, float32 17.8), 12,000 ragged tokens of float16 heads of 64 21.6 us, 64 single tokens 2.8 us.
+// load each: they are made once a step and serve every layer. Bound by instructions (420 a warp of 256 values,
+// 72 % of the issue slots) and by waits for loads: two prompts of 2048 tokens, 8 bfloat16 heads of 128, rows as held wanted,
+// 17.3 us (2.3 TB/s; 14.1 without rotation, float32 17.9), 12,000 ragged tokens of float16 heads of 64 21.9 us, 64 single
+// tokens 2.9 us. Without the rows as held the prompts take 14.6 us for 15.7, the chunks 19.0 for 20.3 (one set of inputs).
 #include <algorithm>
 #include <type_traits>
 

@@ -21,17 +21,18 @@
 //    maximum by 2^4, or a scale times some row's factor 2^11: operands stay within 2^15, and one far below the largest
 //    of its row and group is off by 2^-24 of that at most.  It has to follow the products themselves: with one factor a
 //    warp, of the largest weight and the largest scale, a large value of no weight took the others' bits away.  Packed
-//    products keep its cost small (single tokens 536 us, 531 with one factor; 16 rows 132, 121); a sequence whose weight lies
+//    products keep its cost small (single tokens 535 us, 531 with one factor; 16 rows 132, 121); a sequence whose weight lies
 //    on values 2^-11 and less of all others takes up to 1.3 times as long, as every block asks for new factors.
 // A unit's rows are dealt to WM warps (8 NT each), the keys of a tile to WK; each warp keeps its own m, factors, sum and
 // accumulator, joined through shared memory at the end of a unit.
 //
 // One producer warp keeps a ring of tiles of keys full across unit boundaries. A page's records of a head lie
 // one after another, so whatever part of a page falls into a tile is one bulk copy. Rows of 80 (40) bytes put
-// the words that a warp reads at a time into different banks. About 400 instructions a block of 16 keys of 128
-// channels, half of them on the half-rate integer pipe, bound it: 128 single tokens, 1000 to 32000 keys, 64/8
-// heads of 128: 536 us, 4.9 TB/s of records (floor 383); fp16 588; 64 channels 296 (floor 191); four short
-// sequences 11.9 us. Keys that no row of the unit admits take a scale and a minimum of zero, since 0 x NaN is
+// the words that a warp reads at a time into different banks. About 380 instructions a block of 16 keys of 128
+// channels, half of them on the half-rate integer pipe, in chains that 14 warps an SM do not cover: 55 % of the issue
+// slots and 50 % of that pipe are taken (32 single tokens), and a fixed latency is what a warp waits for most. 128 single
+// tokens, 1000 to 32000 keys, 64/8 heads of 128: 535 us, 4.9 TB/s of records (floor 383); fp16 586; 64 channels 296 (floor
+// 191); four short sequences 11.7 us. Keys that no row of the unit admits take a scale and a minimum of zero, since 0 x NaN is
 // not 0. Every wait is bounded: on expiry the kernel raises an abort flag, goes through its loops without
 // waiting, lets its own copies finish and records SDPA_ERR_TIMEOUT.
 #include <algorithm>
@@ -695,8 +696,9 @@ __global__ void __launch_bounds__(Cfg<H, NT, WM>::kThreads, kCtasPerSm) paged4_m
 }
 
 // Rows per unit: the smallest of 8, 16 and, of 64 channels, 32 that holds all rows of a sequence with max_new
-// tokens, at most the widest.  16 sequences of 2000 to 30000 keys, 8 key heads: 8 / 16 rows of 128 channels 89 / 166 us (400
-// bytes of spills at 16; two warps of eight rows each, without spills, 188), 8 / 16 / 32 rows of 64 75 / 88 / 142.
+// tokens, at most the widest.  16 sequences of 2000 to 30000 keys, 8 key heads, bf16: 8 / 16 rows of 128 channels
+// 79 / 132 us (400 bytes of spills at 16; two warps of eight rows each, without spills, took 188 where that took 166), 8 /
+// 16 / 32 rows of 64 50 / 75 / 130.
 int mma4_tm(const PagedAttn& a) {
   const int64_t rows = (int64_t)a.max_new * a.g.group;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : paged4_mma_rows(a.g.H);

@@ -4,10 +4,10 @@
 // that a score's part is scale * sum(q * code) + minimum * sum(q).  LPK lanes hold a key; the 128 / LPK
 // lane groups of a block take different keys and keep their own running maximum, sum and
 // accumulator of TM query rows, joined in shared memory at the end of a unit (and between CTAs by
-// the joining kernel of the caches in the model's type).  It serves fp32, whose sums the 16-bit
-// tensor products cannot carry, and head sizes that the tensor-core kernels do not tile.  Eight float32 sequences of 500 to
-// 4000 keys, 16/4 heads of 64, 21.2 us (latency); 16 of 500 to 16000 keys, 64/8 heads of 128, 296 us (0.75 TB/s: arithmetic,
-// four rows a unit).  Registers leave two CTAs an SM at four rows.
+// the joining kernel of the caches in the model's type).  It serves fp32, since the tensor-core
+// kernels take a query and a weight as one 16-bit operand each, and head sizes that those do not tile.
+// Eight float32 sequences of 500 to 4000 keys, 16/4 heads of 64, 21.3 us (latency); 16 of 500 to 16000 keys, 64/8 heads
+// of 128, 296 us (0.75 TB/s: arithmetic, four rows a unit).  Registers leave two CTAs an SM at four rows.
 #include <algorithm>
 
 #include "paged4.h"

@@ -14,6 +14,9 @@
 //   warps 12-15   keys and values: a thread has one record of each tile, loads it a tile ahead and writes
 //                 its values, rounded to the type, into the ring in the operands' layout
 //
+// Issue order, softmax roles, joining, abort path and teardown are those of paged_tc.cu, for a ring that warps fill instead of
+// copies: what is mended in a wait or in the abort path of one has to be mended in the other.
+//
 // Every unit makes its operands anew from the codes, which 256 rows share. A code becomes the last bits of 1024
 // (fp16) or 128 (bf16), less that number, times the scale, plus the minimum: exact up to the one rounding to
 // the type, as the tensor cores' operands are 16-bit (half a step, like the keys and values of a cache in the
@@ -21,10 +24,10 @@
 // the unit admits become zeros, since 0 x NaN is not 0. The softmax takes 64 columns of its scores at a time,
 // which fits the registers that 16 warps leave: a running maximum is passed by at most 2^8, and where it has to
 // move, the weights and products made with it are rescaled by a power of two. A chunk of 2048 tokens over 32000
-// keys, 32/8 heads of 128: 868 us, 1224 TFLOP/s (64 % of the measured rate); of 64: 742 us; softmax and record
-// warps wait for one another's issue slots (without the softmax 697). Every wait is bounded: on expiry the
-// kernel raises an abort flag, lets its own copies and products finish, frees its tensor memory and records
-// SDPA_ERR_TIMEOUT.
+// keys, 32/8 heads of 128: 870 us, 1223 TFLOP/s (64 % of the measured rate; pages in the type take 721); of 64: 720 us
+// (625); softmax and record warps wait for one another (without the softmax 697; tensor pipe 45 %, issue slots
+// 46 %). Every wait is bounded: on expiry the kernel raises an abort flag, lets its own copies and products finish,
+// frees its tensor memory and records SDPA_ERR_TIMEOUT.
 #include <algorithm>
 #include <cstdlib>
 #include <type_traits>
@@ -834,8 +837,8 @@ cudaError_t launch_h(bool bf, bool cap, const CUtensorMap& tq, const TcArgs& t, 
 }  // namespace
 
 // More rows of a sequence than the widest unit of the warp-level products holds: 16 of 128 channels, 32 of 64.  16
-// sequences of 2000 to 30000 keys, 8 key heads of 128 / 64: up to 128 rows 229 / 208 us here; 16 rows 166 / 88, 32 rows 279 /
-// 142, 64 rows 493 / 248 there.
+// sequences of 2000 to 30000 keys, 8 key heads of 128 / 64: up to 128 rows 227 / 208 us here; 16 rows 132 / 75, 32 rows 279 /
+// 130, 64 rows 493 / 248 there (64 rows, and 32 of 128, before each row and group had a factor of its own).
 bool paged4_tc_supported(const PagedAttn& a, sdpa_dtype dt) {
   return paged4_mma_supported(a.g.H, a.g.Hv, dt) && (int64_t)a.max_new * a.g.group > paged4_mma_rows(a.g.H);
 }

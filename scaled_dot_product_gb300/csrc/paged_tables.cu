@@ -10,7 +10,7 @@
 // the order of sequences, whatever the number of threads: results do not vary.  The cluster's barrier
 // orders the entries given back before those taken, and the inputs' reads before the outputs that may
 // be the inputs themselves.  Bound by latency (a chain of lengths, scans, barrier, list or table,
-// slot): 64 sequences of a token, one ended, 7.6 us, 2000 sequences with 15,000 tokens 16.4, 48 prompts of 184,000 tokens 7.7.
+// slot): 64 sequences of a token, one ended, 7.5 us, 2000 sequences with 15,000 tokens 16.4, 48 prompts of 184,000 tokens 7.7.
 #include <algorithm>
 
 #include "paged4.h"
@@ -83,10 +83,13 @@ __device__ __forceinline__ void give_back(const int32_t* row, int h, int32_t* li
     }
   }
 }
-// Rows of more entries than this take 16 loads a lane at a time (one ended sequence of 1259 pages: 7.6 us
-// against 8.6), shorter ones four (198 of up to 125 pages: 16.4 against 20.0).
+// Rows of more entries than this take 16 loads a lane at a time, shorter ones four.  16 of 64 sequences ended, of 125 / 256 /
+// 400 / 1259 pages: 12.9 / 12.9 / 13.9 / 29.0 us with 16 loads, 8.9 / 11.8 / 17.6 / 35.7 with four; 200 of 2000: 16.5 / 16.6 /
+// 17.1 / 30.6 and 12.6 / 15.1 / 19.8 / 34.5.
 constexpr int kLongRow = 256;
-constexpr int kClusterTokens = 40000;      // most tokens that one cluster takes
+// Most tokens that one cluster takes.  25,000 / 40,000 / 60,000 tokens of 256 sequences: 7.7 / 9.1 / 11.5 us in one, 8.6 / 8.3 /
+// 8.7 in two kernels; of 1000: 8.5 / 10.2 / 12.8 and 10.7 / 10.1 / 9.5.
+constexpr int kClusterTokens = 40000;
 
 // kRows: positions and slots too; else paged_slots_kernel writes them.
 template <int NT, bool kRows>
@@ -338,6 +341,8 @@ cudaError_t launch_nt(const PagedTables& a, int ctas, cudaStream_t st) {
 
 }  // namespace
 
+// One CTA for few tokens.  256 sequences, 256 / 1024 / 2048 / 4096 tokens: 3.7 / 5.2 / 7.5 / 13.5 us with 256 threads, 4.4 / 4.8 /
+// 5.5 / 7.9 with 1024, 4.4 / 4.8 / 4.7 / 5.4 with eight CTAs.
 cudaError_t launch_paged_tables(const PagedTables& a, cudaStream_t st) {
   if (a.B <= 256 && a.tokens <= 1024) return launch_nt<256, true>(a, 1, st);
   if (a.tokens <= kClusterTokens) return launch_nt<1024, true>(a, a.tokens <= 4096 ? 1 : 8, st);

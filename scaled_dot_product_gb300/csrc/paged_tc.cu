@@ -22,7 +22,8 @@
 // TFLOP/s (64/8 heads of 64: 194 us, 709); single tokens through this kernel 6.4 TB/s.  Running maxima
 // move only when they grow by more than 2^8.  The weights enter the second product rounded to the
 // element type (half a step each), since its operands are 16-bit; their sum takes them unrounded.
-// 168 registers at launch, 252 bytes of spills a thread.  Every wait is bounded: on expiry the kernel
+// 168 registers at launch, 252 bytes of spills a thread.  paged4_tc.cu has the same roles, waits and abort path over
+// records of 4 bits a value: what is mended in one has to be mended in the other.  Every wait is bounded: on expiry the kernel
 // raises an abort flag, lets its own copies and products finish, frees its tensor memory and records
 // SDPA_ERR_TIMEOUT.
 #include <algorithm>

@@ -684,7 +684,11 @@ def sdpa_paged4_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
                      scale: Optional[float] = None, softcap: float = 0.0, causal="lower_right", window: int = -1,
                      head_sink: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, workspace=None,
                      stream=None) -> torch.Tensor:
-    """sdpa_paged_attn over pools of records of 4 bits a value (sdpa_paged4_append), with the same arguments."""
+    """sdpa_paged_attn over pools of records of 4 bits a value (sdpa_paged4_append), with the same arguments.
+
+    max_new (most new tokens of one sequence) chooses the kernel, its rounding and its time: few rows take the codes exactly
+    and round a weight times its scale, more rows round keys, values and weights to the type.  Left out beside cu_new, all
+    rows count as one sequence's, which sends more than a few single tokens to the kernel for chunks."""
     b, entry = _native()
     fn, size, mode = entry["sdpa_paged4_attn"], entry["sdpa_paged4_workspace_size"], _causal(causal)
     call = lambda h: b.paged4_attn(fn, size, h, q, k_pages, v_pages, page_table, kv_lens, cu_new, scale, softcap, mode, window,
